@@ -268,8 +268,7 @@ def prepare(case, seed):
                  head_out=torch.empty(1, dtype=torch.int32, device="cuda"),
                  seq_lens=torch.empty(b, dtype=torch.int32, device="cuda"),
                  cu_new=torch.empty(b + 1, dtype=torch.int32, device="cuda"),
-                 slots=torch.empty(sum(new) + case["pad"], dtype=torch.int32, device="cuda"),
-                 scratch=torch.empty(b, dtype=torch.int32, device="cuda"))
+                 slots=torch.empty(sum(new) + case["pad"], dtype=torch.int32, device="cuda"))
         return s
     heads, d, dt = case["heads"], case["d"], DTYPES[case["dtype"]]
     if case["op"] == "append":
@@ -299,7 +298,6 @@ def prepare(case, seed):
         s.update(total=n, start=torch.zeros(case["seqs"], dtype=torch.int32, device="cuda"),
                  cu=torch.empty(case["seqs"] + 1, dtype=torch.int32, device="cuda"),
                  slots=torch.empty(n, dtype=torch.int32, device="cuda"),
-                 scratch=torch.empty(case["seqs"], dtype=torch.int32, device="cuda"),
                  k_out=torch.empty((n, heads, d), dtype=dt, device="cuda"),
                  v_out=torch.empty((n, heads, d), dtype=dt, device="cuda"))
         return s
@@ -464,15 +462,14 @@ def _own(s):
     import block_sparse_attention_nsa_gb300 as nsa
     if s["op"] == "plan":
         nsa.page_plan(s["ctx_lens"], s["new_lens"], s["free"], s["head"], s["table"], s["page"],
-                      s["pages"], s["slots"], s["seq_lens"], s["cu_new"], s["head_out"],
-                      workspace=s["scratch"])
+                      s["pages"], s["slots"], s["seq_lens"], s["cu_new"], s["head_out"])
         return s["table"], s["seq_lens"], s["cu_new"], s["slots"], s["head_out"]
     if s["op"] == "append":
         nsa.kv4_append(s["pool"], s["k"], s["v"], s["slots"])
         return nsa.kv4_read(s["pool"], s["slots"], s["d"], s["k_out"], s["v_out"])
     if s["op"] == "read":
         nsa.page_slots(s["table"], s["start"], s["seq_lens"], s["page"], s["pool"].shape[0],
-                       s["slots"], s["cu"], workspace=s["scratch"])
+                       s["slots"], s["cu"])
         return (s["slots"], *nsa.kv4_read(s["pool"], s["slots"], s["d"], s["k_out"], s["v_out"]))
     return nsa.kv4_decode(s["q"], s["pool"], s["table"], s["seq_lens"], s["scale"],
                           sel_idx=s["sel"], window=s["window"], out=s["out"], lse=s["lse"],
