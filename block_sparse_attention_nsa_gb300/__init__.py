@@ -9,6 +9,8 @@ Names follow the C ABI in include/nsa_sel_attn.h:
   workspace_size, index, index_view, fwd, bwd, decode, step_host, get_status,
   window_select, fwd_window, bwd_window, gate_combine, gate_combine_bwd,
   compress_kv, cmp_attn_select, profile_enable, profile_collect.
+The 4-bit paged KV cache (include/nsa_kv4.h) is bound in kv4.py and offered here too:
+  page_plan, page_slots, kv4_pool, kv4_append, kv4_read, kv4_decode.
 """
 from __future__ import annotations
 
@@ -18,11 +20,17 @@ from typing import Optional
 
 import torch
 
+from .kv4 import (DEVERR_BAD_INDEX, DEVERR_BAD_SEQLENS, DEVERR_NO_PAGES, kv4_append, kv4_decode,
+                  kv4_decode_workspace_size, kv4_pool, kv4_read, page_plan, page_slots)
+from .kv4 import signatures as _kv4_signatures
+
 __all__ = ["Dims", "NsaError", "load", "workspace_size", "index", "index_view", "fwd", "bwd",
            "decode", "window_select", "fwd_window", "bwd_window", "gate_combine",
            "gate_combine_bwd", "compress_kv", "cmp_attn_select", "cmp_workspace_size",
            "staging_size", "step_host", "get_status", "profile_enable", "profile_collect",
-           "kernel_names", "make_dims", "LIB_PATH"]
+           "kernel_names", "make_dims", "LIB_PATH", "page_plan", "page_slots", "kv4_pool",
+           "kv4_append", "kv4_read", "kv4_decode", "kv4_decode_workspace_size",
+           "DEVERR_BAD_INDEX", "DEVERR_BAD_SEQLENS", "DEVERR_NO_PAGES"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnsa_sel.so")
@@ -94,6 +102,7 @@ def load():
         "nsa_sel_attn_profile_enable": (st, [i32]),
         "nsa_sel_attn_profile_collect": (st, [ctypes.POINTER(i32), ctypes.POINTER(f32)]),
         "nsa_status_string": (ctypes.c_char_p, [st]),
+        **_kv4_signatures(),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
