@@ -61,6 +61,7 @@ cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s);
 cudaError_t launch_kv4_append(int d, bool fp16, const Kv4RowParams &p, cudaStream_t s);
 cudaError_t launch_kv4_read(int d, bool fp16, const Kv4RowParams &p, cudaStream_t s);
 size_t kv4_decode_workspace(int d, int g, bool selected);
+int64_t kv4_decode_tiles(const Kv4DecodeParams &p);
 cudaError_t launch_kv4_decode(int d, bool fp16, const Kv4DecodeParams &p, cudaStream_t s);
 
 }  // namespace nsa

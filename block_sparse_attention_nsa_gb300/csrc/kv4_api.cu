@@ -233,6 +233,7 @@ nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_
   p.lse = lse;
   p.status = device_status;
   p.ws = workspace;
+  if (kv4_decode_tiles(p) >= (int64_t(1) << 31)) return NSA_ERR_UNSUPPORTED;
   return launched(launch_kv4_decode(dims->head_dim, dims->dtype == NSA_FP16, p,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -6,10 +6,10 @@
 // d + d / 8 bytes carry 4 d g operations, so HBM bounds a long cache if the codes become
 // operands in few instructions (at 6.8 TB/s each SM gets 41 codes a clock).
 //
-// Tensor-core form.  Keys are the rows of m16n8k16 (mma.sync: at most 16 query heads are
-// far from the 128 rows of a tcgen05 tile), heads the columns.  A code needs no
-// conversion: masked out of its word as the low bits of an fp16 it IS the subnormal
-// c * 2^-24 (or, at bits 4-7, 16 c * 2^-24), which the tensor core multiplies exactly.
+// Tensor-core form.  Keys are the rows of m16n8k16 (mma.sync: at most 8 query heads are far
+// from the 128 rows of a tcgen05 tile), heads the columns.  A code needs no conversion:
+// masked out of its word as the low bits of an fp16 it IS the subnormal c * 2^-24 (or, at
+// bits 4-7, 16 c * 2^-24), which the tensor core multiplies exactly.
 //   scores  acc_g = sum over the group's dimensions of q^ c, exact products in fp32;
 //           S = C_h (sum_g ks_g acc_g + kz_g Q_g), Q_g = sum q^ over the group, in fp32.
 //           q^ is q times a power of two per head (largest magnitude in [2^14, 2^15)), so
@@ -27,35 +27,46 @@
 // Each warp copies its tiles into its own ring of three by cp.async, K rows in place, V
 // rows reordered so that the four rows that a lane quartet reads together lie in different
 // banks.  K words go to the A operand as they are; V words of two keys are joined by byte
-// permutes, which puts neighbouring keys into one register.
+// permutes, which puts neighbouring keys into one register.  Each lane turns one key's V
+// scales and zeros into fp32 for all, in the place of the tile's own.
 //
-// Work.  kv4_seg_kernel: a known bound on a segment's (sequence, KV head) tiles; 1 to 8
-// warps share a segment, their results meet in shared memory.  kv4_long_kernel: lengths
-// only the device knows; every CTA takes an equal run of the batch's tiles whatever the
-// sequences' lengths, segments that cross a CTA's border leave partial results (at most
-// two a CTA), and kv4_merge_kernel joins those.
+// Work.  A segment is a (sequence, KV head, up to 8 of its query heads).  kv4_seg_kernel:
+// one CTA a segment, its eight warps taking the tiles in turn; for batches whose segments
+// all fit the GPU at once and have few tiles.  kv4_run_kernel: every warp takes an equal
+// run of the batch's tiles in segment order, whatever the lengths, which only the device
+// knows; a segment counts kOver tiles more than it has, about what starting one costs.
+// Segments inside a warp's run are written by that warp; those that cross into the next
+// warp's are joined in the CTA, and those that cross a CTA's border leave partial results
+// (at most two a CTA) for kv4_merge_kernel.
 #include "kv4.cuh"
 
 namespace nsa {
 
 constexpr int kK4Warps = 8;
-constexpr int kK4Stages = 3;
-constexpr int kK4MaxCtas = 320;      // CTAs of the long kernel at most
+constexpr int kK4Threads = kK4Warps * 32;
+constexpr int kK4Heads = 8;          // query heads of a segment at most
+constexpr int kStages = 3;           // tiles of a warp's ring
+constexpr int kOver = 4;             // tiles that a segment's start counts as
+constexpr int kK4MaxCtas = 320;      // CTAs of the run kernel at most
 constexpr float kSlack = 2.f;        // scores may exceed the reference maximum by this much
 constexpr float kPScale = 8192.f;    // P' <= 2^kSlack * kPScale < 65504
+constexpr float kMasked = -3e38f;    // raw score of a key that does not count
 
-// Words of codes that a lane holds of a K row, and groups of a row.
 template <int D>
 struct K4 {
   using T = Kv4Tile<D>;
   static constexpr int kG = T::kG;
-  static constexpr int kW = D / 32;
-  static constexpr int kRing = kK4Stages * T::kBytes;
-  static constexpr int kHeadPair = 2 * D + 2;   // floats of two heads' outputs in the merge area
+  static constexpr int kW = D / 32;             // words of codes that a lane holds of a K row
+  static constexpr int kHeadPair = 2 * D + 2;   // floats of two heads' outputs in an area
+  static constexpr int kRing = kStages * T::kBytes;
+  // A warp's results go to the ring's start; a first part that has to stay while the warp
+  // goes on takes the last stage.
+  static constexpr int kKept = (kStages - 1) * T::kBytes;
   static constexpr int kSmem = kK4Warps * kRing;
+  static_assert(kK4Heads / 2 * kHeadPair * 4 <= T::kBytes, "a stage holds an area");
 };
 
-// Partial results of a segment: g * (D + 2) floats: O (not divided), then m, l per head.
+// Where the parts of a segment that begins in CTA i and ends in another lie.
 struct K4Split {
   int32_t seg, parts;   // parts 0: no segment of this CTA continues in the next
 };
@@ -78,122 +89,148 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
   return x;
 }
-__device__ __forceinline__ float lds_half(uint32_t a) {
-  unsigned short x;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(a));
-  return __half2float(__ushort_as_half(x));
-}
-// The kG halves of row `row` of a parameter array, as floats.
+// The kG halves of entry `i` of a parameter array, packed; and as floats.
 template <int G>
-__device__ __forceinline__ void lds_par(uint32_t arr, int row, float (&x)[G]) {
+__device__ __forceinline__ uint32_t lds_par(uint32_t arr, int i) {
   if constexpr (G == 2) {
-    const float2 f = unpack2<true>(lds32(arr + row * 4));
-    x[0] = f.x;
-    x[1] = f.y;
+    return lds32(arr + i * 4);
   } else {
-    x[0] = lds_half(arr + row * 2);
+    unsigned short x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(arr + i * 2));
+    return x;
   }
+}
+template <int G>
+__device__ __forceinline__ void par_floats(uint32_t u, float (&x)[G]) {
+  const float2 f = unpack2<true>(u);
+  x[0] = f.x;
+  if constexpr (G == 2) x[1] = f.y;
 }
 
 // The query of a segment as B operands, and its sums and scale per head of the score tile.
-template <int D, int NT>
+template <int D>
 struct K4Query {
-  uint32_t f[NT][K4<D>::kW][4];      // [word of the row][dims (0,4), (1,5)/16, (2,6), (3,7)/16]
-  float sum[NT][2][K4<D>::kG];       // heads 2c, 2c + 1 of the lane
-  float mul[NT][2];
+  uint32_t f[K4<D>::kW][4];      // [word of the row][dims (0,4), (1,5)/16, (2,6), (3,7)/16]
+  float sum[2][K4<D>::kG];       // 2^-24 times the sums of q^, heads 2c, 2c + 1 of the lane
+  float mul[2];                  // raw score -> S, > 0
+};
+template <int D>
+struct K4RawQuery {
+  uint4 w[K4<D>::kW];
 };
 
-template <int D, int NT>
+template <int D>
 struct K4State {
-  float o[NT][K4<D>::kG][4][4];      // dims 64 gi + 8 r + 2 e (+1: 16 times), heads 2c, 2c + 1
-  float ps[NT][K4<D>::kG][4];        // sum of P'
-  float oz[NT][2][K4<D>::kG];        // this lane's share of sum p (z + 8 s)
-  float m[NT][2], l[NT][2];          // l: this lane's share
-  float vmax, rinv;                  // largest V scale allowed for, kPScale / it
+  float o[K4<D>::kG][4][4];      // dims 64 gi + 8 r + 2 e (+1: 16 times), heads 2c, 2c + 1
+  float ps[K4<D>::kG][4];        // sum of P'
+  float oz[2][K4<D>::kG];        // this lane's share of sum p (z + 8 s)
+  float m[2], l[2];              // reference maximum; l: this lane's share
+  float thr[2];                  // raw score above which m is raised
+  float vmax, rinv;              // largest V scale allowed for, kPScale / it
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
+    for (int gi = 0; gi < K4<D>::kG; ++gi)
 #pragma unroll
-      for (int gi = 0; gi < K4<D>::kG; ++gi)
+      for (int x = 0; x < 4; ++x) {
+        ps[gi][x] = 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          ps[t][gi][x] = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[t][gi][e][x] = 0.f;
-        }
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        m[t][u] = -INFINITY;
-        l[t][u] = 0.f;
-#pragma unroll
-        for (int gi = 0; gi < K4<D>::kG; ++gi) oz[t][u][gi] = 0.f;
+        for (int e = 0; e < 4; ++e) o[gi][e][x] = 0.f;
       }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      m[u] = thr[u] = -INFINITY;
+      l[u] = 0.f;
+#pragma unroll
+      for (int gi = 0; gi < K4<D>::kG; ++gi) oz[u][gi] = 0.f;
     }
     vmax = 0.f;
     rinv = 0.f;
   }
 };
 
-// q: the segment's g rows of D.  Lane (r, c) holds head r (+ 8) and the dimensions of the K
-// words that it reads.
-template <int D, int NT, bool kFp16>
-__device__ __forceinline__ void load_query(const uint16_t *q, int g, float scale_log2, int lane,
-                                           K4Query<D, NT> &out) {
+// A segment: its sequence, KV head and query heads, its keys [lo, len), its tiles.
+struct K4Seg {
+  int b, h, q0, g;           // q0: first query head, g: how many
+  int len, lo;
+  int first;                 // first tile (32 keys), without a selection
+  int tiles;                 // tiles that exist
+  const int32_t *pages;      // selection: kept pages and their first keys, in shared memory
+  const int32_t *keys;
+};
+
+// Unit u of a sequence: KV head u / parts, its query heads 8 * (u % parts) ...
+__device__ __forceinline__ void set_unit(const Kv4DecodeParams &p, int u, K4Seg &sg) {
+  const int parts = p.g > kK4Heads ? 2 : 1, part = parts == 2 ? u & 1 : 0;
+  sg.h = parts == 2 ? u >> 1 : u;
+  sg.q0 = sg.h * p.g + part * kK4Heads;
+  sg.g = min(kK4Heads, p.g - part * kK4Heads);
+}
+
+// Lane (r, c) holds head r and the dimensions of the K words that it reads.
+template <int D>
+__device__ __forceinline__ void fetch_query(const Kv4DecodeParams &p, const K4Seg &sg, int lane,
+                                            K4RawQuery<D> &raw) {
   constexpr int G = K4<D>::kG, W = K4<D>::kW;
   const int r = lane >> 2, c = lane & 3;
+  const uint16_t *q =
+      static_cast<const uint16_t *>(p.q) + ((int64_t)sg.b * p.h_q + sg.q0 + r) * D;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int head = t * 8 + r;
-    float x[W][8], big = 0.f, sum[G];
+  for (int i = 0; i < W; ++i) {
+    const int w = c * W + i, at = (w % G) * 64 + w / G * 8;
+    raw.w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < sg.g) raw.w[i] = __ldg(reinterpret_cast<const uint4 *>(q + at));
+  }
+}
+
+// Scaled by a power of two per head to a largest magnitude in [2^14, 2^15).  The sums of
+// q^ come from products with rows of ones (16 for the dimensions held as sixteenths).
+template <int D, bool kFp16>
+__device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale_log2, int lane,
+                                           K4Query<D> &out) {
+  constexpr int G = K4<D>::kG, W = K4<D>::kW;
+  const int c = lane & 3;
+  const uint32_t sign = scale_log2 < 0.f ? 0x80008000u : 0u;   // mul stays positive
+  uint32_t top = 0;          // magnitudes of 16-bit floats order as whole numbers
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const int p = c * W + i, j = p / G, gi = p % G;
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (head < g)
-        raw = __ldg(reinterpret_cast<const uint4 *>(q + (int64_t)head * D + gi * 64 + j * 8));
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  for (int i = 0; i < W; ++i) {
+    const uint4 w = raw.w[i];
+    top = __vmaxu2(__vmaxu2(top, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
+    top = __vmaxu2(__vmaxu2(top, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
+  }
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const float2 f = unpack2<kFp16>(top);
+  const float big = fmaxf(f.x, f.y);
+  const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
+  const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);   // 2^(14 - ex)
+  const float lo = up * 0.0625f;
+  float sum[G][4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const float2 f = unpack2<kFp16>(w[u]);
-        x[i][2 * u] = f.x;
-        x[i][2 * u + 1] = f.y;
-        big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-    }
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-    big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
-    const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);   // 2^(14 - ex)
+  for (int gi = 0; gi < G; ++gi)
 #pragma unroll
-    for (int gi = 0; gi < G; ++gi) sum[gi] = 0.f;
+    for (int x = 0; x < 4; ++x) sum[gi][x] = 0.f;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
+  for (int i = 0; i < W; ++i) {
+    const float2 a = unpack2<kFp16>(raw.w[i].x ^ sign), b = unpack2<kFp16>(raw.w[i].y ^ sign);
+    const float2 d = unpack2<kFp16>(raw.w[i].z ^ sign), e = unpack2<kFp16>(raw.w[i].w ^ sign);
+    out.f[i][0] = pack2<true>(a.x * up, d.x * up);
+    out.f[i][1] = pack2<true>(a.y * lo, d.y * lo);
+    out.f[i][2] = pack2<true>(b.x * up, e.x * up);
+    out.f[i][3] = pack2<true>(b.y * lo, e.y * lo);
+    // word c W + i belongs to group i % G
+    mma16816(sum[i % G], 0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u, out.f[i][0],
+             out.f[i][1]);
+    mma16816(sum[i % G], 0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u, out.f[i][2],
+             out.f[i][3]);
+  }
+  // a raw score counts in 2^-24: S = 2^(ex - 14 + 24) |scale| raw.  A scale of 0 keeps the
+  // masked scores below the others.
+  const float mul = fmaxf(ldexpf(fabsf(scale_log2), ex + 10), 1e-30f);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        x[i][u] *= up;
-        sum[i % G] += x[i][u];   // word c W + i belongs to group i % G
-      }
-      out.f[t][i][0] = pack2<true>(x[i][0], x[i][4]);
-      out.f[t][i][1] = pack2<true>(x[i][1] * 0.0625f, x[i][5] * 0.0625f);
-      out.f[t][i][2] = pack2<true>(x[i][2], x[i][6]);
-      out.f[t][i][3] = pack2<true>(x[i][3] * 0.0625f, x[i][7] * 0.0625f);
-    }
-    // acc counts in 2^-24: S = 2^(ex - 14 + 24) scale (sum ks acc + kz Q 2^-24)
-    const float mul = ldexpf(scale_log2, ex + 10);
+  for (int u = 0; u < 2; ++u) {
+    out.mul[u] = __shfl_sync(0xffffffffu, mul, (2 * c + u) * 4);
 #pragma unroll
-    for (int gi = 0; gi < G; ++gi) {
-      sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 1);
-      sum[gi] += __shfl_xor_sync(0xffffffffu, sum[gi], 2);
-      sum[gi] *= 5.9604644775390625e-8f;
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int from = (2 * c + u) * 4;
-      out.mul[t][u] = __shfl_sync(0xffffffffu, mul, from);
-#pragma unroll
-      for (int gi = 0; gi < G; ++gi)
-        out.sum[t][u][gi] = __shfl_sync(0xffffffffu, sum[gi], from);
-    }
+    for (int gi = 0; gi < G; ++gi) out.sum[u][gi] = sum[gi][u] * 5.9604644775390625e-8f;
   }
 }
 
@@ -225,14 +262,59 @@ __device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *tile, i
 }
 
 // One tile: keys key0 ... key0 + 31, of which those in [lo, len) count.
-template <int D, int NT>
+template <int D>
 __device__ __forceinline__ void attend_tile(uint32_t st, int key0, int lo, int len, int lane,
-                                            const K4Query<D, NT> &q, K4State<D, NT> &a) {
+                                            const K4Query<D> &q, K4State<D> &a) {
   using T = Kv4Tile<D>;
   constexpr int G = K4<D>::kG, W = K4<D>::kW;
   const int r = lane >> 2, c = lane & 3;
-  // ---- scores: rows r and r + 8 of both halves, heads 2c and 2c + 1 ----
-  float s[NT][2][4];
+  const bool ragged = key0 < lo || key0 + 32 > len;
+  // ---- the scales and zeros: K's of the lane's rows, V's of key `lane` for everyone ----
+  uint32_t ksu[4], kzu[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ksu[i] = lds_par<G>(st + T::kPar, i * 8 + r);
+    kzu[i] = lds_par<G>(st + T::kPar + T::kArr, i * 8 + r);
+  }
+  float vs[G], vz[G], vtop = 0.f;
+  par_floats<G>(lds_par<G>(st + T::kPar + 2 * T::kArr, lane), vs);
+  par_floats<G>(lds_par<G>(st + T::kPar + 3 * T::kArr, lane), vz);
+  if (ragged && (key0 + lane < lo || key0 + lane >= len)) {   // may be anything
+#pragma unroll
+    for (int gi = 0; gi < G; ++gi) vs[gi] = vz[gi] = 0.f;
+  }
+#pragma unroll
+  for (int gi = 0; gi < G; ++gi) vtop = fmaxf(vtop, vs[gi]);
+  if (__any_sync(0xffffffffu, vtop > a.vmax)) {               // a scale outgrew P's range
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+    const float vnew = __uint_as_float((__float_as_uint(vtop) & 0x7f800000u) + 0x00800000u);
+    const float rnew = __fdiv_rn(kPScale, vnew);              // powers of two: exact
+    const float grow = a.rinv > 0.f ? __fdiv_rn(rnew, a.rinv) : 0.f;
+    a.vmax = vnew;
+    a.rinv = rnew;
+#pragma unroll
+    for (int gi = 0; gi < G; ++gi)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        a.ps[gi][x] *= grow;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a.o[gi][e][x] *= grow;
+      }
+  }
+  __syncwarp();              // all have read the tile's own
+  const uint32_t vpar = st + T::kPar;                         // [32] s / reference, z + 8 s
+  if constexpr (G == 2)
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(vpar + lane * 16),
+                 "f"(vs[0] * a.rinv), "f"(vs[1] * a.rinv), "f"(fmaf(8.f, vs[0], vz[0])),
+                 "f"(fmaf(8.f, vs[1], vz[1]))
+                 : "memory");
+  else
+    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(vpar + lane * 8), "f"(vs[0] * a.rinv),
+                 "f"(fmaf(8.f, vs[0], vz[0]))
+                 : "memory");
+  // ---- raw scores: rows r and r + 8 of both halves, heads 2c and 2c + 1 ----
+  float s[2][4];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     uint32_t w[2][W];
@@ -246,145 +328,101 @@ __device__ __forceinline__ void attend_tile(uint32_t st, int key0, int lo, int l
       else
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[u][0]), "=r"(w[u][1]) : "r"(at));
     }
-    float acc[NT][G][4];
+    float acc[G][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int gi = 0; gi < G; ++gi)
 #pragma unroll
-      for (int gi = 0; gi < G; ++gi)
+      for (int x = 0; x < 4; ++x) acc[gi][x] = 0.f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc[t][gi][x] = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const int gi = i % G;
+    for (int i = 0; i < W; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t x = w[0][i] >> (8 * k), y = w[1][i] >> (8 * k);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma16816(acc[t][gi], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u,
-                   y & 0x00f000f0u, q.f[t][i][2 * k], q.f[t][i][2 * k + 1]);
+        mma16816(acc[i % G], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u,
+                 q.f[i][2 * k], q.f[i][2 * k + 1]);
       }
-    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float ks[G], kz[G];
-      const int row = half * 16 + u * 8 + r;
-      lds_par<G>(st + T::kPar, row, ks);
-      lds_par<G>(st + T::kPar + T::kArr, row, kz);
+      par_floats<G>(ksu[half * 2 + u], ks);
+      par_floats<G>(kzu[half * 2 + u], kz);
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int hd = 0; hd < 2; ++hd) {
+        float x = kz[0] * q.sum[hd][0];
+        if constexpr (G == 2) x = fmaf(kz[1], q.sum[hd][1], x);
 #pragma unroll
-        for (int hd = 0; hd < 2; ++hd) {
-          float x = 0.f;
-#pragma unroll
-          for (int gi = 0; gi < G; ++gi) {
-            x = fmaf(ks[gi], acc[t][gi][2 * u + hd], x);
-            x = fmaf(kz[gi], q.sum[t][hd][gi], x);
-          }
-          s[t][half][2 * u + hd] = x * q.mul[t][hd];
-        }
+        for (int gi = 0; gi < G; ++gi) x = fmaf(ks[gi], acc[gi][2 * u + hd], x);
+        s[half][2 * u + hd] = x;
+      }
     }
   }
-  // ---- V scales and zeros of the lane's four rows ----
-  float vs[4][G], vz[4][G];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    lds_par<G>(st + T::kPar + 2 * T::kArr, i * 8 + r, vs[i]);
-    lds_par<G>(st + T::kPar + 3 * T::kArr, i * 8 + r, vz[i]);
-  }
-  if (key0 < lo || key0 + 32 > len) {
+  if (ragged) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + i * 8 + r;
-      if (key < lo || key >= len) {   // their scales and zeros may be anything
-#pragma unroll
-        for (int gi = 0; gi < G; ++gi) vs[i][gi] = vz[i][gi] = 0.f;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          s[t][i >> 1][(i & 1) * 2] = s[t][i >> 1][(i & 1) * 2 + 1] = -INFINITY;
-      }
+      if (key < lo || key >= len) s[i >> 1][(i & 1) * 2] = s[i >> 1][(i & 1) * 2 + 1] = kMasked;
     }
   }
-  // ---- raise the references where a score or a scale outgrew them ----
-  float top[NT][2], vtop = 0.f;
+  // ---- raise the reference maximum where a score outgrew it ----
+  float top[2];
   bool up = false;
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int hd = 0; hd < 2; ++hd) {
-      top[t][hd] = fmaxf(fmaxf(s[t][0][hd], s[t][0][2 + hd]), fmaxf(s[t][1][hd], s[t][1][2 + hd]));
-      up |= top[t][hd] > a.m[t][hd] + kSlack;
-    }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int gi = 0; gi < G; ++gi) vtop = fmaxf(vtop, vs[i][gi]);
-  up |= vtop > a.vmax;
+  for (int hd = 0; hd < 2; ++hd) {
+    top[hd] = fmaxf(fmaxf(s[0][hd], s[0][2 + hd]), fmaxf(s[1][hd], s[1][2 + hd]));
+    up |= top[hd] > a.thr[hd];
+  }
   if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-    float grow = 1.f;
-    if (vtop > a.vmax) {
-      const float vnew = __uint_as_float((__float_as_uint(vtop) & 0x7f800000u) + 0x00800000u);
-      const float rnew = __fdiv_rn(kPScale, vnew);     // powers of two: exact
-      grow = a.rinv > 0.f ? __fdiv_rn(rnew, a.rinv) : 0.f;
-      a.vmax = vnew;
-      a.rinv = rnew;
-    }
+    for (int hd = 0; hd < 2; ++hd) {
+      float x = top[hd];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      const float mnew = fmaxf(a.m[hd], x * q.mul[hd]), alpha = ex2_approx(a.m[hd] - mnew);
+      a.m[hd] = mnew;
+      a.thr[hd] = __fdividef(mnew + kSlack, q.mul[hd]);
+      a.l[hd] *= alpha;
 #pragma unroll
-      for (int hd = 0; hd < 2; ++hd) {
-        float x = top[t][hd];
+      for (int gi = 0; gi < G; ++gi) {
+        a.oz[hd][gi] *= alpha;
+        a.ps[gi][hd] *= alpha;
+        a.ps[gi][2 + hd] *= alpha;
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-        const float mnew = fmaxf(a.m[t][hd], x), alpha = ex2_approx(a.m[t][hd] - mnew);
-        a.m[t][hd] = mnew;
-        a.l[t][hd] *= alpha;
-        const float both = alpha * grow;
-#pragma unroll
-        for (int gi = 0; gi < G; ++gi) {
-          a.oz[t][hd][gi] *= alpha;
-          a.ps[t][gi][hd] *= both;
-          a.ps[t][gi][2 + hd] *= both;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            a.o[t][gi][e][hd] *= both;
-            a.o[t][gi][e][2 + hd] *= both;
-          }
+        for (int e = 0; e < 4; ++e) {
+          a.o[gi][e][hd] *= alpha;
+          a.o[gi][e][2 + hd] *= alpha;
         }
       }
+    }
   }
+  __syncwarp();              // V's scales and zeros are in place
   // ---- weights ----
-  uint32_t pb[NT][G][2][2];   // B operands: [group][half][k rows 0-7, 8-15]
+  uint32_t pb[G][2][2];      // B operands: [group][half][k rows 0-7, 8-15]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float vsr[G], vc[G];
+    float vsr[G], vc[G], p[2];
+    if constexpr (G == 2)
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(vsr[0]), "=f"(vsr[1]), "=f"(vc[0]), "=f"(vc[1])
+                   : "r"(vpar + (i * 8 + r) * 16));
+    else
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                   : "=f"(vsr[0]), "=f"(vc[0])
+                   : "r"(vpar + (i * 8 + r) * 8));
 #pragma unroll
-    for (int gi = 0; gi < G; ++gi) {
-      vsr[gi] = vs[i][gi] * a.rinv;
-      vc[gi] = fmaf(8.f, vs[i][gi], vz[i][gi]);
+    for (int hd = 0; hd < 2; ++hd) {
+      p[hd] = ex2_approx(fmaf(s[i >> 1][(i & 1) * 2 + hd], q.mul[hd], -a.m[hd]));
+      a.l[hd] += p[hd];
+#pragma unroll
+      for (int gi = 0; gi < G; ++gi) a.oz[hd][gi] = fmaf(p[hd], vc[gi], a.oz[hd][gi]);
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float p[2];
-#pragma unroll
-      for (int hd = 0; hd < 2; ++hd) {
-        p[hd] = ex2_approx(s[t][i >> 1][(i & 1) * 2 + hd] - a.m[t][hd]);
-        a.l[t][hd] += p[hd];
-#pragma unroll
-        for (int gi = 0; gi < G; ++gi) a.oz[t][hd][gi] = fmaf(p[hd], vc[gi], a.oz[t][hd][gi]);
-      }
-#pragma unroll
-      for (int gi = 0; gi < G; ++gi)
-        pb[t][gi][i >> 1][i & 1] =
-            transpose8x8(pack2<true>(p[0] * vsr[gi], p[1] * vsr[gi]));
-    }
+    for (int gi = 0; gi < G; ++gi)
+      pb[gi][i >> 1][i & 1] = transpose8x8(pack2<true>(p[0] * vsr[gi], p[1] * vsr[gi]));
   }
   // ---- output: rows are dimensions, k the keys ----
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    uint32_t w[4][G];   // keys 2c, 2c + 1, 2c + 8, 2c + 9
+    uint32_t w[4][G];        // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t row = st + T::kV + (half * 16 + c + 4 * i) * T::kRow;
@@ -403,57 +441,106 @@ __device__ __forceinline__ void attend_tile(uint32_t st, int key0, int lo, int l
         const uint32_t sel = e < 2 ? 0x5410u : 0x7632u;
         const uint32_t x = __byte_perm(w[0][gi], w[1][gi], sel) >> (8 * (e & 1));
         const uint32_t y = __byte_perm(w[2][gi], w[3][gi], sel) >> (8 * (e & 1));
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-          mma16816(a.o[t][gi][e], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu,
-                   y & 0x00f000f0u, pb[t][gi][half][0], pb[t][gi][half][1]);
+        mma16816(a.o[gi][e], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u,
+                 pb[gi][half][0], pb[gi][half][1]);
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        mma16816(a.ps[t][gi], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u,
-                 pb[t][gi][half][0], pb[t][gi][half][1]);
+      mma16816(a.ps[gi], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb[gi][half][0],
+               pb[gi][half][1]);
     }
   }
 }
 
-// The tiles of a segment and where they lie.
-struct K4Seg {
-  int b, h, len, lo;
-  int first;                 // first tile (32 keys) of the segment, for a segment without selection
-  const int32_t *pages;      // kept pages and their first keys (selection), in shared memory
-  const int32_t *keys;
-};
+// Length of sequence b held to its table row, and the first key that its window shows.
+__device__ __forceinline__ int seq_len(const Kv4DecodeParams &p, int b, int32_t &err) {
+  const int cap = p.width << p.page_log2;
+  const int raw = __ldg(p.lens + b), len = min(max(raw, 0), cap);
+  if (raw != len) err |= NSA_DEVERR_BAD_SEQLENS;
+  return len;
+}
+__device__ __forceinline__ int seq_lo(const Kv4DecodeParams &p, int len) {
+  return p.window > 0 && len > p.window ? len - p.window : 0;
+}
 
-// Runs tiles t0, t0 + step, ... < t1 of a segment through this warp.
-template <int D, int NT>
-__device__ __forceinline__ void run_tiles(const Kv4DecodeParams &p, const K4Seg &sg, int t0,
-                                          int t1, int step, uint32_t ring, int lane,
-                                          const K4Query<D, NT> &q, K4State<D, NT> &a,
-                                          int32_t &err) {
+// Fills a segment's tiles.  With a selection: the kept blocks, valid, first of their value,
+// with a page in the pool, into this warp's lists.
+template <bool kSel>
+__device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg, int32_t *pages,
+                                             int32_t *keys, int lane, int32_t &err) {
+  int blk = -1;
+  if (kSel && lane < p.topk)
+    blk = __ldg(p.sel + ((int64_t)sg.h * p.num_seqs + sg.b) * p.topk + lane);
+  int32_t ignore = 0;        // reported once, where the lengths are first read
+  sg.len = seq_len(p, sg.b, ignore);
+  sg.lo = seq_lo(p, sg.len);
+  sg.first = sg.lo >> 5;
+  sg.tiles = ((sg.len + 31) >> 5) - sg.first;
+  if (kSel) {
+    const int nblk = (sg.len + (1 << p.page_log2) - 1) >> p.page_log2;
+    if (lane < p.topk && (blk < -1 || blk >= nblk)) err |= NSA_DEVERR_BAD_INDEX;
+    bool ok = blk >= 0 && blk < nblk;
+    const uint32_t same = __match_any_sync(0xffffffffu, blk);
+    ok = ok && (same & ((1u << lane) - 1u)) == 0;
+    int pg = -1;
+    if (ok) {
+      pg = __ldg(p.table + (int64_t)sg.b * p.width + blk);
+      if (pg < 0 || pg >= p.num_pages) {
+        ok = false;
+        err |= NSA_DEVERR_BAD_INDEX;
+      }
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, ok);
+    if (ok) {
+      const int at = __popc(m & ((1u << lane) - 1u));
+      pages[at] = pg;
+      keys[at] = blk << p.page_log2;
+    }
+    __syncwarp();
+    sg.pages = pages;
+    sg.keys = keys;
+    sg.tiles = __popc(m) << (p.page_log2 - 5);
+  }
+}
+
+// Tiles t0, t0 + step, ... (count of them) of a segment through this warp's ring: all its
+// stages, or those before a kept part.
+template <int D, bool kSel>
+struct K4Stream {
   using T = Kv4Tile<D>;
-  const int count = t0 < t1 ? (t1 - t0 + step - 1) / step : 0;
-  const int tpl = p.page_log2 - 5;
-  const int in_page = (1 << p.page_log2) - 1;
-  int my_page = -1, my_key = 0;       // of tile 32 * block + lane
-  int keys[kK4Stages];                // first keys of the tiles in the ring, -1: nothing to do
-  auto issue = [&](int n, int &key) {
-    key = -1;
+  const Kv4DecodeParams &p;
+  const K4Seg &sg;
+  const int t0, step, count, lane;
+  const uint32_t ring;
+  const bool full;                    // all stages
+  int my_page, my_key;                // of tile 32 * block + lane
+  uint32_t put, get;                  // stages to fill and to use next
+  int keys[kStages];                  // first keys of the tiles in the ring, -1: nothing to do
+
+  __device__ __forceinline__ K4Stream(const Kv4DecodeParams &p_, const K4Seg &sg_, int t0_,
+                                      int count_, int step_, uint32_t ring_, bool full_, int lane_)
+      : p(p_), sg(sg_), t0(t0_), step(step_), count(count_), lane(lane_), ring(ring_),
+        full(full_), my_page(-1), my_key(0), put(ring_), get(ring_) {}
+
+  __device__ __forceinline__ void next(uint32_t &stage) const {
+    stage += T::kBytes;
+    if (stage == ring + (full ? kStages : kStages - 1) * T::kBytes) stage = ring;
+  }
+  __device__ __forceinline__ int issue(int n, int32_t &err) {
+    int key = -1;
     if (n < count) {
+      const int tpl = p.page_log2 - 5;
       if ((n & 31) == 0) {            // look up the next 32 tiles' pages
         const int i = n + lane, t = t0 + i * step;
         my_page = -1;
         if (i < count) {
-          if (sg.pages) {
+          if (kSel) {
             my_page = sg.pages[t >> tpl];
             my_key = sg.keys[t >> tpl] + ((t & ((1 << tpl) - 1)) << 5);
           } else {
             my_key = (sg.first + t) << 5;
-            if (my_key < sg.len) {
-              my_page = __ldg(p.table + (int64_t)sg.b * p.width + (my_key >> p.page_log2));
-              if (my_page < 0 || my_page >= p.num_pages) {
-                my_page = -1;
-                err |= NSA_DEVERR_BAD_INDEX;
-              }
+            my_page = __ldg(p.table + (int64_t)sg.b * p.width + (my_key >> p.page_log2));
+            if (my_page < 0 || my_page >= p.num_pages) {
+              my_page = -1;
+              err |= NSA_DEVERR_BAD_INDEX;
             }
           }
           if (my_key >= sg.len || my_key + 32 <= sg.lo) my_page = -1;
@@ -463,375 +550,532 @@ __device__ __forceinline__ void run_tiles(const Kv4DecodeParams &p, const K4Seg 
       const int k0 = __shfl_sync(0xffffffffu, my_key, n & 31);
       if (pg >= 0) {
         key = k0;
-        copy_tile<D>(ring + (n % kK4Stages) * T::kBytes,
-                     p.pool + ((((int64_t)pg * p.h_k + sg.h) << tpl) + ((k0 & in_page) >> 5)) *
-                                  (int64_t)T::kBytes,
-                     lane);
+        const int64_t at = (((int64_t)pg * p.h_k + sg.h) << tpl) +
+                           ((k0 & ((1 << p.page_log2) - 1)) >> 5);
+        copy_tile<D>(put, p.pool + at * T::kBytes, lane);
       }
     }
     cp_async_commit();
-  };
-#pragma unroll
-  for (int n = 0; n < kK4Stages - 1; ++n) issue(n, keys[n]);
-  for (int n = 0; n < count; ++n) {
-    issue(n + kK4Stages - 1, keys[kK4Stages - 1]);
-    cp_async_wait_group<kK4Stages - 1>();
-    __syncwarp();
-    if (keys[0] >= 0)
-      attend_tile<D, NT>(ring + (n % kK4Stages) * T::kBytes, keys[0], sg.lo, sg.len, lane, q, a);
-    __syncwarp();                     // the stage is filled again in the next turn
-#pragma unroll
-    for (int i = 0; i + 1 < kK4Stages; ++i) keys[i] = keys[i + 1];
+    next(put);
+    return key;
   }
-  cp_async_wait_all();
-}
-
-// The warp's sums into its merge area (its own ring): O [head pairs], m and l per head.
-template <int D, int NT>
-__device__ __forceinline__ void leave_warp(float *area, float2 *ml, int lane,
-                                           const K4State<D, NT> &a) {
-  constexpr int G = K4<D>::kG;
-  const int r = lane >> 2, c = lane & 3;
-  const float back = a.rinv > 0.f ? __fdiv_rn(1.f, a.rinv) : 0.f;
-  const float o24 = back * 16777216.f;
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-#pragma unroll
-    for (int hd = 0; hd < 2; ++hd) {
-      float l = a.l[t][hd], add[G];
-#pragma unroll
-      for (int gi = 0; gi < G; ++gi) add[gi] = a.oz[t][hd][gi];
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        l += __shfl_xor_sync(0xffffffffu, l, o);
-#pragma unroll
-        for (int gi = 0; gi < G; ++gi) add[gi] += __shfl_xor_sync(0xffffffffu, add[gi], o);
-      }
-      float *dst = area + (t * 4 + c) * K4<D>::kHeadPair + hd * D + 8 * r;
-#pragma unroll
-      for (int gi = 0; gi < G; ++gi) {
-        const float base = fmaf(-8.f * back, a.ps[t][gi][hd], add[gi]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<float2 *>(dst + gi * 64 + 2 * e) =
-              make_float2(fmaf(a.o[t][gi][e][hd], o24, base),
-                          fmaf(a.o[t][gi][e][2 + hd], o24 * 0.0625f, base));
-      }
-      if (r == 0) ml[t * 8 + 2 * c + hd] = make_float2(a.m[t][hd], l);
-    }
+  __device__ __forceinline__ void start(int32_t &err) {
+    keys[0] = issue(0, err);
+    if (full) keys[1] = issue(1, err);
   }
-}
-
-// Joins the areas of `warps` warps; thread `th` of `nth`.  Writes out and lse of a whole
-// segment, or a partial result to `part`.
-template <int D, bool kFp16>
-__device__ __forceinline__ void join_warps(const Kv4DecodeParams &p, int b, int h,
-                                           const float *areas, size_t area_step, const float2 *ml,
-                                           int ml_step, int warps, int th, int nth, float *part) {
-  for (int i = th; i < p.g * (D / 2); i += nth) {
-    const int head = i / (D / 2), dim = 2 * (i % (D / 2));
-    const float *src = areas + (head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim;
-    float M = -INFINITY, l = 0.f, x = 0.f, y = 0.f;
-    for (int w = 0; w < warps; ++w)
-      if (ml[w * ml_step + head].y != 0.f) M = fmaxf(M, ml[w * ml_step + head].x);
-    for (int w = 0; w < warps; ++w) {
-      const float2 v = ml[w * ml_step + head];
-      if (v.y == 0.f) continue;                     // a warp without keys
-      const float wt = ex2_approx(v.x - M);
-      const float2 o = *reinterpret_cast<const float2 *>(src + w * area_step);
-      l = fmaf(wt, v.y, l);
-      x = fmaf(wt, o.x, x);
-      y = fmaf(wt, o.y, y);
-    }
-    if (part) {
-      *reinterpret_cast<float2 *>(part + head * D + dim) = make_float2(x, y);
-      if (dim == 0) *reinterpret_cast<float2 *>(part + p.g * D + 2 * head) = make_float2(M, l);
-    } else {
-      const bool any = l != 0.f;                    // a NaN sum stays one
-      const float inv = any ? 1.f / l : 0.f;
-      const int64_t row = (int64_t)b * p.h_q + h * p.g + head;
-      reinterpret_cast<uint32_t *>(p.out)[(row * D + dim) / 2] = pack2<kFp16>(x * inv, y * inv);
-      if (dim == 0)
-        p.lse[(int64_t)(h * p.g + head) * p.num_seqs + b] =
-            any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
-    }
-  }
-}
-
-// Length of sequence b held to its table row, and the first key that its window shows.
-__device__ __forceinline__ int seq_len(const Kv4DecodeParams &p, int b, int32_t &err) {
-  const int64_t cap = (int64_t)p.width << p.page_log2;
-  const int raw = __ldg(p.lens + b);
-  const int len = static_cast<int>(raw < 0 ? 0 : (raw > cap ? cap : raw));
-  if (raw != len) err |= NSA_DEVERR_BAD_SEQLENS;
-  return len;
-}
-__device__ __forceinline__ int seq_lo(const Kv4DecodeParams &p, int len) {
-  return p.window > 0 && len > p.window ? len - p.window : 0;
-}
-
-// One segment per kWps warps.
-template <int D, int NT, bool kFp16, bool kSel>
-__global__ void __launch_bounds__(kK4Warps * 32, NT == 1 ? 2 : 1)
-    kv4_seg_kernel(Kv4DecodeParams p, int wps) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 ml[kK4Warps][8 * NT];
-  __shared__ int32_t kept_page[kK4Warps][32], kept_key[kK4Warps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int sub = warp / wps, w = warp - sub * wps;      // segment of the CTA, warp of the segment
-  const int64_t seg = (int64_t)blockIdx.x * (kK4Warps / wps) + sub;
-  const bool live = seg < (int64_t)p.num_seqs * p.h_k;
-  K4State<D, NT> a;
-  a.clear();
-  K4Seg sg = {};
-  int32_t err = 0;
-  if (live) {
-    sg.b = static_cast<int>(seg / p.h_k);
-    sg.h = static_cast<int>(seg - (int64_t)sg.b * p.h_k);
-    int blk = -1;
-    if (kSel && lane < p.topk)
-      blk = __ldg(p.sel + ((int64_t)sg.h * p.num_seqs + sg.b) * p.topk + lane);
-    sg.len = seq_len(p, sg.b, err);
-    sg.lo = seq_lo(p, sg.len);
-    int tiles;
-    if (kSel) {
-      // the kept blocks: valid, first of their value, with a page in the pool
-      const int nblk = (sg.len + (1 << p.page_log2) - 1) >> p.page_log2;
-      if (blk < -1 || blk >= nblk) err |= lane < p.topk ? NSA_DEVERR_BAD_INDEX : 0;
-      bool ok = blk >= 0 && blk < nblk;
-      const uint32_t same = __match_any_sync(0xffffffffu, blk);
-      ok = ok && (same & ((1u << lane) - 1u)) == 0;
-      int pg = -1;
-      if (ok) {
-        pg = __ldg(p.table + (int64_t)sg.b * p.width + blk);
-        if (pg < 0 || pg >= p.num_pages) {
-          ok = false;
-          err |= NSA_DEVERR_BAD_INDEX;
-        }
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, ok);
-      if (ok) {
-        const int at = __popc(m & ((1u << lane) - 1u));
-        kept_page[warp][at] = pg;
-        kept_key[warp][at] = blk << p.page_log2;
+  __device__ __forceinline__ void run(const K4Query<D> &q, K4State<D> &a, int32_t &err) {
+    static_assert(kStages == 3, "two tiles ahead, or one beside a kept part");
+    for (int n = 0; n < count; ++n) {
+      if (full) {
+        keys[2] = issue(n + 2, err);
+        cp_async_wait_group<2>();
+      } else {
+        keys[1] = issue(n + 1, err);
+        cp_async_wait_group<1>();
       }
       __syncwarp();
-      sg.pages = kept_page[warp];
-      sg.keys = kept_key[warp];
-      tiles = __popc(m) << (p.page_log2 - 5);
-    } else {
-      sg.first = sg.lo >> 5;
-      tiles = ((sg.len + 31) >> 5) - sg.first;
+      if (keys[0] >= 0) attend_tile<D>(get, keys[0], sg.lo, sg.len, lane, q, a);
+      __syncwarp();                   // the stage is filled again in the next turn
+      next(get);
+      keys[0] = keys[1];
+      keys[1] = keys[2];
     }
-    K4Query<D, NT> q;
-    load_query<D, NT, kFp16>(static_cast<const uint16_t *>(p.q) +
-                                 ((int64_t)sg.b * p.h_q + sg.h * p.g) * D,
-                             p.g, p.scale_log2, lane, q);
-    run_tiles<D, NT>(p, sg, w, tiles, wps, smem_u32(smem) + warp * K4<D>::kRing, lane, q, a, err);
-    err = __reduce_or_sync(0xffffffffu, err);
-    if (err && lane == 0) raise(p.status, err);
-    leave_warp<D, NT>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), ml[warp], lane, a);
+    cp_async_wait_all();
   }
-  __syncthreads();
-  if (live)
-    join_warps<D, kFp16>(p, sg.b, sg.h,
-                         reinterpret_cast<const float *>(smem + sub * wps * K4<D>::kRing),
-                         K4<D>::kRing / 4, ml[sub * wps], 8 * NT, wps, w * 32 + lane, wps * 32,
-                         nullptr);
+};
+
+// The warp's l and zero terms summed over its lanes.
+template <int D>
+__device__ __forceinline__ void sum_lanes(K4State<D> &a) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+    for (int hd = 0; hd < 2; ++hd) {
+      a.l[hd] += __shfl_xor_sync(0xffffffffu, a.l[hd], o);
+#pragma unroll
+      for (int gi = 0; gi < K4<D>::kG; ++gi)
+        a.oz[hd][gi] += __shfl_xor_sync(0xffffffffu, a.oz[hd][gi], o);
+    }
 }
 
-// Tiles of a sequence: at least one, so that an empty one's output is written too.
-__device__ __forceinline__ int seq_tiles(const Kv4DecodeParams &p, int len) {
-  return max(1, ((len + 31) >> 5) - (seq_lo(p, len) >> 5));
+// O times f (per head of the lane) into an area [head pairs].
+template <int D>
+__device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D> &a, float f0,
+                                          float f1) {
+  constexpr int G = K4<D>::kG;
+  const int r = lane >> 2, c = lane & 3;
+  const float back = a.rinv > 0.f ? __fdiv_rn(1.f, a.rinv) : 0.f;   // a power of two
+#pragma unroll
+  for (int hd = 0; hd < 2; ++hd) {
+    const float f = hd ? f1 : f0, fb = f * back, o1 = fb * 16777216.f, o16 = fb * 1048576.f;
+    float *dst = area + c * K4<D>::kHeadPair + hd * D + 8 * r;
+#pragma unroll
+    for (int gi = 0; gi < G; ++gi) {
+      const float base = fmaf(-8.f * fb, a.ps[gi][hd], f * a.oz[hd][gi]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float2 *>(dst + gi * 64 + 2 * e) = make_float2(
+            fmaf(a.o[gi][e][hd], o1, base), fmaf(a.o[gi][e][2 + hd], o16, base));
+    }
+  }
+}
+
+// Final values of dimensions dim and dim + 1 of query head hq.
+template <int D, bool kFp16>
+__device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int hq, int dim, float x,
+                                          float y, float M, float l) {
+  const bool any = l != 0.f;                        // a NaN sum stays one
+  const float inv = any ? __fdividef(1.f, l) : 0.f;
+  const int64_t row = (int64_t)b * p.h_q + hq;
+  reinterpret_cast<uint32_t *>(p.out)[(row * D + dim) >> 1] = pack2<kFp16>(x * inv, y * inv);
+  if (dim == 0)
+    p.lse[(int64_t)hq * p.num_seqs + b] = any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// One CTA per segment.
+template <int D, bool kFp16, bool kSel>
+__global__ void __launch_bounds__(kK4Threads, 2) kv4_seg_kernel(Kv4DecodeParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float4 ml[kK4Warps][kK4Heads / 2];        // m, l of two heads
+  __shared__ float lsum[kK4Warps][kK4Heads];
+  __shared__ int32_t pages[kK4Warps][32], keys[kK4Warps][32];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  K4Seg sg = {};
+  set_unit(p, blockIdx.x, sg);
+  sg.b = blockIdx.y;
+  int32_t err = 0;
+  K4RawQuery<D> raw;
+  fetch_query<D>(p, sg, lane, raw);
+  open_segment<kSel>(p, sg, pages[warp], keys[warp], lane, err);
+  K4Stream<D, kSel> st(p, sg, warp, max(0, (sg.tiles - warp + kK4Warps - 1) / kK4Warps), kK4Warps,
+                       smem_u32(smem) + warp * K4<D>::kRing, true, lane);
+  st.start(err);
+  K4Query<D> q;
+  make_query<D, kFp16>(raw, p.scale_log2, lane, q);
+  K4State<D> a;
+  a.clear();
+  st.run(q, a, err);
+  if (tid == 0) seq_len(p, sg.b, err);
+  err = __reduce_or_sync(0xffffffffu, err);
+  if (err && lane == 0) raise(p.status, err);
+
+  // the warps agree on each head's maximum, scale their sums to it, and add up
+  const int r = lane >> 2, c = lane & 3;
+  sum_lanes(a);
+  if (r == 0) ml[warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
+  __syncthreads();
+  float M0 = -INFINITY, M1 = -INFINITY;                // -inf without keys
+#pragma unroll
+  for (int w = 0; w < kK4Warps; ++w) {
+    const float4 v = ml[w][c];
+    M0 = fmaxf(M0, v.x);
+    M1 = fmaxf(M1, v.z);
+  }
+  const float f0 = a.l[0] != 0.f ? ex2_approx(a.m[0] - M0) : 0.f;
+  const float f1 = a.l[1] != 0.f ? ex2_approx(a.m[1] - M1) : 0.f;
+  if (r == 0) *reinterpret_cast<float2 *>(&lsum[warp][2 * c]) = make_float2(a.l[0] * f0, a.l[1] * f1);
+  leave_out<D>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), lane, a, f0, f1);
+  __syncthreads();
+  for (int i = tid; i < sg.g * (D / 2); i += kK4Threads) {
+    const int head = i / (D / 2), dim = 2 * (i % (D / 2));
+    const uint8_t *src = smem + ((head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim) * 4;
+    float l = 0.f, x = 0.f, y = 0.f, M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kK4Warps; ++w) {
+      const float2 o = *reinterpret_cast<const float2 *>(src + w * K4<D>::kRing);
+      l += lsum[w][head];
+      x += o.x;
+      y += o.y;
+    }
+    if (dim == 0) {
+#pragma unroll
+      for (int w = 0; w < kK4Warps; ++w)
+        M = fmaxf(M, head & 1 ? ml[w][head >> 1].z : ml[w][head >> 1].x);
+    }
+    write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, y, M, l);
+  }
+}
+
+// Tiles that a sequence's segments count as: what they have (with a selection, at most), at
+// least one, so that an empty one's output is written too, and kOver.
+template <bool kSel>
+__device__ __forceinline__ int counted_tiles(const Kv4DecodeParams &p, int len) {
+  int nt = ((len + 31) >> 5) - (seq_lo(p, len) >> 5);
+  if (kSel) {
+    const int nblk = (len + (1 << p.page_log2) - 1) >> p.page_log2;
+    nt = min(nblk, p.topk) << (p.page_log2 - 5);
+  }
+  return max(nt, 1) + kOver;
 }
 
 __device__ __forceinline__ K4Split *splits_of(const Kv4DecodeParams &p) {
   return static_cast<K4Split *>(p.ws);
 }
+// Partial result i: O [heads][D] (not divided by l), then (m, l) per head.
+__host__ __device__ constexpr int part_floats(int d, int g) {
+  return (g < kK4Heads ? g : kK4Heads) * (d + 2);
+}
 template <int D>
-__device__ __forceinline__ float *part_of(const Kv4DecodeParams &p, int64_t i) {
+__device__ __forceinline__ float *part_of(const Kv4DecodeParams &p, int i) {
   return reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + kK4MaxCtas * sizeof(K4Split)) +
-         i * (p.g * (D + 2));
+         (int64_t)i * part_floats(D, p.g);
 }
 
-// Equal runs of the batch's tiles (sequence, head, tile order) for every CTA.
-template <int D, int NT, bool kFp16>
-__global__ void __launch_bounds__(kK4Warps * 32, NT == 1 ? 2 : 1)
-    kv4_long_kernel(Kv4DecodeParams p) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 ml[kK4Warps][8 * NT];
-  __shared__ int64_t wsum[kK4Warps];
-  __shared__ int64_t found_base;
-  __shared__ int found_b;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // the batch's tiles, and the sequence that holds this CTA's first one
-  const int per_thread = (p.num_seqs + kK4Warps * 32 - 1) / (kK4Warps * 32);
-  const int b0 = min(tid * per_thread, p.num_seqs), b1 = min(b0 + per_thread, p.num_seqs);
-  int32_t err = 0;
-  int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += seq_tiles(p, seq_len(p, b, err));
-  int64_t incl = mine;
+__device__ __forceinline__ int warp_incl_sum(int x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
+  return x;
+}
+
+// What a warp's run left for the CTA: a first part (of a segment begun before the run) and
+// a last part (of a segment that goes on behind it).
+struct K4Run {
+  int fb, fu, lb, lu;   // their sequences and units
+  int end;              // first tile behind the segment of the last part
+  int first, last;      // there is one
+  int on;               // the first part covers the whole run and its segment goes on
+  int kept;             // the first part lies in the ring's last stage
+};
+
+// Equal runs of the batch's counted tiles.  whole: a CTA's run is moved to segments' starts,
+// so that no segment is split between CTAs.
+template <int D, bool kFp16, bool kSel>
+__global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams p, int units,
+                                                                int whole) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float4 first_ml[kK4Warps][kK4Heads / 2], last_ml[kK4Warps][kK4Heads / 2];
+  __shared__ float first_f[kK4Warps][kK4Heads], last_f[kK4Warps][kK4Heads];
+  __shared__ int32_t pages[kK4Warps][32], keys[kK4Warps][32];
+  __shared__ K4Run runs[kK4Warps];
+  __shared__ int wsum[kK4Warps], found[kK4Warps + 1][3];   // tile, sequence, its first tile
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // ---- the batch's tiles, and where the runs of this CTA's warps begin ----
+  const int per_thread = (p.num_seqs + kK4Threads - 1) / kK4Threads;
+  const int b0 = min(tid * per_thread, p.num_seqs), b1 = min(b0 + per_thread, p.num_seqs);
+  int32_t err = 0, ignore = 0;
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += counted_tiles<kSel>(p, seq_len(p, b, err));
+  if (blockIdx.x == 0 && err) raise(p.status, err);
+  err = 0;
+  mine *= units;
+  int incl = warp_incl_sum(mine, lane);
   if (lane == 31) wsum[warp] = incl;
-  if (tid == 0) found_b = -1;
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < kK4Warps; ++w) {
     if (w < warp) incl += wsum[w];
     total += wsum[w];
   }
-  total *= p.h_k;
-  // a multiple of the warps, so that no warp idles in a run
-  const int64_t per = (total + (int64_t)gridDim.x * kK4Warps - 1) /
-                      ((int64_t)gridDim.x * kK4Warps) * kK4Warps;
-  const int64_t begin = blockIdx.x * per, end = min(begin + per, total);
-  if (blockIdx.x == 0 && err) raise(p.status, err);
-  err = 0;
-  if (begin < end && mine > 0 && (incl - mine) * p.h_k <= begin && begin < incl * p.h_k) {
-    int64_t base = (incl - mine) * p.h_k;
-    for (int b = b0; b < b1; ++b) {
-      const int64_t nt = (int64_t)seq_tiles(p, seq_len(p, b, err)) * p.h_k;
-      if (begin < base + nt) {
-        found_b = b;
-        found_base = base;
-        break;
+  const int warps = gridDim.x * kK4Warps;
+  int per_warp = (total + warps - 1) / warps;
+  const int per = per_warp * kK4Warps;                     // tiles of a CTA
+  const int from = static_cast<int>(min((int64_t)blockIdx.x * per, (int64_t)total));
+  const int to = min(from + min(per, total - from), total);
+  const int ntargets = whole ? 2 : kK4Warps + 1;
+  for (int k = 0; k < ntargets; ++k) {
+    const int v = whole ? (k ? to : from) : min(from + min(k * per_warp, total - from), to);
+    if (v == total ? tid == 0 : (incl - mine <= v && v < incl)) {
+      int b = b0, base = incl - mine, at = v;
+      if (v == total) {
+        b = p.num_seqs;
+        base = total;
       }
-      base += nt;
+      for (; b < b1; ++b) {
+        const int nt = counted_tiles<kSel>(p, seq_len(p, b, ignore)), all = nt * units;
+        if (v < base + all) {
+          if (whole) at = base + (v - base + nt - 1) / nt * nt;   // the next segment's start
+          if (at == base + all) {
+            ++b;
+            base = at;
+          }
+          break;
+        }
+        base += all;
+      }
+      found[k][0] = at;
+      found[k][1] = b;
+      found[k][2] = base;
     }
   }
   __syncthreads();
-  err = 0;
-  K4Split split = {0, 0};
-  int b = found_b;
-  int64_t base = found_base;               // first tile of (b, head 0)
-  for (int64_t at = begin; at < end;) {
-    int32_t ignore = 0;
+  int at, stop, b, base;                   // this warp's run; the sequence of its first tile
+  if (whole) {
+    const int begin = found[0][0], end = found[1][0];
+    per_warp = (end - begin + kK4Warps - 1) / kK4Warps;
+    at = min(begin + warp * per_warp, end);
+    stop = min(at + per_warp, end);
+    b = found[0][1];
+    base = found[0][2];
+    while (at < stop) {                    // 32 sequences at a time
+      const int n = b + lane < p.num_seqs
+                        ? counted_tiles<kSel>(p, seq_len(p, b + lane, ignore)) * units : 0;
+      const int in = warp_incl_sum(n, lane);
+      const uint32_t past = __ballot_sync(0xffffffffu, at < base + in);
+      const int hit = past ? __ffs(past) - 1 : 31;
+      base += __shfl_sync(0xffffffffu, past ? in - n : in, hit);
+      b += past ? hit : 32;
+      if (past) break;
+    }
+  } else {
+    at = found[warp][0];
+    b = found[warp][1];
+    base = found[warp][2];
+    stop = found[warp + 1][0];
+  }
+  uint8_t *const ring = smem + warp * K4<D>::kRing;
+  K4Run run = {};
+  int unit = -1, nt = 0;
+  K4State<D> a;
+  const int c = lane & 3;
+  while (at < stop) {
     K4Seg sg = {};
     sg.b = b;
-    sg.len = seq_len(p, b, ignore);
-    sg.lo = seq_lo(p, sg.len);
-    sg.first = sg.lo >> 5;
-    const int nt = seq_tiles(p, sg.len);
-    sg.h = static_cast<int>((at - base) / nt);
-    const int64_t seg0 = base + (int64_t)sg.h * nt;
-    const int t0 = static_cast<int>(at - seg0);
-    const int t1 = static_cast<int>(min((int64_t)nt, end - seg0));
-    K4State<D, NT> a;
+    if (unit <= 0) nt = counted_tiles<kSel>(p, seq_len(p, b, ignore));
+    if (unit < 0) unit = (at - base) / nt;
+    set_unit(p, unit, sg);
+    const int seg0 = base + unit * nt;
+    const int v0 = at - seg0, v1 = min(nt, stop - seg0);
     a.clear();
-    {
-      K4Query<D, NT> q;
-      load_query<D, NT, kFp16>(static_cast<const uint16_t *>(p.q) +
-                                   ((int64_t)sg.b * p.h_q + sg.h * p.g) * D,
-                               p.g, p.scale_log2, lane, q);
-      run_tiles<D, NT>(p, sg, t0 + warp, t1, kK4Warps, smem_u32(smem) + warp * K4<D>::kRing, lane,
-                       q, a, err);
+    if (v1 > kOver) {
+      K4RawQuery<D> raw;
+      fetch_query<D>(p, sg, lane, raw);
+      open_segment<kSel>(p, sg, pages[warp], keys[warp], lane, err);
+      const int t0 = max(0, v0 - kOver), t1 = min(v1 - kOver, sg.tiles);
+      K4Stream<D, kSel> st(p, sg, t0, max(0, t1 - t0), 1, smem_u32(ring), !run.kept, lane);
+      st.start(err);
+      K4Query<D> q;
+      make_query<D, kFp16>(raw, p.scale_log2, lane, q);
+      st.run(q, a, err);
     }
-    leave_warp<D, NT>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), ml[warp], lane, a);
-    __syncthreads();
-    float *part = nullptr;
-    if (t0 > 0) {
-      part = part_of<D>(p, 2 * (int64_t)blockIdx.x);
-    } else if (t1 < nt) {
-      part = part_of<D>(p, 2 * (int64_t)blockIdx.x + 1);
-      split.seg = static_cast<int32_t>((int64_t)sg.b * p.h_k + sg.h);
-      split.parts = static_cast<int32_t>((seg0 + nt - 1) / per - blockIdx.x + 1);
+    sum_lanes(a);
+    at = seg0 + v1;
+    const bool goes_on = v1 < nt, first = v0 > 0;
+    if (first || goes_on) {
+      // a part; unless the run goes on, it stays in registers until the CTA's warps agree
+      if (lane < 4)
+        (first ? first_ml : last_ml)[warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
+      if (first) {
+        run.first = 1;
+        run.on = goes_on;
+        run.kept = at < stop;
+        run.fb = b;
+        run.fu = unit;
+        if (run.kept) leave_out<D>(reinterpret_cast<float *>(ring + K4<D>::kKept), lane, a, 1.f, 1.f);
+      } else {
+        run.last = 1;
+        run.lb = b;
+        run.lu = unit;
+        run.end = seg0 + nt;
+      }
+    } else {
+      float *area = reinterpret_cast<float *>(ring);
+      leave_out<D>(area, lane, a, 1.f, 1.f);
+      if (lane < 4) last_ml[warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
+      __syncwarp();
+      for (int i = lane; i < sg.g * (D / 2); i += 32) {
+        const int head = i / (D / 2), dim = 2 * (i % (D / 2));
+        const float2 o = *reinterpret_cast<const float2 *>(
+            area + (head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim);
+        const float4 v = last_ml[warp][head >> 1];
+        write_out<D, kFp16>(p, b, sg.q0 + head, dim, o.x, o.y, head & 1 ? v.z : v.x,
+                            head & 1 ? v.w : v.y);
+      }
+      __syncwarp();                        // read before the ring is filled again
     }
-    join_warps<D, kFp16>(p, sg.b, sg.h, reinterpret_cast<const float *>(smem), K4<D>::kRing / 4,
-                         ml[0], 8 * NT, kK4Warps, tid, kK4Warps * 32, part);
-    at = seg0 + t1;
-    if (t1 == nt && sg.h == p.h_k - 1) {
-      base += (int64_t)nt * p.h_k;
+    if (++unit == units) {
+      unit = 0;
+      base += nt * units;
       ++b;
     }
-    __syncthreads();                       // the areas have been read: the rings may be filled
   }
-  if (tid == 0) splits_of(p)[blockIdx.x] = split;
   err = __reduce_or_sync(0xffffffffu, err);
   if (err && lane == 0) raise(p.status, err);
+  if (lane == 0) runs[warp] = run;
+  if (tid == 0 && !whole) splits_of(p)[blockIdx.x] = K4Split{0, 0};
+  __syncthreads();
+  // ---- join the parts of segments that cross warps ----
+  // A group is a segment's parts in this CTA: a last part of warp `open` (-1: the segment
+  // began in an earlier CTA), then first parts of warps open + 1 ... e - 1; `on`: it goes on
+  // in the next CTA.  Every warp finds its parts' groups, and the factor that takes a part to
+  // its group's maximum.
+  struct Group {
+    int open, e, on;
+  };
+  auto group_of = [&](int open) {
+    Group g = {open, open + 1, 1};
+    while (g.on && g.e < kK4Warps && runs[g.e].first) {
+      g.on = runs[g.e].on;
+      ++g.e;
+    }
+    return g;
+  };
+  Group groups[2] = {{-1, 0, 0}, {-1, 0, 0}};
+#pragma unroll
+  for (int side = 0; side < 2; ++side) {   // 0: the warp's first part, 1: its last
+    if (!(side ? run.last : run.first)) continue;
+    int open = side ? warp : warp - 1;
+    if (!side)
+      while (open >= 0 && runs[open].on) --open;
+    const Group g = group_of(open);
+    groups[side] = g;
+    float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kK4Warps; ++w) {
+      if (w != open && !(w > open && w < g.e)) continue;
+      const float4 v = w == open ? last_ml[w][c] : first_ml[w][c];
+      M0 = fmaxf(M0, v.x);
+      M1 = fmaxf(M1, v.z);
+    }
+    const float4 v = side ? last_ml[warp][c] : first_ml[warp][c];
+    const float f0 = v.y != 0.f ? ex2_approx(v.x - M0) : 0.f;
+    const float f1 = v.w != 0.f ? ex2_approx(v.z - M1) : 0.f;
+    const bool in_area = !side && run.kept;   // already left, with a factor of 1
+    if (!in_area) leave_out<D>(reinterpret_cast<float *>(ring), lane, a, f0, f1);
+    if (lane < 4)
+      *reinterpret_cast<float2 *>(&(side ? last_f : first_f)[warp][2 * c]) = make_float2(f0, f1);
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    if (!(side ? run.last : run.first)) continue;
+    const Group g = groups[side];
+    const int lead = g.open >= 0 ? g.open : 0, n = g.e - lead;     // warps of the group
+    K4Seg sg = {};
+    sg.b = side ? run.lb : run.fb;
+    set_unit(p, side ? run.lu : run.fu, sg);
+    float *part = nullptr;
+    if (g.open < 0) part = part_of<D>(p, 2 * blockIdx.x);
+    else if (g.on) part = part_of<D>(p, 2 * blockIdx.x + 1);
+    if (g.open == warp && side && g.on && lane == 0)
+      splits_of(p)[blockIdx.x] =
+          K4Split{sg.b * units + run.lu, (run.end - 1) / per - static_cast<int>(blockIdx.x) + 1};
+    for (int i = (warp - lead) * 32 + lane; i < sg.g * (D / 2); i += n * 32) {
+      const int head = i / (D / 2), dim = 2 * (i % (D / 2));
+      const int off = ((head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim) * 4;
+      float l = 0.f, x = 0.f, y = 0.f, M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kK4Warps; ++w) {
+        if (w < lead || w >= g.e) continue;
+        const bool fst = w != g.open, kept = fst && runs[w].kept;
+        const float2 o = *reinterpret_cast<const float2 *>(smem + w * K4<D>::kRing +
+                                                           (kept ? K4<D>::kKept : 0) + off);
+        const float f = (fst ? first_f : last_f)[w][head];
+        const float4 v = (fst ? first_ml : last_ml)[w][head >> 1];
+        const float k = kept ? f : 1.f;
+        // a part without keys adds nothing; its maximum is -inf
+        l = fmaf(f, head & 1 ? v.w : v.y, l);
+        M = fmaxf(M, head & 1 ? v.z : v.x);
+        x = fmaf(k, o.x, x);
+        y = fmaf(k, o.y, y);
+      }
+      if (part) {
+        *reinterpret_cast<float2 *>(part + head * D + dim) = make_float2(x, y);
+        if (dim == 0) *reinterpret_cast<float2 *>(part + sg.g * D + 2 * head) = make_float2(M, l);
+      } else {
+        write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, y, M, l);
+      }
+    }
+  }
 }
 
 // Joins the parts of the segment that begins in CTA blockIdx.x and ends in another: its own
-// second part and the following CTAs' first ones.  One CTA per (split, head).
+// second part and the following CTAs' first ones.  One CTA per (split, head): its warps take
+// the parts in turn, eight in flight.
 constexpr int kMergeThreads = 256;
 template <int D, bool kFp16>
-__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParams p) {
-  __shared__ float wt[kK4MaxCtas];
-  __shared__ float red[kMergeThreads / 32][2];
-  __shared__ float acc[kMergeThreads];
+__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParams p, int units) {
+  constexpr int kWarps = kMergeThreads / 32, E = D / 32;
+  __shared__ float acc[kWarps][D];
+  __shared__ float2 wml[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const K4Split sp = splits_of(p)[blockIdx.x];
   if (sp.parts == 0) return;
-  auto part = [&](int i) {
-    return part_of<D>(p, i == 0 ? 2 * (int64_t)blockIdx.x + 1 : 2 * ((int64_t)blockIdx.x + i));
-  };
-  float M = -INFINITY;
-  for (int i = tid; i < sp.parts; i += kMergeThreads) {
-    const float2 v = *reinterpret_cast<const float2 *>(part(i) + p.g * D + 2 * head);
-    if (v.y != 0.f) M = fmaxf(M, v.x);
+  K4Seg sg = {};
+  sg.b = sp.seg / units;
+  set_unit(p, sp.seg - sg.b * units, sg);
+  if (head >= sg.g) return;
+  float M = -INFINITY, l = 0.f, x[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 0.f;
+  for (int i0 = warp; i0 < sp.parts; i0 += 8 * kWarps) {
+    float2 v[8];
+    float o[8][E];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * kWarps;
+      v[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+      if (i < sp.parts) {
+        const float *part = part_of<D>(p, i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i));
+        v[u] = __ldcg(reinterpret_cast<const float2 *>(part + sg.g * D + 2 * head));
+        const float2 *src = reinterpret_cast<const float2 *>(part + head * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float2 y = __ldcg(src + e);
+          o[u][2 * e] = y.x;
+          o[u][2 * e + 1] = y.y;
+        }
+      }
+    }
+    float mnew = M;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) mnew = fmaxf(mnew, v[u].x);
+    const float old = l != 0.f ? ex2_approx(M - mnew) : 0.f;
+    l *= old;
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] *= old;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float w = v[u].y != 0.f ? ex2_approx(v[u].x - mnew) : 0.f;
+      l = fmaf(w, v[u].y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = fmaf(w, o[u][e], x[e]);
+    }
+    M = mnew;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[warp][0] = M;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, red[w][0]);
-  float l = 0.f;
-  for (int i = tid; i < sp.parts; i += kMergeThreads) {
-    const float2 v = *reinterpret_cast<const float2 *>(part(i) + p.g * D + 2 * head);
-    wt[i] = v.y != 0.f ? ex2_approx(v.x - M) : 0.f;
-    l = fmaf(wt[i], v.y, l);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (lane == 0) red[warp][1] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeThreads / 32; ++w) l += red[w][1];
-  constexpr int kRows = kMergeThreads / D;
-  const int dim = tid % D;
-  float x = 0.f;
-#pragma unroll 4
-  for (int i = tid / D; i < sp.parts; i += kRows) {
-    const float w = wt[i];
-    if (w != 0.f) x = fmaf(w, part(i)[head * D + dim], x);
-  }
-  acc[tid] = x;
+  for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = x[e];
+  if (lane == 0) wml[warp] = make_float2(M, l);
   __syncthreads();
   if (tid < D / 2) {
+    M = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wml[w].x);
     float u = 0.f, v = 0.f;
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      u += acc[k * D + 2 * tid];
-      v += acc[k * D + 2 * tid + 1];
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 t = wml[w];
+      const float f = t.y != 0.f ? ex2_approx(t.x - M) : 0.f;
+      l = fmaf(f, t.y, l);
+      u = fmaf(f, acc[w][2 * tid], u);
+      v = fmaf(f, acc[w][2 * tid + 1], v);
     }
-    const bool any = l != 0.f;
-    const float inv = any ? 1.f / l : 0.f;
-    const int b = sp.seg / p.h_k, hq = (sp.seg - b * p.h_k) * p.g + head;
-    reinterpret_cast<uint32_t *>(p.out)[((int64_t)b * p.h_q + hq) * (D / 2) + tid] =
-        pack2<kFp16>(u * inv, v * inv);
-    if (tid == 0)
-      p.lse[(int64_t)hq * p.num_seqs + b] =
-          any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    write_out<D, kFp16>(p, sg.b, sg.q0 + head, 2 * tid, u, v, M, l);
   }
 }
 
 size_t kv4_decode_workspace(int d, int g, bool selected) {
   if (selected) return 0;
-  return kK4MaxCtas * sizeof(K4Split) + 2 * (size_t)kK4MaxCtas * g * (d + 2) * sizeof(float);
+  return kK4MaxCtas * sizeof(K4Split) + 2 * (size_t)kK4MaxCtas * part_floats(d, g) * sizeof(float);
 }
 
-static int sm_count() {
+// Tiles of the whole batch, counted as the run kernel does, at most (its counters have 32 bits).
+int64_t kv4_decode_tiles(const Kv4DecodeParams &p) {
+  const int units = p.h_k * (p.g > kK4Heads ? 2 : 1);
+  return (((int64_t)p.width << p.page_log2) / kKv4Tile + 1 + kOver) * p.num_seqs * units;
+}
+
+static int sm_count(int dev) {
   static int cache[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+  if (dev < 0 || dev >= 64) return 148;
   if (cache[dev] == 0) {
     int n = 0;
     cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
@@ -840,40 +1084,37 @@ static int sm_count() {
   return cache[dev];
 }
 
-template <typename K>
-static cudaError_t allow_smem(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-template <int D, int NT, bool kFp16>
+template <int D, bool kFp16, bool kSel>
 static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   constexpr int smem = K4<D>::kSmem;
-  const int slots = sm_count() * (NT == 1 ? 2 : 1);       // CTAs resident at once
-  const int64_t segs = (int64_t)p.num_seqs * p.h_k;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int ctas = min(sm_count(dev) * 2, kK4MaxCtas);     // resident at once
+  const int units = p.h_k * (p.g > kK4Heads ? 2 : 1);
+  const int64_t segs = (int64_t)p.num_seqs * units;
   // tiles that a segment has at most, as far as the host knows
   int64_t most = ((int64_t)p.width << p.page_log2) / kKv4Tile;
   if (p.window > 0) most = min(most, (int64_t)p.window / kKv4Tile + 2);
-  if (p.sel) most = min(most, (int64_t)p.topk << (p.page_log2 - 5));
-  if (p.sel || most <= 64) {
-    // warps to a segment: as many as still fit the GPU at once, and no more than tiles
-    int wps = 1;
-    while (wps < kK4Warps && segs * (2 * wps) <= (int64_t)slots * kK4Warps && wps < most) wps *= 2;
-    auto *kernel = p.sel ? kv4_seg_kernel<D, NT, kFp16, true> : kv4_seg_kernel<D, NT, kFp16, false>;
-    cudaError_t e = allow_smem(kernel, smem);
+  if (kSel) most = min(most, (int64_t)p.topk << (p.page_log2 - 5));
+  if (segs <= ctas && (kSel || most <= 8 * kK4Warps)) {
+    auto *kernel = kv4_seg_kernel<D, kFp16, kSel>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int per = kK4Warps / wps;
-    kernel<<<static_cast<unsigned>((segs + per - 1) / per), kK4Warps * 32, smem, s>>>(p, wps);
+    kernel<<<dim3(units, p.num_seqs), kK4Threads, smem, s>>>(p);
     return cudaGetLastError();
   }
-  auto *kernel = kv4_long_kernel<D, NT, kFp16>;
-  cudaError_t e = allow_smem(kernel, smem);
+  // With two or more segments of bounded length to a CTA, whole segments a CTA balance well
+  // enough; else segments are split, and the merge follows.
+  const int whole = kSel || (segs >= 2 * ctas && most <= 16 * kK4Warps);
+  auto *kernel = kv4_run_kernel<D, kFp16, kSel>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int ctas = min(slots, kK4MaxCtas);
-  kernel<<<ctas, kK4Warps * 32, smem, s>>>(p);
+  kernel<<<ctas, kK4Threads, smem, s>>>(p, units, whole);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || whole) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, p.g);
+  cfg.gridDim = dim3(ctas, min(p.g, kK4Heads));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -881,17 +1122,17 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, kFp16>, p);
+  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, kFp16>, p, units);
 }
 
 template <int D, bool kFp16>
-static cudaError_t run_decode4_nt(const Kv4DecodeParams &p, cudaStream_t s) {
-  return p.g <= 8 ? run_decode4<D, 1, kFp16>(p, s) : run_decode4<D, 2, kFp16>(p, s);
+static cudaError_t run_decode4_sel(const Kv4DecodeParams &p, cudaStream_t s) {
+  return p.sel ? run_decode4<D, kFp16, true>(p, s) : run_decode4<D, kFp16, false>(p, s);
 }
 
 cudaError_t launch_kv4_decode(int d, bool fp16, const Kv4DecodeParams &p, cudaStream_t s) {
-  if (d == 64) return fp16 ? run_decode4_nt<64, true>(p, s) : run_decode4_nt<64, false>(p, s);
-  return fp16 ? run_decode4_nt<128, true>(p, s) : run_decode4_nt<128, false>(p, s);
+  if (d == 64) return fp16 ? run_decode4_sel<64, true>(p, s) : run_decode4_sel<64, false>(p, s);
+  return fp16 ? run_decode4_sel<128, true>(p, s) : run_decode4_sel<128, false>(p, s);
 }
 
 }  // namespace nsa
