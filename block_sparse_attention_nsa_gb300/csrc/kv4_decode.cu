@@ -28,7 +28,7 @@
 // rows reordered so that the four rows that a lane quartet reads together lie in different
 // banks.  K words go to the A operand as they are; V words of two keys are joined by byte
 // permutes, which puts neighbouring keys into one register.  Each lane turns one key's V
-// scales and zeros into fp32 for all, in the place of the tile's own.
+// scales and zeros into fp32 for all, in the place of the K codes.
 //
 // Work.  A segment is a (sequence, KV head, up to 8 of its query heads).  kv4_seg_kernel:
 // one CTA a segment, its eight warps taking the tiles in turn; for batches whose segments
@@ -73,32 +73,30 @@ struct K4Split {
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same on a zero accumulator.
+__device__ __forceinline__ void mma16816_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                           uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t x;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
-  return x;
 }
 // The kG halves of entry `i` of a parameter array, packed; and as floats.
 template <int G>
-__device__ __forceinline__ uint32_t lds_par(uint32_t arr, int i) {
-  if constexpr (G == 2) {
-    return lds32(arr + i * 4);
-  } else {
-    unsigned short x;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(arr + i * 2));
-    return x;
-  }
+__device__ __forceinline__ uint32_t lds_par(const uint8_t *arr, int i) {
+  if constexpr (G == 2) return reinterpret_cast<const uint32_t *>(arr)[i];
+  else return reinterpret_cast<const uint16_t *>(arr)[i];
 }
 template <int G>
 __device__ __forceinline__ void par_floats(uint32_t u, float (&x)[G]) {
@@ -154,8 +152,7 @@ struct K4Seg {
   int len, lo;
   int first;                 // first tile (32 keys), without a selection
   int tiles;                 // tiles that exist
-  const int32_t *pages;      // selection: kept pages and their first keys, in shared memory
-  const int32_t *keys;
+  int page, key;             // selection: lane i holds the i-th kept block's page and first key
 };
 
 // Unit u of a sequence: KV head u / parts, its query heads 8 * (u % parts) ...
@@ -263,56 +260,12 @@ __device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *tile, i
 
 // One tile: keys key0 ... key0 + 31, of which those in [lo, len) count.
 template <int D>
-__device__ __forceinline__ void attend_tile(uint32_t st, int key0, int lo, int len, int lane,
+__device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int len, int lane,
                                             const K4Query<D> &q, K4State<D> &a) {
   using T = Kv4Tile<D>;
   constexpr int G = K4<D>::kG, W = K4<D>::kW;
   const int r = lane >> 2, c = lane & 3;
   const bool ragged = key0 < lo || key0 + 32 > len;
-  // ---- the scales and zeros: K's of the lane's rows, V's of key `lane` for everyone ----
-  uint32_t ksu[4], kzu[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    ksu[i] = lds_par<G>(st + T::kPar, i * 8 + r);
-    kzu[i] = lds_par<G>(st + T::kPar + T::kArr, i * 8 + r);
-  }
-  float vs[G], vz[G], vtop = 0.f;
-  par_floats<G>(lds_par<G>(st + T::kPar + 2 * T::kArr, lane), vs);
-  par_floats<G>(lds_par<G>(st + T::kPar + 3 * T::kArr, lane), vz);
-  if (ragged && (key0 + lane < lo || key0 + lane >= len)) {   // may be anything
-#pragma unroll
-    for (int gi = 0; gi < G; ++gi) vs[gi] = vz[gi] = 0.f;
-  }
-#pragma unroll
-  for (int gi = 0; gi < G; ++gi) vtop = fmaxf(vtop, vs[gi]);
-  if (__any_sync(0xffffffffu, vtop > a.vmax)) {               // a scale outgrew P's range
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
-    const float vnew = __uint_as_float((__float_as_uint(vtop) & 0x7f800000u) + 0x00800000u);
-    const float rnew = __fdiv_rn(kPScale, vnew);              // powers of two: exact
-    const float grow = a.rinv > 0.f ? __fdiv_rn(rnew, a.rinv) : 0.f;
-    a.vmax = vnew;
-    a.rinv = rnew;
-#pragma unroll
-    for (int gi = 0; gi < G; ++gi)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        a.ps[gi][x] *= grow;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a.o[gi][e][x] *= grow;
-      }
-  }
-  __syncwarp();              // all have read the tile's own
-  const uint32_t vpar = st + T::kPar;                         // [32] s / reference, z + 8 s
-  if constexpr (G == 2)
-    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(vpar + lane * 16),
-                 "f"(vs[0] * a.rinv), "f"(vs[1] * a.rinv), "f"(fmaf(8.f, vs[0], vz[0])),
-                 "f"(fmaf(8.f, vs[1], vz[1]))
-                 : "memory");
-  else
-    asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(vpar + lane * 8), "f"(vs[0] * a.rinv),
-                 "f"(fmaf(8.f, vs[0], vz[0]))
-                 : "memory");
   // ---- raw scores: rows r and r + 8 of both halves, heads 2c and 2c + 1 ----
   float s[2][4];
 #pragma unroll
@@ -320,32 +273,33 @@ __device__ __forceinline__ void attend_tile(uint32_t st, int key0, int lo, int l
     uint32_t w[2][W];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint32_t at = st + (half * 16 + u * 8 + r) * T::kRow + c * (W * 4);
-      if constexpr (W == 4)
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
-                     : "r"(at));
-      else
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[u][0]), "=r"(w[u][1]) : "r"(at));
+      const uint8_t *at = st + (half * 16 + u * 8 + r) * T::kRow + c * (W * 4);
+      if constexpr (W == 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        w[u][0] = x.x; w[u][1] = x.y; w[u][2] = x.z; w[u][3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        w[u][0] = x.x; w[u][1] = x.y;
+      }
     }
     float acc[G][4];
-#pragma unroll
-    for (int gi = 0; gi < G; ++gi)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) acc[gi][x] = 0.f;
 #pragma unroll
     for (int i = 0; i < W; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const uint32_t x = w[0][i] >> (8 * k), y = w[1][i] >> (8 * k);
-        mma16816(acc[i % G], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u,
-                 q.f[i][2 * k], q.f[i][2 * k + 1]);
+        if (i < G && k == 0)
+          mma16816_0(acc[i % G], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u,
+                     y & 0x00f000f0u, q.f[i][2 * k], q.f[i][2 * k + 1]);
+        else
+          mma16816(acc[i % G], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u,
+                   q.f[i][2 * k], q.f[i][2 * k + 1]);
       }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float ks[G], kz[G];
-      par_floats<G>(ksu[half * 2 + u], ks);
-      par_floats<G>(kzu[half * 2 + u], kz);
+      par_floats<G>(lds_par<G>(st + T::kPar, half * 16 + u * 8 + r), ks);
+      par_floats<G>(lds_par<G>(st + T::kPar + T::kArr, half * 16 + u * 8 + r), kz);
 #pragma unroll
       for (int hd = 0; hd < 2; ++hd) {
         float x = kz[0] * q.sum[hd][0];
@@ -356,16 +310,25 @@ __device__ __forceinline__ void attend_tile(uint32_t st, int key0, int lo, int l
       }
     }
   }
+  // ---- V's scales and zeros: lane's key, for everyone ----
+  float vs[G], vz[G];
+  par_floats<G>(lds_par<G>(st + T::kPar + 2 * T::kArr, lane), vs);
+  par_floats<G>(lds_par<G>(st + T::kPar + 3 * T::kArr, lane), vz);
   if (ragged) {
+    if (key0 + lane < lo || key0 + lane >= len) {   // may be anything
+#pragma unroll
+      for (int gi = 0; gi < G; ++gi) vs[gi] = vz[gi] = 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + i * 8 + r;
       if (key < lo || key >= len) s[i >> 1][(i & 1) * 2] = s[i >> 1][(i & 1) * 2 + 1] = kMasked;
     }
   }
-  // ---- raise the reference maximum where a score outgrew it ----
-  float top[2];
-  bool up = false;
+  // ---- raise the references where a score or a scale outgrew them ----
+  float top[2], vtop = vs[0];
+  if constexpr (G == 2) vtop = fmaxf(vtop, vs[1]);
+  bool up = vtop > a.vmax;
 #pragma unroll
   for (int hd = 0; hd < 2; ++hd) {
     top[hd] = fmaxf(fmaxf(s[0][hd], s[0][2 + hd]), fmaxf(s[1][hd], s[1][2 + hd]));
@@ -373,41 +336,57 @@ __device__ __forceinline__ void attend_tile(uint32_t st, int key0, int lo, int l
   }
   if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, o));
+    float grow = 1.f;
+    if (vtop > a.vmax) {
+      const float vnew = __uint_as_float((__float_as_uint(vtop) & 0x7f800000u) + 0x00800000u);
+      const float rnew = __fdiv_rn(kPScale, vnew);   // powers of two: exact
+      grow = a.rinv > 0.f ? __fdiv_rn(rnew, a.rinv) : 0.f;
+      a.vmax = vnew;
+      a.rinv = rnew;
+    }
+#pragma unroll
     for (int hd = 0; hd < 2; ++hd) {
       float x = top[hd];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
       const float mnew = fmaxf(a.m[hd], x * q.mul[hd]), alpha = ex2_approx(a.m[hd] - mnew);
+      const float both = alpha * grow;
       a.m[hd] = mnew;
       a.thr[hd] = __fdividef(mnew + kSlack, q.mul[hd]);
       a.l[hd] *= alpha;
 #pragma unroll
       for (int gi = 0; gi < G; ++gi) {
         a.oz[hd][gi] *= alpha;
-        a.ps[gi][hd] *= alpha;
-        a.ps[gi][2 + hd] *= alpha;
+        a.ps[gi][hd] *= both;
+        a.ps[gi][2 + hd] *= both;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          a.o[gi][e][hd] *= alpha;
-          a.o[gi][e][2 + hd] *= alpha;
+          a.o[gi][e][hd] *= both;
+          a.o[gi][e][2 + hd] *= both;
         }
       }
     }
   }
+  uint8_t *const vpar = st;  // over the K codes, which all have read (the vote): s / reference, z + 8 s
+  if constexpr (G == 2)
+    reinterpret_cast<float4 *>(vpar)[lane] = make_float4(
+        vs[0] * a.rinv, vs[1] * a.rinv, fmaf(8.f, vs[0], vz[0]), fmaf(8.f, vs[1], vz[1]));
+  else
+    reinterpret_cast<float2 *>(vpar)[lane] = make_float2(vs[0] * a.rinv, fmaf(8.f, vs[0], vz[0]));
   __syncwarp();              // V's scales and zeros are in place
   // ---- weights ----
   uint32_t pb[G][2][2];      // B operands: [group][half][k rows 0-7, 8-15]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float vsr[G], vc[G], p[2];
-    if constexpr (G == 2)
-      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                   : "=f"(vsr[0]), "=f"(vsr[1]), "=f"(vc[0]), "=f"(vc[1])
-                   : "r"(vpar + (i * 8 + r) * 16));
-    else
-      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                   : "=f"(vsr[0]), "=f"(vc[0])
-                   : "r"(vpar + (i * 8 + r) * 8));
+    if constexpr (G == 2) {
+      const float4 x = reinterpret_cast<const float4 *>(vpar)[i * 8 + r];
+      vsr[0] = x.x; vsr[1] = x.y; vc[0] = x.z; vc[1] = x.w;
+    } else {
+      const float2 x = reinterpret_cast<const float2 *>(vpar)[i * 8 + r];
+      vsr[0] = x.x; vc[0] = x.y;
+    }
 #pragma unroll
     for (int hd = 0; hd < 2; ++hd) {
       p[hd] = ex2_approx(fmaf(s[i >> 1][(i & 1) * 2 + hd], q.mul[hd], -a.m[hd]));
@@ -425,13 +404,14 @@ __device__ __forceinline__ void attend_tile(uint32_t st, int key0, int lo, int l
     uint32_t w[4][G];        // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t row = st + T::kV + (half * 16 + c + 4 * i) * T::kRow;
-      if constexpr (G == 2)
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
-                     : "=r"(w[i][0]), "=r"(w[i][1])
-                     : "r"(row + ((((r >> 1) ^ (c & 2)) << 4) | ((r & 1) << 3))));
-      else
-        w[i][0] = lds32(row + r * 4);
+      const uint8_t *row = st + T::kV + (half * 16 + c + 4 * i) * T::kRow;
+      if constexpr (G == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(
+            row + ((((r >> 1) ^ (c & 2)) << 4) | ((r & 1) << 3)));
+        w[i][0] = x.x; w[i][1] = x.y;
+      } else {
+        w[i][0] = reinterpret_cast<const uint32_t *>(row)[r];
+      }
     }
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
@@ -462,10 +442,10 @@ __device__ __forceinline__ int seq_lo(const Kv4DecodeParams &p, int len) {
 }
 
 // Fills a segment's tiles.  With a selection: the kept blocks, valid, first of their value,
-// with a page in the pool, into this warp's lists.
+// with a page in the pool (64 words of scratch in shared memory bring them together).
 template <bool kSel>
-__device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg, int32_t *pages,
-                                             int32_t *keys, int lane, int32_t &err) {
+__device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg, uint8_t *scratch,
+                                             int lane, int32_t &err) {
   int blk = -1;
   if (kSel && lane < p.topk)
     blk = __ldg(p.sel + ((int64_t)sg.h * p.num_seqs + sg.b) * p.topk + lane);
@@ -489,14 +469,13 @@ __device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg
       }
     }
     const uint32_t m = __ballot_sync(0xffffffffu, ok);
-    if (ok) {
-      const int at = __popc(m & ((1u << lane) - 1u));
-      pages[at] = pg;
-      keys[at] = blk << p.page_log2;
-    }
+    int2 *list = reinterpret_cast<int2 *>(scratch);
+    if (ok) list[__popc(m & ((1u << lane) - 1u))] = make_int2(pg, blk << p.page_log2);
     __syncwarp();
-    sg.pages = pages;
-    sg.keys = keys;
+    const int2 mine = list[lane];
+    __syncwarp();
+    sg.page = mine.x;
+    sg.key = mine.y;
     sg.tiles = __popc(m) << (p.page_log2 - 5);
   }
 }
@@ -509,20 +488,21 @@ struct K4Stream {
   const Kv4DecodeParams &p;
   const K4Seg &sg;
   const int t0, step, count, lane;
-  const uint32_t ring;
+  uint8_t *const ring;
   const bool full;                    // all stages
-  int my_page, my_key;                // of tile 32 * block + lane
-  uint32_t put, get;                  // stages to fill and to use next
+  const uint8_t *my_tile;             // of tile 32 * block + lane: where it lies (null: nowhere)
+  int my_key;                         // and its first key
+  int put, get;                       // offsets of the stages to fill and to use next
   int keys[kStages];                  // first keys of the tiles in the ring, -1: nothing to do
 
   __device__ __forceinline__ K4Stream(const Kv4DecodeParams &p_, const K4Seg &sg_, int t0_,
-                                      int count_, int step_, uint32_t ring_, bool full_, int lane_)
+                                      int count_, int step_, uint8_t *ring_, bool full_, int lane_)
       : p(p_), sg(sg_), t0(t0_), step(step_), count(count_), lane(lane_), ring(ring_),
-        full(full_), my_page(-1), my_key(0), put(ring_), get(ring_) {}
+        full(full_), my_tile(nullptr), my_key(0), put(0), get(0) {}
 
-  __device__ __forceinline__ void next(uint32_t &stage) const {
+  __device__ __forceinline__ void next(int &stage) const {
     stage += T::kBytes;
-    if (stage == ring + (full ? kStages : kStages - 1) * T::kBytes) stage = ring;
+    if (stage == (full ? kStages : kStages - 1) * T::kBytes) stage = 0;
   }
   __device__ __forceinline__ int issue(int n, int32_t &err) {
     int key = -1;
@@ -530,29 +510,30 @@ struct K4Stream {
       const int tpl = p.page_log2 - 5;
       if ((n & 31) == 0) {            // look up the next 32 tiles' pages
         const int i = n + lane, t = t0 + i * step;
-        my_page = -1;
-        if (i < count) {
-          if (kSel) {
-            my_page = sg.pages[t >> tpl];
-            my_key = sg.keys[t >> tpl] + ((t & ((1 << tpl) - 1)) << 5);
-          } else {
-            my_key = (sg.first + t) << 5;
-            my_page = __ldg(p.table + (int64_t)sg.b * p.width + (my_key >> p.page_log2));
-            if (my_page < 0 || my_page >= p.num_pages) {
-              my_page = -1;
-              err |= NSA_DEVERR_BAD_INDEX;
-            }
+        int pg = -1;
+        if (kSel) {
+          pg = __shfl_sync(0xffffffffu, sg.page, t >> tpl);
+          my_key = __shfl_sync(0xffffffffu, sg.key, t >> tpl) + ((t & ((1 << tpl) - 1)) << 5);
+          if (i >= count) pg = -1;
+        } else if (i < count) {
+          my_key = (sg.first + t) << 5;
+          pg = __ldg(p.table + (int64_t)sg.b * p.width + (my_key >> p.page_log2));
+          if (pg < 0 || pg >= p.num_pages) {
+            pg = -1;
+            err |= NSA_DEVERR_BAD_INDEX;
           }
-          if (my_key >= sg.len || my_key + 32 <= sg.lo) my_page = -1;
         }
+        if (my_key >= sg.len || my_key + 32 <= sg.lo) pg = -1;
+        my_tile = pg < 0 ? nullptr
+                         : p.pool + ((((int64_t)pg * p.h_k + sg.h) << tpl) +
+                                     ((my_key & ((1 << p.page_log2) - 1)) >> 5)) * T::kBytes;
       }
-      const int pg = __shfl_sync(0xffffffffu, my_page, n & 31);
+      const uint8_t *tile = reinterpret_cast<const uint8_t *>(__shfl_sync(
+          0xffffffffu, reinterpret_cast<unsigned long long>(my_tile), n & 31));
       const int k0 = __shfl_sync(0xffffffffu, my_key, n & 31);
-      if (pg >= 0) {
+      if (tile) {
         key = k0;
-        const int64_t at = (((int64_t)pg * p.h_k + sg.h) << tpl) +
-                           ((k0 & ((1 << p.page_log2) - 1)) >> 5);
-        copy_tile<D>(put, p.pool + at * T::kBytes, lane);
+        copy_tile<D>(smem_u32(ring) + put, tile, lane);
       }
     }
     cp_async_commit();
@@ -574,7 +555,7 @@ struct K4Stream {
         cp_async_wait_group<1>();
       }
       __syncwarp();
-      if (keys[0] >= 0) attend_tile<D>(get, keys[0], sg.lo, sg.len, lane, q, a);
+      if (keys[0] >= 0) attend_tile<D>(ring + get, keys[0], sg.lo, sg.len, lane, q, a);
       __syncwarp();                   // the stage is filled again in the next turn
       next(get);
       keys[0] = keys[1];
@@ -638,7 +619,6 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_seg_kernel(Kv4DecodeParams 
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float4 ml[kK4Warps][kK4Heads / 2];        // m, l of two heads
   __shared__ float lsum[kK4Warps][kK4Heads];
-  __shared__ int32_t pages[kK4Warps][32], keys[kK4Warps][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   K4Seg sg = {};
   set_unit(p, blockIdx.x, sg);
@@ -646,9 +626,9 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_seg_kernel(Kv4DecodeParams 
   int32_t err = 0;
   K4RawQuery<D> raw;
   fetch_query<D>(p, sg, lane, raw);
-  open_segment<kSel>(p, sg, pages[warp], keys[warp], lane, err);
+  open_segment<kSel>(p, sg, smem + warp * K4<D>::kRing, lane, err);
   K4Stream<D, kSel> st(p, sg, warp, max(0, (sg.tiles - warp + kK4Warps - 1) / kK4Warps), kK4Warps,
-                       smem_u32(smem) + warp * K4<D>::kRing, true, lane);
+                       smem + warp * K4<D>::kRing, true, lane);
   st.start(err);
   K4Query<D> q;
   make_query<D, kFp16>(raw, p.scale_log2, lane, q);
@@ -730,30 +710,19 @@ __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
   return x;
 }
 
-// What a warp's run left for the CTA: a first part (of a segment begun before the run) and
-// a last part (of a segment that goes on behind it).
-struct K4Run {
-  int fb, fu, lb, lu;   // their sequences and units
-  int end;              // first tile behind the segment of the last part
-  int first, last;      // there is one
-  int on;               // the first part covers the whole run and its segment goes on
-  int kept;             // the first part lies in the ring's last stage
-};
-
 // Equal runs of the batch's counted tiles.  whole: a CTA's run is moved to segments' starts,
 // so that no segment is split between CTAs.
 template <int D, bool kFp16, bool kSel>
 __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams p, int units,
                                                                 int whole) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float4 first_ml[kK4Warps][kK4Heads / 2], last_ml[kK4Warps][kK4Heads / 2];
-  __shared__ float first_f[kK4Warps][kK4Heads], last_f[kK4Warps][kK4Heads];
-  __shared__ int32_t pages[kK4Warps][32], keys[kK4Warps][32];
-  __shared__ K4Run runs[kK4Warps];
-  __shared__ int wsum[kK4Warps], found[kK4Warps + 1][3];   // tile, sequence, its first tile
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // of a warp's parts ([0]: first, [1]: last): m, l of two heads; factors, l times them
+  __shared__ float4 ml[2][kK4Warps][kK4Heads / 2];
+  __shared__ float2 fac[2][kK4Warps][kK4Heads], top[kK4Warps + 1][kK4Heads / 2];
+  __shared__ int pre[kK4Threads], wsum[kK4Warps], flags[kK4Warps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // ---- the batch's tiles, and where the runs of this CTA's warps begin ----
+  // ---- the batch's tiles ----
   const int per_thread = (p.num_seqs + kK4Threads - 1) / kK4Threads;
   const int b0 = min(tid * per_thread, p.num_seqs), b1 = min(b0 + per_thread, p.num_seqs);
   int32_t err = 0, ignore = 0;
@@ -761,77 +730,66 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   for (int b = b0; b < b1; ++b) mine += counted_tiles<kSel>(p, seq_len(p, b, err));
   if (blockIdx.x == 0 && err) raise(p.status, err);
   err = 0;
-  mine *= units;
-  int incl = warp_incl_sum(mine, lane);
-  if (lane == 31) wsum[warp] = incl;
+  pre[tid] = warp_incl_sum(mine * units, lane);
+  if (lane == 31) wsum[warp] = pre[tid];
   __syncthreads();
   int total = 0;
 #pragma unroll
-  for (int w = 0; w < kK4Warps; ++w) {
-    if (w < warp) incl += wsum[w];
-    total += wsum[w];
-  }
-  const int warps = gridDim.x * kK4Warps;
-  int per_warp = (total + warps - 1) / warps;
-  const int per = per_warp * kK4Warps;                     // tiles of a CTA
-  const int from = static_cast<int>(min((int64_t)blockIdx.x * per, (int64_t)total));
-  const int to = min(from + min(per, total - from), total);
-  const int ntargets = whole ? 2 : kK4Warps + 1;
-  for (int k = 0; k < ntargets; ++k) {
-    const int v = whole ? (k ? to : from) : min(from + min(k * per_warp, total - from), to);
-    if (v == total ? tid == 0 : (incl - mine <= v && v < incl)) {
-      int b = b0, base = incl - mine, at = v;
-      if (v == total) {
-        b = p.num_seqs;
-        base = total;
-      }
-      for (; b < b1; ++b) {
-        const int nt = counted_tiles<kSel>(p, seq_len(p, b, ignore)), all = nt * units;
-        if (v < base + all) {
-          if (whole) at = base + (v - base + nt - 1) / nt * nt;   // the next segment's start
-          if (at == base + all) {
-            ++b;
-            base = at;
-          }
-          break;
-        }
-        base += all;
-      }
-      found[k][0] = at;
-      found[k][1] = b;
-      found[k][2] = base;
+  for (int w = 0; w < kK4Warps; ++w) total += wsum[w];
+  // the sequence that holds tile v (< total), and that sequence's first tile
+  auto locate = [&](int v, int &b, int &base) {
+    int chunk = 0, off = 0;                // threads whose sequences lie before v
+    base = 0;
+#pragma unroll
+    for (int w = 0; w < kK4Warps; ++w) {
+      const int x = off + pre[w * 32 + lane];
+      const uint32_t m = __ballot_sync(0xffffffffu, x <= v);
+      chunk += __popc(m);
+      if (m) base = __shfl_sync(0xffffffffu, x, 31 - __clz(m));
+      off += wsum[w];
     }
-  }
-  __syncthreads();
-  int at, stop, b, base;                   // this warp's run; the sequence of its first tile
-  if (whole) {
-    const int begin = found[0][0], end = found[1][0];
-    per_warp = (end - begin + kK4Warps - 1) / kK4Warps;
-    at = min(begin + warp * per_warp, end);
-    stop = min(at + per_warp, end);
-    b = found[0][1];
-    base = found[0][2];
-    while (at < stop) {                    // 32 sequences at a time
+    b = chunk * per_thread;
+    if (per_thread == 1) return;
+    while (b < p.num_seqs) {               // 32 sequences at a time
       const int n = b + lane < p.num_seqs
                         ? counted_tiles<kSel>(p, seq_len(p, b + lane, ignore)) * units : 0;
       const int in = warp_incl_sum(n, lane);
-      const uint32_t past = __ballot_sync(0xffffffffu, at < base + in);
+      const uint32_t past = __ballot_sync(0xffffffffu, v < base + in);
       const int hit = past ? __ffs(past) - 1 : 31;
       base += __shfl_sync(0xffffffffu, past ? in - n : in, hit);
       b += past ? hit : 32;
       if (past) break;
     }
-  } else {
-    at = found[warp][0];
-    b = found[warp][1];
-    base = found[warp][2];
-    stop = found[warp + 1][0];
+  };
+  // ---- this warp's run ----
+  const int warps = gridDim.x * kK4Warps;
+  int per_warp = (total + warps - 1) / warps;
+  const int per = per_warp * kK4Warps;                     // tiles of a CTA
+  int from = static_cast<int>(min((int64_t)blockIdx.x * per, (int64_t)total));
+  int to = from + min(per, total - from);
+  int b = 0, base = 0;
+  if (whole) {                             // from and to move to the next segments' starts
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+      int &v = k ? to : from;
+      if (v >= total) continue;
+      locate(v, b, base);
+      const int nt = counted_tiles<kSel>(p, seq_len(p, b, ignore));
+      v = base + (v - base + nt - 1) / nt * nt;
+    }
+    per_warp = (to - from + kK4Warps - 1) / kK4Warps;
   }
+  int at = from + min(warp * per_warp, to - from);
+  const int stop = at + min(per_warp, to - at);
+  if (at < stop) locate(at, b, base);
   uint8_t *const ring = smem + warp * K4<D>::kRing;
-  K4Run run = {};
+  // What the run leaves for the CTA: a first part, of a segment begun before the run (and
+  // whether that goes on behind it, whether it is kept in the ring's last stage), and a last
+  // part, of a segment that begins in the run and goes on.
+  constexpr int kFirst = 1, kLast = 2, kOn = 4, kKeep = 8;
+  int left = 0, first_b = 0, first_u = 0, last_b = 0, last_u = 0, last_end = 0;
   int unit = -1, nt = 0;
   K4State<D> a;
-  const int c = lane & 3;
   while (at < stop) {
     K4Seg sg = {};
     sg.b = b;
@@ -844,9 +802,9 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     if (v1 > kOver) {
       K4RawQuery<D> raw;
       fetch_query<D>(p, sg, lane, raw);
-      open_segment<kSel>(p, sg, pages[warp], keys[warp], lane, err);
+      open_segment<kSel>(p, sg, ring, lane, err);
       const int t0 = max(0, v0 - kOver), t1 = min(v1 - kOver, sg.tiles);
-      K4Stream<D, kSel> st(p, sg, t0, max(0, t1 - t0), 1, smem_u32(ring), !run.kept, lane);
+      K4Stream<D, kSel> st(p, sg, t0, max(0, t1 - t0), 1, ring, !(left & kKeep), lane);
       st.start(err);
       K4Query<D> q;
       make_query<D, kFp16>(raw, p.scale_log2, lane, q);
@@ -855,33 +813,27 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     sum_lanes(a);
     at = seg0 + v1;
     const bool goes_on = v1 < nt, first = v0 > 0;
-    if (first || goes_on) {
-      // a part; unless the run goes on, it stays in registers until the CTA's warps agree
-      if (lane < 4)
-        (first ? first_ml : last_ml)[warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
-      if (first) {
-        run.first = 1;
-        run.on = goes_on;
-        run.kept = at < stop;
-        run.fb = b;
-        run.fu = unit;
-        if (run.kept) leave_out<D>(reinterpret_cast<float *>(ring + K4<D>::kKept), lane, a, 1.f, 1.f);
-      } else {
-        run.last = 1;
-        run.lb = b;
-        run.lu = unit;
-        run.end = seg0 + nt;
-      }
+    if (lane < 4) ml[first ? 0 : 1][warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
+    if (first) {
+      left |= kFirst | (goes_on ? kOn : 0) | (at < stop ? kKeep : 0);
+      first_b = b;
+      first_u = unit;
+      if (at < stop) leave_out<D>(reinterpret_cast<float *>(ring + K4<D>::kKept), lane, a, 1.f, 1.f);
+    } else if (goes_on) {                  // the run's last: stays in registers
+      left |= kLast;
+      last_b = b;
+      last_u = unit;
+      last_end = seg0 + nt;
     } else {
       float *area = reinterpret_cast<float *>(ring);
       leave_out<D>(area, lane, a, 1.f, 1.f);
-      if (lane < 4) last_ml[warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
       __syncwarp();
+#pragma unroll 1
       for (int i = lane; i < sg.g * (D / 2); i += 32) {
         const int head = i / (D / 2), dim = 2 * (i % (D / 2));
         const float2 o = *reinterpret_cast<const float2 *>(
             area + (head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim);
-        const float4 v = last_ml[warp][head >> 1];
+        const float4 v = ml[1][warp][head >> 1];
         write_out<D, kFp16>(p, b, sg.q0 + head, dim, o.x, o.y, head & 1 ? v.z : v.x,
                             head & 1 ? v.w : v.y);
       }
@@ -895,84 +847,88 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   }
   err = __reduce_or_sync(0xffffffffu, err);
   if (err && lane == 0) raise(p.status, err);
-  if (lane == 0) runs[warp] = run;
+  if (lane == 0) flags[warp] = left;
   if (tid == 0 && !whole) splits_of(p)[blockIdx.x] = K4Split{0, 0};
   __syncthreads();
   // ---- join the parts of segments that cross warps ----
-  // A group is a segment's parts in this CTA: a last part of warp `open` (-1: the segment
-  // began in an earlier CTA), then first parts of warps open + 1 ... e - 1; `on`: it goes on
-  // in the next CTA.  Every warp finds its parts' groups, and the factor that takes a part to
-  // its group's maximum.
-  struct Group {
-    int open, e, on;
+  // A group is a segment's parts in this CTA: the last part of warp `open` (-1: the segment
+  // began in an earlier CTA) and the first parts of the warps behind it, up to the next
+  // warp with a last part.
+  const int fl = lane < kK4Warps ? flags[lane] : 0;
+  const uint32_t firsts = __ballot_sync(0xffffffffu, fl & kFirst);
+  const uint32_t lasts = __ballot_sync(0xffffffffu, fl & kLast);
+  const uint32_t ons = __ballot_sync(0xffffffffu, fl & kOn);
+  const uint32_t keeps = __ballot_sync(0xffffffffu, fl & kKeep);
+  auto members = [&](int open) {           // warps whose first part belongs to the group
+    const uint32_t behind = ~0u << (open + 1), next = lasts & behind;
+    return firsts & behind & (next ? (next ^ (next - 1)) : ~0u);
   };
-  auto group_of = [&](int open) {
-    Group g = {open, open + 1, 1};
-    while (g.on && g.e < kK4Warps && runs[g.e].first) {
-      g.on = runs[g.e].on;
-      ++g.e;
-    }
-    return g;
+  auto opener = [&](int side) {
+    const uint32_t before = lasts & ((1u << warp) - 1u);
+    return side ? warp : 31 - __clz(before);
   };
-  Group groups[2] = {{-1, 0, 0}, {-1, 0, 0}};
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {   // 0: the warp's first part, 1: its last
-    if (!(side ? run.last : run.first)) continue;
-    int open = side ? warp : warp - 1;
-    if (!side)
-      while (open >= 0 && runs[open].on) --open;
-    const Group g = group_of(open);
-    groups[side] = g;
-    float M0 = -INFINITY, M1 = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kK4Warps; ++w) {
-      if (w != open && !(w > open && w < g.e)) continue;
-      const float4 v = w == open ? last_ml[w][c] : first_ml[w][c];
-      M0 = fmaxf(M0, v.x);
-      M1 = fmaxf(M1, v.z);
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    if (!(left & (side ? kLast : kFirst))) continue;
+    const int open = opener(side), r = lane >> 2;
+    const uint32_t in = members(open);
+    float M0 = -INFINITY, M1 = -INFINITY;  // lane (r, c): warp r's part, heads 2c, 2c + 1
+    if (r == open || (in >> r & 1)) {
+      const float4 v = ml[r == open][r][c];
+      M0 = v.x;
+      M1 = v.z;
     }
-    const float4 v = side ? last_ml[warp][c] : first_ml[warp][c];
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+      M0 = fmaxf(M0, __shfl_xor_sync(0xffffffffu, M0, o));
+      M1 = fmaxf(M1, __shfl_xor_sync(0xffffffffu, M1, o));
+    }
+    const float4 v = ml[side][warp][c];
     const float f0 = v.y != 0.f ? ex2_approx(v.x - M0) : 0.f;
     const float f1 = v.w != 0.f ? ex2_approx(v.z - M1) : 0.f;
-    const bool in_area = !side && run.kept;   // already left, with a factor of 1
-    if (!in_area) leave_out<D>(reinterpret_cast<float *>(ring), lane, a, f0, f1);
-    if (lane < 4)
-      *reinterpret_cast<float2 *>(&(side ? last_f : first_f)[warp][2 * c]) = make_float2(f0, f1);
+    const bool kept = !side && (left & kKeep);   // left already, without its factor
+    if (!kept) leave_out<D>(reinterpret_cast<float *>(ring), lane, a, f0, f1);
+    if (lane < 4) {
+      fac[side][warp][2 * c] = make_float2(kept ? f0 : 1.f, v.y * f0);
+      fac[side][warp][2 * c + 1] = make_float2(kept ? f1 : 1.f, v.w * f1);
+      top[open + 1][c] = make_float2(M0, M1);    // the same from all of the group
+    }
   }
   __syncthreads();
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
-    if (!(side ? run.last : run.first)) continue;
-    const Group g = groups[side];
-    const int lead = g.open >= 0 ? g.open : 0, n = g.e - lead;     // warps of the group
+    if (!(left & (side ? kLast : kFirst))) continue;
+    const int open = opener(side);
+    const uint32_t in = members(open), all = in | (open >= 0 ? 1u << open : 0u);
+    const bool on = in ? ons >> (31 - __clz(in)) & 1 : true;
     K4Seg sg = {};
-    sg.b = side ? run.lb : run.fb;
-    set_unit(p, side ? run.lu : run.fu, sg);
+    sg.b = side ? last_b : first_b;
+    set_unit(p, side ? last_u : first_u, sg);
     float *part = nullptr;
-    if (g.open < 0) part = part_of<D>(p, 2 * blockIdx.x);
-    else if (g.on) part = part_of<D>(p, 2 * blockIdx.x + 1);
-    if (g.open == warp && side && g.on && lane == 0)
-      splits_of(p)[blockIdx.x] =
-          K4Split{sg.b * units + run.lu, (run.end - 1) / per - static_cast<int>(blockIdx.x) + 1};
-    for (int i = (warp - lead) * 32 + lane; i < sg.g * (D / 2); i += n * 32) {
+    if (open < 0) part = part_of<D>(p, 2 * blockIdx.x);
+    else if (on) part = part_of<D>(p, 2 * blockIdx.x + 1);
+    if (side && on && lane == 0)
+      splits_of(p)[blockIdx.x] = K4Split{
+          sg.b * units + last_u, (last_end - 1) / per - static_cast<int>(blockIdx.x) + 1};
+    const int th = __popc(all & ((1u << warp) - 1u)) * 32 + lane, nth = __popc(all) * 32;
+#pragma unroll 1
+    for (int i = th; i < sg.g * (D / 2); i += nth) {
       const int head = i / (D / 2), dim = 2 * (i % (D / 2));
       const int off = ((head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim) * 4;
-      float l = 0.f, x = 0.f, y = 0.f, M = -INFINITY;
+      float l = 0.f, x = 0.f, y = 0.f;
 #pragma unroll
       for (int w = 0; w < kK4Warps; ++w) {
-        if (w < lead || w >= g.e) continue;
-        const bool fst = w != g.open, kept = fst && runs[w].kept;
-        const float2 o = *reinterpret_cast<const float2 *>(smem + w * K4<D>::kRing +
-                                                           (kept ? K4<D>::kKept : 0) + off);
-        const float f = (fst ? first_f : last_f)[w][head];
-        const float4 v = (fst ? first_ml : last_ml)[w][head >> 1];
-        const float k = kept ? f : 1.f;
-        // a part without keys adds nothing; its maximum is -inf
-        l = fmaf(f, head & 1 ? v.w : v.y, l);
-        M = fmaxf(M, head & 1 ? v.z : v.x);
-        x = fmaf(k, o.x, x);
-        y = fmaf(k, o.y, y);
+        if (!(all >> w & 1)) continue;
+        const bool fst = w != open;
+        const float2 o = *reinterpret_cast<const float2 *>(
+            smem + w * K4<D>::kRing + (fst && (keeps >> w & 1) ? K4<D>::kKept : 0) + off);
+        const float2 f = fac[!fst][w][head];
+        l += f.y;
+        x = fmaf(f.x, o.x, x);
+        y = fmaf(f.x, o.y, y);
       }
+      const float2 m2 = top[open + 1][head >> 1];
+      const float M = head & 1 ? m2.y : m2.x;
       if (part) {
         *reinterpret_cast<float2 *>(part + head * D + dim) = make_float2(x, y);
         if (dim == 0) *reinterpret_cast<float2 *>(part + sg.g * D + 2 * head) = make_float2(M, l);
