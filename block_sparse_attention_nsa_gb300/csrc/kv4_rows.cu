@@ -6,165 +6,249 @@
 // HBM bounds both directions: 4 d bytes of 16-bit K and V against d + d / 8 stored.
 //
 // Eight lanes own a group, eight dimensions each: one 16-byte access of the 16-bit row,
-// three shuffles for the minimum and maximum, one 32-bit word of codes.  A warp covers
-// K and V of one (token, head) at d = 128, of two at d = 64, so that its code words fill
-// whole 32-byte sectors.
+// three shuffles for the minimum and maximum, one 32-bit word of codes.  A warp covers four
+// groups of a token (K and V of one head at d = 128, of two at d = 64), whose code words
+// fill whole 32-byte sectors, and takes kRows consecutive tokens, whose loads it issues
+// together.
 #include "kv4.cuh"
 
 namespace nsa {
 
 constexpr int kRowThreads = 256;
+constexpr int kRows = 4;
 constexpr float kHalfMax = 65504.f;
 
-// Where a thread's group lies: row, head, K or V, group of the row.
-struct RowGroup {
-  int t, h, kv, gi;
+// A lane's place: its warp's first token, and its group of every token.
+struct RowPlace {
+  int t0, h, kv, gi, j;
+  bool live;
 };
 template <int D>
-__device__ __forceinline__ RowGroup row_group(int64_t i, int h_k) {
-  constexpr int kG = Kv4Tile<D>::kG;
-  RowGroup r;
-  r.gi = static_cast<int>(i % kG);
-  r.kv = static_cast<int>(i / kG % 2);
-  const int64_t th = i / (2 * kG);
-  r.t = static_cast<int>(th / h_k);
-  r.h = static_cast<int>(th - (int64_t)r.t * h_k);
+__device__ __forceinline__ RowPlace row_place(const Kv4RowParams &p) {
+  constexpr int kG = Kv4Tile<D>::kG, kHeads = 2 / kG;      // heads of a warp
+  const int lane = threadIdx.x & 31, part = lane >> 3;
+  const unsigned units = (p.h_k + kHeads - 1) / kHeads;    // warps to a token
+  const uint64_t task = (uint64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  uint32_t tb, u;
+  if (task >> 32) {
+    tb = static_cast<uint32_t>(task / units);
+    u = static_cast<uint32_t>(task - (uint64_t)tb * units);
+  } else {
+    tb = static_cast<uint32_t>(task) / units;
+    u = static_cast<uint32_t>(task) - tb * units;
+  }
+  RowPlace r;
+  r.t0 = static_cast<int>(min((uint64_t)tb * kRows, (uint64_t)p.n));
+  r.h = kG == 2 ? u : 2 * u + (part >> 1);
+  r.kv = kG == 2 ? part >> 1 : part & 1;
+  r.gi = kG == 2 ? part & 1 : 0;
+  r.j = lane & 7;
+  r.live = r.h < p.h_k;
   return r;
+}
+
+// The slots of a warp's tokens, -1 where there is none or it is not valid.
+__device__ __forceinline__ void load_slots(const Kv4RowParams &p, int t0, int (&slot)[kRows]) {
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    slot[k] = t0 + k < p.n ? __ldg(p.slots + t0 + k) : -1;
+    if (slot[k] < 0 || (slot[k] >> p.page_log2) >= p.num_pages) {
+      bad |= slot[k] != -1;
+      slot[k] = -1;
+    }
+  }
+  if (bad && (threadIdx.x & 31) == 0) raise(p.status, NSA_DEVERR_BAD_INDEX);
 }
 
 // The tile that holds a slot of head h.
 template <int D>
-__device__ __forceinline__ uint8_t *slot_tile(uint8_t *pool, int h_k, int page_log2, int h,
-                                              int slot) {
-  const int64_t page = slot >> page_log2;
-  const int in = slot & ((1 << page_log2) - 1);
-  return pool + ((page * h_k + h) * (int64_t)((1 << page_log2) / kKv4Tile) + in / kKv4Tile) *
-                    Kv4Tile<D>::kBytes;
+__device__ __forceinline__ uint8_t *slot_tile(const Kv4RowParams &p, int h, int slot) {
+  const int64_t page = slot >> p.page_log2;
+  const int in = slot & ((1 << p.page_log2) - 1);
+  return p.pool + (((page * p.h_k + h) << (p.page_log2 - 5)) + in / kKv4Tile) * Kv4Tile<D>::kBytes;
 }
 
-// (x - zero) / scale to the nearest whole number, ties to even, in 0 ... 15: the rounded
-// product with 1 / scale is at most one off, and only next to a border; its residual
-// x - zero - c * scale, exact in one fused step, says which side it is on.
-__device__ __forceinline__ uint32_t code4(float x, float zero, float scale, float inv) {
-  const float t = __fsub_rn(x, zero);
-  const float m = __fadd_rn(__fmul_rn(t, inv), 12582912.f);   // 1.5 * 2^23: rounds to a whole number
-  float c = __fsub_rn(m, 12582912.f);
-  const float r = __fmaf_rn(-c, scale, t), half = 0.5f * scale;
-  const bool odd = __float_as_uint(m) & 1u;
-  if (fabsf(r) > half || (fabsf(r) == half && odd)) c += r > 0.f ? 1.f : -1.f;
-  return static_cast<uint32_t>(fminf(fmaxf(c, 0.f), 15.f));
+// Larger of two pairs of 16-bit floats; a NaN stays.
+template <bool kFp16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  if constexpr (kFp16) {
+    const __half2 m = __hmax2_nan(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+  } else {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a),
+                                         *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+  }
+}
+template <bool kFp16>
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  if constexpr (kFp16) {
+    const __half2 m = __hmin2_nan(*reinterpret_cast<__half2 *>(&a), *reinterpret_cast<__half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+  } else {
+    const __nv_bfloat162 m = __hmin2_nan(*reinterpret_cast<__nv_bfloat162 *>(&a),
+                                         *reinterpret_cast<__nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&m);
+  }
+}
+// a[i] of four, by selects.
+template <typename V>
+__device__ __forceinline__ V pick(const V (&a)[kRows], int i) {
+  static_assert(kRows == 4, "two bits choose a row");
+  return i & 2 ? (i & 1 ? a[3] : a[2]) : (i & 1 ? a[1] : a[0]);
+}
+
+// x / y for inv = 1 / y rounded: the product, corrected by its exact residual, is the correctly
+// rounded quotient (Markstein, 1990).
+__device__ __forceinline__ float quotient(float x, float y, float inv) {
+  const float q = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-q, y, x), inv, q);
+}
+
+// The eight codes of a lane: (x - zero) / scale to the nearest whole number, ties to even, as
+// adding 1.5 * 2^23 rounds.  kHeld: held to finite x and to 0 ... 15, which most groups need
+// no step for.
+template <bool kFp16, bool kHeld>
+__device__ __forceinline__ uint32_t code_word(const uint32_t (&w4)[4], float zero, float scale,
+                                              float inv) {
+  uint32_t word = 0;
+#pragma unroll
+  for (int u = 3; u >= 0; --u) {         // the lowest nibble last: each step shifts by four bits
+    const float2 f = unpack2<kFp16>(w4[u]);
+#pragma unroll
+    for (int k = 1; k >= 0; --k) {
+      float x = k ? f.y : f.x;
+      if (kHeld) x = fminf(fmaxf(x, -kHalfMax), kHalfMax);
+      float q = quotient(__fsub_rn(x, zero), scale, inv);
+      if (kHeld) q = fminf(fmaxf(q, 0.f), 15.f);
+      word = word * 16u + __float_as_uint(__fadd_rn(q, 12582912.f));
+    }
+  }
+  return word - 0x4b400000u * 0x11111111u;   // less the bits of 1.5 * 2^23 in each of the eight
 }
 
 template <int D, bool kFp16>
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowParams p) {
   using T = Kv4Tile<D>;
-  const int lane = threadIdx.x & 31, j = lane & 7;
-  const int64_t groups = (int64_t)p.n * p.h_k * 2 * T::kG;
-  const int64_t i = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) >> 3;
-  const bool in = i < groups;
-  const RowGroup r = row_group<D>(in ? i : 0, p.h_k);
-  const int slot = in ? p.slots[r.t] : -1;
-  const bool good = slot >= 0 && (slot >> p.page_log2) < p.num_pages;
-  if (in && slot != -1 && !good && r.h == 0 && r.kv == 0 && r.gi == 0 && j == 0)
-    raise(p.status, NSA_DEVERR_BAD_INDEX);
-  uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-  if (good) {
-    const uint16_t *src = static_cast<const uint16_t *>(r.kv ? p.v : p.k) +
-                          r.t * (r.kv ? p.v_ts : p.k_ts) + r.h * (r.kv ? p.v_hs : p.k_hs) +
-                          r.gi * 64 + j * 8;
-    raw = *reinterpret_cast<const uint4 *>(src);
-  }
-  const uint32_t w4[4] = {raw.x, raw.y, raw.z, raw.w};
-  float x[8];
-  bool nan = false;
-  float lo = kHalfMax, hi = -kHalfMax;
+  const RowPlace r = row_place<D>(p);
+  int slot[kRows];
+  load_slots(p, r.t0, slot);
+  const int64_t ts = r.kv ? p.v_ts : p.k_ts, hs = r.kv ? p.v_hs : p.k_hs;
+  const uint16_t *src = static_cast<const uint16_t *>(r.kv ? p.v : p.k) + r.t0 * ts + r.h * hs +
+                        r.gi * 64 + r.j * 8;
+  uint4 raw[kRows];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const float2 f = unpack2<kFp16>(w4[u]);
-    x[2 * u] = f.x;
-    x[2 * u + 1] = f.y;
+  for (int k = 0; k < kRows; ++k) {
+    raw[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (r.live && slot[k] >= 0)
+      raw[k] = __ldcs(reinterpret_cast<const uint4 *>(src + k * ts));
+  }
+  // the groups' smallest (negated) and largest values, packed
+  uint32_t ends[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    const uint32_t lo = min2<kFp16>(min2<kFp16>(raw[k].x, raw[k].y), min2<kFp16>(raw[k].z, raw[k].w));
+    const uint32_t hi = max2<kFp16>(max2<kFp16>(raw[k].x, raw[k].y), max2<kFp16>(raw[k].z, raw[k].w));
+    uint32_t e = max2<kFp16>(__byte_perm(lo, hi, 0x5410) ^ 0x8000u, __byte_perm(lo, hi, 0x7632) ^ 0x8000u);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) e = max2<kFp16>(e, __shfl_xor_sync(0xffffffffu, e, o));
+    ends[k] = e;
+  }
+  // Lane j works out the zero and scale of row j % 4 for the others of its group, and stores
+  // one of the two.
+  const int mine = r.j & 3, my_slot = pick(slot, mine);
+  const float2 e = unpack2<kFp16>(pick(ends, mine));
+  const bool nan = e.x != e.x || e.y != e.y;
+  const float low = -e.x, high = e.y;
+  const float lo = fminf(fmaxf(low, -kHalfMax), kHalfMax);
+  const float hi = fminf(fmaxf(high, -kHalfMax), kHalfMax);
+  const __half zh = nan ? __ushort_as_half(0x7fff) : __float2half_rn(lo);
+  const float my_zero = __half2float(zh);
+  const __half sh = nan ? __ushort_as_half(0)
+                        : __float2half_rn(quotient(__fsub_rn(hi, my_zero), 15.f, 1.f / 15.f));
+  const float my_scale = __half2float(sh), my_inv = __frcp_rn(my_scale);
+  const uint32_t both = __half_as_ushort(zh) | static_cast<uint32_t>(__half_as_ushort(sh)) << 16;
+  const bool stored = r.live && my_slot >= 0;
+  // no code can leave 0 ... 15 where zero is not above the smallest value and the largest
+  // is not 15.5 steps above it
+  const bool held = __any_sync(0xffffffffu, stored && !(my_zero <= low &&
+                                                        high - my_zero < 15.4f * my_scale));
+  if (stored) {
+    const int row = my_slot & (kKv4Tile - 1), which = r.j >> 2;   // 0: scale, 1: zero
+    *reinterpret_cast<__half *>(slot_tile<D>(p, r.h, my_slot) + T::kPar +
+                                (2 * r.kv + which) * T::kArr + (row * T::kG + r.gi) * 2) =
+        which ? zh : sh;
   }
 #pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    nan |= x[u] != x[u];
-    x[u] = fminf(fmaxf(x[u], -kHalfMax), kHalfMax);
-    lo = fminf(lo, x[u]);
-    hi = fmaxf(hi, x[u]);
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-  }
-  nan = (__ballot_sync(0xffffffffu, nan) >> (lane & 24) & 0xffu) != 0;
-  __half zh = __float2half_rn(lo);
-  const float zero = __half2float(zh);
-  __half sh = __float2half_rn(__fdiv_rn(__fsub_rn(hi, zero), 15.f));
-  if (nan) {
-    zh = __ushort_as_half(0x7fff);
-    sh = __ushort_as_half(0);
-  }
-  const float scale = __half2float(sh), inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
-  uint32_t word = 0;
-  if (scale > 0.f) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) word |= code4(x[u], zero, scale, inv) << (4 * u);
-  }
-  if (good) {
-    uint8_t *tile = slot_tile<D>(p.pool, p.h_k, p.page_log2, r.h, slot);
-    const int row = slot & (kKv4Tile - 1);
-    *reinterpret_cast<uint32_t *>(tile + r.kv * T::kV + row * T::kRow +
-                                  (j * T::kG + r.gi) * 4) = word;
-    if (j < 2)   // scale, zero
-      *reinterpret_cast<__half *>(tile + T::kPar + (2 * r.kv + j) * T::kArr +
-                                  (row * T::kG + r.gi) * 2) = j ? zh : sh;
+  for (int k = 0; k < kRows; ++k) {
+    const int from = (threadIdx.x & 24) + k;
+    const uint32_t zs = __shfl_sync(0xffffffffu, both, from);
+    const float inv = __shfl_sync(0xffffffffu, my_inv, from);
+    const float2 f = unpack2<true>(zs);
+    const uint32_t w4[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+    uint32_t word = held ? code_word<kFp16, true>(w4, f.x, f.y, inv)
+                         : code_word<kFp16, false>(w4, f.x, f.y, inv);
+    if (!(f.y > 0.f)) word = 0;
+    if (r.live && slot[k] >= 0)
+      *reinterpret_cast<uint32_t *>(slot_tile<D>(p, r.h, slot[k]) + r.kv * T::kV +
+                                    (slot[k] & (kKv4Tile - 1)) * T::kRow + (r.j * T::kG + r.gi) * 4) =
+          word;
   }
 }
 
 template <int D, bool kFp16>
 __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(Kv4RowParams p) {
   using T = Kv4Tile<D>;
-  const int j = threadIdx.x & 7;
-  const int64_t groups = (int64_t)p.n * p.h_k * 2 * T::kG;
-  const int64_t i = ((int64_t)blockIdx.x * kRowThreads + threadIdx.x) >> 3;
-  if (i >= groups) return;
-  const RowGroup r = row_group<D>(i, p.h_k);
-  const int slot = p.slots[r.t];
-  const bool good = slot >= 0 && (slot >> p.page_log2) < p.num_pages;
-  uint4 out = make_uint4(0u, 0u, 0u, 0u);
-  if (good) {
-    const uint8_t *tile = slot_tile<D>(p.pool, p.h_k, p.page_log2, r.h, slot);
-    const int row = slot & (kKv4Tile - 1);
-    const uint32_t word = *reinterpret_cast<const uint32_t *>(
-        tile + r.kv * T::kV + row * T::kRow + (j * T::kG + r.gi) * 4);
-    const __half *par = reinterpret_cast<const __half *>(tile + T::kPar + 2 * r.kv * T::kArr) +
-                        row * T::kG + r.gi;
-    const float scale = __half2float(par[0]), zero = __half2float(par[T::kArr / 2]);
+  const RowPlace r = row_place<D>(p);
+  int slot[kRows];
+  load_slots(p, r.t0, slot);
+  if (!r.live) return;
+  uint32_t word[kRows];
+  __half scale[kRows], zero[kRows];
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    word[k] = 0;
+    scale[k] = zero[k] = __ushort_as_half(0);
+    if (slot[k] >= 0) {
+      const uint8_t *tile = slot_tile<D>(p, r.h, slot[k]);
+      const int row = slot[k] & (kKv4Tile - 1);
+      word[k] = __ldg(reinterpret_cast<const uint32_t *>(tile + r.kv * T::kV + row * T::kRow +
+                                                         (r.j * T::kG + r.gi) * 4));
+      const __half *par = reinterpret_cast<const __half *>(tile + T::kPar + 2 * r.kv * T::kArr) +
+                          row * T::kG + r.gi;
+      scale[k] = __ldg(par);
+      zero[k] = __ldg(par + T::kArr / 2);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRows; ++k) {
+    if (r.t0 + k >= p.n) break;
+    const float s = __half2float(scale[k]), z = __half2float(zero[k]);
+    // codes n and n + 4 as the low bits of two fp16s above 1024; the difference is exact
     float x[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u)   // code * scale is exact: the only fp32 rounding is the sum's
-      x[u] = fmaf(static_cast<float>(word >> (4 * u) & 15u), scale, zero);
-    out = make_uint4(pack2<kFp16>(x[0], x[1]), pack2<kFp16>(x[2], x[3]), pack2<kFp16>(x[4], x[5]),
-                     pack2<kFp16>(x[6], x[7]));
-  } else if (slot != -1 && r.h == 0 && r.kv == 0 && r.gi == 0 && j == 0) {
-    raise(p.status, NSA_DEVERR_BAD_INDEX);
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t c2 = (word[k] >> (4 * u) & 0x000f000fu) | 0x64006400u;
+      const __half2 c = __hsub2(*reinterpret_cast<const __half2 *>(&c2), __float2half2_rn(1024.f));
+      x[u] = fmaf(__low2float(c), s, z);   // code * scale is exact: only the sum rounds
+      x[u + 4] = fmaf(__high2float(c), s, z);
+    }
+    uint16_t *dst = static_cast<uint16_t *>(r.kv ? p.v_out : p.k_out) +
+                    ((int64_t)(r.t0 + k) * p.h_k + r.h) * D + r.gi * 64 + r.j * 8;
+    __stcs(reinterpret_cast<uint4 *>(dst),
+           make_uint4(pack2<kFp16>(x[0], x[1]), pack2<kFp16>(x[2], x[3]), pack2<kFp16>(x[4], x[5]),
+                      pack2<kFp16>(x[6], x[7])));
   }
-  uint16_t *dst = static_cast<uint16_t *>(r.kv ? p.v_out : p.k_out) +
-                  ((int64_t)r.t * p.h_k + r.h) * D + r.gi * 64 + j * 8;
-  *reinterpret_cast<uint4 *>(dst) = out;
-}
-
-template <int D>
-static unsigned row_grid(const Kv4RowParams &p) {
-  const int64_t threads = (int64_t)p.n * p.h_k * 2 * Kv4Tile<D>::kG * 8;
-  return static_cast<unsigned>((threads + kRowThreads - 1) / kRowThreads);
 }
 
 template <int D>
 static cudaError_t run_rows(bool append, bool fp16, const Kv4RowParams &p, cudaStream_t s) {
   auto *kernel = append ? (fp16 ? kv4_append_kernel<D, true> : kv4_append_kernel<D, false>)
                         : (fp16 ? kv4_read_kernel<D, true> : kv4_read_kernel<D, false>);
-  kernel<<<row_grid<D>(p), kRowThreads, 0, s>>>(p);
+  const int64_t heads = 2 / Kv4Tile<D>::kG, warps = kRowThreads / 32;
+  const int64_t tasks = ((int64_t)p.n + kRows - 1) / kRows * ((p.h_k + heads - 1) / heads);
+  kernel<<<static_cast<unsigned>((tasks + warps - 1) / warps), kRowThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
