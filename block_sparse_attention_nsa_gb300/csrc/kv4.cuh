@@ -57,6 +57,32 @@ __device__ __forceinline__ void raise(int32_t *status, int32_t bits) {
   if (status) set_status(status, bits);
 }
 
+// Kernels of this group start while the one before them on the stream still runs (their
+// launch overlaps its end) and touch no memory before it has finished.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+inline cudaError_t launch_kv4(void (*kernel)(P...), dim3 grid, int threads, size_t smem, int cluster,
+                              cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s);
 cudaError_t launch_kv4_append(int d, bool fp16, const Kv4RowParams &p, cudaStream_t s);
 cudaError_t launch_kv4_read(int d, bool fp16, const Kv4RowParams &p, cudaStream_t s);

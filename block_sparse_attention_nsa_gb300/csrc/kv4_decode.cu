@@ -613,21 +613,22 @@ __device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int h
     p.lse[(int64_t)hq * p.num_seqs + b] = any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// One CTA per segment.
-template <int D, bool kFp16, bool kSel>
-__global__ void __launch_bounds__(kK4Threads, 2) kv4_seg_kernel(Kv4DecodeParams p) {
+// One CTA of kWarps per segment.
+template <int D, bool kFp16, bool kSel, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float4 ml[kK4Warps][kK4Heads / 2];        // m, l of two heads
-  __shared__ float lsum[kK4Warps][kK4Heads];
+  __shared__ float4 ml[kWarps][kK4Heads / 2];          // m, l of two heads
+  __shared__ float lsum[kWarps][kK4Heads];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   K4Seg sg = {};
   set_unit(p, blockIdx.x, sg);
   sg.b = blockIdx.y;
   int32_t err = 0;
+  after_previous();
   K4RawQuery<D> raw;
   fetch_query<D>(p, sg, lane, raw);
   open_segment<kSel>(p, sg, smem + warp * K4<D>::kRing, lane, err);
-  K4Stream<D, kSel> st(p, sg, warp, max(0, (sg.tiles - warp + kK4Warps - 1) / kK4Warps), kK4Warps,
+  K4Stream<D, kSel> st(p, sg, warp, max(0, (sg.tiles - warp + kWarps - 1) / kWarps), kWarps,
                        smem + warp * K4<D>::kRing, true, lane);
   st.start(err);
   K4Query<D> q;
@@ -646,7 +647,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_seg_kernel(Kv4DecodeParams 
   __syncthreads();
   float M0 = -INFINITY, M1 = -INFINITY;                // -inf without keys
 #pragma unroll
-  for (int w = 0; w < kK4Warps; ++w) {
+  for (int w = 0; w < kWarps; ++w) {
     const float4 v = ml[w][c];
     M0 = fmaxf(M0, v.x);
     M1 = fmaxf(M1, v.z);
@@ -656,12 +657,12 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_seg_kernel(Kv4DecodeParams 
   if (r == 0) *reinterpret_cast<float2 *>(&lsum[warp][2 * c]) = make_float2(a.l[0] * f0, a.l[1] * f1);
   leave_out<D>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), lane, a, f0, f1);
   __syncthreads();
-  for (int i = tid; i < sg.g * (D / 2); i += kK4Threads) {
+  for (int i = tid; i < sg.g * (D / 2); i += kWarps * 32) {
     const int head = i / (D / 2), dim = 2 * (i % (D / 2));
     const uint8_t *src = smem + ((head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim) * 4;
     float l = 0.f, x = 0.f, y = 0.f, M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kK4Warps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       const float2 o = *reinterpret_cast<const float2 *>(src + w * K4<D>::kRing);
       l += lsum[w][head];
       x += o.x;
@@ -669,7 +670,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_seg_kernel(Kv4DecodeParams 
     }
     if (dim == 0) {
 #pragma unroll
-      for (int w = 0; w < kK4Warps; ++w)
+      for (int w = 0; w < kWarps; ++w)
         M = fmaxf(M, head & 1 ? ml[w][head >> 1].z : ml[w][head >> 1].x);
     }
     write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, y, M, l);
@@ -721,7 +722,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   __shared__ float2 fac[2][kK4Warps][kK4Heads], top[kK4Warps + 1][kK4Heads / 2];
   __shared__ int pre[kK4Threads], wsum[kK4Warps], flags[kK4Warps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  after_previous();
   // ---- the batch's tiles ----
   const int per_thread = (p.num_seqs + kK4Threads - 1) / kK4Threads;
   const int b0 = min(tid * per_thread, p.num_seqs), b1 = min(b0 + per_thread, p.num_seqs);
@@ -949,7 +950,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParam
   __shared__ float acc[kWarps][D];
   __shared__ float2 wml[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
   const K4Split sp = splits_of(p)[blockIdx.x];
   if (sp.parts == 0) return;
   K4Seg sg = {};
@@ -1040,13 +1041,20 @@ static int sm_count(int dev) {
   return cache[dev];
 }
 
+template <typename K>
+static cudaError_t launch_big(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s,
+                              const Kv4DecodeParams &p) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  return e != cudaSuccess ? e : launch_kv4(kernel, grid, threads, smem, 1, s, p);
+}
+
 template <int D, bool kFp16, bool kSel>
 static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
-  constexpr int smem = K4<D>::kSmem;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int ctas = min(sm_count(dev) * 2, kK4MaxCtas);     // resident at once
+  const int sms = sm_count(dev), ctas = min(sms * 2, kK4MaxCtas);   // resident at once
   const int units = p.h_k * (p.g > kK4Heads ? 2 : 1);
   const int64_t segs = (int64_t)p.num_seqs * units;
   // tiles that a segment has at most, as far as the host knows
@@ -1054,31 +1062,23 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   if (p.window > 0) most = min(most, (int64_t)p.window / kKv4Tile + 2);
   if (kSel) most = min(most, (int64_t)p.topk << (p.page_log2 - 5));
   if (segs <= ctas && (kSel || most <= 8 * kK4Warps)) {
-    auto *kernel = kv4_seg_kernel<D, kFp16, kSel>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    kernel<<<dim3(units, p.num_seqs), kK4Threads, smem, s>>>(p);
-    return cudaGetLastError();
+    // sixteen warps where every segment has an SM to itself and the tiles for them
+    const dim3 grid(units, p.num_seqs);
+    if (segs <= sms && most > kK4Warps)
+      return launch_big(kv4_seg_kernel<D, kFp16, kSel, 16>, grid, 512, 16 * K4<D>::kRing, s, p);
+    return launch_big(kv4_seg_kernel<D, kFp16, kSel, 8>, grid, 256, 8 * K4<D>::kRing, s, p);
   }
   // With two or more segments of bounded length to a CTA, whole segments a CTA balance well
   // enough; else segments are split, and the merge follows.
   const int whole = kSel || (segs >= 2 * ctas && most <= 16 * kK4Warps);
   auto *kernel = kv4_run_kernel<D, kFp16, kSel>;
+  constexpr int smem = K4<D>::kSmem;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<ctas, kK4Threads, smem, s>>>(p, units, whole);
-  e = cudaGetLastError();
+  e = launch_kv4(kernel, dim3(ctas), kK4Threads, smem, 1, s, p, units, whole);
   if (e != cudaSuccess || whole) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, min(p.g, kK4Heads));
-  cfg.blockDim = dim3(kMergeThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<D, kFp16>, p, units);
+  return launch_kv4(kv4_merge_kernel<D, kFp16>, dim3(ctas, min(p.g, kK4Heads)), kMergeThreads, 0, 1,
+                    s, p, units);
 }
 
 template <int D, bool kFp16>

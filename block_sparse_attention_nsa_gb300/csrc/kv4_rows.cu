@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowParams p)
   using T = Kv4Tile<D>;
   const RowPlace r = row_place<D>(p);
   int slot[kRows];
+  after_previous();
   load_slots(p, r.t0, slot);
   const int64_t ts = r.kv ? p.v_ts : p.k_ts, hs = r.kv ? p.v_hs : p.k_hs;
   const uint16_t *src = static_cast<const uint16_t *>(r.kv ? p.v : p.k) + r.t0 * ts + r.h * hs +
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(Kv4RowParams p) {
   using T = Kv4Tile<D>;
   const RowPlace r = row_place<D>(p);
   int slot[kRows];
+  after_previous();
   load_slots(p, r.t0, slot);
   if (!r.live) return;
   uint32_t word[kRows];
@@ -248,8 +250,8 @@ static cudaError_t run_rows(bool append, bool fp16, const Kv4RowParams &p, cudaS
                         : (fp16 ? kv4_read_kernel<D, true> : kv4_read_kernel<D, false>);
   const int64_t heads = 2 / Kv4Tile<D>::kG, warps = kRowThreads / 32;
   const int64_t tasks = ((int64_t)p.n + kRows - 1) / kRows * ((p.h_k + heads - 1) / heads);
-  kernel<<<static_cast<unsigned>((tasks + warps - 1) / warps), kRowThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kv4(kernel, dim3(static_cast<unsigned>((tasks + warps - 1) / warps)), kRowThreads, 0,
+                    1, s, p);
 }
 
 cudaError_t launch_kv4_append(int d, bool fp16, const Kv4RowParams &p, cudaStream_t s) {

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_kernel(PageParams p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x, ncta = gridDim.x;
   const int64_t cap = (int64_t)p.width * p.page;   // tokens that a table row can hold
+  after_previous();
   int free0 = 0, avail = 0;
   int32_t err = 0;
   if (kPlan) {
@@ -149,19 +150,8 @@ cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   const bool one = p.max_slots <= kPlanOneCta;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(one ? 1 : kPlanCluster);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = one ? 1 : kPlanCluster;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  const int ctas = one ? 1 : kPlanCluster;
+  return launch_kv4(kernel, dim3(ctas), kPlanThreads, smem, ctas, s, p);
 }
 
 }  // namespace nsa

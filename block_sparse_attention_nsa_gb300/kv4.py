@@ -50,9 +50,15 @@ def signatures():
     }
 
 
+_handle = None
+
+
 def _lib():
-    from . import load
-    return load()
+    global _handle
+    if _handle is None:
+        from . import load
+        _handle = load()
+    return _handle
 
 
 def _fail(code: int, where: str):
@@ -70,11 +76,8 @@ def _kv4_dims(*sizes):
     return Kv4Dims(*sizes)
 
 
-def _dtype_code(dtype, where):
-    code = _DTYPES.get(dtype)
-    if code is None:
-        _fail(2, f"{where}: dtype {dtype}")
-    return code
+_current_device = torch.cuda.current_device
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _check(name, t, dtype, shape, dev):
@@ -88,13 +91,13 @@ def _check(name, t, dtype, shape, dev):
 def _device(t):
     """The index of t's device, which has to be the current one."""
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"tensors have to be on the current CUDA device, got {t.device}")
     return dev
 
 
 def _raw(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, dev, stream):
@@ -195,14 +198,16 @@ def kv4_pool(num_pages: int, page_size: int, h_k: int, head_dim: int, device="cu
 def _pool_dims(pool, head_dim, dtype, where):
     """Kv4Dims of a pool: its page size follows from the bytes of a page."""
     dev = _device(pool)
-    _check("pool", pool, torch.uint8, pool.shape, dev)
-    if pool.dim() != 3:
-        raise ValueError("pool: [num_pages, h_k, page_bytes] expected")
+    if pool.dtype is not torch.uint8 or pool.dim() != 3 or not pool.is_contiguous():
+        raise ValueError("pool: a contiguous uint8 tensor [num_pages, h_k, page_bytes] expected")
     pages, h_k, size = pool.shape
     page_size, rest = divmod(size, head_dim + head_dim // 8)
     if rest:
         raise ValueError(f"pool: {size} bytes a page are no whole tokens of head_dim {head_dim}")
-    return _kv4_dims(pages, page_size, h_k, head_dim, _dtype_code(dtype, where)), dev
+    code = _DTYPES.get(dtype)
+    if code is None:
+        _fail(2, f"{where}: dtype {dtype}")
+    return _kv4_dims(pages, page_size, h_k, head_dim, code), dev
 
 
 def kv4_append(pool, k, v, slot_map, device_status=None, stream=None):
@@ -279,22 +284,24 @@ def kv4_decode(q, pool, block_table, seq_lens, scale: float, sel_idx=None, windo
     if q.dim() != 3:
         raise ValueError("q [B, h_q, d] expected")
     b, h_q, d = q.shape
-    dims, dev = _pool_dims(pool, d, q.dtype, "kv4_decode")
-    h_k = pool.shape[1]
-    _check("q", q, q.dtype, (b, h_q, d), dev)
+    dtype, i32 = q.dtype, torch.int32
+    dims, dev = _pool_dims(pool, d, dtype, "kv4_decode")
+    h_k = dims.h_k
     width = block_table.shape[-1]
-    _check("block_table", block_table, torch.int32, (b, width), dev)
-    _check("seq_lens", seq_lens, torch.int32, (b,), dev)
+    if not q.is_contiguous() or q.get_device() != dev:
+        _check("q", q, dtype, q.shape, dev)
+    _check("block_table", block_table, i32, (b, width), dev)
+    _check("seq_lens", seq_lens, i32, (b,), dev)
     topk, sel = 0, None
     if sel_idx is not None:
         topk, sel = sel_idx.shape[-1], sel_idx.data_ptr()
-        _check("sel_idx", sel_idx, torch.int32, (h_k, b, topk), dev)
+        _check("sel_idx", sel_idx, i32, (h_k, b, topk), dev)
         if topk == 0:
             raise ValueError("sel_idx: at least one slot expected")
     if out is None:
-        out = _empty((b, h_q, d), q.dtype, dev, stream)
+        out = _empty((b, h_q, d), dtype, dev, stream)
     else:
-        _check("out", out, q.dtype, (b, h_q, d), dev)
+        _check("out", out, dtype, (b, h_q, d), dev)
     if lse is None:
         lse = _empty((h_q, b), torch.float32, dev, stream)
     else:
@@ -304,7 +311,7 @@ def kv4_decode(q, pool, block_table, seq_lens, scale: float, sel_idx=None, windo
         if need:
             workspace = _empty((need,), torch.uint8, dev, stream)
     else:
-        _check("workspace", workspace, torch.uint8, (workspace.numel(),), dev)
+        _check("workspace", workspace, torch.uint8, workspace.shape, dev)
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     code = _lib().nsa_kv4_decode(
         dims, b, h_q, width, topk, window, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(),
