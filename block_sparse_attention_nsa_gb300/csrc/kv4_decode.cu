@@ -57,7 +57,7 @@ struct K4 {
   using T = Kv4Tile<D>;
   static constexpr int kG = T::kG;
   static constexpr int kW = D / 32;             // words of codes that a lane holds of a K row
-  static constexpr int kHeadPair = 2 * D + 2;   // floats of two heads' outputs in an area
+  static constexpr int kHeadPair = 2 * D + 4;   // floats of two heads' outputs in an area
   static constexpr int kRing = kStages * T::kBytes;
   // A warp's results go to the ring's start; a first part that has to stay while the warp
   // goes on takes the last stage.
@@ -231,36 +231,46 @@ __device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale
   }
 }
 
+// A lane's offsets into a tile that take more than a shift to form: where its V chunks are
+// copied to and where its V words lie.  The empty asm keeps them in registers (formed again
+// for every tile they cost about 15 of its instructions).
+template <int D>
+struct K4Lane {
+  int vput, vget;
+  __device__ __forceinline__ explicit K4Lane(int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    // keys 2c and 2c + 1 go to rows c and c + 4 of their eight; at d = 128 rows with bit 1 set
+    // swap their halves
+    if constexpr (D == 128) {
+      const int row = (r >> 1) + 4 * (r & 1);             // of key lane / 4, chunk lane % 4
+      vput = row * 64 + ((c ^ (row & 2)) << 4);
+      vget = c * 64 + ((((r >> 1) ^ (c & 2)) << 4) | ((r & 1) << 3));
+    } else {
+      const int kk = lane >> 1;                           // key lane / 2, chunk lane % 2
+      vput = ((kk & 8) + ((kk & 7) >> 1) + 4 * (kk & 1)) * 32 + (lane & 1) * 16;
+      vget = c * 32 + r * 4;
+    }
+    asm("" : "+r"(vput), "+r"(vget));
+  }
+};
+
 // Copies a record tile into a stage of the ring (cp.async, not committed here).
 template <int D>
-__device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *tile, int lane) {
+__device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *tile, int lane, int vput) {
   using T = Kv4Tile<D>;
+  constexpr int kChunks = T::kV / 512;                    // per lane, of K and of V
   const uint8_t *src = tile + lane * 16;
-  if constexpr (D == 128) {
-    // chunk k * 32 + lane: rows of 4 chunks
-    const int kr = lane >> 2, q = lane & 3;
-    const int slot = (kr >> 1) + 4 * (kr & 1);          // place of keys 2c, 2c + 1: c, c + 4
-    const uint32_t vdst = stage + T::kV + slot * 64 + ((q ^ (slot & 2)) << 4);
+  const uint32_t kdst = stage + lane * 16, vdst = stage + T::kV + vput;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) cp_async16(stage + (k * 32 + lane) * 16, src + k * 512, 16u);
+  for (int k = 0; k < kChunks; ++k) cp_async16(kdst + k * 512, src + k * 512, 16u);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) cp_async16(vdst + k * 512, src + T::kV + k * 512, 16u);
-    cp_async16(stage + T::kPar + lane * 16, src + T::kPar, 16u);
-  } else {
-    const int kk = lane >> 1;                           // rows of 2 chunks
-    const int slot = (kk & 8) + ((kk & 7) >> 1) + 4 * (kk & 1);
-    const uint32_t vdst = stage + T::kV + slot * 32 + (lane & 1) * 16;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) cp_async16(stage + (k * 32 + lane) * 16, src + k * 512, 16u);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) cp_async16(vdst + k * 512, src + T::kV + k * 512, 16u);
-    if (lane < 16) cp_async16(stage + T::kPar + lane * 16, src + T::kPar, 16u);
-  }
+  for (int k = 0; k < kChunks; ++k) cp_async16(vdst + k * 512, src + T::kV + k * 512, 16u);
+  if (D == 128 || lane < 16) cp_async16(kdst + T::kPar, src + T::kPar, 16u);
 }
 
 // One tile: keys key0 ... key0 + 31, of which those in [lo, len) count.
 template <int D>
-__device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int len, int lane,
+__device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int len, int lane, int vget,
                                             const K4Query<D> &q, K4State<D> &a) {
   using T = Kv4Tile<D>;
   constexpr int G = K4<D>::kG, W = K4<D>::kW;
@@ -273,7 +283,7 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
     uint32_t w[2][W];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const uint8_t *at = st + (half * 16 + u * 8 + r) * T::kRow + c * (W * 4);
+      const uint8_t *at = st + (half * 16 + u * 8) * T::kRow + lane * (W * 4);
       if constexpr (W == 4) {
         const uint4 x = *reinterpret_cast<const uint4 *>(at);
         w[u][0] = x.x; w[u][1] = x.y; w[u][2] = x.z; w[u][3] = x.w;
@@ -404,13 +414,12 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
     uint32_t w[4][G];        // keys 2c, 2c + 1, 2c + 8, 2c + 9
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint8_t *row = st + T::kV + (half * 16 + c + 4 * i) * T::kRow;
+      const uint8_t *at = st + T::kV + (half * 16 + 4 * i) * T::kRow + vget;
       if constexpr (G == 2) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(
-            row + ((((r >> 1) ^ (c & 2)) << 4) | ((r & 1) << 3)));
+        const uint2 x = *reinterpret_cast<const uint2 *>(at);
         w[i][0] = x.x; w[i][1] = x.y;
       } else {
-        w[i][0] = reinterpret_cast<const uint32_t *>(row)[r];
+        w[i][0] = *reinterpret_cast<const uint32_t *>(at);
       }
     }
 #pragma unroll
@@ -490,6 +499,7 @@ struct K4Stream {
   const int t0, step, count, lane;
   uint8_t *const ring;
   const bool full;                    // all stages
+  const K4Lane<D> at;
   const uint8_t *my_tile;             // of tile 32 * block + lane: where it lies (null: nowhere)
   int my_key;                         // and its first key
   int put, get;                       // offsets of the stages to fill and to use next
@@ -498,7 +508,7 @@ struct K4Stream {
   __device__ __forceinline__ K4Stream(const Kv4DecodeParams &p_, const K4Seg &sg_, int t0_,
                                       int count_, int step_, uint8_t *ring_, bool full_, int lane_)
       : p(p_), sg(sg_), t0(t0_), step(step_), count(count_), lane(lane_), ring(ring_),
-        full(full_), my_tile(nullptr), my_key(0), put(0), get(0) {}
+        full(full_), at(lane_), my_tile(nullptr), my_key(0), put(0), get(0) {}
 
   __device__ __forceinline__ void next(int &stage) const {
     stage += T::kBytes;
@@ -533,7 +543,7 @@ struct K4Stream {
       const int k0 = __shfl_sync(0xffffffffu, my_key, n & 31);
       if (tile) {
         key = k0;
-        copy_tile<D>(smem_u32(ring) + put, tile, lane);
+        copy_tile<D>(smem_u32(ring) + put, tile, lane, at.vput);
       }
     }
     cp_async_commit();
@@ -555,7 +565,7 @@ struct K4Stream {
         cp_async_wait_group<1>();
       }
       __syncwarp();
-      if (keys[0] >= 0) attend_tile<D>(ring + get, keys[0], sg.lo, sg.len, lane, q, a);
+      if (keys[0] >= 0) attend_tile<D>(ring + get, keys[0], sg.lo, sg.len, lane, at.vget, q, a);
       __syncwarp();                   // the stage is filled again in the next turn
       next(get);
       keys[0] = keys[1];
@@ -601,14 +611,15 @@ __device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D
   }
 }
 
-// Final values of dimensions dim and dim + 1 of query head hq.
+// Final values of dimensions dim ... dim + 3 of query head hq.
 template <int D, bool kFp16>
-__device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int hq, int dim, float x,
-                                          float y, float M, float l) {
+__device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int hq, int dim, float4 x,
+                                          float M, float l) {
   const bool any = l != 0.f;                        // a NaN sum stays one
   const float inv = any ? __fdividef(1.f, l) : 0.f;
   const int64_t row = (int64_t)b * p.h_q + hq;
-  reinterpret_cast<uint32_t *>(p.out)[(row * D + dim) >> 1] = pack2<kFp16>(x * inv, y * inv);
+  reinterpret_cast<uint2 *>(p.out)[(row * D + dim) >> 2] =
+      make_uint2(pack2<kFp16>(x.x * inv, x.y * inv), pack2<kFp16>(x.z * inv, x.w * inv));
   if (dim == 0)
     p.lse[(int64_t)hq * p.num_seqs + b] = any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
@@ -657,23 +668,26 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4De
   if (r == 0) *reinterpret_cast<float2 *>(&lsum[warp][2 * c]) = make_float2(a.l[0] * f0, a.l[1] * f1);
   leave_out<D>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), lane, a, f0, f1);
   __syncthreads();
-  for (int i = tid; i < sg.g * (D / 2); i += kWarps * 32) {
-    const int head = i / (D / 2), dim = 2 * (i % (D / 2));
+  for (int i = tid; i < sg.g * (D / 4); i += kWarps * 32) {
+    const int head = i / (D / 4), dim = 4 * (i % (D / 4));
     const uint8_t *src = smem + ((head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim) * 4;
-    float l = 0.f, x = 0.f, y = 0.f, M = -INFINITY;
+    float l = 0.f, M = -INFINITY;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 o = *reinterpret_cast<const float2 *>(src + w * K4<D>::kRing);
+      const float4 o = *reinterpret_cast<const float4 *>(src + w * K4<D>::kRing);
       l += lsum[w][head];
-      x += o.x;
-      y += o.y;
+      x.x += o.x;
+      x.y += o.y;
+      x.z += o.z;
+      x.w += o.w;
     }
     if (dim == 0) {
 #pragma unroll
       for (int w = 0; w < kWarps; ++w)
         M = fmaxf(M, head & 1 ? ml[w][head >> 1].z : ml[w][head >> 1].x);
     }
-    write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, y, M, l);
+    write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, M, l);
   }
 }
 
@@ -830,13 +844,12 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
       leave_out<D>(area, lane, a, 1.f, 1.f);
       __syncwarp();
 #pragma unroll 1
-      for (int i = lane; i < sg.g * (D / 2); i += 32) {
-        const int head = i / (D / 2), dim = 2 * (i % (D / 2));
-        const float2 o = *reinterpret_cast<const float2 *>(
+      for (int i = lane; i < sg.g * (D / 4); i += 32) {
+        const int head = i / (D / 4), dim = 4 * (i % (D / 4));
+        const float4 o = *reinterpret_cast<const float4 *>(
             area + (head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim);
         const float4 v = ml[1][warp][head >> 1];
-        write_out<D, kFp16>(p, b, sg.q0 + head, dim, o.x, o.y, head & 1 ? v.z : v.x,
-                            head & 1 ? v.w : v.y);
+        write_out<D, kFp16>(p, b, sg.q0 + head, dim, o, head & 1 ? v.z : v.x, head & 1 ? v.w : v.y);
       }
       __syncwarp();                        // read before the ring is filled again
     }
@@ -913,28 +926,33 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
           sg.b * units + last_u, (last_end - 1) / per - static_cast<int>(blockIdx.x) + 1};
     const int th = __popc(all & ((1u << warp) - 1u)) * 32 + lane, nth = __popc(all) * 32;
 #pragma unroll 1
-    for (int i = th; i < sg.g * (D / 2); i += nth) {
-      const int head = i / (D / 2), dim = 2 * (i % (D / 2));
+    for (int i = th; i < sg.g * (D / 4); i += nth) {
+      const int head = i / (D / 4), dim = 4 * (i % (D / 4));
       const int off = ((head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim) * 4;
-      float l = 0.f, x = 0.f, y = 0.f;
+      float l = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kK4Warps; ++w) {
         if (!(all >> w & 1)) continue;
         const bool fst = w != open;
-        const float2 o = *reinterpret_cast<const float2 *>(
+        const float4 o = *reinterpret_cast<const float4 *>(
             smem + w * K4<D>::kRing + (fst && (keeps >> w & 1) ? K4<D>::kKept : 0) + off);
         const float2 f = fac[!fst][w][head];
         l += f.y;
-        x = fmaf(f.x, o.x, x);
-        y = fmaf(f.x, o.y, y);
+        x.x = fmaf(f.x, o.x, x.x);
+        x.y = fmaf(f.x, o.y, x.y);
+        x.z = fmaf(f.x, o.z, x.z);
+        x.w = fmaf(f.x, o.w, x.w);
       }
       const float2 m2 = top[open + 1][head >> 1];
       const float M = head & 1 ? m2.y : m2.x;
       if (part) {
-        *reinterpret_cast<float2 *>(part + head * D + dim) = make_float2(x, y);
+        float2 *dst = reinterpret_cast<float2 *>(part + head * D + dim);
+        dst[0] = make_float2(x.x, x.y);
+        dst[1] = make_float2(x.z, x.w);
         if (dim == 0) *reinterpret_cast<float2 *>(part + sg.g * D + 2 * head) = make_float2(M, l);
       } else {
-        write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, y, M, l);
+        write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, M, l);
       }
     }
   }
@@ -947,7 +965,7 @@ constexpr int kMergeThreads = 256;
 template <int D, bool kFp16>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParams p, int units) {
   constexpr int kWarps = kMergeThreads / 32, E = D / 32;
-  __shared__ float acc[kWarps][D];
+  __shared__ __align__(16) float acc[kWarps][D];
   __shared__ float2 wml[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, head = blockIdx.y;
   after_previous();
@@ -1001,21 +1019,24 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParam
   for (int e = 0; e < E; ++e) acc[warp][lane * E + e] = x[e];
   if (lane == 0) wml[warp] = make_float2(M, l);
   __syncthreads();
-  if (tid < D / 2) {
+  if (tid < D / 4) {
     M = -INFINITY;
     l = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wml[w].x);
-    float u = 0.f, v = 0.f;
+    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float2 t = wml[w];
       const float f = t.y != 0.f ? ex2_approx(t.x - M) : 0.f;
+      const float4 o = *reinterpret_cast<const float4 *>(&acc[w][4 * tid]);
       l = fmaf(f, t.y, l);
-      u = fmaf(f, acc[w][2 * tid], u);
-      v = fmaf(f, acc[w][2 * tid + 1], v);
+      u.x = fmaf(f, o.x, u.x);
+      u.y = fmaf(f, o.y, u.y);
+      u.z = fmaf(f, o.z, u.z);
+      u.w = fmaf(f, o.w, u.w);
     }
-    write_out<D, kFp16>(p, sg.b, sg.q0 + head, 2 * tid, u, v, M, l);
+    write_out<D, kFp16>(p, sg.b, sg.q0 + head, 4 * tid, u, M, l);
   }
 }
 
