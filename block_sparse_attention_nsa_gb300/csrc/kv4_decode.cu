@@ -753,16 +753,14 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   for (int w = 0; w < kK4Warps; ++w) total += wsum[w];
   // the sequence that holds tile v (< total), and that sequence's first tile
   auto locate = [&](int v, int &b, int &base) {
-    int chunk = 0, off = 0;                // threads whose sequences lie before v
-    base = 0;
+    int w = 0, off = 0;                    // the warp whose sequences hold it, the tiles before
 #pragma unroll
-    for (int w = 0; w < kK4Warps; ++w) {
-      const int x = off + pre[w * 32 + lane];
-      const uint32_t m = __ballot_sync(0xffffffffu, x <= v);
-      chunk += __popc(m);
-      if (m) base = __shfl_sync(0xffffffffu, x, 31 - __clz(m));
-      off += wsum[w];
-    }
+    for (int k = 0; k + 1 < kK4Warps; ++k)
+      if (v >= off + wsum[w]) off += wsum[w++];
+    const int x = off + pre[w * 32 + lane];
+    const uint32_t before = __ballot_sync(0xffffffffu, x <= v);
+    const int chunk = w * 32 + __popc(before);   // threads whose sequences lie before it
+    base = before ? __shfl_sync(0xffffffffu, x, __popc(before) - 1) : off;
     b = chunk * per_thread;
     if (per_thread == 1) return;
     while (b < p.num_seqs) {               // 32 sequences at a time
@@ -784,14 +782,16 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   int to = from + min(per, total - from);
   int b = 0, base = 0;
   if (whole) {                             // from and to move to the next segments' starts
-#pragma unroll 1
+    int vb[2] = {from, to}, sb[2], sbase[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) locate(min(vb[k], total - 1), sb[k], sbase[k]);
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
-      int &v = k ? to : from;
-      if (v >= total) continue;
-      locate(v, b, base);
-      const int nt = counted_tiles<kSel>(p, seq_len(p, b, ignore));
-      v = base + (v - base + nt - 1) / nt * nt;
+      const int nt = counted_tiles<kSel>(p, seq_len(p, sb[k], ignore));
+      vb[k] = min(sbase[k] + (vb[k] - sbase[k] + nt - 1) / nt * nt, total);
     }
+    from = vb[0];
+    to = vb[1];
     per_warp = (to - from + kK4Warps - 1) / kK4Warps;
   }
   int at = from + min(warp * per_warp, to - from);
