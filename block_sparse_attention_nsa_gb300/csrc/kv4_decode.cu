@@ -735,6 +735,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   __shared__ float4 ml[2][kK4Warps][kK4Heads / 2];
   __shared__ float2 fac[2][kK4Warps][kK4Heads], top[kK4Warps + 1][kK4Heads / 2];
   __shared__ int pre[kK4Threads], wsum[kK4Warps], flags[kK4Warps];
+  __shared__ int4 groups[kK4Warps + 1];    // of the group that warp i - 1 opens: sequence, unit, end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
   after_previous();
   // ---- the batch's tiles ----
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   // whether that goes on behind it, whether it is kept in the ring's last stage), and a last
   // part, of a segment that begins in the run and goes on.
   constexpr int kFirst = 1, kLast = 2, kOn = 4, kKeep = 8;
-  int left = 0, first_b = 0, first_u = 0, last_b = 0, last_u = 0, last_end = 0;
+  int left = 0;
   int unit = -1, nt = 0;
   K4State<D> a;
   while (at < stop) {
@@ -831,14 +832,11 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     if (lane < 4) ml[first ? 0 : 1][warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
     if (first) {
       left |= kFirst | (goes_on ? kOn : 0) | (at < stop ? kKeep : 0);
-      first_b = b;
-      first_u = unit;
+      if (warp == 0 && lane == 0) groups[0] = make_int4(b, unit, 0, 0);
       if (at < stop) leave_out<D>(reinterpret_cast<float *>(ring + K4<D>::kKept), lane, a, 1.f, 1.f);
     } else if (goes_on) {                  // the run's last: stays in registers
       left |= kLast;
-      last_b = b;
-      last_u = unit;
-      last_end = seg0 + nt;
+      if (lane == 0) groups[warp + 1] = make_int4(b, unit, seg0 + nt, 0);
     } else {
       float *area = reinterpret_cast<float *>(ring);
       leave_out<D>(area, lane, a, 1.f, 1.f);
@@ -909,31 +907,34 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     }
   }
   __syncthreads();
+  // Group i is the one that warp i - 1 opens.  A small one is a single warp's work.
+  const bool small = min(p.g, kK4Heads) * (D / 4) <= 64;
+  const int th = small ? lane : tid, nth = small ? 32 : kK4Threads;
 #pragma unroll 1
-  for (int side = 0; side < 2; ++side) {
-    if (!(left & (side ? kLast : kFirst))) continue;
-    const int open = opener(side);
+  for (uint32_t todo = lasts << 1 | (members(-1) ? 1u : 0u); todo; todo &= todo - 1) {
+    const int gr = __ffs(todo) - 1, open = gr - 1;
+    if (small && (gr & (kK4Warps - 1)) != warp) continue;
     const uint32_t in = members(open), all = in | (open >= 0 ? 1u << open : 0u);
     const bool on = in ? ons >> (31 - __clz(in)) & 1 : true;
+    const int4 who = groups[gr];
     K4Seg sg = {};
-    sg.b = side ? last_b : first_b;
-    set_unit(p, side ? last_u : first_u, sg);
+    sg.b = who.x;
+    set_unit(p, who.y, sg);
     float *part = nullptr;
     if (open < 0) part = part_of<D>(p, 2 * blockIdx.x);
     else if (on) part = part_of<D>(p, 2 * blockIdx.x + 1);
-    if (side && on && lane == 0)
+    if (open >= 0 && on && th == 0)
       splits_of(p)[blockIdx.x] = K4Split{
-          sg.b * units + last_u, (last_end - 1) / per - static_cast<int>(blockIdx.x) + 1};
-    const int th = __popc(all & ((1u << warp) - 1u)) * 32 + lane, nth = __popc(all) * 32;
+          sg.b * units + who.y, (who.z - 1) / per - static_cast<int>(blockIdx.x) + 1};
 #pragma unroll 1
     for (int i = th; i < sg.g * (D / 4); i += nth) {
       const int head = i / (D / 4), dim = 4 * (i % (D / 4));
       const int off = ((head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim) * 4;
       float l = 0.f;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kK4Warps; ++w) {
-        if (!(all >> w & 1)) continue;
+#pragma unroll 2
+      for (uint32_t m = all; m; m &= m - 1) {
+        const int w = __ffs(m) - 1;
         const bool fst = w != open;
         const float4 o = *reinterpret_cast<const float4 *>(
             smem + w * K4<D>::kRing + (fst && (keeps >> w & 1) ? K4<D>::kKept : 0) + off);
@@ -944,7 +945,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
         x.z = fmaf(f.x, o.z, x.z);
         x.w = fmaf(f.x, o.w, x.w);
       }
-      const float2 m2 = top[open + 1][head >> 1];
+      const float2 m2 = top[gr][head >> 1];
       const float M = head & 1 ? m2.y : m2.x;
       if (part) {
         float2 *dst = reinterpret_cast<float2 *>(part + head * D + dim);
@@ -1040,6 +1041,9 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParam
   }
 }
 
+// Query heads of one segment are at most kK4Heads: segments of a KV head.
+static int head_parts(int g) { return g > kK4Heads ? 2 : 1; }
+
 size_t kv4_decode_workspace(int d, int g, bool selected) {
   if (selected) return 0;
   return kK4MaxCtas * sizeof(K4Split) + 2 * (size_t)kK4MaxCtas * part_floats(d, g) * sizeof(float);
@@ -1047,7 +1051,7 @@ size_t kv4_decode_workspace(int d, int g, bool selected) {
 
 // Tiles of the whole batch, counted as the run kernel does, at most (its counters have 32 bits).
 int64_t kv4_decode_tiles(const Kv4DecodeParams &p) {
-  const int units = p.h_k * (p.g > kK4Heads ? 2 : 1);
+  const int units = p.h_k * head_parts(p.g);
   return (((int64_t)p.width << p.page_log2) / kKv4Tile + 1 + kOver) * p.num_seqs * units;
 }
 
@@ -1076,7 +1080,7 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const int sms = sm_count(dev), ctas = min(sms * 2, kK4MaxCtas);   // resident at once
-  const int units = p.h_k * (p.g > kK4Heads ? 2 : 1);
+  const int units = p.h_k * head_parts(p.g);
   const int64_t segs = (int64_t)p.num_seqs * units;
   // tiles that a segment has at most, as far as the host knows
   int64_t most = ((int64_t)p.width << p.page_log2) / kKv4Tile;
@@ -1089,9 +1093,11 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
       return launch_big(kv4_seg_kernel<D, kFp16, kSel, 16>, grid, 512, 16 * K4<D>::kRing, s, p);
     return launch_big(kv4_seg_kernel<D, kFp16, kSel, 8>, grid, 256, 8 * K4<D>::kRing, s, p);
   }
-  // With two or more segments of bounded length to a CTA, whole segments a CTA balance well
-  // enough; else segments are split, and the merge follows.
-  const int whole = kSel || (segs >= 2 * ctas && most <= 16 * kK4Warps);
+  // Whole segments to a CTA leave its share up to a segment off: little from six segments of
+  // bounded length a CTA on.  Selected segments have at most 128 tiles and stay whole below
+  // that too (200 ragged sequences, 16 blocks, g = 16, 2.6 segments a CTA: 24.4 us, against
+  // 26.5 us split and merged).  Else segments are split, and the merge follows.
+  const int whole = kSel || (segs >= 6 * ctas && most <= 16 * kK4Warps);
   auto *kernel = kv4_run_kernel<D, kFp16, kSel>;
   constexpr int smem = K4<D>::kSmem;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
