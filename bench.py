@@ -38,14 +38,18 @@ TRAFFIC = {"sources_sha256": "a3fded1d5a79fbe509a33ae2e9196e6d9f2b75e216b583d0ec
                      "bwd_main": {"4": 2803539200 + 4798355456}}}
 
 
+# The sources that the captured kernels are built from (the paged cache's are not among them).
+CAPTURED_SOURCES = ("api.cu", "bwd.cu", "common.cuh", "compress.cu", "compress.cuh", "decode.cu",
+                    "fwd.cu", "index_build.cu", "noalloc.cu", "window.cu")
+
+
 def kernel_sources_hash() -> str:
-    import glob
     import hashlib
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "block_sparse_attention_nsa_gb300", "csrc")
-    for f in sorted(glob.glob(os.path.join(csrc, "*.cu")) + glob.glob(os.path.join(csrc, "*.cuh"))):
-        with open(f, "rb") as fh:
-            h.update(os.path.basename(f).encode() + b"\0" + fh.read())
+    for name in sorted(CAPTURED_SOURCES):
+        with open(os.path.join(csrc, name), "rb") as fh:
+            h.update(name.encode() + b"\0" + fh.read())
     return h.hexdigest()
 
 
@@ -550,9 +554,43 @@ def decode_sweep(torch, dev):
             "us": ms * 1e3, "algorithmic_bytes": kv_bytes + io_bytes, "GB/s": gbs,
             "frac_of_measured_hbm": gbs / peaks()[2],
             "useful_tflops": 4.0 * d * g * kept * blk / (ms * 1e-3) / 1e12}
+        outd[f"kv4_decode_b{B}_{L // 1024}k_g{g}"] = kv4_leg(torch, nsa, q, k, v, sel, inp["scale"],
+                                                            blk, kept, io_bytes, out, lse)
         del q, k, v, out
         torch.cuda.empty_cache()
     return outd
+
+
+def kv4_leg(torch, nsa, q, k, v, sel, scale, blk, kept, io_bytes, out, lse):
+    """The same decode over 4-bit pages that hold the same caches (a stored token takes
+    d + d / 8 bytes of a head instead of 4 d), and the caches' append and read."""
+    n, h_k, d = k.shape
+    b = q.shape[0]
+    i32 = dict(dtype=torch.int32, device=k.device)
+    pages = n // blk
+    pool = nsa.kv4_pool(pages, blk, h_k, d, device=k.device)
+    table = torch.full((b, pages // b), -1, **i32)
+    lens, new = torch.zeros(b, **i32), torch.full((b,), n // b, **i32)
+    free = torch.randperm(pages, device=k.device).int()
+    slots, lens, _, _ = nsa.page_plan(lens, new, free, torch.zeros(1, **i32), table, blk, pages, n)
+    kr, vr = torch.empty_like(k), torch.empty_like(v)
+    calls = {"append": lambda: nsa.kv4_append(pool, k, v, slots),
+             "read": lambda: nsa.kv4_read(pool, slots, d, kr, vr),
+             "decode": lambda: nsa.kv4_decode(q, pool, table, lens, scale, sel_idx=sel, out=out,
+                                              lse=lse)}
+    stored = d + d // 8
+    nbytes = {"append": n * h_k * (4 * d + stored), "read": n * h_k * (4 * d + stored),
+              "decode": kept * blk * stored + io_bytes}
+    res = {}
+    for name, call in calls.items():
+        for _ in range(3):
+            call()
+        torch.cuda.synchronize()
+        us = dist(time_reps(torch, call, 50))["median"] * 1e3
+        gbs = nbytes[name] / us / 1e3
+        res[name] = {"us": us, "algorithmic_bytes": nbytes[name], "GB/s": gbs,
+                     "frac_of_measured_hbm": gbs / peaks()[2]}
+    return res
 
 
 def run_reference(args, rank, world):

@@ -128,7 +128,8 @@ NSA_API nsa_status nsa_kv4_read(const nsa_kv4_dims *dims, int32_t n, const void 
  *                or table_width * P and sets NSA_DEVERR_BAD_SEQLENS; the keys of a page id
  *                outside the pool are left out and set NSA_DEVERR_BAD_INDEX.
  *   workspace    at least nsa_kv4_decode_workspace_size bytes, 16-byte aligned (NULL when
- *                that is 0); its contents carry nothing from one call to the next.
+ *                that is 0); its contents carry nothing from one call to the next.  Calls that
+ *                may overlap on the GPU need workspaces of their own.
  * num_seqs * h_k * (table_width * page_size / 32 + 5), twice that for h_q / h_k > 8, has to
  * stay below 2^31 (NSA_ERR_UNSUPPORTED).
  * Rows of the pool behind a sequence's end, and tokens before its window, may hold

@@ -322,6 +322,103 @@ def test_decode_is_repeatable():
         assert torch.equal(o, out) and torch.equal(l, lse)
 
 
+def test_decode_nan_value_stays_in_its_group_and_sequence():
+    """A stored NaN in V reaches its 64 dimensions of the sequence that attends to it; one
+    behind a window reaches nothing."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    lens, page, h_k, g, d = (500, 200), 64, 1, 3, 128
+    pool, table, _ = make_cache(lens, page, h_k, d, 34)
+    q = torch.randn(2, g, d, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16)
+    ref = kv4.attend(q.double().numpy(), pool, table, lens, page, 0.1)
+    slot = table[0, 2] * page + 5                       # position 133 of sequence 0
+    code, scale, zero = kv4.get_row(pool, page, d, slot, 0, 1)
+    zero[1] = np.float16("nan")
+    kv4.put_row(pool, page, d, slot, 0, 1, code * 0, scale, zero)
+    args = (q.cuda(), _dev(pool), _dev(table), _dev(np.int32(lens)), 0.1)
+    out, lse = nsa.kv4_decode(*args)
+    assert out[0, :, 64:].isnan().all() and lse.isfinite().all()
+    ref[0][0, :, :64] = kv4.attend(q.double().numpy(), pool, table, lens, page, 0.1)[0][0, :, :64]
+    out[0, :, 64:] = torch.from_numpy(ref[0][0, :, 64:]).to(out)
+    check_decode(out, lse, ref, torch.bfloat16)
+    ref = kv4.attend(q.double().numpy(), pool, table, lens, page, 0.1, window=366)   # from 134 on
+    out, lse = nsa.kv4_decode(*args, window=366)
+    check_decode(out, lse, ref, torch.bfloat16)
+
+
+def test_pool_beyond_32_bit_offsets():
+    """Pages whose bytes lie past 2^32: the same rows in a small pool read and attend alike."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d, n = 128, 8, 2, 128, 700
+    far, near = nsa.kv4_pool(33000, page, h_k, d), nsa.kv4_pool(8, page, h_k, d)
+    assert far.numel() > (1 << 32)
+    gen = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(n, h_k, d, generator=gen).half().cuda() for _ in range(2))
+    q = torch.randn(1, h_k * g, d, generator=gen).half().cuda()
+    lens, zero = _dev(np.int32([n])), _dev(np.int32([0]))
+    got = []
+    for pool, first in ((far, 32990), (near, 1)):
+        table = torch.arange(first, first + 6, dtype=torch.int32, device="cuda").view(1, 6)
+        slots, _ = nsa.page_slots(table, zero, lens, page, pool.shape[0], n)
+        nsa.kv4_append(pool, k, v, slots)
+        kr, vr = nsa.kv4_read(pool, slots, d, dtype=torch.float16)
+        got.append((kr, vr) + tuple(nsa.kv4_decode(q, pool, table, lens, 0.1)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    # 4 bits keep a normal row to within half a step of about a third
+    assert (got[0][0].float() - k.float()).abs().max() < 0.5
+
+
+def test_steps_in_a_graph_between_streams():
+    """Append and decode captured on a forked stream, behind a torch kernel and before one: each
+    replay sees what the last one left."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d, b = 32, 2, 2, 64, 3
+    pool = nsa.kv4_pool(12, page, h_k, d)
+    table = torch.arange(12, dtype=torch.int32, device="cuda").view(b, 4)
+    lens = torch.zeros(b, dtype=torch.int32, device="cuda")
+    step = torch.ones(b, dtype=torch.int32, device="cuda")
+    k, v = (torch.zeros(b, h_k, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros(b, h_k * g, d, dtype=torch.bfloat16, device="cuda")
+    src = torch.zeros(3, b, h_k, d, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(nsa.kv4_decode_workspace_size(12, page, h_k, d, b, h_k * g),
+                     dtype=torch.uint8, device="cuda")
+    out, total = torch.empty_like(q), torch.zeros_like(q, dtype=torch.float32)
+    lse = torch.empty(h_k * g, b, device="cuda")
+    slots = torch.empty(b, dtype=torch.int32, device="cuda")
+    cu = torch.empty(b + 1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+
+    def body():
+        main = torch.cuda.current_stream()
+        k.copy_(src[0])
+        v.copy_(src[1])
+        q.copy_(src[2].repeat_interleave(g, 1))
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            nsa.page_slots(table, lens, step, page, 12, slots, cu)
+            nsa.kv4_append(pool, k, v, slots)
+            lens.add_(step)
+            nsa.kv4_decode(q, pool, table, lens, 0.3, out=out, lse=lse, workspace=ws)
+        main.wait_stream(side)
+        total.add_(out.float())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        body()
+    gen = torch.Generator().manual_seed(4)
+    want = torch.zeros(b, h_k * g, d, dtype=torch.float64)
+    for n in range(1, 41):
+        x = torch.randn(3, b, h_k, d, generator=gen).to(torch.bfloat16)
+        src.copy_(x)
+        graph.replay()
+        qn = x[2].repeat_interleave(g, 1)
+        ref = kv4.attend(qn.double().numpy(), pool.cpu().numpy(), table.cpu().numpy(), [n] * b,
+                         page, 0.3)
+        check_decode(out, lse, ref, torch.bfloat16)
+        want += out.double().cpu()
+    assert lens.tolist() == [40] * b
+    torch.testing.assert_close(total.double().cpu(), want, rtol=0, atol=40 * 40 * 2.0 ** -24)
+
+
 # ---- a serving loop -------------------------------------------------------------------
 @pytest.mark.parametrize("page,d", [(64, 128), (32, 64)])
 def test_serving_steps(page, d):
