@@ -105,11 +105,25 @@ __device__ __forceinline__ void par_floats(uint32_t u, float (&x)[G]) {
   if constexpr (G == 2) x[1] = f.y;
 }
 
+// K codes 0, 1, 4, 5 (k = 0) or 2, 3, 6, 7 of a word, in the places that the masks take.  The
+// tensor core truncates its sums relative to the largest exponent, and a subnormal's leading
+// zeros count against it: fp16's 11-bit queries, which feel that (a lone key's score was
+// 1.5e-6 off, bf16's 5.5e-7), get their codes two bits further up, for one more shift a word.
+template <bool kFp16>
+struct K4Up {
+  static constexpr int kBits = kFp16 ? 2 : 0;
+};
+template <bool kFp16>
+__device__ __forceinline__ uint32_t code_pairs(uint32_t w, int k) {
+  if (kFp16) return k ? w >> 6 : w << 2;
+  return k ? w >> 8 : w;
+}
+
 // The query of a segment as B operands, and its sums and scale per head of the score tile.
 template <int D>
 struct K4Query {
   uint32_t f[K4<D>::kW][4];      // [word of the row][dims (0,4), (1,5)/16, (2,6), (3,7)/16]
-  float sum[2][K4<D>::kG];       // 2^-24 times the sums of q^, heads 2c, 2c + 1 of the lane
+  float sum[2][K4<D>::kG];       // sums of q^ in the raw scores' unit, heads 2c, 2c + 1 of the lane
   float mul[2];                  // raw score -> S, > 0
 };
 template <int D>
@@ -220,14 +234,15 @@ __device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale
     mma16816(sum[i % G], 0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u, out.f[i][2],
              out.f[i][3]);
   }
-  // a raw score counts in 2^-24: S = 2^(ex - 14 + 24) |scale| raw.  A scale of 0 keeps the
-  // masked scores below the others.
-  const float mul = fmaxf(ldexpf(fabsf(scale_log2), ex + 10), 1e-30f);
+  // a raw score counts in 2^-24 (2^-22): S = 2^(ex - 14 + 24) |scale| raw.  A scale of 0 keeps
+  // the masked scores below the others.
+  constexpr int kUp = K4Up<kFp16>::kBits;
+  const float mul = fmaxf(ldexpf(fabsf(scale_log2), ex + 10 - kUp), 1e-30f);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     out.mul[u] = __shfl_sync(0xffffffffu, mul, (2 * c + u) * 4);
 #pragma unroll
-    for (int gi = 0; gi < G; ++gi) out.sum[u][gi] = sum[gi][u] * 5.9604644775390625e-8f;
+    for (int gi = 0; gi < G; ++gi) out.sum[u][gi] = sum[gi][u] * (5.9604644775390625e-8f * (1 << kUp));
   }
 }
 
@@ -269,7 +284,7 @@ __device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *tile, i
 }
 
 // One tile: keys key0 ... key0 + 31, of which those in [lo, len) count.
-template <int D>
+template <int D, bool kFp16>
 __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int len, int lane, int vget,
                                             const K4Query<D> &q, K4State<D> &a) {
   using T = Kv4Tile<D>;
@@ -297,13 +312,14 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
     for (int i = 0; i < W; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const uint32_t x = w[0][i] >> (8 * k), y = w[1][i] >> (8 * k);
+        constexpr uint32_t kLow = 0x000f000fu << K4Up<kFp16>::kBits, kHigh = kLow << 4;
+        const uint32_t x = code_pairs<kFp16>(w[0][i], k), y = code_pairs<kFp16>(w[1][i], k);
         if (i < G && k == 0)
-          mma16816_0(acc[i % G], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u,
-                     y & 0x00f000f0u, q.f[i][2 * k], q.f[i][2 * k + 1]);
+          mma16816_0(acc[i % G], x & kLow, y & kLow, x & kHigh, y & kHigh, q.f[i][2 * k],
+                     q.f[i][2 * k + 1]);
         else
-          mma16816(acc[i % G], x & 0x000f000fu, y & 0x000f000fu, x & 0x00f000f0u, y & 0x00f000f0u,
-                   q.f[i][2 * k], q.f[i][2 * k + 1]);
+          mma16816(acc[i % G], x & kLow, y & kLow, x & kHigh, y & kHigh, q.f[i][2 * k],
+                   q.f[i][2 * k + 1]);
       }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -491,7 +507,7 @@ __device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg
 
 // Tiles t0, t0 + step, ... (count of them) of a segment through this warp's ring: all its
 // stages, or those before a kept part.
-template <int D, bool kSel>
+template <int D, bool kFp16, bool kSel>
 struct K4Stream {
   using T = Kv4Tile<D>;
   const Kv4DecodeParams &p;
@@ -565,7 +581,7 @@ struct K4Stream {
         cp_async_wait_group<1>();
       }
       __syncwarp();
-      if (keys[0] >= 0) attend_tile<D>(ring + get, keys[0], sg.lo, sg.len, lane, at.vget, q, a);
+      if (keys[0] >= 0) attend_tile<D, kFp16>(ring + get, keys[0], sg.lo, sg.len, lane, at.vget, q, a);
       __syncwarp();                   // the stage is filled again in the next turn
       next(get);
       keys[0] = keys[1];
@@ -639,7 +655,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4De
   K4RawQuery<D> raw;
   fetch_query<D>(p, sg, lane, raw);
   open_segment<kSel>(p, sg, smem + warp * K4<D>::kRing, lane, err);
-  K4Stream<D, kSel> st(p, sg, warp, max(0, (sg.tiles - warp + kWarps - 1) / kWarps), kWarps,
+  K4Stream<D, kFp16, kSel> st(p, sg, warp, max(0, (sg.tiles - warp + kWarps - 1) / kWarps), kWarps,
                        smem + warp * K4<D>::kRing, true, lane);
   st.start(err);
   K4Query<D> q;
@@ -820,7 +836,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
       fetch_query<D>(p, sg, lane, raw);
       open_segment<kSel>(p, sg, ring, lane, err);
       const int t0 = max(0, v0 - kOver), t1 = min(v1 - kOver, sg.tiles);
-      K4Stream<D, kSel> st(p, sg, t0, max(0, t1 - t0), 1, ring, !(left & kKeep), lane);
+      K4Stream<D, kFp16, kSel> st(p, sg, t0, max(0, t1 - t0), 1, ring, !(left & kKeep), lane);
       st.start(err);
       K4Query<D> q;
       make_query<D, kFp16>(raw, p.scale_log2, lane, q);
