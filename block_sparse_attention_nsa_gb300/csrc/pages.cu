@@ -98,26 +98,41 @@ __global__ void __launch_bounds__(kPlanThreads) page_kernel(PageParams p) {
   bool bad = false;
   for (int64_t t0 = ((int64_t)rank * kPlanThreads + tid) * 4; t0 < p.max_slots;
        t0 += (int64_t)ncta * kPlanThreads * 4) {
+    // the four tokens' pages are looked up together
+    const int32_t *from[4];
+    int32_t *open[4];
+    uint32_t rest[4];
     int32_t out[4];
     int b = t0 < total ? upper_index(cu, p.num_seqs, static_cast<int>(t0)) : 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int t = static_cast<int>(min(t0 + u, (int64_t)INT32_MAX));
-      out[u] = -1;
-      if (t >= total) continue;
-      while (t >= cu[b + 1]) ++b;           // t < total = cu[B]: b stays below B
-      const int h = head[b];
-      if (h < 0) continue;
-      const uint32_t c = start[b], pos = c + static_cast<uint32_t>(t - cu[b]);
-      const uint32_t j = pos / p.page, r = pos - j * p.page;
-      const uint32_t have = (c + p.page - 1) / p.page;
-      const bool fresh = kPlan && j >= have;
-      int32_t *entry = p.table + (int64_t)b * p.width + j;
-      const int pg = fresh ? p.free_pages[h + (j - have)] : *entry;
-      const bool good = pg >= 0 && pg < p.num_pages;
-      if (fresh && r == 0) *entry = good ? pg : -1;
-      if (good) out[u] = static_cast<int32_t>(pg * p.page + r);
-      else bad = true;
+      from[u] = nullptr;
+      open[u] = nullptr;
+      rest[u] = 0;
+      if (t < total) {
+        while (t >= cu[b + 1]) ++b;         // t < total = cu[B]: b stays below B
+        const int h = head[b];
+        const uint32_t c = start[b], pos = c + static_cast<uint32_t>(t - cu[b]);
+        const uint32_t j = pos / p.page, have = (c + p.page - 1) / p.page;
+        rest[u] = pos - j * p.page;
+        if (h >= 0) {
+          int32_t *entry = p.table + (int64_t)b * p.width + j;
+          const bool fresh = kPlan && j >= have;
+          from[u] = fresh ? p.free_pages + h + (j - have) : entry;
+          if (fresh && rest[u] == 0) open[u] = entry;
+        }
+      }
+    }
+    int pg[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) pg[u] = from[u] ? *from[u] : -1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool good = pg[u] >= 0 && pg[u] < p.num_pages;
+      if (open[u]) *open[u] = good ? pg[u] : -1;
+      out[u] = good ? static_cast<int32_t>(pg[u] * p.page + rest[u]) : -1;
+      bad |= from[u] && !good;
     }
     if (wide && t0 + 4 <= p.max_slots) {
       *reinterpret_cast<int4 *>(p.slots + t0) = make_int4(out[0], out[1], out[2], out[3]);
