@@ -29,7 +29,9 @@ nsa_status check_kv4(const nsa_kv4_dims *d) {
   if (d->dtype != NSA_BF16 && d->dtype != NSA_FP16) return NSA_ERR_UNSUPPORTED;
   if (d->head_dim != 64 && d->head_dim != 128) return NSA_ERR_UNSUPPORTED;
   if (d->page_size != 32 && d->page_size != 64 && d->page_size != 128) return NSA_ERR_UNSUPPORTED;
-  if ((int64_t)d->num_pages * d->page_size >= (int64_t(1) << 31)) return NSA_ERR_UNSUPPORTED;
+  const int64_t tokens = (int64_t)d->num_pages * d->page_size;
+  if (tokens >= (int64_t(1) << 31) || tokens / kKv4Tile * d->h_k >= (int64_t(1) << 32))
+    return NSA_ERR_UNSUPPORTED;
   return NSA_OK;
 }
 
@@ -233,7 +235,7 @@ nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_
   p.lse = lse;
   p.status = device_status;
   p.ws = workspace;
-  if (kv4_decode_tiles(p) >= (int64_t(1) << 31)) return NSA_ERR_UNSUPPORTED;
+  if (kv4_decode_tiles(p) >= (int64_t(1) << 30)) return NSA_ERR_UNSUPPORTED;
   return launched(launch_kv4_decode(dims->head_dim, dims->dtype == NSA_FP16, p,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }

@@ -61,12 +61,14 @@ __device__ __forceinline__ void load_slots(const Kv4RowParams &p, int t0, int (&
   if (bad && (threadIdx.x & 31) == 0) raise(p.status, NSA_DEVERR_BAD_INDEX);
 }
 
-// The tile that holds a slot of head h.
+// Offset of the tile that holds a slot of head h (tiles are counted in 32 bits: 2^32 of them
+// would be 9 TB).
 template <int D>
-__device__ __forceinline__ uint8_t *slot_tile(const Kv4RowParams &p, int h, int slot) {
-  const int64_t page = slot >> p.page_log2;
-  const int in = slot & ((1 << p.page_log2) - 1);
-  return p.pool + (((page * p.h_k + h) << (p.page_log2 - 5)) + in / kKv4Tile) * Kv4Tile<D>::kBytes;
+__device__ __forceinline__ int64_t slot_tile(const Kv4RowParams &p, int h, int slot) {
+  const uint32_t page = static_cast<uint32_t>(slot) >> p.page_log2;
+  const uint32_t in = slot & ((1 << p.page_log2) - 1);
+  const uint32_t tile = ((page * p.h_k + h) << (p.page_log2 - 5)) + (in >> 5);
+  return (int64_t)tile * Kv4Tile<D>::kBytes;
 }
 
 // Larger of two pairs of 16-bit floats; a NaN stays.
@@ -177,7 +179,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowParams p)
                                                         high - my_zero < 15.4f * my_scale));
   if (stored) {
     const int row = my_slot & (kKv4Tile - 1), which = r.j >> 2;   // 0: scale, 1: zero
-    *reinterpret_cast<__half *>(slot_tile<D>(p, r.h, my_slot) + T::kPar +
+    *reinterpret_cast<__half *>(p.pool + slot_tile<D>(p, r.h, my_slot) + T::kPar +
                                 (2 * r.kv + which) * T::kArr + (row * T::kG + r.gi) * 2) =
         which ? zh : sh;
   }
@@ -192,7 +194,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowParams p)
                          : code_word<kFp16, false>(w4, f.x, f.y, inv);
     if (!(f.y > 0.f)) word = 0;
     if (r.live && slot[k] >= 0)
-      *reinterpret_cast<uint32_t *>(slot_tile<D>(p, r.h, slot[k]) + r.kv * T::kV +
+      *reinterpret_cast<uint32_t *>(p.pool + slot_tile<D>(p, r.h, slot[k]) + r.kv * T::kV +
                                     (slot[k] & (kKv4Tile - 1)) * T::kRow + (r.j * T::kG + r.gi) * 4) =
           word;
   }
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(Kv4RowParams p) {
     word[k] = 0;
     scale[k] = zero[k] = __ushort_as_half(0);
     if (slot[k] >= 0) {
-      const uint8_t *tile = slot_tile<D>(p, r.h, slot[k]);
+      const uint8_t *tile = p.pool + slot_tile<D>(p, r.h, slot[k]);
       const int row = slot[k] & (kKv4Tile - 1);
       word[k] = __ldg(reinterpret_cast<const uint32_t *>(tile + r.kv * T::kV + row * T::kRow +
                                                          (r.j * T::kG + r.gi) * 4));

@@ -89,7 +89,7 @@ NSA_API nsa_status nsa_page_slots(const nsa_page_dims *dims, const int32_t *bloc
 typedef struct {
     int32_t num_pages; /* pages of the pool; num_pages * page_size < 2^31 */
     int32_t page_size; /* 32, 64 or 128 */
-    int32_t h_k;       /* KV heads */
+    int32_t h_k;       /* KV heads; num_pages * page_size / 32 * h_k < 2^32 */
     int32_t head_dim;  /* 64 or 128 */
     int32_t dtype;     /* nsa_dtype of k, v, q and out */
 } nsa_kv4_dims;
@@ -131,7 +131,7 @@ NSA_API nsa_status nsa_kv4_read(const nsa_kv4_dims *dims, int32_t n, const void 
  *                that is 0); its contents carry nothing from one call to the next.  Calls that
  *                may overlap on the GPU need workspaces of their own.
  * num_seqs * h_k * (table_width * page_size / 32 + 5), twice that for h_q / h_k > 8, has to
- * stay below 2^31 (NSA_ERR_UNSUPPORTED).
+ * stay below 2^30 (NSA_ERR_UNSUPPORTED).
  * Rows of the pool behind a sequence's end, and tokens before its window, may hold
  * anything, NaN included. */
 NSA_API nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_q,

@@ -66,6 +66,7 @@ def test_row_refusals(lib):
                dict(dtype=2), dict(num_pages=1 << 25)):
         assert append(_kv4(**kw)) == 2, kw
     assert append(_kv4(h_k=0)) == 1
+    assert append(_kv4(num_pages=1 << 24, h_k=128)) == 2         # 2^32 tiles
     assert append(_kv4(h_k=1 << 20), n=1 << 20) == 2
     assert append(n=0, k=None, v=None, slots=None) == 0          # nothing to do
 
@@ -92,7 +93,8 @@ def test_decode_refusals(lib):
                dict(lse=None), dict(q=FAKE + 8), dict(out=FAKE + 8), dict(pool=FAKE + 8),
                dict(lse=FAKE + 2), dict(sel=FAKE + 2), dict(ws=FAKE + 8), dict(st=FAKE + 2)):
         assert decode(**kw) == 1, kw
-    for kw in (dict(h_q=34), dict(topk=33), dict(width=1 << 26), dict(b=1 << 28)):
+    for kw in (dict(h_q=34), dict(topk=33), dict(width=1 << 26), dict(b=1 << 28),
+               dict(b=1 << 10, width=1 << 18)):
         assert decode(**kw) == 2, kw
     size = ctypes.c_size_t()
     assert lib.nsa_kv4_decode_workspace_size(_kv4(), 2, 8, 0, ctypes.byref(size)) == 0
