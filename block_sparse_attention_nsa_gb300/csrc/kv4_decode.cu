@@ -15,10 +15,13 @@
 //           q^ is q times a power of two per head (largest magnitude in [2^14, 2^15)), so
 //           that fp16 holds bf16's and fp16's values: it loses only what is 2^-38 of the
 //           largest.
-//   output  O_g = sum_i P'_i c_i - 8 sum_i P'_i + sum_i p_i (z_i + 8 s_i), P' = p s rounded to
-//           fp16 (the one rounding: 2^-11 of a weight, on codes counted from their middle),
-//           P' scaled by a power of two that follows the largest s seen.  The second term
-//           takes one more product with a row of ones, the third stays in fp32.
+//   output  O_g = sum_i P'_i c_i - sum_i P'_i m_i + sum_i p_i (z_i + m_i s_i), P' = p s rounded to
+//           fp16 (the one rounding: 2^-11 of a weight, on codes counted from m),
+//           P' scaled by a power of two that follows the largest s seen.  m is 8, the codes'
+//           middle, where the output is bf16, and where it is fp16, whose rounding is as
+//           small as P''s, the code nearest to a value of 0, so that the error of a term is
+//           2^-11 of the value itself.  The second term takes one more product with a row of
+//           ones (middles), the third stays in fp32.
 // The softmax runs online: the reference maximum of a head is raised (and the sums
 // rescaled) only when a score exceeds it by 2 in the exponent, which one vote per tile
 // finds, so most tiles need no shuffles.
@@ -134,8 +137,8 @@ struct K4RawQuery {
 template <int D>
 struct K4State {
   float o[K4<D>::kG][4][4];      // dims 64 gi + 8 r + 2 e (+1: 16 times), heads 2c, 2c + 1
-  float ps[K4<D>::kG][4];        // sum of P'
-  float oz[2][K4<D>::kG];        // this lane's share of sum p (z + 8 s)
+  float ps[K4<D>::kG][4];        // sum of P' (fp16: of P' times the key's middle)
+  float oz[2][K4<D>::kG];        // this lane's share of sum p (z + middle * s)
   float m[2], l[2];              // reference maximum; l: this lane's share
   float thr[2];                  // raw score above which m is raised
   float vmax, rinv;              // largest V scale allowed for, kPScale / it
@@ -394,12 +397,26 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
       }
     }
   }
-  uint8_t *const vpar = st;  // over the K codes, which all have read (the vote): s / reference, z + 8 s
+  // over the K codes, which all have read (the vote): s / reference, z + middle * s, and for fp16
+  // the middles
+  uint8_t *const vpar = st, *const vmid = st + 512;
+  float mid[G];
+#pragma unroll
+  for (int gi = 0; gi < G; ++gi) {
+    mid[gi] = 8.f;
+    if (kFp16) {
+      const __half m = __float2half_rn(
+          vs[gi] > 0.f ? fminf(fmaxf(__fdividef(-vz[gi], vs[gi]), 0.f), 15.f) : 0.f);
+      reinterpret_cast<__half *>(vmid)[gi * 32 + lane] = m;
+      mid[gi] = __half2float(m);
+    }
+  }
   if constexpr (G == 2)
-    reinterpret_cast<float4 *>(vpar)[lane] = make_float4(
-        vs[0] * a.rinv, vs[1] * a.rinv, fmaf(8.f, vs[0], vz[0]), fmaf(8.f, vs[1], vz[1]));
+    reinterpret_cast<float4 *>(vpar)[lane] =
+        make_float4(vs[0] * a.rinv, vs[1] * a.rinv, fmaf(mid[0], vs[0], vz[0]),
+                    fmaf(mid[1], vs[1], vz[1]));
   else
-    reinterpret_cast<float2 *>(vpar)[lane] = make_float2(vs[0] * a.rinv, fmaf(8.f, vs[0], vz[0]));
+    reinterpret_cast<float2 *>(vpar)[lane] = make_float2(vs[0] * a.rinv, fmaf(mid[0], vs[0], vz[0]));
   __syncwarp();              // V's scales and zeros are in place
   // ---- weights ----
   uint32_t pb[G][2][2];      // B operands: [group][half][k rows 0-7, 8-15]
@@ -449,8 +466,14 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
         mma16816(a.o[gi][e], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u,
                  pb[gi][half][0], pb[gi][half][1]);
       }
-      mma16816(a.ps[gi], 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u, pb[gi][half][0],
-               pb[gi][half][1]);
+      // bf16: P' summed by ones; fp16: weighted by the middles, of keys 2c, 2c + 1 and + 8
+      uint32_t m0 = 0x3c003c00u, m1 = 0x3c003c00u;
+      if (kFp16) {
+        const uint32_t *m = reinterpret_cast<const uint32_t *>(vmid + gi * 64 + half * 32);
+        m0 = m[c];
+        m1 = m[c + 4];
+      }
+      mma16816(a.ps[gi], m0, m0, m1, m1, pb[gi][half][0], pb[gi][half][1]);
     }
   }
 }
@@ -606,7 +629,7 @@ __device__ __forceinline__ void sum_lanes(K4State<D> &a) {
 }
 
 // O times f (per head of the lane) into an area [head pairs].
-template <int D>
+template <int D, bool kFp16>
 __device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D> &a, float f0,
                                           float f1) {
   constexpr int G = K4<D>::kG;
@@ -618,7 +641,7 @@ __device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D
     float *dst = area + c * K4<D>::kHeadPair + hd * D + 8 * r;
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
-      const float base = fmaf(-8.f * fb, a.ps[gi][hd], f * a.oz[hd][gi]);
+      const float base = fmaf(kFp16 ? -fb : -8.f * fb, a.ps[gi][hd], f * a.oz[hd][gi]);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<float2 *>(dst + gi * 64 + 2 * e) = make_float2(
@@ -682,7 +705,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4De
   const float f0 = a.l[0] != 0.f ? ex2_approx(a.m[0] - M0) : 0.f;
   const float f1 = a.l[1] != 0.f ? ex2_approx(a.m[1] - M1) : 0.f;
   if (r == 0) *reinterpret_cast<float2 *>(&lsum[warp][2 * c]) = make_float2(a.l[0] * f0, a.l[1] * f1);
-  leave_out<D>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), lane, a, f0, f1);
+  leave_out<D, kFp16>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), lane, a, f0, f1);
   __syncthreads();
   for (int i = tid; i < sg.g * (D / 4); i += kWarps * 32) {
     const int head = i / (D / 4), dim = 4 * (i % (D / 4));
@@ -849,13 +872,13 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     if (first) {
       left |= kFirst | (goes_on ? kOn : 0) | (at < stop ? kKeep : 0);
       if (warp == 0 && lane == 0) groups[0] = make_int4(b, unit, 0, 0);
-      if (at < stop) leave_out<D>(reinterpret_cast<float *>(ring + K4<D>::kKept), lane, a, 1.f, 1.f);
+      if (at < stop) leave_out<D, kFp16>(reinterpret_cast<float *>(ring + K4<D>::kKept), lane, a, 1.f, 1.f);
     } else if (goes_on) {                  // the run's last: stays in registers
       left |= kLast;
       if (lane == 0) groups[warp + 1] = make_int4(b, unit, seg0 + nt, 0);
     } else {
       float *area = reinterpret_cast<float *>(ring);
-      leave_out<D>(area, lane, a, 1.f, 1.f);
+      leave_out<D, kFp16>(area, lane, a, 1.f, 1.f);
       __syncwarp();
 #pragma unroll 1
       for (int i = lane; i < sg.g * (D / 4); i += 32) {
@@ -915,7 +938,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     const float f0 = v.y != 0.f ? ex2_approx(v.x - M0) : 0.f;
     const float f1 = v.w != 0.f ? ex2_approx(v.z - M1) : 0.f;
     const bool kept = !side && (left & kKeep);   // left already, without its factor
-    if (!kept) leave_out<D>(reinterpret_cast<float *>(ring), lane, a, f0, f1);
+    if (!kept) leave_out<D, kFp16>(reinterpret_cast<float *>(ring), lane, a, f0, f1);
     if (lane < 4) {
       fac[side][warp][2 * c] = make_float2(kept ? f0 : 1.f, v.y * f0);
       fac[side][warp][2 * c + 1] = make_float2(kept ? f1 : 1.f, v.w * f1);
