@@ -108,24 +108,60 @@ __device__ __forceinline__ float quotient(float x, float y, float inv) {
   return __fmaf_rn(__fmaf_rn(-q, y, x), inv, q);
 }
 
+// Two fp32 operations in one instruction, each rounded to nearest.
+struct Pair {
+  unsigned long long v;
+  __device__ __forceinline__ Pair() {}
+  __device__ __forceinline__ Pair(float a, float b) {
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b));
+  }
+  __device__ __forceinline__ float2 get() const {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+  }
+};
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d.v) : "l"(a.v), "l"(b.v));
+  return d;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return d;
+}
+
 // The eight codes of a lane: (x - zero) / scale to the nearest whole number, ties to even, as
 // adding 1.5 * 2^23 rounds.  kHeld: held to finite x and to 0 ... 15, which most groups need
 // no step for.
 template <bool kFp16, bool kHeld>
 __device__ __forceinline__ uint32_t code_word(const uint32_t (&w4)[4], float zero, float scale,
                                               float inv) {
+  const Pair minus_zero(-zero, -zero), minus_scale(-scale, -scale), inv2(inv, inv);
+  const Pair magic(12582912.f, 12582912.f);
   uint32_t word = 0;
 #pragma unroll
   for (int u = 3; u >= 0; --u) {         // the lowest nibble last: each step shifts by four bits
-    const float2 f = unpack2<kFp16>(w4[u]);
-#pragma unroll
-    for (int k = 1; k >= 0; --k) {
-      float x = k ? f.y : f.x;
-      if (kHeld) x = fminf(fmaxf(x, -kHalfMax), kHalfMax);
-      float q = quotient(__fsub_rn(x, zero), scale, inv);
-      if (kHeld) q = fminf(fmaxf(q, 0.f), 15.f);
-      word = word * 16u + __float_as_uint(__fadd_rn(q, 12582912.f));
+    float2 f = unpack2<kFp16>(w4[u]);
+    if (kHeld) {
+      f.x = fminf(fmaxf(f.x, -kHalfMax), kHalfMax);
+      f.y = fminf(fmaxf(f.y, -kHalfMax), kHalfMax);
     }
+    const Pair t = Pair(f.x, f.y) + minus_zero, q0 = t * inv2;
+    Pair q = fma(fma(q0, minus_scale, t), inv2, q0);   // as quotient(), two at a time
+    if (kHeld) {
+      const float2 g = q.get();
+      q = Pair(fminf(fmaxf(g.x, 0.f), 15.f), fminf(fmaxf(g.y, 0.f), 15.f));
+    }
+    const float2 m = (q + magic).get();
+    word = word * 16u + __float_as_uint(m.y);
+    word = word * 16u + __float_as_uint(m.x);
   }
   return word - 0x4b400000u * 0x11111111u;   // less the bits of 1.5 * 2^23 in each of the eight
 }
