@@ -127,7 +127,7 @@ template <int D>
 struct K4Query {
   uint32_t f[K4<D>::kW][4];      // [word of the row][dims (0,4), (1,5)/16, (2,6), (3,7)/16]
   float sum[2][K4<D>::kG];       // sums of q^ in the raw scores' unit, heads 2c, 2c + 1 of the lane
-  float mul[2];                  // raw score -> S, > 0
+  Pair mul;                      // raw score -> S, > 0
 };
 template <int D>
 struct K4RawQuery {
@@ -138,8 +138,8 @@ template <int D>
 struct K4State {
   float o[K4<D>::kG][4][4];      // dims 64 gi + 8 r + 2 e (+1: 16 times), heads 2c, 2c + 1
   float ps[K4<D>::kG][4];        // sum of P' (fp16: of P' times the key's middle)
-  float oz[2][K4<D>::kG];        // this lane's share of sum p (z + middle * s)
-  float m[2], l[2];              // reference maximum; l: this lane's share
+  Pair oz[K4<D>::kG];            // this lane's share of sum p (z + middle * s), of both heads
+  Pair minus_m, l;               // reference maximum, negated; l: this lane's share
   float thr[2];                  // raw score above which m is raised
   float vmax, rinv;              // largest V scale allowed for, kPScale / it
   __device__ __forceinline__ void clear() {
@@ -151,13 +151,11 @@ struct K4State {
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[gi][e][x] = 0.f;
       }
+    minus_m = Pair(INFINITY, INFINITY);
+    thr[0] = thr[1] = -INFINITY;
+    l = Pair(0.f, 0.f);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      m[u] = thr[u] = -INFINITY;
-      l[u] = 0.f;
-#pragma unroll
-      for (int gi = 0; gi < K4<D>::kG; ++gi) oz[u][gi] = 0.f;
-    }
+    for (int gi = 0; gi < K4<D>::kG; ++gi) oz[gi] = Pair(0.f, 0.f);
     vmax = 0.f;
     rinv = 0.f;
   }
@@ -241,9 +239,9 @@ __device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale
   // the masked scores below the others.
   constexpr int kUp = K4Up<kFp16>::kBits;
   const float mul = fmaxf(ldexpf(fabsf(scale_log2), ex + 10 - kUp), 1e-30f);
+  out.mul = Pair(__shfl_sync(0xffffffffu, mul, 8 * c), __shfl_sync(0xffffffffu, mul, 8 * c + 4));
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    out.mul[u] = __shfl_sync(0xffffffffu, mul, (2 * c + u) * 4);
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) out.sum[u][gi] = sum[gi][u] * (5.9604644775390625e-8f * (1 << kUp));
   }
@@ -374,19 +372,21 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
       a.vmax = vnew;
       a.rinv = rnew;
     }
+    const float2 mul = q.mul.get(), mm = a.minus_m.get();
+    float alpha[2], minus[2];
 #pragma unroll
     for (int hd = 0; hd < 2; ++hd) {
       float x = top[hd];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      const float mnew = fmaxf(a.m[hd], x * q.mul[hd]), alpha = ex2_approx(a.m[hd] - mnew);
-      const float both = alpha * grow;
-      a.m[hd] = mnew;
-      a.thr[hd] = __fdividef(mnew + kSlack, q.mul[hd]);
-      a.l[hd] *= alpha;
+      const float old = -(hd ? mm.y : mm.x), k = hd ? mul.y : mul.x;
+      const float mnew = fmaxf(old, x * k);
+      alpha[hd] = ex2_approx(old - mnew);
+      minus[hd] = -mnew;
+      a.thr[hd] = __fdividef(mnew + kSlack, k);
+      const float both = alpha[hd] * grow;
 #pragma unroll
       for (int gi = 0; gi < G; ++gi) {
-        a.oz[hd][gi] *= alpha;
         a.ps[gi][hd] *= both;
         a.ps[gi][2 + hd] *= both;
 #pragma unroll
@@ -396,6 +396,11 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
         }
       }
     }
+    const Pair al(alpha[0], alpha[1]);
+    a.minus_m = Pair(minus[0], minus[1]);
+    a.l = a.l * al;
+#pragma unroll
+    for (int gi = 0; gi < G; ++gi) a.oz[gi] = a.oz[gi] * al;
   }
   // over the K codes, which all have read (the vote): s / reference, z + middle * s, and for fp16
   // the middles
@@ -422,7 +427,11 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
   uint32_t pb[G][2][2];      // B operands: [group][half][k rows 0-7, 8-15]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float vsr[G], vc[G], p[2];
+    const float2 e = fma(Pair(s[i >> 1][(i & 1) * 2], s[i >> 1][(i & 1) * 2 + 1]), q.mul,
+                         a.minus_m).get();
+    const Pair p(ex2_approx(e.x), ex2_approx(e.y));
+    a.l = a.l + p;
+    float vsr[G], vc[G];
     if constexpr (G == 2) {
       const float4 x = reinterpret_cast<const float4 *>(vpar)[i * 8 + r];
       vsr[0] = x.x; vsr[1] = x.y; vc[0] = x.z; vc[1] = x.w;
@@ -431,15 +440,11 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
       vsr[0] = x.x; vc[0] = x.y;
     }
 #pragma unroll
-    for (int hd = 0; hd < 2; ++hd) {
-      p[hd] = ex2_approx(fmaf(s[i >> 1][(i & 1) * 2 + hd], q.mul[hd], -a.m[hd]));
-      a.l[hd] += p[hd];
-#pragma unroll
-      for (int gi = 0; gi < G; ++gi) a.oz[hd][gi] = fmaf(p[hd], vc[gi], a.oz[hd][gi]);
+    for (int gi = 0; gi < G; ++gi) {
+      a.oz[gi] = fma(p, Pair(vc[gi], vc[gi]), a.oz[gi]);
+      const float2 w = (p * Pair(vsr[gi], vsr[gi])).get();
+      pb[gi][i >> 1][i & 1] = transpose8x8(pack2<true>(w.x, w.y));
     }
-#pragma unroll
-    for (int gi = 0; gi < G; ++gi)
-      pb[gi][i >> 1][i & 1] = transpose8x8(pack2<true>(p[0] * vsr[gi], p[1] * vsr[gi]));
   }
   // ---- output: rows are dimensions, k the keys ----
 #pragma unroll
@@ -614,24 +619,39 @@ struct K4Stream {
   }
 };
 
-// The warp's l and zero terms summed over its lanes.
+// A warp's maxima, sums and zero terms, over its lanes.
 template <int D>
-__device__ __forceinline__ void sum_lanes(K4State<D> &a) {
+struct K4Sums {
+  float m[2], l[2], oz[2][K4<D>::kG];
+  __device__ __forceinline__ explicit K4Sums(const K4State<D> &a) {
+    const float2 mm = a.minus_m.get(), ll = a.l.get();
+    m[0] = -mm.x;
+    m[1] = -mm.y;
+    l[0] = ll.x;
+    l[1] = ll.y;
 #pragma unroll
-  for (int o = 4; o < 32; o <<= 1)
-#pragma unroll
-    for (int hd = 0; hd < 2; ++hd) {
-      a.l[hd] += __shfl_xor_sync(0xffffffffu, a.l[hd], o);
-#pragma unroll
-      for (int gi = 0; gi < K4<D>::kG; ++gi)
-        a.oz[hd][gi] += __shfl_xor_sync(0xffffffffu, a.oz[hd][gi], o);
+    for (int gi = 0; gi < K4<D>::kG; ++gi) {
+      const float2 z = a.oz[gi].get();
+      oz[0][gi] = z.x;
+      oz[1][gi] = z.y;
     }
-}
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+      for (int hd = 0; hd < 2; ++hd) {
+        l[hd] += __shfl_xor_sync(0xffffffffu, l[hd], o);
+#pragma unroll
+        for (int gi = 0; gi < K4<D>::kG; ++gi)
+          oz[hd][gi] += __shfl_xor_sync(0xffffffffu, oz[hd][gi], o);
+      }
+  }
+  __device__ __forceinline__ float4 pairs() const { return make_float4(m[0], l[0], m[1], l[1]); }
+};
 
 // O times f (per head of the lane) into an area [head pairs].
 template <int D, bool kFp16>
-__device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D> &a, float f0,
-                                          float f1) {
+__device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D> &a,
+                                          const K4Sums<D> &sums, float f0, float f1) {
   constexpr int G = K4<D>::kG;
   const int r = lane >> 2, c = lane & 3;
   const float back = a.rinv > 0.f ? __fdiv_rn(1.f, a.rinv) : 0.f;   // a power of two
@@ -641,7 +661,7 @@ __device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D
     float *dst = area + c * K4<D>::kHeadPair + hd * D + 8 * r;
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
-      const float base = fmaf(kFp16 ? -fb : -8.f * fb, a.ps[gi][hd], f * a.oz[hd][gi]);
+      const float base = fmaf(kFp16 ? -fb : -8.f * fb, a.ps[gi][hd], f * sums.oz[hd][gi]);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<float2 *>(dst + gi * 64 + 2 * e) = make_float2(
@@ -692,8 +712,8 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4De
 
   // the warps agree on each head's maximum, scale their sums to it, and add up
   const int r = lane >> 2, c = lane & 3;
-  sum_lanes(a);
-  if (r == 0) ml[warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
+  const K4Sums<D> sums(a);
+  if (r == 0) ml[warp][c] = sums.pairs();
   __syncthreads();
   float M0 = -INFINITY, M1 = -INFINITY;                // -inf without keys
 #pragma unroll
@@ -702,10 +722,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4De
     M0 = fmaxf(M0, v.x);
     M1 = fmaxf(M1, v.z);
   }
-  const float f0 = a.l[0] != 0.f ? ex2_approx(a.m[0] - M0) : 0.f;
-  const float f1 = a.l[1] != 0.f ? ex2_approx(a.m[1] - M1) : 0.f;
-  if (r == 0) *reinterpret_cast<float2 *>(&lsum[warp][2 * c]) = make_float2(a.l[0] * f0, a.l[1] * f1);
-  leave_out<D, kFp16>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), lane, a, f0, f1);
+  const float f0 = sums.l[0] != 0.f ? ex2_approx(sums.m[0] - M0) : 0.f;
+  const float f1 = sums.l[1] != 0.f ? ex2_approx(sums.m[1] - M1) : 0.f;
+  if (r == 0)
+    *reinterpret_cast<float2 *>(&lsum[warp][2 * c]) = make_float2(sums.l[0] * f0, sums.l[1] * f1);
+  leave_out<D, kFp16>(reinterpret_cast<float *>(smem + warp * K4<D>::kRing), lane, a, sums, f0, f1);
   __syncthreads();
   for (int i = tid; i < sg.g * (D / 4); i += kWarps * 32) {
     const int head = i / (D / 4), dim = 4 * (i % (D / 4));
@@ -865,20 +886,21 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
       make_query<D, kFp16>(raw, p.scale_log2, lane, q);
       st.run(q, a, err);
     }
-    sum_lanes(a);
+    const K4Sums<D> sums(a);
     at = seg0 + v1;
     const bool goes_on = v1 < nt, first = v0 > 0;
-    if (lane < 4) ml[first ? 0 : 1][warp][c] = make_float4(a.m[0], a.l[0], a.m[1], a.l[1]);
+    if (lane < 4) ml[first ? 0 : 1][warp][c] = sums.pairs();
     if (first) {
       left |= kFirst | (goes_on ? kOn : 0) | (at < stop ? kKeep : 0);
       if (warp == 0 && lane == 0) groups[0] = make_int4(b, unit, 0, 0);
-      if (at < stop) leave_out<D, kFp16>(reinterpret_cast<float *>(ring + K4<D>::kKept), lane, a, 1.f, 1.f);
+      if (at < stop) leave_out<D, kFp16>(reinterpret_cast<float *>(ring + K4<D>::kKept), lane, a, sums, 1.f,
+                                           1.f);
     } else if (goes_on) {                  // the run's last: stays in registers
       left |= kLast;
       if (lane == 0) groups[warp + 1] = make_int4(b, unit, seg0 + nt, 0);
     } else {
       float *area = reinterpret_cast<float *>(ring);
-      leave_out<D, kFp16>(area, lane, a, 1.f, 1.f);
+      leave_out<D, kFp16>(area, lane, a, sums, 1.f, 1.f);
       __syncwarp();
 #pragma unroll 1
       for (int i = lane; i < sg.g * (D / 4); i += 32) {
@@ -938,7 +960,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     const float f0 = v.y != 0.f ? ex2_approx(v.x - M0) : 0.f;
     const float f1 = v.w != 0.f ? ex2_approx(v.z - M1) : 0.f;
     const bool kept = !side && (left & kKeep);   // left already, without its factor
-    if (!kept) leave_out<D, kFp16>(reinterpret_cast<float *>(ring), lane, a, f0, f1);
+    if (!kept) leave_out<D, kFp16>(reinterpret_cast<float *>(ring), lane, a, K4Sums<D>(a), f0, f1);
     if (lane < 4) {
       fac[side][warp][2 * c] = make_float2(kept ? f0 : 1.f, v.y * f0);
       fac[side][warp][2 * c + 1] = make_float2(kept ? f1 : 1.f, v.w * f1);
