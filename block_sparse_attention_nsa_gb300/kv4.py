@@ -66,14 +66,21 @@ def _fail(code: int, where: str):
     raise NsaError(code, where)
 
 
+def _held(sizes, where):
+    """ctypes would wrap what 32 bits do not hold."""
+    if not all(-2 ** 31 <= x < 2 ** 31 for x in sizes):
+        _fail(2, f"{where}: sizes {sizes} beyond 32 bits")
+    return sizes
+
+
 @functools.lru_cache(maxsize=4096)
 def _page_dims(*sizes):
-    return PageDims(*sizes)
+    return PageDims(*_held(sizes, "page dims"))
 
 
 @functools.lru_cache(maxsize=4096)
 def _kv4_dims(*sizes):
-    return Kv4Dims(*sizes)
+    return Kv4Dims(*_held(sizes, "kv4 dims"))
 
 
 _current_device = torch.cuda.current_device
@@ -224,6 +231,8 @@ def kv4_append(pool, k, v, slot_map, device_status=None, stream=None):
     if ke != 1 or ve != 1 or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("k and v need a contiguous last dimension, on the pool's device")
     _check("slot_map", slot_map, torch.int32, (n,), dev)
+    if n >> 31:
+        _fail(2, "kv4_append: rows beyond 32 bits")
     code = _lib().nsa_kv4_append(dims, n, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
                                  slot_map.data_ptr(), pool.data_ptr(),
                                  _status(device_status, dev), _raw(stream, dev))
@@ -235,12 +244,15 @@ def kv4_append(pool, k, v, slot_map, device_status=None, stream=None):
 def kv4_read(pool, slot_map, head_dim: int, k=None, v=None, dtype: torch.dtype = torch.bfloat16,
              device_status=None, stream=None):
     """The cached rows of slot_map int32 [n] as k, v [n, h_k, head_dim] (zeros where the slot
-    is -1), in the dtype of k where it is given."""
+    is -1), in the dtype of k where it is given.  head_dim has to be the one that the pool was
+    made for: the pool's bytes do not say (64 tokens of 128 dimensions are as many as 128 of 64)."""
     if k is not None:
         dtype = k.dtype
     dims, dev = _pool_dims(pool, head_dim, dtype, "kv4_read")
     n = slot_map.numel()
     _check("slot_map", slot_map, torch.int32, (n,), dev)
+    if n >> 31:
+        _fail(2, "kv4_read: rows beyond 32 bits")
     shape = (n, pool.shape[1], head_dim)
     if k is None:
         k = _empty(shape, dtype, dev, stream)
@@ -312,6 +324,10 @@ def kv4_decode(q, pool, block_table, seq_lens, scale: float, sel_idx=None, windo
             workspace = _empty((need,), torch.uint8, dev, stream)
     else:
         _check("workspace", workspace, torch.uint8, workspace.shape, dev)
+    if not -1 < window < 0x7fffffff:      # beyond every length, or negative (refused below)
+        window = 0x7fffffff if window > 0 else -1
+    if width >> 31 or b >> 31:
+        _fail(2, "kv4_decode: sizes beyond 32 bits")
     ws, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     code = _lib().nsa_kv4_decode(
         dims, b, h_q, width, topk, window, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(),

@@ -24,6 +24,9 @@
  * to even, within 0 ... 15, and 0 where scale is 0.  A group that holds a NaN is stored
  * with a NaN zero: all of it reads as NaN.
  *
+ * The bytes of a pool do not say its head_dim (64 tokens of d = 128 are as many as 128 of
+ * d = 64): calls on one pool name the same.
+ *
  * A slot is the place of one token in the pool: page * P + position within the page.
  * slot_map entries of -1 belong to no token (padding).
  */

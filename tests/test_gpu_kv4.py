@@ -147,6 +147,7 @@ def test_decode_matches_oracle(d, page, h_k, g, dtype, topk, window):
 
 @pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 511, 513])
 def test_decode_lengths_around_tiles(n):
+    _decode((n,), 64, 1, 4, 128, "bf16", n, window=2 ** 40)
     _decode((n,), 64, 1, 4, 128, "bf16", n)
     _decode((n,), 32, 2, 1, 64, "fp16", n, topk=16)
     _decode((n,), 128, 1, 3, 128, "fp16", n, window=32)
@@ -247,6 +248,9 @@ def test_decode_rejects():
     assert e.value.code == 1
     with pytest.raises(nsa.NsaError) as e:
         nsa.kv4_decode(q, pool, table, lens, 0.1, window=-1)
+    assert e.value.code == 1
+    with pytest.raises(nsa.NsaError) as e:
+        nsa.kv4_decode(q, pool, table, lens, 0.1, window=-2 ** 40)
     assert e.value.code == 1
     with pytest.raises(nsa.NsaError) as e:                                  # 33 slots
         nsa.kv4_decode(q, pool, table, lens, 0.1,
@@ -417,6 +421,45 @@ def test_steps_in_a_graph_between_streams():
         want += out.double().cpu()
     assert lens.tolist() == [40] * b
     torch.testing.assert_close(total.double().cpu(), want, rtol=0, atol=40 * 40 * 2.0 ** -24)
+
+
+def test_calls_on_two_streams_and_between_torch_kernels():
+    """Unsynchronised loops on two streams, each call behind a torch kernel that writes its
+    inputs and before one that reads its outputs: the same sums as with a wait after each."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d = 64, 2, 4, 128
+    sets = []
+    for seed, lens in ((61, (4000, 5, 900)), (62, (3000,) * 5)):
+        pool, table, _ = make_cache(lens, page, h_k, d, seed)
+        gen = torch.Generator().manual_seed(seed)
+        qs = torch.randn(12, len(lens), h_k * g, d, generator=gen).to(torch.bfloat16).cuda()
+        sel = make_selection(lens, page, h_k, 8, seed)
+        need = nsa.kv4_decode_workspace_size(pool.shape[0], page, h_k, d, len(lens), h_k * g)
+        sets.append(dict(pool=_dev(pool), table=_dev(table), lens=_dev(np.int32(lens)), qs=qs,
+                         q=torch.empty_like(qs[0]), sel=_dev(sel), stream=torch.cuda.Stream(),
+                         ws=torch.empty(need, dtype=torch.uint8, device="cuda")))
+
+    def loop(s, wait):
+        total = torch.zeros(s["q"].shape, device="cuda")
+        for q in s["qs"]:
+            for sel in (None, s["sel"]):
+                s["q"].copy_(q)
+                out, _ = nsa.kv4_decode(s["q"], s["pool"], s["table"], s["lens"], 0.1, sel_idx=sel,
+                                        workspace=s["ws"])
+                total.add_(out.float())
+                if wait:
+                    torch.cuda.synchronize()
+        return total
+    want = [loop(s, True) for s in sets]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s in sets:
+            with torch.cuda.stream(s["stream"]):
+                got.append(loop(s, False))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
 
 
 # ---- a serving loop -------------------------------------------------------------------

@@ -116,3 +116,6 @@ def test_python_refuses_cpu_tensors(lib):
         nsa.kv4_read(torch.zeros(2, 2, 9216, dtype=torch.uint8), x[0], 128)
     with pytest.raises(nsa.NsaError):
         nsa.kv4_pool(2, 16, 2, 128, device="cpu")
+    with pytest.raises(nsa.NsaError) as e:
+        nsa.kv4_pool(2 ** 32 + 2, 64, 2, 128, device="cpu")      # would wrap to 2
+    assert e.value.code == 2
