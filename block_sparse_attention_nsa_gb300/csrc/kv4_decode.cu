@@ -34,13 +34,13 @@
 // scales and zeros into fp32 for all, in the place of the K codes.
 //
 // Work.  A segment is a (sequence, KV head, up to 8 of its query heads).  kv4_seg_kernel:
-// one CTA a segment, its eight warps taking the tiles in turn; for batches whose segments
-// all fit the GPU at once and have few tiles.  kv4_run_kernel: every warp takes an equal
-// run of the batch's tiles in segment order, whatever the lengths, which only the device
-// knows; a segment counts kOver tiles more than it has, about what starting one costs.
-// Segments inside a warp's run are written by that warp; those that cross into the next
-// warp's are joined in the CTA, and those that cross a CTA's border leave partial results
-// (at most two a CTA) for kv4_merge_kernel.
+// one CTA of 1 to 16 warps a segment, the warps taking its tiles in turn; for segments whose
+// tiles have a bound that the host knows (a selection, a window, a short table).
+// kv4_run_kernel: every warp takes an equal run of the batch's tiles in segment order,
+// whatever the lengths, which only the device knows; a segment counts kOver tiles more than
+// it has, about what starting one costs.  Segments inside a warp's run are written by that
+// warp; those that cross into the next warp's are joined in the CTA, and those that cross a
+// CTA's border leave partial results (at most two a CTA) for kv4_merge_kernel.
 #include "kv4.cuh"
 
 namespace nsa {
@@ -685,14 +685,14 @@ __device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int h
 
 // One CTA of kWarps per segment.
 template <int D, bool kFp16, bool kSel, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4DecodeParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4DecodeParams p, int units) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float4 ml[kWarps][kK4Heads / 2];          // m, l of two heads
   __shared__ float lsum[kWarps][kK4Heads];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   K4Seg sg = {};
-  set_unit(p, blockIdx.x, sg);
-  sg.b = blockIdx.y;
+  sg.b = static_cast<int>(blockIdx.x / static_cast<unsigned>(units));
+  set_unit(p, static_cast<int>(blockIdx.x) - sg.b * units, sg);
   int32_t err = 0;
   after_previous();
   K4RawQuery<D> raw;
@@ -751,16 +751,10 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4De
   }
 }
 
-// Tiles that a sequence's segments count as: what they have (with a selection, at most), at
-// least one, so that an empty one's output is written too, and kOver.
-template <bool kSel>
+// Tiles that a sequence's segments count as: what they have, at least one, so that an empty
+// one's output is written too, and kOver.
 __device__ __forceinline__ int counted_tiles(const Kv4DecodeParams &p, int len) {
-  int nt = ((len + 31) >> 5) - (seq_lo(p, len) >> 5);
-  if (kSel) {
-    const int nblk = (len + (1 << p.page_log2) - 1) >> p.page_log2;
-    nt = min(nblk, p.topk) << (p.page_log2 - 5);
-  }
-  return max(nt, 1) + kOver;
+  return max(((len + 31) >> 5) - (seq_lo(p, len) >> 5), 1) + kOver;
 }
 
 __device__ __forceinline__ K4Split *splits_of(const Kv4DecodeParams &p) {
@@ -785,11 +779,9 @@ __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
   return x;
 }
 
-// Equal runs of the batch's counted tiles.  whole: a CTA's run is moved to segments' starts,
-// so that no segment is split between CTAs.
-template <int D, bool kFp16, bool kSel>
-__global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams p, int units,
-                                                                int whole) {
+// Equal runs of the batch's counted tiles.
+template <int D, bool kFp16>
+__global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams p, int units) {
   extern __shared__ __align__(128) uint8_t smem[];
   // of a warp's parts ([0]: first, [1]: last): m, l of two heads; factors, l times them
   __shared__ float4 ml[2][kK4Warps][kK4Heads / 2];
@@ -803,7 +795,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   const int b0 = min(tid * per_thread, p.num_seqs), b1 = min(b0 + per_thread, p.num_seqs);
   int32_t err = 0, ignore = 0;
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += counted_tiles<kSel>(p, seq_len(p, b, err));
+  for (int b = b0; b < b1; ++b) mine += counted_tiles(p, seq_len(p, b, err));
   if (blockIdx.x == 0 && err) raise(p.status, err);
   err = 0;
   pre[tid] = warp_incl_sum(mine * units, lane);
@@ -826,7 +818,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     if (per_thread == 1) return;
     while (b < p.num_seqs) {               // 32 sequences at a time
       const int n = b + lane < p.num_seqs
-                        ? counted_tiles<kSel>(p, seq_len(p, b + lane, ignore)) * units : 0;
+                        ? counted_tiles(p, seq_len(p, b + lane, ignore)) * units : 0;
       const int in = warp_incl_sum(n, lane);
       const uint32_t past = __ballot_sync(0xffffffffu, v < base + in);
       const int hit = past ? __ffs(past) - 1 : 31;
@@ -837,25 +829,11 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   };
   // ---- this warp's run ----
   const int warps = gridDim.x * kK4Warps;
-  int per_warp = (total + warps - 1) / warps;
+  const int per_warp = (total + warps - 1) / warps;
   const int per = per_warp * kK4Warps;                     // tiles of a CTA
-  int from = static_cast<int>(min((int64_t)blockIdx.x * per, (int64_t)total));
-  int to = from + min(per, total - from);
-  int b = 0, base = 0;
-  if (whole) {                             // from and to move to the next segments' starts
-    int vb[2] = {from, to}, sb[2], sbase[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) locate(min(vb[k], total - 1), sb[k], sbase[k]);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int nt = counted_tiles<kSel>(p, seq_len(p, sb[k], ignore));
-      vb[k] = min(sbase[k] + (vb[k] - sbase[k] + nt - 1) / nt * nt, total);
-    }
-    from = vb[0];
-    to = vb[1];
-    per_warp = (to - from + kK4Warps - 1) / kK4Warps;
-  }
-  int at = from + min(warp * per_warp, to - from);
+  const int from = static_cast<int>(min((int64_t)blockIdx.x * per, (int64_t)total));
+  const int to = from + min(per, total - from);
+  int at = from + min(warp * per_warp, to - from), b = 0, base = 0;
   const int stop = at + min(per_warp, to - at);
   if (at < stop) locate(at, b, base);
   uint8_t *const ring = smem + warp * K4<D>::kRing;
@@ -869,7 +847,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   while (at < stop) {
     K4Seg sg = {};
     sg.b = b;
-    if (unit <= 0) nt = counted_tiles<kSel>(p, seq_len(p, b, ignore));
+    if (unit <= 0) nt = counted_tiles(p, seq_len(p, b, ignore));
     if (unit < 0) unit = (at - base) / nt;
     set_unit(p, unit, sg);
     const int seg0 = base + unit * nt;
@@ -878,9 +856,9 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     if (v1 > kOver) {
       K4RawQuery<D> raw;
       fetch_query<D>(p, sg, lane, raw);
-      open_segment<kSel>(p, sg, ring, lane, err);
+      open_segment<false>(p, sg, ring, lane, err);
       const int t0 = max(0, v0 - kOver), t1 = min(v1 - kOver, sg.tiles);
-      K4Stream<D, kFp16, kSel> st(p, sg, t0, max(0, t1 - t0), 1, ring, !(left & kKeep), lane);
+      K4Stream<D, kFp16, false> st(p, sg, t0, max(0, t1 - t0), 1, ring, !(left & kKeep), lane);
       st.start(err);
       K4Query<D> q;
       make_query<D, kFp16>(raw, p.scale_log2, lane, q);
@@ -921,7 +899,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   err = __reduce_or_sync(0xffffffffu, err);
   if (err && lane == 0) raise(p.status, err);
   if (lane == 0) flags[warp] = left;
-  if (tid == 0 && !whole) splits_of(p)[blockIdx.x] = K4Split{0, 0};
+  if (tid == 0) splits_of(p)[blockIdx.x] = K4Split{0, 0};
   __syncthreads();
   // ---- join the parts of segments that cross warps ----
   // A group is a segment's parts in this CTA: the last part of warp `open` (-1: the segment
@@ -1127,12 +1105,36 @@ static int sm_count(int dev) {
   return cache[dev];
 }
 
-template <typename K>
-static cudaError_t launch_big(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t s,
-                              const Kv4DecodeParams &p) {
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
-  return e != cudaSuccess ? e : launch_kv4(kernel, grid, threads, smem, 1, s, p);
+template <int D, bool kFp16, bool kSel, int kWarps>
+static cudaError_t run_segs(const Kv4DecodeParams &p, int units, cudaStream_t s) {
+  auto *kernel = kv4_seg_kernel<D, kFp16, kSel, kWarps>;
+  constexpr int smem = kWarps * K4<D>::kRing;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kv4(kernel, dim3(static_cast<unsigned>(p.num_seqs) * units), kWarps * 32, smem, 1, s,
+                    p, units);
+}
+
+// Warps to a segment: an SM holds 16, and a segment's fixed cost is that of kSegCost tiles a
+// warp, so that W warps take (all SMs' warps / 16 in flight) about
+//   max(1, segs W / (16 SMs)) * (kSegCost + most / W).
+// Measured (W = 2 / 4 / 8): 800 segments of 32 tiles 28.9 / 21.6 / 23.0 us (run kernel, whole
+// segments: 24.5), 2048 of 17 (d = 64) 15.8 / 16.8 / 26.1 us (17.6).
+constexpr int kSegCost = 4;
+constexpr int kSegTiles = 128;       // longest segments of the kernel
+static int seg_warps(int64_t segs, int64_t most, int sms) {
+  int best = 1;
+  double least = 0.;
+  for (int w = 1; w <= 16; w *= 2) {
+    const double waves = static_cast<double>(segs) * w / (16. * sms);
+    const double t = (waves > 1. ? waves : 1.) * (kSegCost + (most + w - 1) / w);
+    if (w == 1 || t < least) {
+      best = w;
+      least = t;
+    }
+  }
+  return best;
 }
 
 template <int D, bool kFp16, bool kSel>
@@ -1140,31 +1142,27 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int sms = sm_count(dev), ctas = min(sms * 2, kK4MaxCtas);   // resident at once
-  const int units = p.h_k * head_parts(p.g);
-  const int64_t segs = (int64_t)p.num_seqs * units;
+  const int sms = sm_count(dev), units = p.h_k * head_parts(p.g);
   // tiles that a segment has at most, as far as the host knows
   int64_t most = ((int64_t)p.width << p.page_log2) / kKv4Tile;
   if (p.window > 0) most = min(most, (int64_t)p.window / kKv4Tile + 2);
   if (kSel) most = min(most, (int64_t)p.topk << (p.page_log2 - 5));
-  if (segs <= ctas && (kSel || most <= 8 * kK4Warps)) {
-    // sixteen warps where every segment has an SM to itself and the tiles for them
-    const dim3 grid(units, p.num_seqs);
-    if (segs <= sms && most > kK4Warps)
-      return launch_big(kv4_seg_kernel<D, kFp16, kSel, 16>, grid, 512, 16 * K4<D>::kRing, s, p);
-    return launch_big(kv4_seg_kernel<D, kFp16, kSel, 8>, grid, 256, 8 * K4<D>::kRing, s, p);
+  if (kSel || most <= kSegTiles) {
+    switch (seg_warps((int64_t)p.num_seqs * units, most, sms)) {
+      case 1: return run_segs<D, kFp16, kSel, 1>(p, units, s);
+      case 2: return run_segs<D, kFp16, kSel, 2>(p, units, s);
+      case 4: return run_segs<D, kFp16, kSel, 4>(p, units, s);
+      case 8: return run_segs<D, kFp16, kSel, 8>(p, units, s);
+      default: return run_segs<D, kFp16, kSel, 16>(p, units, s);
+    }
   }
-  // Whole segments to a CTA leave its share up to a segment off: little from six segments of
-  // bounded length a CTA on.  Selected segments have at most 128 tiles and stay whole below
-  // that too (200 ragged sequences, 16 blocks, g = 16, 2.6 segments a CTA: 24.4 us, against
-  // 26.5 us split and merged).  Else segments are split, and the merge follows.
-  const int whole = kSel || (segs >= 6 * ctas && most <= 16 * kK4Warps);
-  auto *kernel = kv4_run_kernel<D, kFp16, kSel>;
+  const int ctas = min(sms * 2, kK4MaxCtas);               // resident at once
+  auto *kernel = kv4_run_kernel<D, kFp16>;
   constexpr int smem = K4<D>::kSmem;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_kv4(kernel, dim3(ctas), kK4Threads, smem, 1, s, p, units, whole);
-  if (e != cudaSuccess || whole) return e;
+  e = launch_kv4(kernel, dim3(ctas), kK4Threads, smem, 1, s, p, units);
+  if (e != cudaSuccess) return e;
   return launch_kv4(kv4_merge_kernel<D, kFp16>, dim3(ctas, min(p.g, kK4Heads)), kMergeThreads, 0, 1,
                     s, p, units);
 }

@@ -143,6 +143,8 @@ RAGGED = (1000, 1, 64, 0, 777, 33, 2049)
 @pytest.mark.parametrize("topk,window", [(16, 0), (0, 0), (0, 100), (5, 90), (32, 0), (1, 0), (0, 1)])
 def test_decode_matches_oracle(d, page, h_k, g, dtype, topk, window):
     _decode(RAGGED, page, h_k, g, d, dtype, 10 * d + page + g, topk, window)
+    if not topk and not window:      # a table with room for long caches: lengths from the device alone
+        _decode(RAGGED, page, h_k, g, d, dtype, 10 * d + page + g, width=300)
 
 
 @pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 257, 511, 513])
@@ -151,13 +153,29 @@ def test_decode_lengths_around_tiles(n):
     _decode((n,), 64, 1, 4, 128, "bf16", n)
     _decode((n,), 32, 2, 1, 64, "fp16", n, topk=16)
     _decode((n,), 128, 1, 3, 128, "fp16", n, window=32)
+    _decode((n, 0, n), 64, 2, 4, 128, "bf16", n, width=200)
+
+
+@pytest.mark.parametrize("b", [1, 5, 40, 170, 400])
+def test_decode_batches_of_selections(b):
+    """Batches for which a segment gets 16, 8, 4, 2 warps and one."""
+    rng = np.random.default_rng(b)
+    lens = tuple(int(x) for x in rng.integers(1, 700, b))
+    _decode(lens, 32, 4, 1, 64, "bf16", b, topk=3)
+    _decode(lens, 64, 2, 9, 64, "fp16", b, topk=12)
+    _decode(lens, 32, 8, 1, 64, "fp16", b, window=20)
 
 
 def test_decode_long_axis_and_many_sequences():
     _decode((20011,), 64, 2, 4, 128, "bf16", 5)
     _decode((9000, 1, 17000), 128, 1, 16, 64, "fp16", 6)
     rng = np.random.default_rng(7)
-    _decode(tuple(int(x) for x in rng.integers(0, 300, 700)), 32, 1, 2, 64, "bf16", 7)
+    many = tuple(int(x) for x in rng.integers(0, 300, 700))
+    _decode(many, 32, 1, 2, 64, "bf16", 7)
+    _decode(many, 32, 1, 2, 64, "bf16", 7, width=200)
+    _decode(many[:300], 64, 2, 12, 128, "fp16", 9, width=100)
+    _decode((9000, 5, 7000, 4500), 64, 2, 4, 128, "bf16", 10, window=5000)
+    _decode((9000, 5, 7000, 4500), 32, 1, 1, 64, "fp16", 11, window=4200)
     _decode(tuple(int(x) for x in rng.integers(0, 40, 900)), 32, 3, 1, 64, "bf16", 8, window=7)
 
 
@@ -430,7 +448,7 @@ def test_calls_on_two_streams_and_between_torch_kernels():
     page, h_k, g, d = 64, 2, 4, 128
     sets = []
     for seed, lens in ((61, (4000, 5, 900)), (62, (3000,) * 5)):
-        pool, table, _ = make_cache(lens, page, h_k, d, seed)
+        pool, table, _ = make_cache(lens, page, h_k, d, seed, width=80)
         gen = torch.Generator().manual_seed(seed)
         qs = torch.randn(12, len(lens), h_k * g, d, generator=gen).to(torch.bfloat16).cuda()
         sel = make_selection(lens, page, h_k, 8, seed)
