@@ -9,7 +9,7 @@
 // Tensor-core form.  Keys are the rows of m16n8k16 (mma.sync: at most 8 query heads are far
 // from the 128 rows of a tcgen05 tile), heads the columns.  A code needs no conversion:
 // masked out of its word as the low bits of an fp16 it IS the subnormal c * 2^-24 (or, at
-// bits 4-7, 16 c * 2^-24), which the tensor core multiplies exactly.
+// bits 4-7, 16 c * 2^-24; K's two bits further up), which the tensor core multiplies exactly.
 //   scores  acc_g = sum over the group's dimensions of q^ c, exact products in fp32;
 //           S = C_h (sum_g ks_g acc_g + kz_g Q_g), Q_g = sum q^ over the group, in fp32.
 //           q^ is q times a power of two per head (largest magnitude in [2^14, 2^15)), so
@@ -110,16 +110,11 @@ __device__ __forceinline__ void par_floats(uint32_t u, float (&x)[G]) {
 
 // K codes 0, 1, 4, 5 (k = 0) or 2, 3, 6, 7 of a word, in the places that the masks take.  The
 // tensor core truncates its sums relative to the largest exponent, and a subnormal's leading
-// zeros count against it: fp16's 11-bit queries, which feel that (a lone key's score was
-// 1.5e-6 off, bf16's 5.5e-7), get their codes two bits further up, for one more shift a word.
-template <bool kFp16>
-struct K4Up {
-  static constexpr int kBits = kFp16 ? 2 : 0;
-};
-template <bool kFp16>
+// zeros count against it: codes two bits further up than they lie, for one more shift a word,
+// took a lone key's score from 1.5e-6 (fp16) and 5.6e-7 (bf16) off to 2.4e-7 and 1.5e-7.
+constexpr int kUp = 2;
 __device__ __forceinline__ uint32_t code_pairs(uint32_t w, int k) {
-  if (kFp16) return k ? w >> 6 : w << 2;
-  return k ? w >> 8 : w;
+  return k ? w >> (8 - kUp) : w << kUp;
 }
 
 // The query of a segment as B operands, and its sums and scale per head of the score tile.
@@ -235,9 +230,8 @@ __device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale
     mma16816(sum[i % G], 0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u, out.f[i][2],
              out.f[i][3]);
   }
-  // a raw score counts in 2^-24 (2^-22): S = 2^(ex - 14 + 24) |scale| raw.  A scale of 0 keeps
-  // the masked scores below the others.
-  constexpr int kUp = K4Up<kFp16>::kBits;
+  // a raw score counts in 2^-22: S = 2^(ex - 14 + 22) |scale| raw.  A scale of 0 keeps the
+  // masked scores below the others.
   const float mul = fmaxf(ldexpf(fabsf(scale_log2), ex + 10 - kUp), 1e-30f);
   out.mul = Pair(__shfl_sync(0xffffffffu, mul, 8 * c), __shfl_sync(0xffffffffu, mul, 8 * c + 4));
 #pragma unroll
@@ -313,8 +307,8 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
     for (int i = 0; i < W; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        constexpr uint32_t kLow = 0x000f000fu << K4Up<kFp16>::kBits, kHigh = kLow << 4;
-        const uint32_t x = code_pairs<kFp16>(w[0][i], k), y = code_pairs<kFp16>(w[1][i], k);
+        constexpr uint32_t kLow = 0x000f000fu << kUp, kHigh = kLow << 4;
+        const uint32_t x = code_pairs(w[0][i], k), y = code_pairs(w[1][i], k);
         if (i < G && k == 0)
           mma16816_0(acc[i % G], x & kLow, y & kLow, x & kHigh, y & kHigh, q.f[i][2 * k],
                      q.f[i][2 * k + 1]);
