@@ -41,6 +41,11 @@
 // it has, about what starting one costs.  Segments inside a warp's run are written by that
 // warp; those that cross into the next warp's are joined in the CTA, and those that cross a
 // CTA's border leave partial results (at most two a CTA) for kv4_merge_kernel.
+//
+// Measured (d = 128, bf16): a tile costs 551 warp instructions and, with 16 warps on an SM,
+// 240 to 250 cycles, against 198 that its bytes take at 6.78 TB/s.  64 sequences of 8K, 16
+// selected blocks, g = 4 (37.8 MB): 12.7 us; one of 64K in full: 18.7 us; eight of them
+// (302 MB): 59.9 us, 5.05 TB/s.
 #include "kv4.cuh"
 
 namespace nsa {

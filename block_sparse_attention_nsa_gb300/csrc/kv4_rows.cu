@@ -9,7 +9,9 @@
 // three shuffles for the minimum and maximum, one 32-bit word of codes.  A warp covers four
 // groups of a token (K and V of one head at d = 128, of two at d = 64), whose code words
 // fill whole 32-byte sectors, and takes kRows consecutive tokens, whose loads it issues
-// together.
+// together.  64K tokens of 4 heads at d = 128 (172 MB, 25.4 us at the measured 6.78 TB/s):
+// append 41.0 us (4.2 TB/s, instruction issue 77 % busy before its packed steps), read 30.5 us
+// (5.6 TB/s).
 #include "kv4.cuh"
 
 namespace nsa {

