@@ -95,6 +95,15 @@ def _check(name, t, dtype, shape, dev):
                          f"{t.device}")
 
 
+_i32 = torch.int32
+
+
+def _ints(name, t, n, dev):
+    """A contiguous int32 tensor of n entries on the current device (cheaper than _check)."""
+    if t.dtype is not _i32 or t.numel() != n or t.get_device() != dev or not t.is_contiguous():
+        _check(name, t, _i32, (n,), dev)
+
+
 def _device(t):
     """The index of t's device, which has to be the current one."""
     dev = t.get_device()
@@ -117,15 +126,17 @@ def _empty(shape, dtype, dev, stream):
 def _status(t, dev):
     if t is None:
         return None
-    _check("device_status", t, torch.int32, (1,), dev)
+    _ints("device_status", t, 1, dev)
     return t.data_ptr()
 
 
 def _slot_map(slot_map, dev, stream):
+    """slot_map (or a new one of that many entries) and its length."""
     if isinstance(slot_map, int):
-        return _empty((slot_map,), torch.int32, dev, stream)
-    _check("slot_map", slot_map, torch.int32, (slot_map.numel(),), dev)
-    return slot_map
+        return _empty((slot_map,), _i32, dev, stream), slot_map
+    n = slot_map.numel()
+    _ints("slot_map", slot_map, n, dev)
+    return slot_map, n
 
 
 def page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_size: int,
@@ -138,31 +149,32 @@ def page_plan(ctx_lens, new_lens, free_pages, free_head, block_table, page_size:
     int32 [M] or its length M.  Returns slot_map (packed in request order, -1 behind the
     last token), seq_lens = ctx + new (may be ctx_lens), cu_new [B + 1] and head_out [1]
     (may be free_head)."""
-    dev, i32 = _device(block_table), torch.int32
+    dev = _device(block_table)
     b, width = block_table.shape
-    _check("block_table", block_table, i32, (b, width), dev)
-    _check("ctx_lens", ctx_lens, i32, (b,), dev)
-    _check("new_lens", new_lens, i32, (b,), dev)
-    _check("free_pages", free_pages, i32, (free_pages.numel(),), dev)
-    _check("free_head", free_head, i32, (1,), dev)
-    slot_map = _slot_map(slot_map, dev, stream)
+    free = free_pages.numel()
+    _ints("block_table", block_table, b * width, dev)
+    _ints("ctx_lens", ctx_lens, b, dev)
+    _ints("new_lens", new_lens, b, dev)
+    _ints("free_pages", free_pages, free, dev)
+    _ints("free_head", free_head, 1, dev)
+    slot_map, slots = _slot_map(slot_map, dev, stream)
     if seq_lens is None:
-        seq_lens = _empty((b,), i32, dev, stream)
+        seq_lens = _empty((b,), _i32, dev, stream)
     else:
-        _check("seq_lens", seq_lens, i32, (b,), dev)
+        _ints("seq_lens", seq_lens, b, dev)
     if cu_new is None:
-        cu_new = _empty((b + 1,), i32, dev, stream)
+        cu_new = _empty((b + 1,), _i32, dev, stream)
     else:
-        _check("cu_new", cu_new, i32, (b + 1,), dev)
+        _ints("cu_new", cu_new, b + 1, dev)
     if head_out is None:
-        head_out = _empty((1,), i32, dev, stream)
+        head_out = _empty((1,), _i32, dev, stream)
     else:
-        _check("head_out", head_out, i32, (1,), dev)
-    dims = _page_dims(b, page_size, width, num_pages, free_pages.numel(), slot_map.numel())
+        _ints("head_out", head_out, 1, dev)
     code = _lib().nsa_page_plan(
-        dims, ctx_lens.data_ptr(), new_lens.data_ptr(), free_pages.data_ptr(),
-        free_head.data_ptr(), block_table.data_ptr(), slot_map.data_ptr(), seq_lens.data_ptr(),
-        cu_new.data_ptr(), head_out.data_ptr(), _status(device_status, dev), _raw(stream, dev))
+        _page_dims(b, page_size, width, num_pages, free, slots), ctx_lens.data_ptr(),
+        new_lens.data_ptr(), free_pages.data_ptr(), free_head.data_ptr(), block_table.data_ptr(),
+        slot_map.data_ptr(), seq_lens.data_ptr(), cu_new.data_ptr(), head_out.data_ptr(),
+        None if device_status is None else _status(device_status, dev), _raw(stream, dev))
     if code:
         _fail(code, "page_plan")
     return slot_map, seq_lens, cu_new, head_out
@@ -173,20 +185,20 @@ def page_slots(block_table, start, count, page_size: int, num_pages: int, slot_m
     """Slots of cached tokens: positions start[b] ... start[b] + count[b] - 1 of each
     request, packed in request order, -1 behind the last.  slot_map int32 [M] or its length
     M.  Returns slot_map and cu int32 [B + 1], the requests' offsets in it."""
-    dev, i32 = _device(block_table), torch.int32
+    dev = _device(block_table)
     b, width = block_table.shape
-    _check("block_table", block_table, i32, (b, width), dev)
-    _check("start", start, i32, (b,), dev)
-    _check("count", count, i32, (b,), dev)
-    slot_map = _slot_map(slot_map, dev, stream)
+    _ints("block_table", block_table, b * width, dev)
+    _ints("start", start, b, dev)
+    _ints("count", count, b, dev)
+    slot_map, slots = _slot_map(slot_map, dev, stream)
     if cu is None:
-        cu = _empty((b + 1,), i32, dev, stream)
+        cu = _empty((b + 1,), _i32, dev, stream)
     else:
-        _check("cu", cu, i32, (b + 1,), dev)
-    dims = _page_dims(b, page_size, width, num_pages, 0, slot_map.numel())
-    code = _lib().nsa_page_slots(dims, block_table.data_ptr(), start.data_ptr(), count.data_ptr(),
-                                 slot_map.data_ptr(), cu.data_ptr(), _status(device_status, dev),
-                                 _raw(stream, dev))
+        _ints("cu", cu, b + 1, dev)
+    code = _lib().nsa_page_slots(
+        _page_dims(b, page_size, width, num_pages, 0, slots), block_table.data_ptr(),
+        start.data_ptr(), count.data_ptr(), slot_map.data_ptr(), cu.data_ptr(),
+        None if device_status is None else _status(device_status, dev), _raw(stream, dev))
     if code:
         _fail(code, "page_slots")
     return slot_map, cu
@@ -202,40 +214,48 @@ def kv4_pool(num_pages: int, page_size: int, h_k: int, head_dim: int, device="cu
     return torch.zeros((num_pages, h_k, size.value), dtype=torch.uint8, device=device)
 
 
-def _pool_dims(pool, head_dim, dtype, where):
-    """Kv4Dims of a pool: its page size follows from the bytes of a page."""
-    dev = _device(pool)
-    if pool.dtype is not torch.uint8 or pool.dim() != 3 or not pool.is_contiguous():
-        raise ValueError("pool: a contiguous uint8 tensor [num_pages, h_k, page_bytes] expected")
-    pages, h_k, size = pool.shape
+@functools.lru_cache(maxsize=4096)
+def _pool_layout(shape, head_dim, dtype, where):
+    """Kv4Dims of a pool's shape: its page size follows from the bytes of a page."""
+    pages, h_k, size = shape
     page_size, rest = divmod(size, head_dim + head_dim // 8)
     if rest:
         raise ValueError(f"pool: {size} bytes a page are no whole tokens of head_dim {head_dim}")
     code = _DTYPES.get(dtype)
     if code is None:
         _fail(2, f"{where}: dtype {dtype}")
-    return _kv4_dims(pages, page_size, h_k, head_dim, code), dev
+    return _kv4_dims(pages, page_size, h_k, head_dim, code)
+
+
+def _pool_dims(pool, head_dim, dtype, where):
+    dev = _device(pool)
+    shape = pool.shape
+    if pool.dtype is not torch.uint8 or len(shape) != 3 or not pool.is_contiguous():
+        raise ValueError("pool: a contiguous uint8 tensor [num_pages, h_k, page_bytes] expected")
+    return _pool_layout(shape, head_dim, dtype, where), dev
 
 
 def kv4_append(pool, k, v, slot_map, device_status=None, stream=None):
     """Quantises the rows of k and v [n, h_k, d] into the slots of slot_map int32 [n] (-1: no
     slot).  k and v may be strided views whose last dimension is contiguous.  Each slot at
     most once.  Returns pool."""
-    if k.dim() != 3 or k.shape != v.shape or k.dtype is not v.dtype:
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or shape != v.shape or dtype is not v.dtype:
         raise ValueError("k and v of one shape [n, h_k, d] and dtype expected")
-    n, h_k, d = k.shape
-    dims, dev = _pool_dims(pool, d, k.dtype, "kv4_append")
-    if h_k != pool.shape[1]:
-        raise ValueError(f"k has {h_k} heads, the pool {pool.shape[1]}")
+    n, h_k, d = shape
+    dims, dev = _pool_dims(pool, d, dtype, "kv4_append")
+    if h_k != dims.h_k:
+        raise ValueError(f"k has {h_k} heads, the pool {dims.h_k}")
     (kt, kh, ke), (vt, vh, ve) = k.stride(), v.stride()
     if ke != 1 or ve != 1 or k.get_device() != dev or v.get_device() != dev:
         raise ValueError("k and v need a contiguous last dimension, on the pool's device")
-    _check("slot_map", slot_map, torch.int32, (n,), dev)
+    _ints("slot_map", slot_map, n, dev)
     if n >> 31:
         _fail(2, "kv4_append: rows beyond 32 bits")
     code = _lib().nsa_kv4_append(dims, n, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
                                  slot_map.data_ptr(), pool.data_ptr(),
-                                 _status(device_status, dev), _raw(stream, dev))
+                                 None if device_status is None else _status(device_status, dev),
+                                 _raw(stream, dev))
     if code:
         _fail(code, "kv4_append")
     return pool
@@ -250,10 +270,10 @@ def kv4_read(pool, slot_map, head_dim: int, k=None, v=None, dtype: torch.dtype =
         dtype = k.dtype
     dims, dev = _pool_dims(pool, head_dim, dtype, "kv4_read")
     n = slot_map.numel()
-    _check("slot_map", slot_map, torch.int32, (n,), dev)
+    _ints("slot_map", slot_map, n, dev)
     if n >> 31:
         _fail(2, "kv4_read: rows beyond 32 bits")
-    shape = (n, pool.shape[1], head_dim)
+    shape = (n, dims.h_k, head_dim)
     if k is None:
         k = _empty(shape, dtype, dev, stream)
     else:
@@ -263,7 +283,9 @@ def kv4_read(pool, slot_map, head_dim: int, k=None, v=None, dtype: torch.dtype =
     else:
         _check("v", v, dtype, shape, dev)
     code = _lib().nsa_kv4_read(dims, n, pool.data_ptr(), slot_map.data_ptr(), k.data_ptr(),
-                               v.data_ptr(), _status(device_status, dev), _raw(stream, dev))
+                               v.data_ptr(),
+                               None if device_status is None else _status(device_status, dev),
+                               _raw(stream, dev))
     if code:
         _fail(code, "kv4_read")
     return k, v
@@ -293,27 +315,29 @@ def kv4_decode(q, pool, block_table, seq_lens, scale: float, sel_idx=None, windo
     it is None, within the last `window` tokens where that is > 0.  Returns out [B, h_q, d]
     and lse float32 [h_q, B].  workspace: uint8, at least kv4_decode_workspace_size bytes;
     allocated here when None and needed."""
-    if q.dim() != 3:
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
         raise ValueError("q [B, h_q, d] expected")
-    b, h_q, d = q.shape
-    dtype, i32 = q.dtype, torch.int32
+    b, h_q, d = shape
     dims, dev = _pool_dims(pool, d, dtype, "kv4_decode")
     h_k = dims.h_k
-    width = block_table.shape[-1]
     if not q.is_contiguous() or q.get_device() != dev:
-        _check("q", q, dtype, q.shape, dev)
-    _check("block_table", block_table, i32, (b, width), dev)
-    _check("seq_lens", seq_lens, i32, (b,), dev)
+        _check("q", q, dtype, shape, dev)
+    rows, width = block_table.shape
+    if rows != b:
+        raise ValueError(f"block_table of {rows} rows for {b} sequences")
+    _ints("block_table", block_table, b * width, dev)
+    _ints("seq_lens", seq_lens, b, dev)
     topk, sel = 0, None
     if sel_idx is not None:
         topk, sel = sel_idx.shape[-1], sel_idx.data_ptr()
-        _check("sel_idx", sel_idx, i32, (h_k, b, topk), dev)
+        _check("sel_idx", sel_idx, _i32, (h_k, b, topk), dev)
         if topk == 0:
             raise ValueError("sel_idx: at least one slot expected")
     if out is None:
-        out = _empty((b, h_q, d), dtype, dev, stream)
+        out = _empty(shape, dtype, dev, stream)
     else:
-        _check("out", out, dtype, (b, h_q, d), dev)
+        _check("out", out, dtype, shape, dev)
     if lse is None:
         lse = _empty((h_q, b), torch.float32, dev, stream)
     else:
@@ -323,7 +347,9 @@ def kv4_decode(q, pool, block_table, seq_lens, scale: float, sel_idx=None, windo
         if need:
             workspace = _empty((need,), torch.uint8, dev, stream)
     else:
-        _check("workspace", workspace, torch.uint8, workspace.shape, dev)
+        if (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()
+                or workspace.get_device() != dev):
+            _check("workspace", workspace, torch.uint8, workspace.shape, dev)
     if not -1 < window < 0x7fffffff:      # beyond every length, or negative (refused below)
         window = 0x7fffffff if window > 0 else -1
     if width >> 31 or b >> 31:
@@ -332,7 +358,8 @@ def kv4_decode(q, pool, block_table, seq_lens, scale: float, sel_idx=None, windo
     code = _lib().nsa_kv4_decode(
         dims, b, h_q, width, topk, window, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(),
         seq_lens.data_ptr(), sel, scale, out.data_ptr(), lse.data_ptr(),
-        _status(device_status, dev), ws, ws_bytes, _raw(stream, dev))
+        None if device_status is None else _status(device_status, dev), ws, ws_bytes,
+        _raw(stream, dev))
     if code:
         _fail(code, "kv4_decode")
     return out, lse
