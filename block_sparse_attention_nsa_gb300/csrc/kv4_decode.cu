@@ -34,8 +34,9 @@
 // scales and zeros into fp32 for all, in the place of the K codes.
 //
 // Work.  A segment is a (sequence, KV head, up to 8 of its query heads).  kv4_seg_kernel:
-// one CTA of 1 to 16 warps a segment, the warps taking its tiles in turn; for segments whose
-// tiles have a bound that the host knows (a selection, a window, a short table).
+// one CTA of 1 to 16 warps a segment, or a cluster of up to 8 CTAs where few segments would
+// leave SMs idle, the warps taking its tiles in turn; for segments whose tiles have a bound
+// that the host knows (a selection, a window, a short table).
 // kv4_run_kernel: every warp takes an equal run of the batch's tiles in segment order,
 // whatever the lengths, which only the device knows; a segment counts kOver tiles more than
 // it has, about what starting one costs.  Segments inside a warp's run are written by that
@@ -682,23 +683,50 @@ __device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int h
     p.lse[(int64_t)hq * p.num_seqs + b] = any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-// One CTA of kWarps per segment.
-template <int D, bool kFp16, bool kSel, int kWarps>
-__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4DecodeParams p, int units) {
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// kWarps warps per segment, in one CTA; kCluster: in each of a cluster's `parts` CTAs.
+template <int D, bool kFp16, bool kSel, int kWarps, bool kCluster>
+__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
+    kv4_seg_kernel(Kv4DecodeParams p, int units, int parts) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float4 ml[kWarps][kK4Heads / 2];          // m, l of two heads
   __shared__ float lsum[kWarps][kK4Heads];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   K4Seg sg = {};
-  sg.b = static_cast<int>(blockIdx.x / static_cast<unsigned>(units));
-  set_unit(p, static_cast<int>(blockIdx.x) - sg.b * units, sg);
+  const unsigned seg = kCluster ? blockIdx.x / parts : blockIdx.x;
+  const int rank = kCluster ? blockIdx.x - seg * parts : 0, step = kCluster ? parts * kWarps : kWarps;
+  sg.b = static_cast<int>(seg / static_cast<unsigned>(units));
+  set_unit(p, static_cast<int>(seg) - sg.b * units, sg);
   int32_t err = 0;
   after_previous();
   K4RawQuery<D> raw;
   fetch_query<D>(p, sg, lane, raw);
   open_segment<kSel>(p, sg, smem + warp * K4<D>::kRing, lane, err);
-  K4Stream<D, kFp16, kSel> st(p, sg, warp, max(0, (sg.tiles - warp + kWarps - 1) / kWarps), kWarps,
-                       smem + warp * K4<D>::kRing, true, lane);
+  const int first = rank * kWarps + warp;
+  K4Stream<D, kFp16, kSel> st(p, sg, first, max(0, (sg.tiles - first + step - 1) / step), step,
+                              smem + warp * K4<D>::kRing, true, lane);
   st.start(err);
   K4Query<D> q;
   make_query<D, kFp16>(raw, p.scale_log2, lane, q);
@@ -708,6 +736,10 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4De
   if (tid == 0) seq_len(p, sg.b, err);
   err = __reduce_or_sync(0xffffffffu, err);
   if (err && lane == 0) raise(p.status, err);
+  __shared__ float2 part_ml[kCluster ? kK4Heads : 1];
+  // a CTA's own sums, where no area lies: the last stage of the first warp's ring
+  float *const part = reinterpret_cast<float *>(smem + K4<D>::kKept);
+  static_assert(kK4Heads * D * 4 <= Kv4Tile<D>::kBytes, "a stage holds a CTA's sums");
 
   // the warps agree on each head's maximum, scale their sums to it, and add up
   const int r = lane >> 2, c = lane & 3;
@@ -746,7 +778,46 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) kv4_seg_kernel(Kv4De
       for (int w = 0; w < kWarps; ++w)
         M = fmaxf(M, head & 1 ? ml[w][head >> 1].z : ml[w][head >> 1].x);
     }
-    write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, M, l);
+    if (!kCluster) {
+      write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, M, l);
+    } else {
+      *reinterpret_cast<float4 *>(part + head * D + dim) = x;
+      if (dim == 0) part_ml[head] = make_float2(M, l);
+    }
+  }
+  if constexpr (kCluster) {
+    // the CTAs' sums, from their shared memory, each CTA adding up a share of the outputs
+    cluster_sync();
+    const uint32_t mine = smem_u32(part), mine_ml = smem_u32(part_ml);
+    for (int i = rank + parts * tid; i < sg.g * (D / 4); i += parts * kWarps * 32) {
+      const int head = i / (D / 4), dim = 4 * (i % (D / 4));
+      float2 v[8];
+      float4 o[8];
+      float M = -INFINITY, l = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        v[k] = make_float2(-INFINITY, 0.f);
+        if (k < parts) {
+          v[k] = ld_cluster2(in_cta(mine_ml + head * 8, k));
+          o[k] = ld_cluster4(in_cta(mine + (head * D + dim) * 4, k));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) M = fmaxf(M, v[k].x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (v[k].y == 0.f) continue;                   // a CTA without keys, or none
+        const float w = ex2_approx(v[k].x - M);
+        l = fmaf(w, v[k].y, l);
+        x.x = fmaf(w, o[k].x, x.x);
+        x.y = fmaf(w, o[k].y, x.y);
+        x.z = fmaf(w, o[k].z, x.z);
+        x.w = fmaf(w, o[k].w, x.w);
+      }
+      write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, M, l);
+    }
+    cluster_sync();                                    // no CTA leaves while it is read
   }
 }
 
@@ -1104,15 +1175,15 @@ static int sm_count(int dev) {
   return cache[dev];
 }
 
-template <int D, bool kFp16, bool kSel, int kWarps>
-static cudaError_t run_segs(const Kv4DecodeParams &p, int units, cudaStream_t s) {
-  auto *kernel = kv4_seg_kernel<D, kFp16, kSel, kWarps>;
+template <int D, bool kFp16, bool kSel, int kWarps, bool kCluster = false>
+static cudaError_t run_segs(const Kv4DecodeParams &p, int units, int parts, cudaStream_t s) {
+  auto *kernel = kv4_seg_kernel<D, kFp16, kSel, kWarps, kCluster>;
   constexpr int smem = kWarps * K4<D>::kRing;
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_kv4(kernel, dim3(static_cast<unsigned>(p.num_seqs) * units), kWarps * 32, smem, 1, s,
-                    p, units);
+  return launch_kv4(kernel, dim3(static_cast<unsigned>(p.num_seqs) * units * parts), kWarps * 32,
+                    smem, parts, s, p, units, parts);
 }
 
 // Warps to a segment: an SM holds 16, and a segment's fixed cost is that of kSegCost tiles a
@@ -1121,7 +1192,6 @@ static cudaError_t run_segs(const Kv4DecodeParams &p, int units, cudaStream_t s)
 // Measured (W = 2 / 4 / 8): 800 segments of 32 tiles 28.9 / 21.6 / 23.0 us (run kernel, whole
 // segments: 24.5), 2048 of 17 (d = 64) 15.8 / 16.8 / 26.1 us (17.6).
 constexpr int kSegCost = 4;
-constexpr int kSegTiles = 128;       // longest segments of the kernel
 static int seg_warps(int64_t segs, int64_t most, int sms) {
   int best = 1;
   double least = 0.;
@@ -1135,6 +1205,12 @@ static int seg_warps(int64_t segs, int64_t most, int sms) {
   }
   return best;
 }
+// CTAs of eight warps to a segment: as many as idle SMs and its tiles allow.
+static int seg_ctas(int64_t segs, int64_t most, int sms) {
+  int c = 1;
+  while (c < 8 && segs * (2 * c) <= sms && most >= 8 * (2 * c)) c *= 2;
+  return c;
+}
 
 template <int D, bool kFp16, bool kSel>
 static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
@@ -1146,13 +1222,16 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   int64_t most = ((int64_t)p.width << p.page_log2) / kKv4Tile;
   if (p.window > 0) most = min(most, (int64_t)p.window / kKv4Tile + 2);
   if (kSel) most = min(most, (int64_t)p.topk << (p.page_log2 - 5));
-  if (kSel || most <= kSegTiles) {
-    switch (seg_warps((int64_t)p.num_seqs * units, most, sms)) {
-      case 1: return run_segs<D, kFp16, kSel, 1>(p, units, s);
-      case 2: return run_segs<D, kFp16, kSel, 2>(p, units, s);
-      case 4: return run_segs<D, kFp16, kSel, 4>(p, units, s);
-      case 8: return run_segs<D, kFp16, kSel, 8>(p, units, s);
-      default: return run_segs<D, kFp16, kSel, 16>(p, units, s);
+  const int64_t segs = (int64_t)p.num_seqs * units;
+  const int cluster = seg_ctas(segs, most, sms);
+  if (kSel || most <= 128) {
+    if (cluster > 1) return run_segs<D, kFp16, kSel, 8, true>(p, units, cluster, s);
+    switch (seg_warps(segs, most, sms)) {
+      case 1: return run_segs<D, kFp16, kSel, 1>(p, units, 1, s);
+      case 2: return run_segs<D, kFp16, kSel, 2>(p, units, 1, s);
+      case 4: return run_segs<D, kFp16, kSel, 4>(p, units, 1, s);
+      case 8: return run_segs<D, kFp16, kSel, 8>(p, units, 1, s);
+      default: return run_segs<D, kFp16, kSel, 16>(p, units, 1, s);
     }
   }
   const int ctas = min(sms * 2, kK4MaxCtas);               // resident at once
