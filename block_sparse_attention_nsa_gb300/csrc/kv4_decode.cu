@@ -1205,11 +1205,21 @@ static int seg_warps(int64_t segs, int64_t most, int sms) {
   }
   return best;
 }
-// CTAs of eight warps to a segment: as many as idle SMs and its tiles allow.
+// CTAs of eight warps to a segment: as many as the SMs hold and its tiles allow.
 static int seg_ctas(int64_t segs, int64_t most, int sms) {
   int c = 1;
-  while (c < 8 && segs * (2 * c) <= sms && most >= 8 * (2 * c)) c *= 2;
+  while (c < 8 && segs * (2 * c) <= 2 * sms && most >= 8 * (2 * c)) c *= 2;
   return c;
+}
+// Segments of at most `most` tiles in CTAs of their own, or equal runs?  An SM takes about
+// 0.125 us a tile; the first cost 4.2 us besides, at the bound's length on every SM, the
+// second 8.9 (prefix, partial results, merge) at the true lengths.  Measured, g = 4, d = 128,
+// segments / runs: 1 x 4096 tokens 6.5 / 8.8 us, 8 x 4096 9.5 / 13.3, 64 x 2048 20.0 / 27.7,
+// 64 x 4096 33.5 / 38.3; ragged up to that length 8 x 4096 8.0 / 9.2, 64 x 2048 14.2 / 13.8,
+// 64 x 4096 23.6 / 16.0.
+static bool seg_better(int64_t segs, int64_t most, int ctas, int sms) {
+  const int64_t on_sm = (segs * ctas + sms - 1) / sms;
+  return 4.2 + 0.125 * most / ctas * on_sm < 8.9 + 0.125 * segs * most / sms;
 }
 
 template <int D, bool kFp16, bool kSel>
@@ -1224,7 +1234,7 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   if (kSel) most = min(most, (int64_t)p.topk << (p.page_log2 - 5));
   const int64_t segs = (int64_t)p.num_seqs * units;
   const int cluster = seg_ctas(segs, most, sms);
-  if (kSel || most <= 128) {
+  if (kSel || seg_better(segs, most, cluster, sms)) {
     if (cluster > 1) return run_segs<D, kFp16, kSel, 8, true>(p, units, cluster, s);
     switch (seg_warps(segs, most, sms)) {
       case 1: return run_segs<D, kFp16, kSel, 1>(p, units, 1, s);
