@@ -6,11 +6,10 @@
 // HBM bounds both directions: 4 d bytes of 16-bit K and V against d + d / 8 stored.
 //
 // Eight lanes own a group, eight dimensions each: one 16-byte access of the 16-bit row,
-// three shuffles for the minimum and maximum, one 32-bit word of codes.  A warp covers four
-// groups of a token (K and V of one head at d = 128, of two at d = 64), whose code words
-// fill whole 32-byte sectors, and takes kRows consecutive tokens, whose loads it issues
-// together.  64K tokens of 4 heads at d = 128 (172 MB, 25.4 us at the measured 6.78 TB/s):
-// append 41.0 us (4.2 TB/s, instruction issue 77 % busy before its packed steps), read 30.5 us
+// three shuffles for the minimum and maximum, one 32-bit word of codes.  A warp covers K and V
+// of one head, of one token at a time (two at d = 64), so that code words fill whole 32-byte
+// sectors, and takes kRows consecutive tokens, whose loads it issues together.  64K tokens of 4 heads at d = 128 (172 MB, 25.4 us at the measured 6.78 TB/s):
+// append 40.0 us (4.3 TB/s, instruction issue 77 % busy before its packed steps), read 30.8 us
 // (5.6 TB/s).
 #include "kv4.cuh"
 
@@ -20,32 +19,34 @@ constexpr int kRowThreads = 256;
 constexpr int kRows = 4;
 constexpr float kHalfMax = 65504.f;
 
-// A lane's place: its warp's first token, and its group of every token.
+// Tokens of a warp: kRows in turn, at d = 64 two such runs side by side.
+template <int D>
+constexpr int kWarpTokens = kRows * 128 / D;
+
+// A lane's place: its first token, and its group of every token.
 struct RowPlace {
   int t0, h, kv, gi, j;
-  bool live;
 };
 template <int D>
 __device__ __forceinline__ RowPlace row_place(const Kv4RowParams &p) {
-  constexpr int kG = Kv4Tile<D>::kG, kHeads = 2 / kG;      // heads of a warp
+  constexpr int kG = Kv4Tile<D>::kG;
   const int lane = threadIdx.x & 31, part = lane >> 3;
-  const unsigned units = (p.h_k + kHeads - 1) / kHeads;    // warps to a token
   const uint64_t task = (uint64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  uint32_t tb, u;
+  uint32_t tb, h;                                          // a warp has one head
   if (task >> 32) {
-    tb = static_cast<uint32_t>(task / units);
-    u = static_cast<uint32_t>(task - (uint64_t)tb * units);
+    tb = static_cast<uint32_t>(task / p.h_k);
+    h = static_cast<uint32_t>(task - (uint64_t)tb * p.h_k);
   } else {
-    tb = static_cast<uint32_t>(task) / units;
-    u = static_cast<uint32_t>(task) - tb * units;
+    tb = static_cast<uint32_t>(task) / static_cast<uint32_t>(p.h_k);
+    h = static_cast<uint32_t>(task) - tb * p.h_k;
   }
   RowPlace r;
-  r.t0 = static_cast<int>(min((uint64_t)tb * kRows, (uint64_t)p.n));
-  r.h = kG == 2 ? u : 2 * u + (part >> 1);
+  const uint64_t t0 = (uint64_t)tb * kWarpTokens<D> + (kG == 2 ? 0 : (part >> 1) * kRows);
+  r.t0 = static_cast<int>(min(t0, (uint64_t)p.n));
+  r.h = h;
   r.kv = kG == 2 ? part >> 1 : part & 1;
   r.gi = kG == 2 ? part & 1 : 0;
   r.j = lane & 7;
-  r.live = r.h < p.h_k;
   return r;
 }
 
@@ -60,7 +61,7 @@ __device__ __forceinline__ void load_slots(const Kv4RowParams &p, int t0, int (&
       slot[k] = -1;
     }
   }
-  if (bad && (threadIdx.x & 31) == 0) raise(p.status, NSA_DEVERR_BAD_INDEX);
+  if (bad && (threadIdx.x & 15) == 0) raise(p.status, NSA_DEVERR_BAD_INDEX);
 }
 
 // Offset of the tile that holds a slot of head h (tiles are counted in 32 bits: 2^32 of them
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowParams p)
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
     raw[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (r.live && slot[k] >= 0)
+    if (slot[k] >= 0)
       raw[k] = __ldcs(reinterpret_cast<const uint4 *>(src + k * ts));
   }
   // the groups' smallest (negated) and largest values, packed
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowParams p)
                         : __float2half_rn(quotient(__fsub_rn(hi, my_zero), 15.f, 1.f / 15.f));
   const float my_scale = __half2float(sh), my_inv = __frcp_rn(my_scale);
   const uint32_t both = __half_as_ushort(zh) | static_cast<uint32_t>(__half_as_ushort(sh)) << 16;
-  const bool stored = r.live && my_slot >= 0;
+  const bool stored = my_slot >= 0;
   // no code can leave 0 ... 15 where zero is not above the smallest value and the largest
   // is not 15.5 steps above it
   const bool held = __any_sync(0xffffffffu, stored && !(my_zero <= low &&
@@ -202,7 +203,7 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(Kv4RowParams p)
     uint32_t word = held ? code_word<kFp16, true>(w4, f.x, f.y, inv)
                          : code_word<kFp16, false>(w4, f.x, f.y, inv);
     if (!(f.y > 0.f)) word = 0;
-    if (r.live && slot[k] >= 0)
+    if (slot[k] >= 0)
       *reinterpret_cast<uint32_t *>(p.pool + slot_tile<D>(p, r.h, slot[k]) + r.kv * T::kV +
                                     (slot[k] & (kKv4Tile - 1)) * T::kRow + (r.j * T::kG + r.gi) * 4) =
           word;
@@ -216,7 +217,6 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(Kv4RowParams p) {
   int slot[kRows];
   after_previous();
   load_slots(p, r.t0, slot);
-  if (!r.live) return;
   uint32_t word[kRows];
   __half scale[kRows], zero[kRows];
 #pragma unroll
@@ -259,8 +259,8 @@ template <int D>
 static cudaError_t run_rows(bool append, bool fp16, const Kv4RowParams &p, cudaStream_t s) {
   auto *kernel = append ? (fp16 ? kv4_append_kernel<D, true> : kv4_append_kernel<D, false>)
                         : (fp16 ? kv4_read_kernel<D, true> : kv4_read_kernel<D, false>);
-  const int64_t heads = 2 / Kv4Tile<D>::kG, warps = kRowThreads / 32;
-  const int64_t tasks = ((int64_t)p.n + kRows - 1) / kRows * ((p.h_k + heads - 1) / heads);
+  const int64_t warps = kRowThreads / 32;
+  const int64_t tasks = ((int64_t)p.n + kWarpTokens<D> - 1) / kWarpTokens<D> * p.h_k;
   return launch_kv4(kernel, dim3(static_cast<unsigned>((tasks + warps - 1) / warps)), kRowThreads, 0,
                     1, s, p);
 }

@@ -33,7 +33,7 @@ def _rows(n, h, d, dtype, seed):
 
 @pytest.mark.parametrize("n,h,d,page,dtype", [(1, 1, 64, 32, "bf16"), (33, 3, 128, 64, "fp16"),
                                               (257, 2, 64, 128, "fp16"), (130, 4, 128, 32, "bf16"),
-                                              (5, 5, 128, 128, "bf16")])
+                                              (5, 5, 128, 128, "bf16"), (43, 5, 64, 32, "bf16")])
 def test_append_and_read(n, h, d, page, dtype):
     import block_sparse_attention_nsa_gb300 as nsa
     dt = DTYPES[dtype]
