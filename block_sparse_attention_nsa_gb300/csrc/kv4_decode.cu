@@ -34,7 +34,7 @@
 // scales and zeros into fp32 for all, in the place of the K codes.
 //
 // Work.  A segment is a (sequence, KV head, up to 8 of its query heads).  kv4_seg_kernel:
-// one CTA of 1 to 16 warps a segment, or a cluster of up to 8 CTAs where few segments would
+// one CTA of 1 to 8 warps a segment, or a cluster of up to 8 CTAs where few segments would
 // leave SMs idle, the warps taking its tiles in turn; for segments whose tiles have a bound
 // that the host knows (a selection, a window, a short table).
 // kv4_run_kernel: every warp takes an equal run of the batch's tiles in segment order,
@@ -43,16 +43,19 @@
 // warp; those that cross into the next warp's are joined in the CTA, and those that cross a
 // CTA's border leave partial results (at most two a CTA) for kv4_merge_kernel.
 //
-// Measured (d = 128, bf16): a tile costs 551 warp instructions and, with 16 warps on an SM,
-// 240 to 250 cycles, against 198 that its bytes take at 6.78 TB/s.  64 sequences of 8K, 16
-// selected blocks, g = 4 (37.8 MB): 12.7 us; one of 64K in full: 18.7 us; eight of them
-// (302 MB): 59.9 us, 5.05 TB/s.
+// Measured (d = 128, bf16): a tile costs about 550 warp instructions and, with 12 warps on an
+// SM, 220 to 230 cycles, against 198 that its bytes take at 6.78 TB/s.  64 sequences of 8K, 16
+// selected blocks, g = 4 (37.8 MB): 11.7 us; one of 64K in full: 17.1 us; eight of them
+// (302 MB): 57.2 us, 5.28 TB/s.
 #include "kv4.cuh"
 
 namespace nsa {
 
-constexpr int kK4Warps = 8;
-constexpr int kK4Threads = kK4Warps * 32;
+// Warps that an SM holds.  At d = 128 twelve: a warp then has 168 registers instead of 128, and
+// the compiler's order of a tile's loads and products gains more than the four warps lose (64 x 8K,
+// 16 blocks: 12.9 -> 11.7 us; 8 x 64K in full: 59.8 -> 57.0).  At d = 64 126 registers do.
+template <int D>
+constexpr int kSmWarps = D == 128 ? 12 : 16;
 constexpr int kK4Heads = 8;          // query heads of a segment at most
 constexpr int kStages = 3;           // tiles of a warp's ring
 constexpr int kOver = 4;             // tiles that a segment's start counts as
@@ -71,7 +74,7 @@ struct K4 {
   // A warp's results go to the ring's start; a first part that has to stay while the warp
   // goes on takes the last stage.
   static constexpr int kKept = (kStages - 1) * T::kBytes;
-  static constexpr int kSmem = kK4Warps * kRing;
+  static constexpr int kRunWarps = kSmWarps<D> / 2, kRunThreads = kRunWarps * 32;   // two CTAs an SM
   static_assert(kK4Heads / 2 * kHeadPair * 4 <= T::kBytes, "a stage holds an area");
 };
 
@@ -708,7 +711,7 @@ __device__ __forceinline__ void cluster_sync() {
 
 // kWarps warps per segment, in one CTA; kCluster: in each of a cluster's `parts` CTAs.
 template <int D, bool kFp16, bool kSel, int kWarps, bool kCluster>
-__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps)
+__global__ void __launch_bounds__(kWarps * 32, kSmWarps<D> / kWarps)
     kv4_seg_kernel(Kv4DecodeParams p, int units, int parts) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float4 ml[kWarps][kK4Heads / 2];          // m, l of two heads
@@ -851,17 +854,19 @@ __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
 
 // Equal runs of the batch's counted tiles.
 template <int D, bool kFp16>
-__global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams p, int units) {
+__global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
+    kv4_run_kernel(Kv4DecodeParams p, int units) {
+  constexpr int kWarps = K4<D>::kRunWarps, kThreads = K4<D>::kRunThreads;
   extern __shared__ __align__(128) uint8_t smem[];
   // of a warp's parts ([0]: first, [1]: last): m, l of two heads; factors, l times them
-  __shared__ float4 ml[2][kK4Warps][kK4Heads / 2];
-  __shared__ float2 fac[2][kK4Warps][kK4Heads], top[kK4Warps + 1][kK4Heads / 2];
-  __shared__ int pre[kK4Threads], wsum[kK4Warps], flags[kK4Warps];
-  __shared__ int4 groups[kK4Warps + 1];    // of the group that warp i - 1 opens: sequence, unit, end
+  __shared__ float4 ml[2][kWarps][kK4Heads / 2];
+  __shared__ float2 fac[2][kWarps][kK4Heads], top[kWarps + 1][kK4Heads / 2];
+  __shared__ int pre[kThreads], wsum[kWarps], flags[kWarps];
+  __shared__ int4 groups[kWarps + 1];    // of the group that warp i - 1 opens: sequence, unit, end
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = lane & 3;
   after_previous();
   // ---- the batch's tiles ----
-  const int per_thread = (p.num_seqs + kK4Threads - 1) / kK4Threads;
+  const int per_thread = (p.num_seqs + kThreads - 1) / kThreads;
   const int b0 = min(tid * per_thread, p.num_seqs), b1 = min(b0 + per_thread, p.num_seqs);
   int32_t err = 0, ignore = 0;
   int mine = 0;
@@ -873,12 +878,12 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   __syncthreads();
   int total = 0;
 #pragma unroll
-  for (int w = 0; w < kK4Warps; ++w) total += wsum[w];
+  for (int w = 0; w < kWarps; ++w) total += wsum[w];
   // the sequence that holds tile v (< total), and that sequence's first tile
   auto locate = [&](int v, int &b, int &base) {
     int w = 0, off = 0;                    // the warp whose sequences hold it, the tiles before
 #pragma unroll
-    for (int k = 0; k + 1 < kK4Warps; ++k)
+    for (int k = 0; k + 1 < kWarps; ++k)
       if (v >= off + wsum[w]) off += wsum[w++];
     const int x = off + pre[w * 32 + lane];
     const uint32_t before = __ballot_sync(0xffffffffu, x <= v);
@@ -898,9 +903,9 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
     }
   };
   // ---- this warp's run ----
-  const int warps = gridDim.x * kK4Warps;
+  const int warps = gridDim.x * kWarps;
   const int per_warp = (total + warps - 1) / warps;
-  const int per = per_warp * kK4Warps;                     // tiles of a CTA
+  const int per = per_warp * kWarps;                     // tiles of a CTA
   const int from = static_cast<int>(min((int64_t)blockIdx.x * per, (int64_t)total));
   const int to = from + min(per, total - from);
   int at = from + min(warp * per_warp, to - from), b = 0, base = 0;
@@ -975,7 +980,7 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   // A group is a segment's parts in this CTA: the last part of warp `open` (-1: the segment
   // began in an earlier CTA) and the first parts of the warps behind it, up to the next
   // warp with a last part.
-  const int fl = lane < kK4Warps ? flags[lane] : 0;
+  const int fl = lane < kWarps ? flags[lane] : 0;
   const uint32_t firsts = __ballot_sync(0xffffffffu, fl & kFirst);
   const uint32_t lasts = __ballot_sync(0xffffffffu, fl & kLast);
   const uint32_t ons = __ballot_sync(0xffffffffu, fl & kOn);
@@ -1018,11 +1023,11 @@ __global__ void __launch_bounds__(kK4Threads, 2) kv4_run_kernel(Kv4DecodeParams 
   __syncthreads();
   // Group i is the one that warp i - 1 opens.  A small one is a single warp's work.
   const bool small = min(p.g, kK4Heads) * (D / 4) <= 64;
-  const int th = small ? lane : tid, nth = small ? 32 : kK4Threads;
+  const int th = small ? lane : tid, nth = small ? 32 : kThreads;
 #pragma unroll 1
   for (uint32_t todo = lasts << 1 | (members(-1) ? 1u : 0u); todo; todo &= todo - 1) {
     const int gr = __ffs(todo) - 1, open = gr - 1;
-    if (small && (gr & (kK4Warps - 1)) != warp) continue;
+    if (small && gr % kWarps != warp) continue;
     const uint32_t in = members(open), all = in | (open >= 0 ? 1u << open : 0u);
     const bool on = in ? ons >> (31 - __clz(in)) & 1 : true;
     const int4 who = groups[gr];
@@ -1186,26 +1191,34 @@ static cudaError_t run_segs(const Kv4DecodeParams &p, int units, int parts, cuda
                     smem, parts, s, p, units, parts);
 }
 
-// Warps to a segment: an SM holds 16, and a segment's fixed cost is that of kSegCost tiles a
-// warp, so that W warps take (all SMs' warps / 16 in flight) about
-//   max(1, segs W / (16 SMs)) * (kSegCost + most / W).
-// Measured (W = 2 / 4 / 8): 800 segments of 32 tiles 28.9 / 21.6 / 23.0 us (run kernel, whole
-// segments: 24.5), 2048 of 17 (d = 64) 15.8 / 16.8 / 26.1 us (17.6).
-constexpr int kSegCost = 4;
+// Warps to a segment: an SM holds `room` warps, and a segment's fixed cost is that of one to two
+// tiles a warp, so that W warps take about waves * (1.5 + tiles / W), rounded up.  `waves` lies
+// between segments / room in the GPU, which ragged lengths come near, and its next whole number,
+// which equal lengths take.  More warps where two are equal: then fewer CTAs fit an SM, and they
+// spread evenly.  Over 77 measured batches (160 to 2432 segments of 6 to 34 tiles, equal and
+// ragged) the choice takes 3 % longer than the best W on average and 19 % at most; d = 128, W =
+// 1 / 2 / 3 / 4 / 6: 256 segments of 32 tiles 23.0 / 19.3 / 17.1 / 14.5 / 11.8 us, 512 of 32 33.6 /
+// 24.1 / 18.8 / 23.6 / 22.3, 800 ragged to 32 37.7 / 25.8 / 22.0 / 19.6 / 22.9, 1216 of 8 15.4 /
+// 17.2 / 16.9 / 18.7 / 23.0.
+template <int D>
 static int seg_warps(int64_t segs, int64_t most, int sms) {
+  constexpr int kRoom = kSmWarps<D>;
   int best = 1;
   double least = 0.;
-  for (int w = 1; w <= 16; w *= 2) {
-    const double waves = static_cast<double>(segs) * w / (16. * sms);
-    const double t = (waves > 1. ? waves : 1.) * (kSegCost + (most + w - 1) / w);
-    if (w == 1 || t < least) {
+  for (int w = 1; w <= kRoom / 2; ++w) {
+    if (kRoom % w) continue;
+    const int64_t slots = (int64_t)sms * (kRoom / w);
+    const double part = static_cast<double>(segs) / static_cast<double>(slots);
+    const double waves = 0.75 * (part > 1. ? part : 1.) + 0.25 * ((segs + slots - 1) / slots);
+    const double t = waves * (1.5 + (most + w - 1) / w);
+    if (w == 1 || t <= least) {
       best = w;
       least = t;
     }
   }
   return best;
 }
-// CTAs of eight warps to a segment: as many as the SMs hold and its tiles allow.
+// CTAs (of eight warps, or of half an SM's) to a segment: as many as the SMs hold and its tiles allow.
 static int seg_ctas(int64_t segs, int64_t most, int sms) {
   int c = 1;
   while (c < 8 && segs * (2 * c) <= 2 * sms && most >= 8 * (2 * c)) c *= 2;
@@ -1214,9 +1227,9 @@ static int seg_ctas(int64_t segs, int64_t most, int sms) {
 // Segments of at most `most` tiles in CTAs of their own, or equal runs?  An SM takes about
 // 0.125 us a tile; the first cost 4.2 us besides, at the bound's length on every SM, the
 // second 8.9 (prefix, partial results, merge) at the true lengths.  Measured, g = 4, d = 128,
-// segments / runs: 1 x 4096 tokens 6.5 / 8.8 us, 8 x 4096 9.5 / 13.3, 64 x 2048 20.0 / 27.7,
-// 64 x 4096 33.5 / 38.3; ragged up to that length 8 x 4096 8.0 / 9.2, 64 x 2048 14.2 / 13.8,
-// 64 x 4096 23.6 / 16.0.
+// segments / runs: 1 x 4096 tokens 6.3 / 8.3 us, 1 x 8192 8.3 / 9.6, 16 x 4096 13.3 / 17.2; with
+// 16 warps an SM 64 x 4096 33.5 / 38.3; ragged up to that length 8 x 4096 8.0 / 9.2, 64 x 2048
+// 14.2 / 13.8, 64 x 4096 23.6 / 16.0.
 static bool seg_better(int64_t segs, int64_t most, int ctas, int sms) {
   const int64_t on_sm = (segs * ctas + sms - 1) / sms;
   return 4.2 + 0.125 * most / ctas * on_sm < 8.9 + 0.125 * segs * most / sms;
@@ -1235,21 +1248,29 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   const int64_t segs = (int64_t)p.num_seqs * units;
   const int cluster = seg_ctas(segs, most, sms);
   if (kSel || seg_better(segs, most, cluster, sms)) {
-    if (cluster > 1) return run_segs<D, kFp16, kSel, 8, true>(p, units, cluster, s);
-    switch (seg_warps(segs, most, sms)) {
+    constexpr int kHalf = kSmWarps<D> / 2;
+    if (segs * cluster <= sms) {                           // an SM for each CTA
+      if (cluster == 1) return run_segs<D, kFp16, kSel, 8>(p, units, 1, s);
+      return run_segs<D, kFp16, kSel, 8, true>(p, units, cluster, s);
+    }
+    if (cluster > 1) return run_segs<D, kFp16, kSel, kHalf, true>(p, units, cluster, s);
+    const int warps = seg_warps<D>(segs, most, sms);
+    if constexpr (D == 128) {
+      if (warps == 3) return run_segs<D, kFp16, kSel, 3>(p, units, 1, s);
+    }
+    switch (warps) {
       case 1: return run_segs<D, kFp16, kSel, 1>(p, units, 1, s);
       case 2: return run_segs<D, kFp16, kSel, 2>(p, units, 1, s);
       case 4: return run_segs<D, kFp16, kSel, 4>(p, units, 1, s);
-      case 8: return run_segs<D, kFp16, kSel, 8>(p, units, 1, s);
-      default: return run_segs<D, kFp16, kSel, 16>(p, units, 1, s);
+      default: return run_segs<D, kFp16, kSel, kHalf>(p, units, 1, s);
     }
   }
   const int ctas = min(sms * 2, kK4MaxCtas);               // resident at once
   auto *kernel = kv4_run_kernel<D, kFp16>;
-  constexpr int smem = K4<D>::kSmem;
+  constexpr int threads = K4<D>::kRunThreads, smem = K4<D>::kRunWarps * K4<D>::kRing;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_kv4(kernel, dim3(ctas), kK4Threads, smem, 1, s, p, units);
+  e = launch_kv4(kernel, dim3(ctas), threads, smem, 1, s, p, units);
   if (e != cudaSuccess) return e;
   return launch_kv4(kv4_merge_kernel<D, kFp16>, dim3(ctas, min(p.g, kK4Heads)), kMergeThreads, 0, 1,
                     s, p, units);
