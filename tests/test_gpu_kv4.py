@@ -166,6 +166,17 @@ def test_decode_batches_of_selections(b):
     _decode(lens, 32, 8, 1, 64, "fp16", b, window=20)
 
 
+@pytest.mark.parametrize("b", [2, 19, 36, 50, 70, 160, 300])
+def test_decode_batches_of_selections_at_128(b):
+    """Eight KV heads: segments that share an SM by one, two, three, four, six and twelve, and
+    clusters of one and of two CTAs an SM; a second call with an empty sequence in the middle."""
+    rng = np.random.default_rng(b + 1000)
+    lens = [int(x) for x in rng.integers(1, 600, b)]
+    _decode(tuple(lens), 32, 8, 2, 128, "bf16", b, topk=16)
+    lens[b // 2] = 0
+    _decode(tuple(lens), 32, 8, 1, 128, "fp16", b, topk=4)
+
+
 def test_decode_long_axis_and_many_sequences():
     _decode((20011,), 64, 2, 4, 128, "bf16", 5)
     _decode((9000, 1, 17000), 128, 1, 16, 64, "fp16", 6)
