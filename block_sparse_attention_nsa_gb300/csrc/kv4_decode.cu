@@ -15,13 +15,12 @@
 //           q^ is q times a power of two per head (largest magnitude in [2^14, 2^15)), so
 //           that fp16 holds bf16's and fp16's values: it loses only what is 2^-38 of the
 //           largest.
-//   output  O_g = sum_i P'_i c_i - sum_i P'_i m_i + sum_i p_i (z_i + m_i s_i), P' = p s rounded to
-//           fp16 (the one rounding: 2^-11 of a weight, on codes counted from m),
-//           P' scaled by a power of two that follows the largest s seen.  m is 8, the codes'
-//           middle, where the output is bf16, and where it is fp16, whose rounding is as
-//           small as P''s, the code nearest to a value of 0, so that the error of a term is
-//           2^-11 of the value itself.  The second term takes one more product with a row of
-//           ones (middles), the third stays in fp32.
+//   output  O_g = sum_i P'_i (c_i - m) + sum_i p_i (z_i + m s_i), P' = p s scaled by a power of
+//           two that follows the largest s seen; the second sum is in fp32.  For bf16 P' is
+//           rounded to fp16 (2^-11 of a weight, on codes counted from their middle m = 8, by
+//           one more product with a row of ones): far below the output's own rounding.  For
+//           fp16, whose rounding is as small, P' is the sum of two fp16 numbers (2^-22) and
+//           m = 0: twice the products, no row of ones.
 // The softmax runs online: the reference maximum of a head is raised (and the sums
 // rescaled) only when a score exceeds it by 2 in the exponent, which one vote per tile
 // finds, so most tiles need no shuffles.
@@ -43,10 +42,10 @@
 // warp; those that cross into the next warp's are joined in the CTA, and those that cross a
 // CTA's border leave partial results (at most two a CTA) for kv4_merge_kernel.
 //
-// Measured (d = 128, bf16): a tile costs about 550 warp instructions and, with 12 warps on an
-// SM, 220 to 230 cycles, against 198 that its bytes take at 6.78 TB/s.  64 sequences of 8K, 16
-// selected blocks, g = 4 (37.8 MB): 11.7 us; one of 64K in full: 17.1 us; eight of them
-// (302 MB): 57.2 us, 5.28 TB/s.
+// Measured (d = 128, bf16): a tile costs about 530 warp instructions, its start and join
+// included, and, with 12 warps on an SM, 230 cycles, against 198 that its bytes take at 6.78
+// TB/s.  64 sequences of 8K, 16 selected blocks, g = 4 (37.8 MB): 12.0 us; one of 64K in full:
+// 17.4 us; eight of them (302 MB): 58.3 us, 5.18 TB/s.
 #include "kv4.cuh"
 
 namespace nsa {
@@ -117,10 +116,14 @@ __device__ __forceinline__ void par_floats(uint32_t u, float (&x)[G]) {
   if constexpr (G == 2) x[1] = f.y;
 }
 
-// K codes 0, 1, 4, 5 (k = 0) or 2, 3, 6, 7 of a word, in the places that the masks take.  The
-// tensor core truncates its sums relative to the largest exponent, and a subnormal's leading
-// zeros count against it: codes two bits further up than they lie, for one more shift a word,
-// took a lone key's score from 1.5e-6 (fp16) and 5.6e-7 (bf16) off to 2.4e-7 and 1.5e-7.
+// Codes 0, 1, 4, 5 (k = 0) or 2, 3, 6, 7 of a word of K (of V: the low or the high byte of both
+// halves), in the places that the masks take.  The tensor core truncates its sums relative to the
+// largest exponent, and a subnormal's leading zeros count against it: codes two bits further up
+// than they lie, for one more shift a word, took a lone key's score from 1.5e-6 (fp16) and 5.6e-7
+// (bf16) off to 2.4e-7 and 1.5e-7.  V's sums are all truncated the same way, so that it adds up
+// where a long cache's values cancel: fp16 outputs over 64K tokens were 4.6e-4 off, now 2.1e-4
+// (their own rounding: 1.9e-4), with two bits and P' in two parts, for 2 % of the time; codes at
+// the top of the subnormals (2.0e-4) cost 4 % more.
 constexpr int kUp = 2;
 __device__ __forceinline__ uint32_t code_pairs(uint32_t w, int k) {
   return k ? w >> (8 - kUp) : w << kUp;
@@ -141,8 +144,8 @@ struct K4RawQuery {
 template <int D>
 struct K4State {
   float o[K4<D>::kG][4][4];      // dims 64 gi + 8 r + 2 e (+1: 16 times), heads 2c, 2c + 1
-  float ps[K4<D>::kG][4];        // sum of P' (fp16: of P' times the key's middle)
-  Pair oz[K4<D>::kG];            // this lane's share of sum p (z + middle * s), of both heads
+  float ps[K4<D>::kG][4];        // sum of P' (bf16)
+  Pair oz[K4<D>::kG];            // this lane's share of sum p (z + m s), of both heads
   Pair minus_m, l;               // reference maximum, negated; l: this lane's share
   float thr[2];                  // raw score above which m is raised
   float vmax, rinv;              // largest V scale allowed for, kPScale / it
@@ -295,6 +298,7 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
   constexpr int G = K4<D>::kG, W = K4<D>::kW;
   const int r = lane >> 2, c = lane & 3;
   const bool ragged = key0 < lo || key0 + 32 > len;
+  constexpr uint32_t kLow = 0x000f000fu << kUp, kHigh = kLow << 4;
   // ---- raw scores: rows r and r + 8 of both halves, heads 2c and 2c + 1 ----
   float s[2][4];
 #pragma unroll
@@ -316,7 +320,6 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
     for (int i = 0; i < W; ++i)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        constexpr uint32_t kLow = 0x000f000fu << kUp, kHigh = kLow << 4;
         const uint32_t x = code_pairs(w[0][i], k), y = code_pairs(w[1][i], k);
         if (i < G && k == 0)
           mma16816_0(acc[i % G], x & kLow, y & kLow, x & kHigh, y & kHigh, q.f[i][2 * k],
@@ -405,29 +408,19 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) a.oz[gi] = a.oz[gi] * al;
   }
-  // over the K codes, which all have read (the vote): s / reference, z + middle * s, and for fp16
-  // the middles
-  uint8_t *const vpar = st, *const vmid = st + 512;
-  float mid[G];
-#pragma unroll
-  for (int gi = 0; gi < G; ++gi) {
-    mid[gi] = 8.f;
-    if (kFp16) {
-      const __half m = __float2half_rn(
-          vs[gi] > 0.f ? fminf(fmaxf(__fdividef(-vz[gi], vs[gi]), 0.f), 15.f) : 0.f);
-      reinterpret_cast<__half *>(vmid)[gi * 32 + lane] = m;
-      mid[gi] = __half2float(m);
-    }
-  }
+  // over the K codes, which all have read (the vote): s / reference, z + m s
+  uint8_t *const vpar = st;
+  constexpr float kMiddle = kFp16 ? 0.f : 8.f;
   if constexpr (G == 2)
     reinterpret_cast<float4 *>(vpar)[lane] =
-        make_float4(vs[0] * a.rinv, vs[1] * a.rinv, fmaf(mid[0], vs[0], vz[0]),
-                    fmaf(mid[1], vs[1], vz[1]));
+        make_float4(vs[0] * a.rinv, vs[1] * a.rinv, fmaf(kMiddle, vs[0], vz[0]),
+                    fmaf(kMiddle, vs[1], vz[1]));
   else
-    reinterpret_cast<float2 *>(vpar)[lane] = make_float2(vs[0] * a.rinv, fmaf(mid[0], vs[0], vz[0]));
+    reinterpret_cast<float2 *>(vpar)[lane] = make_float2(vs[0] * a.rinv, fmaf(kMiddle, vs[0], vz[0]));
   __syncwarp();              // V's scales and zeros are in place
   // ---- weights ----
   uint32_t pb[G][2][2];      // B operands: [group][half][k rows 0-7, 8-15]
+  uint32_t pl[G][2][2];      // what they leave of P' (fp16)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 e = fma(Pair(s[i >> 1][(i & 1) * 2], s[i >> 1][(i & 1) * 2 + 1]), q.mul,
@@ -446,7 +439,12 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
     for (int gi = 0; gi < G; ++gi) {
       a.oz[gi] = fma(p, Pair(vc[gi], vc[gi]), a.oz[gi]);
       const float2 w = (p * Pair(vsr[gi], vsr[gi])).get();
-      pb[gi][i >> 1][i & 1] = transpose8x8(pack2<true>(w.x, w.y));
+      const uint32_t hi = pack2<true>(w.x, w.y);
+      pb[gi][i >> 1][i & 1] = transpose8x8(hi);
+      if (kFp16) {
+        const float2 h = unpack2<true>(hi);
+        pl[gi][i >> 1][i & 1] = transpose8x8(pack2<true>(w.x - h.x, w.y - h.y));
+      }
     }
   }
   // ---- output: rows are dimensions, k the keys ----
@@ -469,19 +467,16 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
       for (int e = 0; e < 4; ++e) {
         // dims 2e, 2e + 1 of the word: byte e of the four keys' words
         const uint32_t sel = e < 2 ? 0x5410u : 0x7632u;
-        const uint32_t x = __byte_perm(w[0][gi], w[1][gi], sel) >> (8 * (e & 1));
-        const uint32_t y = __byte_perm(w[2][gi], w[3][gi], sel) >> (8 * (e & 1));
-        mma16816(a.o[gi][e], x & 0x000f000fu, x & 0x00f000f0u, y & 0x000f000fu, y & 0x00f000f0u,
-                 pb[gi][half][0], pb[gi][half][1]);
+        const uint32_t x = code_pairs(__byte_perm(w[0][gi], w[1][gi], sel), e & 1);
+        const uint32_t y = code_pairs(__byte_perm(w[2][gi], w[3][gi], sel), e & 1);
+        mma16816(a.o[gi][e], x & kLow, x & kHigh, y & kLow, y & kHigh, pb[gi][half][0],
+                 pb[gi][half][1]);
+        if (kFp16)
+          mma16816(a.o[gi][e], x & kLow, x & kHigh, y & kLow, y & kHigh, pl[gi][half][0],
+                 pl[gi][half][1]);
       }
-      // bf16: P' summed by ones; fp16: weighted by the middles, of keys 2c, 2c + 1 and + 8
-      uint32_t m0 = 0x3c003c00u, m1 = 0x3c003c00u;
-      if (kFp16) {
-        const uint32_t *m = reinterpret_cast<const uint32_t *>(vmid + gi * 64 + half * 32);
-        m0 = m[c];
-        m1 = m[c + 4];
-      }
-      mma16816(a.ps[gi], m0, m0, m1, m1, pb[gi][half][0], pb[gi][half][1]);
+      constexpr uint32_t kOnes = 0x3c003c00u;
+      if (!kFp16) mma16816(a.ps[gi], kOnes, kOnes, kOnes, kOnes, pb[gi][half][0], pb[gi][half][1]);
     }
   }
 }
@@ -660,11 +655,11 @@ __device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D
   const float back = a.rinv > 0.f ? __fdiv_rn(1.f, a.rinv) : 0.f;   // a power of two
 #pragma unroll
   for (int hd = 0; hd < 2; ++hd) {
-    const float f = hd ? f1 : f0, fb = f * back, o1 = fb * 16777216.f, o16 = fb * 1048576.f;
+    const float f = hd ? f1 : f0, fb = f * back, o1 = fb * (16777216.f / (1 << kUp)), o16 = o1 * 0.0625f;
     float *dst = area + c * K4<D>::kHeadPair + hd * D + 8 * r;
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
-      const float base = fmaf(kFp16 ? -fb : -8.f * fb, a.ps[gi][hd], f * sums.oz[hd][gi]);
+      const float z = f * sums.oz[hd][gi], base = kFp16 ? z : fmaf(-8.f * fb, a.ps[gi][hd], z);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<float2 *>(dst + gi * 64 + 2 * e) = make_float2(

@@ -49,10 +49,13 @@ def check_decode(out, lse, ref, dtype):
     scores   each is a sum of d products in fp32, off by at most d 2^-24 of the sum of their
              magnitudes (`big`), and the exponential and logarithm by 2^-20;
     lse      the scores' bound and fp32's own rounding of lse and its sums;
-    out      half a step of the output type; weights times the step of V rounded to fp16:
-             2^-11 of p * step times a code counted from 8 (at most 8 steps) where the output
-             is bf16, from the code nearest to a value of 0 (at most the value) where it is
-             fp16; twice the scores' bound on every weight, and 2^-18 for the fp32 sums."""
+    out      half a step of the output type; where it is bf16, weights times the step of V
+             rounded to fp16: 2^-11 of p * step times a code counted from 8 (at most 8 steps);
+             where it is fp16, those weights in two parts (2^-22) and sums of 16 products that
+             are cut below 2^-24 of the largest exponent, a code's up to 8 leading zeros
+             counted in: 17 * 2^-16 of the largest p * step, 2^-15 of its 8 steps, and less
+             than four times that with the sums so far; twice the scores' bound on every
+             weight, and 2^-18 for the fp32 sums."""
     r_out, r_lse, big, pv, ps = ref
     d = r_out.shape[-1]
     got, gl = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
@@ -64,7 +67,7 @@ def check_decode(out, lse, ref, dtype):
     assert (off <= tol).all(), f"lse off by {(off / tol).max():.2f} of its bound"
     half = torch.finfo(dtype).eps / 2
     tiny = 2.0 ** -25 if dtype is torch.float16 else 0.0
-    term = pv if dtype is torch.float16 else ps
+    term = ps * (2.0 ** -2 if dtype is torch.float16 else 1.0)
     tol = half * np.abs(r_out) + tiny + 2.0 ** -11 * term + (2 * ds[..., None] + 2.0 ** -18) * (pv + ps)
     tol[~fin.T] = 0
     off = np.abs(got - r_out)

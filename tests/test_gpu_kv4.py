@@ -190,6 +190,20 @@ def test_decode_long_axis_and_many_sequences():
     _decode(tuple(int(x) for x in rng.integers(0, 40, 900)), 32, 3, 1, 64, "bf16", 8, window=7)
 
 
+@pytest.mark.parametrize("d,page", [(64, 128), (128, 64)])
+def test_decode_long_fp16_loses_little(d, page):
+    """Over a long cache the values cancel, so that an error of one sign in every sum shows: the
+    kernel may add at most half of what the output's own rounding to fp16 costs."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    lens = (60011, 30002)
+    pool, table, _ = make_cache(lens, page, 1, d, 77)
+    q = torch.randn(2, 2, d, generator=torch.Generator().manual_seed(78)).half()
+    out, _ = nsa.kv4_decode(q.cuda(), _dev(pool), _dev(table), _dev(np.int32(lens)), d ** -0.5)
+    ref = kv4.attend(q.double().numpy(), pool, table, lens, page, d ** -0.5, None, 0)[0]
+    rounding = np.linalg.norm(ref.astype(np.float16) - ref)
+    assert np.linalg.norm(out.double().cpu().numpy() - ref) <= 1.5 * rounding
+
+
 def test_decode_spread_of_scores_and_magnitudes():
     # a peaked softmax, a negative scale, and tokens whose K and V differ by 2^12
     _decode(RAGGED, 64, 2, 4, 128, "bf16", 21, scale=2.0)
