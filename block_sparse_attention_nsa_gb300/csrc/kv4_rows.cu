@@ -8,9 +8,9 @@
 // Eight lanes own a group, eight dimensions each: one 16-byte access of the 16-bit row,
 // three shuffles for the minimum and maximum, one 32-bit word of codes.  A warp covers K and V
 // of one head, of one token at a time (two at d = 64), so that code words fill whole 32-byte
-// sectors, and takes kRows consecutive tokens, whose loads it issues together.  64K tokens of 4 heads at d = 128 (172 MB, 25.4 us at the measured 6.78 TB/s):
-// append 40.0 us (4.3 TB/s, instruction issue 77 % busy before its packed steps), read 30.8 us
-// (5.6 TB/s).
+// sectors, and takes kRows consecutive tokens, whose loads it issues together.  64K tokens of 4
+// heads at d = 128 (172 MB, 25.4 us at the measured 6.78 TB/s): append 40.0 us (4.3 TB/s, 76 % of
+// the issue slots busy), read 30.8 us (5.6 TB/s, 77 %).
 #include "kv4.cuh"
 
 namespace nsa {
