@@ -19,8 +19,11 @@
 //           two that follows the largest s seen; the second sum is in fp32.  For bf16 P' is
 //           rounded to fp16 (2^-11 of a weight, on codes counted from their middle m = 8, by
 //           one more product with a row of ones): far below the output's own rounding.  For
-//           fp16, whose rounding is as small, P' is the sum of two fp16 numbers (2^-22) and
-//           m = 0: twice the products, no row of ones.
+//           fp16, whose rounding is as small, P' is the sum of two fp16 numbers (2^-22).
+//           There m is 0 over a few tiles; over more the sums would grow so far above what
+//           is left of them that their truncation showed (64K keys: 7.5e-4 of the output,
+//           2.1e-4 being its rounding; now 2.1e-4), and 8 sum P'_i is taken off after every
+//           tile, in fp32, for 5 to 7 % of the time.
 // The softmax runs online: the reference maximum of a head is raised (and the sums
 // rescaled) only when a score exceeds it by 2 in the exponent, which one vote per tile
 // finds, so most tiles need no shuffles.
@@ -60,6 +63,8 @@ constexpr int kStages = 3;           // tiles of a warp's ring
 constexpr int kOver = 4;             // tiles that a segment's start counts as
 constexpr int kK4MaxCtas = 320;      // CTAs of the run kernel at most
 constexpr float kSlack = 2.f;        // scores may exceed the reference maximum by this much
+constexpr float kMiddle = 8.f;       // of the codes
+constexpr int kFewTiles = 12, kFewKeys = 2048;  // of a warp, of a segment: fp16 sums need no centre
 constexpr float kPScale = 8192.f;    // P' <= 2^kSlack * kPScale < 65504
 constexpr float kMasked = -3e38f;    // raw score of a key that does not count
 
@@ -121,9 +126,9 @@ __device__ __forceinline__ void par_floats(uint32_t u, float (&x)[G]) {
 // largest exponent, and a subnormal's leading zeros count against it: codes two bits further up
 // than they lie, for one more shift a word, took a lone key's score from 1.5e-6 (fp16) and 5.6e-7
 // (bf16) off to 2.4e-7 and 1.5e-7.  V's sums are all truncated the same way, so that it adds up
-// where a long cache's values cancel: fp16 outputs over 64K tokens were 4.6e-4 off, now 2.1e-4
-// (their own rounding: 1.9e-4), with two bits and P' in two parts, for 2 % of the time; codes at
-// the top of the subnormals (2.0e-4) cost 4 % more.
+// where a long cache's values cancel: with weights as exact as here fp16 outputs over 64K tokens
+// were 4.4e-4 off, with the two bits 1.1e-4; codes at the top of the subnormals cost 4 % of the
+// time and gave little more.
 constexpr int kUp = 2;
 __device__ __forceinline__ uint32_t code_pairs(uint32_t w, int k) {
   return k ? w >> (8 - kUp) : w << kUp;
@@ -293,12 +298,13 @@ __device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *tile, i
 // One tile: keys key0 ... key0 + 31, of which those in [lo, len) count.
 template <int D, bool kFp16>
 __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int len, int lane, int vget,
-                                            const K4Query<D> &q, K4State<D> &a) {
+                                            const K4Query<D> &q, K4State<D> &a, bool centre) {
   using T = Kv4Tile<D>;
   constexpr int G = K4<D>::kG, W = K4<D>::kW;
-  const int r = lane >> 2, c = lane & 3;
+  const int r = lane >> 2;
   const bool ragged = key0 < lo || key0 + 32 > len;
   constexpr uint32_t kLow = 0x000f000fu << kUp, kHigh = kLow << 4;
+  constexpr uint32_t kOnes = 0x3c003c00u;
   // ---- raw scores: rows r and r + 8 of both halves, heads 2c and 2c + 1 ----
   float s[2][4];
 #pragma unroll
@@ -410,17 +416,18 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
   }
   // over the K codes, which all have read (the vote): s / reference, z + m s
   uint8_t *const vpar = st;
-  constexpr float kMiddle = kFp16 ? 0.f : 8.f;
+  const float middle = !kFp16 || centre ? kMiddle : 0.f;
+  const float unm = middle * -a.vmax * (1.f / kPScale);   // takes it off what hi leaves of P'
   if constexpr (G == 2)
     reinterpret_cast<float4 *>(vpar)[lane] =
-        make_float4(vs[0] * a.rinv, vs[1] * a.rinv, fmaf(kMiddle, vs[0], vz[0]),
-                    fmaf(kMiddle, vs[1], vz[1]));
+        make_float4(vs[0] * a.rinv, vs[1] * a.rinv, fmaf(middle, vs[0], vz[0]),
+                    fmaf(middle, vs[1], vz[1]));
   else
-    reinterpret_cast<float2 *>(vpar)[lane] = make_float2(vs[0] * a.rinv, fmaf(kMiddle, vs[0], vz[0]));
+    reinterpret_cast<float2 *>(vpar)[lane] = make_float2(vs[0] * a.rinv, fmaf(middle, vs[0], vz[0]));
   __syncwarp();              // V's scales and zeros are in place
   // ---- weights ----
   uint32_t pb[G][2][2];      // B operands: [group][half][k rows 0-7, 8-15]
-  uint32_t pl[G][2][2];      // what they leave of P' (fp16)
+  uint32_t pl[G][2][2];      // what hi leaves of P' (fp16)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 e = fma(Pair(s[i >> 1][(i & 1) * 2], s[i >> 1][(i & 1) * 2 + 1]), q.mul,
@@ -443,7 +450,9 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
       pb[gi][i >> 1][i & 1] = transpose8x8(hi);
       if (kFp16) {
         const float2 h = unpack2<true>(hi);
-        pl[gi][i >> 1][i & 1] = transpose8x8(pack2<true>(w.x - h.x, w.y - h.y));
+        const float2 rest = make_float2(w.x - h.x, w.y - h.y);
+        pl[gi][i >> 1][i & 1] = transpose8x8(pack2<true>(rest.x, rest.y));
+        a.oz[gi] = fma(Pair(rest.x, rest.y), Pair(unm, unm), a.oz[gi]);
       }
     }
   }
@@ -473,10 +482,28 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
                  pb[gi][half][1]);
         if (kFp16)
           mma16816(a.o[gi][e], x & kLow, x & kHigh, y & kLow, y & kHigh, pl[gi][half][0],
-                 pl[gi][half][1]);
+                   pl[gi][half][1]);
       }
-      constexpr uint32_t kOnes = 0x3c003c00u;
       if (!kFp16) mma16816(a.ps[gi], kOnes, kOnes, kOnes, kOnes, pb[gi][half][0], pb[gi][half][1]);
+    }
+  }
+  if (kFp16 && centre) {
+#pragma unroll
+    for (int gi = 0; gi < G; ++gi) {
+      float t[4];              // the tile's sum of P', heads 2c and 2c + 1 (twice)
+      mma16816_0(t, kOnes, kOnes, kOnes, kOnes, pb[gi][0][0], pb[gi][0][1]);
+      mma16816(t, kOnes, kOnes, kOnes, kOnes, pb[gi][1][0], pb[gi][1][1]);
+      constexpr float kUnit = -kMiddle / (16777216.f / (1 << kUp));
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int row = 0; row < 2; ++row) {
+          const float unit = row ? 16.f * kUnit : kUnit;
+          float *o = a.o[gi][e] + 2 * row;
+          const float2 x = fma(Pair(t[0], t[1]), Pair(unit, unit), Pair(o[0], o[1])).get();
+          o[0] = x.x;
+          o[1] = x.y;
+        }
     }
   }
 }
@@ -598,6 +625,7 @@ struct K4Stream {
   }
   __device__ __forceinline__ void run(const K4Query<D> &q, K4State<D> &a, int32_t &err) {
     static_assert(kStages == 3, "two tiles ahead, or one beside a kept part");
+    const bool centre = kFp16 && (count > kFewTiles || sg.tiles > kFewKeys / 32);
     for (int n = 0; n < count; ++n) {
       if (full) {
         keys[2] = issue(n + 2, err);
@@ -607,7 +635,7 @@ struct K4Stream {
         cp_async_wait_group<1>();
       }
       __syncwarp();
-      if (keys[0] >= 0) attend_tile<D, kFp16>(ring + get, keys[0], sg.lo, sg.len, lane, at.vget, q, a);
+      if (keys[0] >= 0) attend_tile<D, kFp16>(ring + get, keys[0], sg.lo, sg.len, lane, at.vget, q, a, centre);
       __syncwarp();                   // the stage is filled again in the next turn
       next(get);
       keys[0] = keys[1];
@@ -659,7 +687,7 @@ __device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D
     float *dst = area + c * K4<D>::kHeadPair + hd * D + 8 * r;
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
-      const float z = f * sums.oz[hd][gi], base = kFp16 ? z : fmaf(-8.f * fb, a.ps[gi][hd], z);
+      const float z = f * sums.oz[hd][gi], base = kFp16 ? z : fmaf(-kMiddle * fb, a.ps[gi][hd], z);
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         *reinterpret_cast<float2 *>(dst + gi * 64 + 2 * e) = make_float2(

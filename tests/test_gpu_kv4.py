@@ -204,6 +204,24 @@ def test_decode_long_fp16_loses_little(d, page):
     assert np.linalg.norm(out.double().cpu().numpy() - ref) <= 1.5 * rounding
 
 
+def test_decode_fp16_many_tiles_a_warp():
+    """As above, where one warp adds up a whole sequence: 250 sequences that share their pages,
+    8 KV heads, all 32 blocks selected (128 tiles of 32 keys)."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    n, d, page, h_k, b = 4096, 64, 128, 8, 250
+    pool, table, _ = make_cache((n,), page, h_k, d, 79)
+    table = np.repeat(table, b, 0)
+    lens = np.full(b, n, np.int32)
+    sel = np.broadcast_to(np.arange(n // page, dtype=np.int32), (h_k, b, n // page)).copy()
+    q = torch.randn(b, h_k, d, generator=torch.Generator().manual_seed(80)).half()
+    out, _ = nsa.kv4_decode(q.cuda(), _dev(pool), _dev(table), _dev(lens), d ** -0.5,
+                            sel_idx=_dev(sel))
+    ref = kv4.attend(q[:3].double().numpy(), pool, table[:3], lens[:3], page, d ** -0.5,
+                     sel[:, :3], 0)[0]
+    rounding = np.linalg.norm(ref.astype(np.float16) - ref)
+    assert np.linalg.norm(out[:3].double().cpu().numpy() - ref) <= 1.5 * rounding
+
+
 def test_decode_spread_of_scores_and_magnitudes():
     # a peaked softmax, a negative scale, and tokens whose K and V differ by 2^12
     _decode(RAGGED, 64, 2, 4, 128, "bf16", 21, scale=2.0)
