@@ -17,13 +17,20 @@
 //           largest.
 //   output  O_g = sum_i P'_i (c_i - m) + sum_i p_i (z_i + m s_i), P' = p s scaled by a power of
 //           two that follows the largest s seen; the second sum is in fp32.  For bf16 P' is
-//           rounded to fp16 (2^-11 of a weight, on codes counted from their middle m = 8, by
-//           one more product with a row of ones): far below the output's own rounding.  For
-//           fp16, whose rounding is as small, P' is the sum of two fp16 numbers (2^-22).
-//           There m is 0 over a few tiles; over more the sums would grow so far above what
-//           is left of them that their truncation showed (64K keys: 7.5e-4 of the output,
-//           2.1e-4 being its rounding; now 2.1e-4), and 8 sum P'_i is taken off after every
-//           tile, in fp32, for 5 to 7 % of the time.
+//           rounded to fp16 (2^-11 of a weight, on codes counted from their middle m = 7.5, by
+//           one more product with a row of ones): below the output's own rounding, to which
+//           it adds 0.4 % (64 x 8K selected: 1.4e-4 of the output beside 1.66e-3); a second part
+//           took 9 % more time there (12.0 -> 13.1 us).  For fp16, whose rounding is as small, P'
+//           is the sum of two fp16 numbers (2^-22), and m is 0 over a few tiles.
+//           The tensor core cuts its sums towards zero, by up to 2^-24 of the largest exponent in
+//           each product: an error of one sign that grows with a run, while the values that it
+//           is measured by cancel.  Where it would show (K4Stream::run has the rule) a tile's
+//           sums start at -m sum P', so that they end near what is left of them, and are added
+//           to the warp's in fp32, rounded to nearest.  Over 288 / 1026 / 4098 tiles a warp the
+//           outputs are then 1.54 / 1.64 / 1.46e-3 (bf16; 2.1 / 15 / 5.1e-3 without) and 1.92 /
+//           2.13 / 2.12e-4 (fp16; 8 sum P' taken off after each tile: 2.1 / 8.3 / 17e-4) from
+//           exact, their own rounding being 1.4 to 1.6e-3 and 1.8 to 2.1e-4, for 2 to 7 % of
+//           bf16's time.
 // The softmax runs online: the reference maximum of a head is raised (and the sums
 // rescaled) only when a score exceeds it by 2 in the exponent, which one vote per tile
 // finds, so most tiles need no shuffles.
@@ -63,8 +70,11 @@ constexpr int kStages = 3;           // tiles of a warp's ring
 constexpr int kOver = 4;             // tiles that a segment's start counts as
 constexpr int kK4MaxCtas = 320;      // CTAs of the run kernel at most
 constexpr float kSlack = 2.f;        // scores may exceed the reference maximum by this much
-constexpr float kMiddle = 8.f;       // of the codes
-constexpr int kFewTiles = 12, kFewKeys = 2048;  // of a warp, of a segment: fp16 sums need no centre
+constexpr float kMiddle = 7.5f;      // of the codes
+// Where sums need no centre.  What they lose grows with a warp's tiles and, next to what is left of
+// the values, with the square root of the segment's keys: 2.6e-8 of a bf16 output times tiles *
+// sqrt(keys), so that the bound below stands for 2e-4, an eighth of its rounding.
+constexpr int kFewTiles = 12, kFewKeys = 2048, kFewSquare = 1 << 21;
 constexpr float kPScale = 8192.f;    // P' <= 2^kSlack * kPScale < 65504
 constexpr float kMasked = -3e38f;    // raw score of a key that does not count
 
@@ -95,7 +105,17 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The same on a zero accumulator.
+// The same on accumulators of other registers, and on zeros.
+__device__ __forceinline__ void mma16816_c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                           uint32_t a3, uint32_t b0, uint32_t b1, Pair c01,
+                                           Pair c23) {
+  const float2 x = c01.get(), y = c23.get();
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %12, %13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(x.x), "f"(x.y), "f"(y.x),
+        "f"(y.y));
+}
 __device__ __forceinline__ void mma16816_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                            uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -295,6 +315,30 @@ __device__ __forceinline__ void copy_tile(uint32_t stage, const uint8_t *tile, i
   if (D == 128 || lane < 16) cp_async16(kdst + T::kPar, src + T::kPar, 16u);
 }
 
+// The V words of a half tile: a lane's of keys 2c, 2c + 1, 2c + 8 and 2c + 9.
+template <int D>
+__device__ __forceinline__ void v_words(const uint8_t *st, int vget, int half,
+                                        uint32_t (&w)[4][K4<D>::kG]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t *at = st + Kv4Tile<D>::kV + (half * 16 + 4 * i) * Kv4Tile<D>::kRow + vget;
+    if constexpr (K4<D>::kG == 2) {
+      const uint2 x = *reinterpret_cast<const uint2 *>(at);
+      w[i][0] = x.x; w[i][1] = x.y;
+    } else {
+      w[i][0] = *reinterpret_cast<const uint32_t *>(at);
+    }
+  }
+}
+// Dimensions 2e, 2e + 1 of the words of group gi: byte e of the four keys, in the masks' places.
+template <int G>
+__device__ __forceinline__ void v_codes(const uint32_t (&w)[4][G], int gi, int e, uint32_t &x,
+                                        uint32_t &y) {
+  const uint32_t sel = e < 2 ? 0x5410u : 0x7632u;
+  x = code_pairs(__byte_perm(w[0][gi], w[1][gi], sel), e & 1);
+  y = code_pairs(__byte_perm(w[2][gi], w[3][gi], sel), e & 1);
+}
+
 // One tile: keys key0 ... key0 + 31, of which those in [lo, len) count.
 template <int D, bool kFp16>
 __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int len, int lane, int vget,
@@ -457,27 +501,56 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
     }
   }
   // ---- output: rows are dimensions, k the keys ----
+  if (centre) {
+    // The tile's sums start at -m sum P' and are added to the warp's, rounded to nearest.
+    uint32_t w[2][4][G];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    uint32_t w[4][G];        // keys 2c, 2c + 1, 2c + 8, 2c + 9
+    for (int half = 0; half < 2; ++half) v_words<D>(st, vget, half, w[half]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint8_t *at = st + T::kV + (half * 16 + 4 * i) * T::kRow + vget;
-      if constexpr (G == 2) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(at);
-        w[i][0] = x.x; w[i][1] = x.y;
-      } else {
-        w[i][0] = *reinterpret_cast<const uint32_t *>(at);
+    for (int gi = 0; gi < G; ++gi) {
+      float t[4];              // sum of P', heads 2c and 2c + 1 (twice)
+      mma16816_0(t, kOnes, kOnes, kOnes, kOnes, pb[gi][0][0], pb[gi][0][1]);
+      mma16816(t, kOnes, kOnes, kOnes, kOnes, pb[gi][1][0], pb[gi][1][1]);
+      constexpr float kUnit = -kMiddle / (16777216.f / (1 << kUp));
+      const Pair c1 = Pair(t[0], t[1]) * Pair(kUnit, kUnit);
+      const Pair c16 = Pair(t[0], t[1]) * Pair(16.f * kUnit, 16.f * kUnit);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float sum[4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t x, y;
+          v_codes<G>(w[half], gi, e, x, y);
+          if (half == 0)
+            mma16816_c(sum, x & kLow, x & kHigh, y & kLow, y & kHigh, pb[gi][0][0], pb[gi][0][1],
+                       c1, c16);
+          else
+            mma16816(sum, x & kLow, x & kHigh, y & kLow, y & kHigh, pb[gi][1][0], pb[gi][1][1]);
+          if (kFp16)
+            mma16816(sum, x & kLow, x & kHigh, y & kLow, y & kHigh, pl[gi][half][0],
+                     pl[gi][half][1]);
+        }
+        float *o = a.o[gi][e];
+#pragma unroll
+        for (int x = 0; x < 4; x += 2) {
+          const float2 y = (Pair(o[x], o[x + 1]) + Pair(sum[x], sum[x + 1])).get();
+          o[x] = y.x;
+          o[x + 1] = y.y;
+        }
       }
     }
+    return;
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t w[4][G];
+    v_words<D>(st, vget, half, w);
 #pragma unroll
     for (int gi = 0; gi < G; ++gi) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        // dims 2e, 2e + 1 of the word: byte e of the four keys' words
-        const uint32_t sel = e < 2 ? 0x5410u : 0x7632u;
-        const uint32_t x = code_pairs(__byte_perm(w[0][gi], w[1][gi], sel), e & 1);
-        const uint32_t y = code_pairs(__byte_perm(w[2][gi], w[3][gi], sel), e & 1);
+        uint32_t x, y;
+        v_codes<G>(w, gi, e, x, y);
         mma16816(a.o[gi][e], x & kLow, x & kHigh, y & kLow, y & kHigh, pb[gi][half][0],
                  pb[gi][half][1]);
         if (kFp16)
@@ -485,25 +558,6 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
                    pl[gi][half][1]);
       }
       if (!kFp16) mma16816(a.ps[gi], kOnes, kOnes, kOnes, kOnes, pb[gi][half][0], pb[gi][half][1]);
-    }
-  }
-  if (kFp16 && centre) {
-#pragma unroll
-    for (int gi = 0; gi < G; ++gi) {
-      float t[4];              // the tile's sum of P', heads 2c and 2c + 1 (twice)
-      mma16816_0(t, kOnes, kOnes, kOnes, kOnes, pb[gi][0][0], pb[gi][0][1]);
-      mma16816(t, kOnes, kOnes, kOnes, kOnes, pb[gi][1][0], pb[gi][1][1]);
-      constexpr float kUnit = -kMiddle / (16777216.f / (1 << kUp));
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int row = 0; row < 2; ++row) {
-          const float unit = row ? 16.f * kUnit : kUnit;
-          float *o = a.o[gi][e] + 2 * row;
-          const float2 x = fma(Pair(t[0], t[1]), Pair(unit, unit), Pair(o[0], o[1])).get();
-          o[0] = x.x;
-          o[1] = x.y;
-        }
     }
   }
 }
@@ -625,7 +679,8 @@ struct K4Stream {
   }
   __device__ __forceinline__ void run(const K4Query<D> &q, K4State<D> &a, int32_t &err) {
     static_assert(kStages == 3, "two tiles ahead, or one beside a kept part");
-    const bool centre = kFp16 && (count > kFewTiles || sg.tiles > kFewKeys / 32);
+    const bool centre = kFp16 ? count > kFewTiles || sg.tiles > kFewKeys / 32
+                              : (int64_t)count * count * sg.tiles > kFewSquare;
     for (int n = 0; n < count; ++n) {
       if (full) {
         keys[2] = issue(n + 2, err);
