@@ -76,7 +76,6 @@ constexpr float kMiddle = 7.5f;      // of the codes
 // sqrt(keys), so that the bound below stands for 2e-4, an eighth of its rounding.
 constexpr int kFewTiles = 12, kFewKeys = 2048, kFewSquare = 1 << 21;
 constexpr float kPScale = 8192.f;    // P' <= 2^kSlack * kPScale < 65504
-constexpr float kMasked = -3e38f;    // raw score of a key that does not count
 
 template <int D>
 struct K4 {
@@ -159,7 +158,7 @@ template <int D>
 struct K4Query {
   uint32_t f[K4<D>::kW][4];      // [word of the row][dims (0,4), (1,5)/16, (2,6), (3,7)/16]
   float sum[2][K4<D>::kG];       // sums of q^ in the raw scores' unit, heads 2c, 2c + 1 of the lane
-  Pair mul;                      // raw score -> S, > 0
+  Pair mul;                      // raw score -> S, >= 0
 };
 template <int D>
 struct K4RawQuery {
@@ -172,7 +171,7 @@ struct K4State {
   float ps[K4<D>::kG][4];        // sum of P' (bf16)
   Pair oz[K4<D>::kG];            // this lane's share of sum p (z + m s), of both heads
   Pair minus_m, l;               // reference maximum, negated; l: this lane's share
-  float thr[2];                  // raw score above which m is raised
+  float thr[2];                  // score above which m is raised
   float vmax, rinv;              // largest V scale allowed for, kPScale / it
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -267,9 +266,8 @@ __device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale
     mma16816(sum[i % G], 0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u, out.f[i][2],
              out.f[i][3]);
   }
-  // a raw score counts in 2^-22: S = 2^(ex - 14 + 22) |scale| raw.  A scale of 0 keeps the
-  // masked scores below the others.
-  const float mul = fmaxf(ldexpf(fabsf(scale_log2), ex + 10 - kUp), 1e-30f);
+  // a raw score counts in 2^-22: S = 2^(ex - 14 + 22) |scale| raw
+  const float mul = ldexpf(fabsf(scale_log2), ex + 10 - kUp);
   out.mul = Pair(__shfl_sync(0xffffffffu, mul, 8 * c), __shfl_sync(0xffffffffu, mul, 8 * c + 4));
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -349,7 +347,7 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
   const bool ragged = key0 < lo || key0 + 32 > len;
   constexpr uint32_t kLow = 0x000f000fu << kUp, kHigh = kLow << 4;
   constexpr uint32_t kOnes = 0x3c003c00u;
-  // ---- raw scores: rows r and r + 8 of both halves, heads 2c and 2c + 1 ----
+  // ---- scores: rows r and r + 8 of both halves, heads 2c and 2c + 1 ----
   float s[2][4];
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
@@ -391,6 +389,11 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
         for (int gi = 0; gi < G; ++gi) x = fmaf(ks[gi], acc[gi][2 * u + hd], x);
         s[half][2 * u + hd] = x;
       }
+      // rounded here: a reference rounded by itself would leave large scores' differences from
+      // it as far off as they are large
+      const float2 y = (Pair(s[half][2 * u], s[half][2 * u + 1]) * q.mul).get();
+      s[half][2 * u] = y.x;
+      s[half][2 * u + 1] = y.y;
     }
   }
   // ---- V's scales and zeros: lane's key, for everyone ----
@@ -405,7 +408,7 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + i * 8 + r;
-      if (key < lo || key >= len) s[i >> 1][(i & 1) * 2] = s[i >> 1][(i & 1) * 2 + 1] = kMasked;
+      if (key < lo || key >= len) s[i >> 1][(i & 1) * 2] = s[i >> 1][(i & 1) * 2 + 1] = -INFINITY;
     }
   }
   // ---- raise the references where a score or a scale outgrew them ----
@@ -428,18 +431,17 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
       a.vmax = vnew;
       a.rinv = rnew;
     }
-    const float2 mul = q.mul.get(), mm = a.minus_m.get();
+    const float2 mm = a.minus_m.get();
     float alpha[2], minus[2];
 #pragma unroll
     for (int hd = 0; hd < 2; ++hd) {
       float x = top[hd];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      const float old = -(hd ? mm.y : mm.x), k = hd ? mul.y : mul.x;
-      const float mnew = fmaxf(old, x * k);
+      const float old = -(hd ? mm.y : mm.x), mnew = fmaxf(old, x);
       alpha[hd] = ex2_approx(old - mnew);
       minus[hd] = -mnew;
-      a.thr[hd] = __fdividef(mnew + kSlack, k);
+      a.thr[hd] = mnew + kSlack;
       const float both = alpha[hd] * grow;
 #pragma unroll
       for (int gi = 0; gi < G; ++gi) {
@@ -474,8 +476,7 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
   uint32_t pl[G][2][2];      // what hi leaves of P' (fp16)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 e = fma(Pair(s[i >> 1][(i & 1) * 2], s[i >> 1][(i & 1) * 2 + 1]), q.mul,
-                         a.minus_m).get();
+    const float2 e = (Pair(s[i >> 1][(i & 1) * 2], s[i >> 1][(i & 1) * 2 + 1]) + a.minus_m).get();
     const Pair p(ex2_approx(e.x), ex2_approx(e.y));
     a.l = a.l + p;
     float vsr[G], vc[G];
