@@ -43,7 +43,7 @@ struct Kv4RowParams {
 
 struct Kv4DecodeParams {
   int num_seqs, h_q, h_k, g, num_pages, page_log2, width, topk, window;
-  float scale_log2;
+  float scale;
   const void *q;
   const uint8_t *pool;
   const int32_t *table, *lens, *sel;                 // sel null: every block

@@ -225,7 +225,7 @@ nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_
   p.width = table_width;
   p.topk = topk;
   p.window = window;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale = scale;
   p.q = q;
   p.pool = static_cast<const uint8_t *>(pool);
   p.table = block_table;

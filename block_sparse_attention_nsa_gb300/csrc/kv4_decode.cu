@@ -76,6 +76,8 @@ constexpr float kMiddle = 7.5f;      // of the codes
 // sqrt(keys), so that the bound below stands for 2e-4, an eighth of its rounding.
 constexpr int kFewTiles = 12, kFewKeys = 2048, kFewSquare = 1 << 21;
 constexpr float kPScale = 8192.f;    // P' <= 2^kSlack * kPScale < 65504
+constexpr int kUp = 2;               // bits that codes are moved up by (code_pairs)
+constexpr int kMulTop = 118;         // a score's factor stays below 2^(kMulTop + 2)
 
 template <int D>
 struct K4 {
@@ -148,7 +150,6 @@ __device__ __forceinline__ void par_floats(uint32_t u, float (&x)[G]) {
 // where a long cache's values cancel: with weights as exact as here fp16 outputs over 64K tokens
 // were 4.4e-4 off, with the two bits 1.1e-4; codes at the top of the subnormals cost 4 % of the
 // time and gave little more.
-constexpr int kUp = 2;
 __device__ __forceinline__ uint32_t code_pairs(uint32_t w, int k) {
   return k ? w >> (8 - kUp) : w << kUp;
 }
@@ -225,17 +226,12 @@ __device__ __forceinline__ void fetch_query(const Kv4DecodeParams &p, const K4Se
   }
 }
 
-// Scaled by a power of two per head to a largest magnitude in [2^14, 2^15).  The sums of
-// q^ come from products with rows of ones (16 for the dimensions held as sixteenths).
+// The exponent of the largest magnitude of lane (r, c)'s head r.
 template <int D, bool kFp16>
-__device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale_log2, int lane,
-                                           K4Query<D> &out) {
-  constexpr int G = K4<D>::kG, W = K4<D>::kW;
-  const int c = lane & 3;
-  const uint32_t sign = scale_log2 < 0.f ? 0x80008000u : 0u;   // mul stays positive
+__device__ __forceinline__ int query_exponent(const K4RawQuery<D> &raw) {
   uint32_t top = 0;          // magnitudes of 16-bit floats order as whole numbers
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
+  for (int i = 0; i < K4<D>::kW; ++i) {
     const uint4 w = raw.w[i];
     top = __vmaxu2(__vmaxu2(top, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
     top = __vmaxu2(__vmaxu2(top, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
@@ -243,8 +239,28 @@ __device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale
   top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
   const float2 f = unpack2<kFp16>(top);
-  const float big = fmaxf(f.x, f.y);
-  const int ex = max(static_cast<int>(__float_as_uint(big) >> 23) - 127, -100);
+  return max(static_cast<int>(__float_as_uint(fmaxf(f.x, f.y)) >> 23) - 127, -100);
+}
+
+// A raw score counts in 2^-22, of a query scaled by 2^(14 - ex): S = 2^(ex + 8) |scale| raw.  A
+// factor past 2^(kMulTop + 2) could overflow where S does not: `over` powers of two are left
+// out of it, and of the scores, and put back into the maximum at the end.  The keys' weights do not
+// miss them: what a query in fp16 keeps of such a head makes scores that are equal or differ by
+// far more than 2^over times what an exponential tells apart.
+__device__ __forceinline__ int score_over(float scale, int ex) {
+  return max(0, static_cast<int>((__float_as_uint(scale) & 0x7fffffffu) >> 23) - 127 + ex + 10 -
+                    kUp - kMulTop);
+}
+
+// Scaled by a power of two per head to a largest magnitude in [2^14, 2^15).  The sums of
+// q^ come from products with rows of ones (16 for the dimensions held as sixteenths).
+template <int D, bool kFp16>
+__device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale, int lane,
+                                           K4Query<D> &out) {
+  constexpr int G = K4<D>::kG, W = K4<D>::kW;
+  const int c = lane & 3;
+  const uint32_t sign = scale < 0.f ? 0x80008000u : 0u;   // mul stays positive
+  const int ex = query_exponent<D, kFp16>(raw);
   const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);   // 2^(14 - ex)
   const float lo = up * 0.0625f;
   float sum[G][4];
@@ -266,8 +282,7 @@ __device__ __forceinline__ void make_query(const K4RawQuery<D> &raw, float scale
     mma16816(sum[i % G], 0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u, out.f[i][2],
              out.f[i][3]);
   }
-  // a raw score counts in 2^-22: S = 2^(ex - 14 + 22) |scale| raw
-  const float mul = ldexpf(fabsf(scale_log2), ex + 10 - kUp);
+  const float mul = ldexpf(fabsf(scale), ex + 10 - kUp - score_over(scale, ex)) * 1.4426950408889634f;
   out.mul = Pair(__shfl_sync(0xffffffffu, mul, 8 * c), __shfl_sync(0xffffffffu, mul, 8 * c + 4));
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -698,6 +713,17 @@ struct K4Stream {
       keys[1] = keys[2];
     }
     cp_async_wait_all();
+    const float2 mul = q.mul.get();
+    constexpr float kLarge = 1.f * (1ull << 59) * (1ull << 59);   // 2^kMulTop
+    static_assert(kMulTop == 118, "");
+    if (__any_sync(0xffffffffu, fmaxf(mul.x, mul.y) >= kLarge)) {   // powers may have been left out
+      K4RawQuery<D> raw;
+      fetch_query<D>(p, sg, lane, raw);
+      const int over = score_over(p.scale, query_exponent<D, kFp16>(raw)), c = lane & 3;
+      const float2 mm = a.minus_m.get();
+      const int o0 = __shfl_sync(0xffffffffu, over, 8 * c), o1 = __shfl_sync(0xffffffffu, over, 8 * c + 4);
+      a.minus_m = Pair(ldexpf(mm.x, o0), ldexpf(mm.y, o1));
+    }
   }
 };
 
@@ -811,7 +837,7 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps<D> / kWarps)
                               smem + warp * K4<D>::kRing, true, lane);
   st.start(err);
   K4Query<D> q;
-  make_query<D, kFp16>(raw, p.scale_log2, lane, q);
+  make_query<D, kFp16>(raw, p.scale, lane, q);
   K4State<D> a;
   a.clear();
   st.run(q, a, err);
@@ -1015,7 +1041,7 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
       K4Stream<D, kFp16, false> st(p, sg, t0, max(0, t1 - t0), 1, ring, !(left & kKeep), lane);
       st.start(err);
       K4Query<D> q;
-      make_query<D, kFp16>(raw, p.scale_log2, lane, q);
+      make_query<D, kFp16>(raw, p.scale, lane, q);
       st.run(q, a, err);
     }
     const K4Sums<D> sums(a);

@@ -1,4 +1,5 @@
-"""Paged decode of large numbers: scores so large that one key takes all of a row's weight."""
+"""Paged decode at the ends of its number ranges: queries, scales and scores as large as the types
+hold, where one key takes all of a row's weight."""
 import numpy as np
 import pytest
 import torch
@@ -65,6 +66,34 @@ def _check_one_hot(q, pool, table, lens, page, scale, **kw):
             slack = (2.0 ** -11 + 2.0 ** -18) * ps[b, hq] + 2.0 ** -18 * pv[b, hq]
             assert (np.abs(got[b, hq] - want) <= half * np.abs(want) + slack + 2.0 ** -24).all(), (b, hq)
     assert clear >= q.shape[0] * q.shape[1] // 2 and int(status.item()) == 0
+
+
+@pytest.mark.parametrize("exponent", [100, 118, 120, 121, 122, 123, 125])
+@pytest.mark.parametrize("d,shift", [(128, 0.0), (64, 0.0), (128, 3.0)])
+def test_queries_up_to_the_largest(exponent, d, shift):
+    """bf16 queries of magnitudes up to 2^127, whose scores fp32 holds; with K shifted to positive
+    values every score of the second half's heads is negative."""
+    lens, page, h_k, g = (300, 1, 70), 64, 2, 4
+    pool, table = _caches(lens, page, h_k, d, 3, k_mag=0.05, k_shift=0.05 * shift)
+    q = torch.randn(3, h_k * g, d, generator=torch.Generator().manual_seed(4))
+    if shift:
+        q = q.abs()
+        q[:, g:] *= -1
+    q = (q.clamp(-3.5, 3.5) * 2.0 ** exponent).to(torch.bfloat16)
+    assert q.isfinite().all()
+    for width in (None, 2500):        # segments, and runs that leave parts to a merge
+        t = table if width is None else np.pad(table, ((0, 0), (0, width - table.shape[1])),
+                                               constant_values=-1)
+        _check_one_hot(q, pool, t, lens, page, (0.25 if shift else -0.25))
+
+
+@pytest.mark.parametrize("dtype,scale", [("fp16", 1e32), ("fp16", -3e36), ("fp16", 3.3e38),
+                                         ("bf16", 1e30), ("bf16", 2.5e38)])
+def test_scales_up_to_the_largest(dtype, scale):
+    lens, page, h_k, g, d = (300, 70), 32, 1, 4, 64
+    pool, table = _caches(lens, page, h_k, d, 5)
+    q = torch.randn(2, g, d, generator=torch.Generator().manual_seed(6)) * min(1.0, 1e36 / abs(scale))
+    _check_one_hot(q.to(DTYPES[dtype]), pool, table, lens, page, scale)
 
 
 @pytest.mark.parametrize("mag", [30.0, 1e3, 2e4])
