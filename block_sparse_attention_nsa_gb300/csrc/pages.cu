@@ -161,8 +161,11 @@ cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s) {
   auto *kernel = plan ? page_kernel<true> : page_kernel<false>;
   const size_t smem = (3 * static_cast<size_t>(p.num_seqs) + 1) * sizeof(int32_t);
   if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    // the largest plan's, whatever this one's: the limit is the kernel's, and another host thread may
+    // be between its own and its launch
+    constexpr int kMost = (3 * kMaxPlanSeqs + 1) * static_cast<int>(sizeof(int32_t));
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
   }
   const bool one = p.max_slots <= kPlanOneCta;
