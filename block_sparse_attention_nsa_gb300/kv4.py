@@ -84,7 +84,10 @@ def _kv4_dims(*sizes):
 
 
 _current_device = torch.cuda.current_device
-_current_stream = torch._C._cuda_getCurrentRawStream
+# The current stream's handle without a Stream object around it; builds of
+# torch without CUDA do not have this name.
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _check(name, t, dtype, shape, dev):
