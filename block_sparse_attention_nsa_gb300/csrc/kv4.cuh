@@ -87,7 +87,9 @@ __device__ __forceinline__ void raise(int32_t *status, int32_t bits) {
 }
 
 // Kernels of this group start while the one before them on the stream still runs (their
-// launch overlaps its end) and touch no memory before it has finished.
+// launch overlaps its end) and touch no memory before it has finished.  They read with plain loads:
+// what a read-only load (ld.global.nc, __ldg) takes must not change while the kernel runs, which
+// for these began with the writer's end still to come, and the compiler may move one ahead of the wait.
 __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -222,7 +222,7 @@ __device__ __forceinline__ void fetch_query(const Kv4DecodeParams &p, const K4Se
   for (int i = 0; i < W; ++i) {
     const int w = c * W + i, at = (w % G) * 64 + w / G * 8;
     raw.w[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < sg.g) raw.w[i] = __ldg(reinterpret_cast<const uint4 *>(q + at));
+    if (r < sg.g) raw.w[i] = *reinterpret_cast<const uint4 *>(q + at);
   }
 }
 
@@ -581,7 +581,7 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
 // Length of sequence b held to its table row, and the first key that its window shows.
 __device__ __forceinline__ int seq_len(const Kv4DecodeParams &p, int b, int32_t &err) {
   const int cap = p.width << p.page_log2;
-  const int raw = __ldg(p.lens + b), len = min(max(raw, 0), cap);
+  const int raw = p.lens[b], len = min(max(raw, 0), cap);
   if (raw != len) err |= NSA_DEVERR_BAD_SEQLENS;
   return len;
 }
@@ -596,7 +596,7 @@ __device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg
                                              int lane, int32_t &err) {
   int blk = -1;
   if (kSel && lane < p.topk)
-    blk = __ldg(p.sel + ((int64_t)sg.h * p.num_seqs + sg.b) * p.topk + lane);
+    blk = p.sel[((int64_t)sg.h * p.num_seqs + sg.b) * p.topk + lane];
   int32_t ignore = 0;        // reported once, where the lengths are first read
   sg.len = seq_len(p, sg.b, ignore);
   sg.lo = seq_lo(p, sg.len);
@@ -610,7 +610,7 @@ __device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg
     ok = ok && (same & ((1u << lane) - 1u)) == 0;
     int pg = -1;
     if (ok) {
-      pg = __ldg(p.table + (int64_t)sg.b * p.width + blk);
+      pg = p.table[(int64_t)sg.b * p.width + blk];
       if (pg < 0 || pg >= p.num_pages) {
         ok = false;
         err |= NSA_DEVERR_BAD_INDEX;
@@ -666,7 +666,7 @@ struct K4Stream {
           if (i >= count) pg = -1;
         } else if (i < count) {
           my_key = (sg.first + t) << 5;
-          pg = __ldg(p.table + (int64_t)sg.b * p.width + (my_key >> p.page_log2));
+          pg = p.table[(int64_t)sg.b * p.width + (my_key >> p.page_log2)];
           if (pg < 0 || pg >= p.num_pages) {
             pg = -1;
             err |= NSA_DEVERR_BAD_INDEX;

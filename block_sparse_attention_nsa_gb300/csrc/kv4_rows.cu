@@ -55,7 +55,7 @@ __device__ __forceinline__ void load_slots(const Kv4RowParams &p, int t0, int (&
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    slot[k] = t0 + k < p.n ? __ldg(p.slots + t0 + k) : -1;
+    slot[k] = t0 + k < p.n ? p.slots[t0 + k] : -1;
     if (slot[k] < 0 || (slot[k] >> p.page_log2) >= p.num_pages) {
       bad |= slot[k] != -1;
       slot[k] = -1;
@@ -226,12 +226,12 @@ __global__ void __launch_bounds__(kRowThreads) kv4_read_kernel(Kv4RowParams p) {
     if (slot[k] >= 0) {
       const uint8_t *tile = p.pool + slot_tile<D>(p, r.h, slot[k]);
       const int row = slot[k] & (kKv4Tile - 1);
-      word[k] = __ldg(reinterpret_cast<const uint32_t *>(tile + r.kv * T::kV + row * T::kRow +
-                                                         (r.j * T::kG + r.gi) * 4));
+      word[k] = *reinterpret_cast<const uint32_t *>(tile + r.kv * T::kV + row * T::kRow +
+                                                   (r.j * T::kG + r.gi) * 4);
       const __half *par = reinterpret_cast<const __half *>(tile + T::kPar + 2 * r.kv * T::kArr) +
                           row * T::kG + r.gi;
-      scale[k] = __ldg(par);
-      zero[k] = __ldg(par + T::kArr / 2);
+      scale[k] = *par;
+      zero[k] = par[T::kArr / 2];
     }
   }
 #pragma unroll
