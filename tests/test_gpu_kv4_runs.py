@@ -112,3 +112,143 @@ def test_runs_with_many_segments(d, page, h_k, g, dtype, most, count, last, wind
     assert (a[dead.t()] == 0).all() and (c[dead.t()] == 0).all()
     near = (lse[:, perm.cuda()] - l2).abs()
     assert (near[~dead] <= 2.0 ** -16).all()
+
+
+def _wide(lens, page, h_k, g, d, seed, dtype=torch.bfloat16, width=2000):
+    import block_sparse_attention_nsa_gb300 as nsa
+    pool, table, _ = make_cache(lens, page, h_k, d, seed, width=width)
+    q = torch.randn(len(lens), h_k * g, d, generator=torch.Generator().manual_seed(seed)).to(dtype)
+    s = dict(pool=pool, table=table, q=q, lens=lens, dq=q.cuda(), dpool=_dev(pool),
+             dtab=_dev(table), dlens=_dev(np.int32(lens)), out=torch.empty_like(q).cuda(),
+             lse=torch.empty(h_k * g, len(lens), device="cuda"))
+    s["ws"] = _workspace(nsa, pool.shape[0], page, h_k, d, len(lens), h_k * g)
+    return s
+
+
+def _oracle_check(s, page, scale):
+    ref = kv4.attend(s["q"].double().numpy(), s["pool"], s["table"], s["lens"], page, scale)
+    check_decode(s["out"], s["lse"], ref, s["q"].dtype)
+
+
+def test_runs_on_another_stream_in_graphs_and_with_a_shared_workspace():
+    """Two shapes on a stream of their own, then captured into graphs that share a workspace and are
+    replayed in turn, while their lengths change in place."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d = 64, 2, 4, 128
+    side = torch.cuda.Stream()
+    sets = [_wide(lens, page, h_k, g, d, seed)
+            for seed, lens in ((41, (5000, 3)), (42, (900, 4000, 1)))]
+    ws = max((s["ws"] for s in sets), key=torch.numel)
+    torch.cuda.synchronize()
+    for s in sets:
+        nsa.kv4_decode(s["dq"], s["dpool"], s["dtab"], s["dlens"], 0.1, out=s["out"], lse=s["lse"],
+                       workspace=ws, stream=side)
+    side.synchronize()
+    assert (ws != 0xff).any()
+    for s in sets:
+        _oracle_check(s, page, 0.1)
+    graphs = []
+    for s in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            nsa.kv4_decode(s["dq"], s["dpool"], s["dtab"], s["dlens"], 0.1, out=s["out"],
+                           lse=s["lse"], workspace=ws)
+        graphs.append(graph)
+    for k in range(4):
+        ws.fill_(0xff)                   # nothing is carried over
+        for s, graph in zip(sets, graphs):
+            s["lens"] = tuple(max(0, n - 700 * k) for n in s["lens"])
+            s["dlens"].copy_(_dev(np.int32(s["lens"])))
+            graph.replay()
+        torch.cuda.synchronize()
+        assert (ws != 0xff).any()
+        for s in sets:
+            _oracle_check(s, page, 0.1)
+
+
+def test_runs_on_two_streams_and_between_torch_kernels():
+    """Unsynchronised loops on two streams, each call behind a torch kernel that writes its query and
+    before one that reads its output, several shapes in turn on one workspace: the same sums as
+    with a wait after each."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d = 64, 2, 4, 128
+    loops = []
+    for seed in (61, 63):
+        sets = [_wide(lens, page, h_k, g, d, seed + k, width=1500 + 200 * k)
+                for k, lens in enumerate(((4000, 5, 900), (3000,) * 5))]
+        qs = [torch.randn((12,) + s["q"].shape, generator=torch.Generator().manual_seed(seed))
+              .to(torch.bfloat16).cuda() for s in sets]
+        loops.append((sets, qs, max((s["ws"] for s in sets), key=torch.numel), torch.cuda.Stream()))
+
+    def run(sets, qs, ws, wait):
+        totals = [torch.zeros(s["q"].shape, device="cuda") for s in sets]
+        for k in range(12):
+            for s, q, total in zip(sets, qs, totals):
+                s["dq"].copy_(q[k])
+                nsa.kv4_decode(s["dq"], s["dpool"], s["dtab"], s["dlens"], 0.1, out=s["out"],
+                               lse=s["lse"], workspace=ws)
+                total.add_(s["out"].float())
+                if wait:
+                    torch.cuda.synchronize()
+        return totals
+    want = [run(s, q, w, True) for s, q, w, _ in loops]
+    assert all((w != 0xff).any() for _, _, w, _ in loops)
+    for _ in range(3):
+        got = []
+        for s, q, w, stream in loops:
+            with torch.cuda.stream(stream):
+                stream.wait_stream(torch.cuda.default_stream())
+                got.append(run(s, q, w, False))
+        torch.cuda.synchronize()
+        for a, b in zip(sum(got, []), sum(want, [])):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("graphed", [False, True])
+def test_steps_of_plan_append_and_runs(graphed):
+    """Serving steps back to back, without a wait or as one captured step that is replayed: a plan
+    that opens pages, an append into them, a decode over everything cached, each launched while the
+    one before it ends, behind a torch kernel that makes the step's rows."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d, b, steps = 32, 2, 2, 64, 5, 70
+    pages, width = 40, 4000
+    gen = torch.Generator().manual_seed(4)
+    rows = torch.randn(steps, 3, b, h_k, d, generator=gen).to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pool = nsa.kv4_pool(pages, page, h_k, d)
+    table = torch.full((b, width), -1, **i32)
+    free = torch.randperm(pages, generator=gen).int().cuda()
+    head, lens, one = torch.zeros(1, **i32), torch.zeros(b, **i32), torch.ones(b, **i32)
+    slots, cu, status = torch.empty(b, **i32), torch.empty(b + 1, **i32), torch.zeros(1, **i32)
+    at, drows = torch.zeros((), dtype=torch.int64, device="cuda"), rows.cuda()
+    kvq = torch.empty_like(drows[0])
+    q = torch.empty(b, h_k * g, d, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(h_k * g, b, device="cuda")
+    outs = torch.zeros((steps,) + out.shape, dtype=out.dtype, device="cuda")
+    lses = torch.zeros((steps,) + lse.shape, device="cuda")
+    ws = _workspace(nsa, pages, page, h_k, d, b, h_k * g)
+
+    def step():
+        kvq.copy_(drows.index_select(0, at.view(1))[0])
+        q.copy_(kvq[2].repeat_interleave(g, 1))
+        nsa.page_plan(lens, one, free, head, table, page, pages, slots, lens, cu, head, status)
+        nsa.kv4_append(pool, kvq[0], kvq[1], slots, status)
+        nsa.kv4_decode(q, pool, table, lens, 0.3, out=out, lse=lse, workspace=ws,
+                       device_status=status)
+        outs.index_copy_(0, at.view(1), out.unsqueeze(0))
+        lses.index_copy_(0, at.view(1), lse.unsqueeze(0))
+        at.add_(1)
+    if graphed:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    for _ in range(steps):
+        graph.replay() if graphed else step()
+    torch.cuda.synchronize()
+    assert (ws != 0xff).any() and int(status.item()) == 0 and lens.tolist() == [steps] * b
+    assert int(head.item()) == b * -(-steps // page)
+    hpool, htab = pool.cpu().numpy(), table.cpu().numpy()
+    for t in (0, 1, 30, 31, 32, 33, 63, 64, steps - 1):
+        ref = kv4.attend(rows[t, 2].repeat_interleave(g, 1).double().numpy(), hpool, htab,
+                         [t + 1] * b, page, 0.3)
+        check_decode(outs[t], lses[t], ref, torch.bfloat16)
