@@ -40,6 +40,25 @@ def test_long_runs_lose_little(d, h_k, b, dtype):
     assert off <= (1.055 if dt is torch.bfloat16 else 1.25) * np.linalg.norm(rounded - ref)
 
 
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "fp16"), (64, "bf16"), (128, "bf16")])
+def test_selections_of_a_whole_sequence_by_one_warp(d, dtype):
+    """850 sequences of 8 KV heads: 6800 segments of 128 tiles, each one warp's on 148, 152 and 160
+    SMs.  The bounds are test_long_runs_lose_little's."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    dt, n, page, h_k, b = DTYPES[dtype], 4096, 128, 8, 850
+    pool, table, lens = _repeated(b, n, page, h_k, d, 79)
+    sel = np.broadcast_to(np.arange(n // page, dtype=np.int32), (h_k, b, n // page)).copy()
+    q = torch.randn(b, h_k, d, generator=torch.Generator().manual_seed(80)).to(dt)
+    out, _ = nsa.kv4_decode(q.cuda(), _dev(pool), _dev(table), _dev(lens), d ** -0.5,
+                            sel_idx=_dev(sel))
+    rows = [0, 7, 424, 849]
+    ref = kv4.attend(q[rows].double().numpy(), pool, table[:4], lens[:4], page, d ** -0.5,
+                     sel[:, :4])[0]
+    rounded = torch.from_numpy(ref).to(dt).double().numpy()
+    off = np.linalg.norm(out[rows].double().cpu().numpy() - ref)
+    assert off <= (1.055 if dt is torch.bfloat16 else 1.25) * np.linalg.norm(rounded - ref)
+
+
 # ---- equal runs over a batch: kv4_run_kernel and kv4_merge_kernel ----------------------
 # A table much wider than the lengths leaves the host no bound on a segment's tiles, and makes the call
 # take equal runs of tiles.  A workspace filled with 0xff shows whether it did: runs write it.
