@@ -54,8 +54,8 @@ nsa_status check_rows(const nsa_kv4_dims *d, int32_t n, const void *pool, const 
   nsa_status st = check_kv4(d);
   if (st != NSA_OK) return st;
   if (n < 0) return NSA_ERR_INVALID_ARG;
-  // one thread per eight values: the grid has to stay below 2^31 CTAs of 256
-  if ((int64_t)n * d->h_k * d->head_dim / 4 >= (int64_t(1) << 38)) return NSA_ERR_UNSUPPORTED;
+  // a CTA takes eight heads' rows of 512 / d tokens (kv4_rows.cu): the grid stays below 2^30
+  if ((int64_t)n * d->h_k >= (int64_t(1) << 38) / (d->head_dim / 4)) return NSA_ERR_UNSUPPORTED;
   if (n > 0 && (!slots || (d->num_pages > 0 && !pool))) return NSA_ERR_INVALID_ARG;
   if (!on(slots, 4) || !on(pool, 16) || !on(status, 4)) return NSA_ERR_INVALID_ARG;
   return NSA_OK;
