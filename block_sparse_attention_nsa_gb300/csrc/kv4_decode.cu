@@ -6,15 +6,17 @@
 // d + d / 8 bytes carry 4 d g operations, so HBM bounds a long cache if the codes become
 // operands in few instructions (at 6.8 TB/s each SM gets 41 codes a clock).
 //
-// Tensor-core form.  Keys are the rows of m16n8k16 (mma.sync: at most 8 query heads are far
-// from the 128 rows of a tcgen05 tile), heads the columns.  A code needs no conversion:
-// masked out of its word as the low bits of an fp16 it IS the subnormal c * 2^-24 (or, at
-// bits 4-7, 16 c * 2^-24; K's two bits further up), which the tensor core multiplies exactly.
+// Tensor-core form.  Keys are the rows of m16n8k16, heads the columns.  (mma.sync takes its
+// operands from registers, where the codes are unpacked; a tcgen05 tile of 128 keys would want them
+// written to shared or tensor memory as 16-bit numbers first, four times their bytes, for a
+// tensor pipe that is at most 30 % busy as it is.)  A code needs no conversion: masked out of its
+// word as the low bits of an fp16 it IS the subnormal c * 2^-24 (or, at bits 4-7, 16 c * 2^-24;
+// both two bits further up, see kUp), which the tensor core multiplies exactly.
 //   scores  acc_g = sum over the group's dimensions of q^ c, exact products in fp32;
 //           S = C_h (sum_g ks_g acc_g + kz_g Q_g), Q_g = sum q^ over the group, in fp32.
 //           q^ is q times a power of two per head (largest magnitude in [2^14, 2^15)), so
 //           that fp16 holds bf16's and fp16's values: it loses only what is 2^-38 of the
-//           largest.
+//           largest (2^-34 in the half of the dimensions that is held in sixteenths).
 //   output  O_g = sum_i P'_i (c_i - m) + sum_i p_i (z_i + m s_i), P' = p s scaled by a power of
 //           two that follows the largest s seen; the second sum is in fp32.  For bf16 P' is
 //           rounded to fp16 (2^-11 of a weight, on codes counted from their middle m = 7.5, by
@@ -53,9 +55,10 @@
 // CTA's border leave partial results (at most two a CTA) for kv4_merge_kernel.
 //
 // Measured (d = 128, bf16): a tile costs about 530 warp instructions, its start and join
-// included, and, with 12 warps on an SM, 230 cycles, against 198 that its bytes take at 6.78
-// TB/s.  64 sequences of 8K, 16 selected blocks, g = 4 (37.8 MB): 12.0 us; one of 64K in full:
-// 17.4 us; eight of them (302 MB): 58.3 us, 5.18 TB/s.
+// included (567 with its sums added in fp32), and, with 12 warps on an SM, 230 to 240 cycles,
+// against 198 that its bytes take at 6.78 TB/s.  64 sequences of 8K, 16 selected blocks, g = 4 (37.8
+// MB): 11.9 us (three such batches in turn; behind an L2 flush 16 to 18); one of 64K in full: 17.4 us;
+// eight of them (302 MB): 60.1 us, 5.03 TB/s.
 #include "kv4.cuh"
 
 namespace nsa {
@@ -1332,9 +1335,10 @@ static int seg_ctas(int64_t segs, int64_t most, int sms) {
 // Segments of at most `most` tiles in CTAs of their own, or equal runs?  An SM takes about
 // 0.125 us a tile; the first cost 4.2 us besides, at the bound's length on every SM, the
 // second 8.9 (prefix, partial results, merge) at the true lengths.  Measured, g = 4, d = 128,
-// segments / runs: 1 x 4096 tokens 6.3 / 8.3 us, 1 x 8192 8.3 / 9.6, 16 x 4096 13.3 / 17.2; with
-// 16 warps an SM 64 x 4096 33.5 / 38.3; ragged up to that length 8 x 4096 8.0 / 9.2, 64 x 2048
-// 14.2 / 13.8, 64 x 4096 23.6 / 16.0.
+// segments / runs: 1 x 4096 tokens 6.4 / 8.5 us, 1 x 8192 8.5 / 9.7, 8 x 4096 9.2 / 13.1, 16 x 4096
+// 12.8 / 16.5, 64 x 2048 18.6 / 26.2, 64 x 4096 31.3 / 38.0 (the one of these where the estimate
+// takes the slower); ragged up to that length 8 x 4096 8.2 / 9.9, 64 x 2048 14.0 / 12.5, 64 x 4096
+// 24.5 / 14.2.
 static bool seg_better(int64_t segs, int64_t most, int ctas, int sms) {
   const int64_t on_sm = (segs * ctas + sms - 1) / sms;
   return 4.2 + 0.125 * most / ctas * on_sm < 8.9 + 0.125 * segs * most / sms;
