@@ -459,7 +459,7 @@ __device__ __forceinline__ void attend_tile(uint8_t *st, int key0, int lo, int l
       const float old = -(hd ? mm.y : mm.x), mnew = fmaxf(old, x);
       alpha[hd] = ex2_approx(old - mnew);
       minus[hd] = -mnew;
-      a.thr[hd] = mnew + kSlack;
+      a.thr[hd] = __fadd_rd(mnew, kSlack);   // never more: P' has no room for another power of two
       const float both = alpha[hd] * grow;
 #pragma unroll
       for (int gi = 0; gi < G; ++gi) {

@@ -106,3 +106,37 @@ def test_scores_of_any_size(mag, d, dtype):
     q = torch.randn(2, h_k * g, d, generator=torch.Generator().manual_seed(8)) * mag
     q = q.clamp(-6e4, 6e4).to(DTYPES[dtype])
     _check_one_hot(q, pool, table, lens, page, d ** -0.5)
+
+
+@pytest.mark.parametrize("base", [2.0 ** 22, 2.0 ** 24, 1.2 * 2.0 ** 24, 1.2 * 2.0 ** 25, -1.2 * 2.0 ** 25,
+                                  1.2 * 2.0 ** 26, 2.0 ** 30])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_large_scores_that_rise_by_small_steps(base, dtype):
+    """Scores of about `base` in units of the exponent's base 2, whose spacing is then a few such units:
+    steps of one spacing, in whatever order a warp meets them.  All tokens have one row of V, so that
+    the output is that row whatever a rounding does to the weights."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    d, page, n, dt = 128, 64, 4096, DTYPES[dtype]
+    gen = torch.Generator().manual_seed(9)
+    q = torch.zeros(1, 2, d, dtype=dt)
+    q[..., 0], q[..., 64] = 2.0 ** 15, 2.0
+    a = float(torch.tensor(abs(base) / 2.0 ** 15).half())
+    step = max(4.0, 2.0 ** (np.floor(np.log2(a * 2.0 ** 15)) - 23)) / 2.0
+    k = torch.empty(n, 1, d)
+    k[..., :64] = a if base > 0 else -a                # a flat group: its zero alone
+    k[..., 64:] = (torch.randint(0, 4, (n // 32,), generator=gen) * step).repeat_interleave(32).view(n, 1, 1)
+    v = (torch.arange(d) % 16 * 0.9990234375).expand(n, 1, d)
+    pool, slots = nsa.kv4_pool(n // page, page, 1, d), _dev(np.arange(n, dtype=np.int32))
+    nsa.kv4_append(pool, k.half().cuda(), v.half().contiguous().cuda(), slots)
+    _, vr = nsa.kv4_read(pool, slots[:1], d, dtype=torch.float16)
+    want = vr[0, 0].double().cpu()
+    scale = 1 / 1.4426950408889634
+    for width in (n // page, 2500):
+        table = np.full((1, width), -1, np.int32)
+        table[0, :n // page] = np.arange(n // page)
+        out, lse = nsa.kv4_decode(q.cuda(), pool, _dev(table), _dev(np.int32([n])), scale)
+        s = (q[0, 0].double() @ k[:, 0].half().double().t()) * scale
+        tol = 2.0 ** -18 * want.abs() + torch.finfo(dt).eps / 2 * want.abs() + 2.0 ** -11 * 8
+        assert ((out.double().cpu() - want).abs() <= tol).all()
+        # the score's roundings: of the product, of the factor, of log2 e
+        assert ((lse.double().cpu() - torch.logsumexp(s, 0)).abs() <= 2.0 ** -21 * s.abs().max() + 1e-5).all()
