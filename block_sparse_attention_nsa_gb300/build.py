@@ -13,7 +13,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnsa_sel.so")
 SOURCES = ["api.cu", "index_build.cu", "fwd.cu", "bwd.cu", "noalloc.cu", "decode.cu", "window.cu",
-           "compress.cu", "pages.cu", "kv4_rows.cu", "kv4_decode.cu", "kv4_api.cu"]
+           "compress.cu", "pages.cu", "kv4_rows.cu", "kv4_decode.cu", "kv4_api.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,7 +38,7 @@ def _stale(target: str, deps) -> bool:
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    headers += [os.path.join(ROOT, "include", f) for f in ("nsa_sel_attn.h", "nsa_kv4.h")]
+    headers += [os.path.join(ROOT, "include", f) for f in ("nsa_sel_attn.h", "nsa_kv4.h", "nsa_rope.h")]
     objs = []
     jobs = []
     for src in SOURCES:
