@@ -11,6 +11,8 @@ Names follow the C ABI in include/nsa_sel_attn.h:
   compress_kv, cmp_attn_select, profile_enable, profile_collect.
 The 4-bit paged KV cache (include/nsa_kv4.h) is bound in kv4.py and offered here too:
   page_plan, page_slots, kv4_pool, kv4_append, kv4_read, kv4_decode.
+The life of its pages is bound in pages.py:
+  page_fork, page_free, page_compact, page_copy.
 Rotary positions (include/nsa_rope.h) are bound in rope.py:
   rope_freqs, rope, rope_bwd.
 """
@@ -25,6 +27,8 @@ import torch
 from .kv4 import (DEVERR_BAD_INDEX, DEVERR_BAD_SEQLENS, DEVERR_NO_PAGES, kv4_append, kv4_decode,
                   kv4_decode_workspace_size, kv4_pool, kv4_read, page_plan, page_slots)
 from .kv4 import signatures as _kv4_signatures
+from .pages import page_compact, page_copy, page_fork, page_free
+from .pages import signatures as _pages_signatures
 from .rope import rope, rope_bwd, rope_freqs
 from .rope import signatures as _rope_signatures
 
@@ -35,7 +39,7 @@ __all__ = ["Dims", "NsaError", "load", "workspace_size", "index", "index_view", 
            "kernel_names", "make_dims", "LIB_PATH", "page_plan", "page_slots", "kv4_pool",
            "kv4_append", "kv4_read", "kv4_decode", "kv4_decode_workspace_size",
            "DEVERR_BAD_INDEX", "DEVERR_BAD_SEQLENS", "DEVERR_NO_PAGES", "rope_freqs", "rope",
-           "rope_bwd"]
+           "rope_bwd", "page_fork", "page_free", "page_compact", "page_copy"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnsa_sel.so")
@@ -108,6 +112,7 @@ def load():
         "nsa_sel_attn_profile_collect": (st, [ctypes.POINTER(i32), ctypes.POINTER(f32)]),
         "nsa_status_string": (ctypes.c_char_p, [st]),
         **_kv4_signatures(),
+        **_pages_signatures(),
         **_rope_signatures(),
     }
     for name, (res, args) in sig.items():

@@ -1,5 +1,5 @@
 // kv4.cuh -- the 4-bit paged KV cache: record layout, launch parameters and small
-// device helpers shared by pages.cu, kv4_rows.cu, kv4_decode.cu and kv4_api.cu.  The
+// device helpers shared by pages.cu, page_ops.cu, rope.cu, kv4_rows.cu, kv4_decode.cu and kv4_api.cu.  The
 // record is described in include/nsa_kv4.h.
 #pragma once
 
@@ -16,6 +16,19 @@ struct PageParams {
   const int32_t *free_pages, *free_head;
   int32_t *table;                // read; in a plan its new entries are written too
   int32_t *slots, *seq_out, *cu_out, *head_out;
+  int32_t *status;               // may be null
+};
+
+// Forks, frees and compactions of the pages of a cache (page_ops.cu).
+constexpr int kMaxOpsPages = 1 << 22;   // a cluster of eight keeps a bit and a count per page
+
+struct PageOpsParams {
+  int num_seqs, page, width, num_pages, num_free, count;
+  const int32_t *table_in, *shares_in;   // compaction: may be the outputs
+  int32_t *table, *lens;
+  const int32_t *rows_from, *rows_to, *fork_lens;
+  const int32_t *head_in;
+  int32_t *shares, *free_pages, *head_out, *copy_src, *copy_dst;
   int32_t *status;               // may be null
 };
 
@@ -86,6 +99,17 @@ __device__ __forceinline__ void raise(int32_t *status, int32_t bits) {
   if (status) set_status(status, bits);
 }
 
+// A shared-memory address of another CTA of the cluster, and the cluster's barrier.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Kernels of this group start while the one before them on the stream still runs (their
 // launch overlaps its end) and touch no memory before it has finished.  They read with plain loads:
 // what a read-only load (ld.global.nc, __ldg) takes must not change while the kernel runs, which
@@ -115,6 +139,10 @@ inline cudaError_t launch_kv4(void (*kernel)(P...), dim3 grid, int threads, size
 }
 
 cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s);
+enum class PageOp { kFork, kFree, kCompact };
+cudaError_t launch_page_op(PageOp op, const PageOpsParams &p, cudaStream_t s);
+cudaError_t launch_page_copy(int num_pages, int64_t page_bytes, int n, void *pool, const int32_t *src,
+                             const int32_t *dst, int32_t *status, cudaStream_t s);
 cudaError_t launch_kv4_append(int d, bool fp16, const Kv4RowParams &p, cudaStream_t s);
 cudaError_t launch_kv4_read(int d, bool fp16, const Kv4RowParams &p, cudaStream_t s);
 size_t kv4_decode_workspace(int d, int g, bool selected);

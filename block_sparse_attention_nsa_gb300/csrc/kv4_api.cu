@@ -1,6 +1,7 @@
 // kv4_api.cu -- the C ABI of include/nsa_kv4.h: argument checks and launches.
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 
 #include "kv4.cuh"
 
@@ -21,6 +22,41 @@ nsa_status check_pages(const nsa_page_dims *d) {
   if ((int64_t)d->table_width * d->page_size >= most || (int64_t)d->num_pages * d->page_size >= most)
     return NSA_ERR_UNSUPPORTED;
   return NSA_OK;
+}
+
+nsa_status check_ops(const nsa_page_ops_dims *d, bool rows) {
+  if (!d) return NSA_ERR_INVALID_ARG;
+  if (d->num_seqs < 1 || d->page_size < 1 || d->table_width < 1 || d->num_pages < 0 ||
+      d->num_free < 0 || d->count < 0)
+    return NSA_ERR_INVALID_ARG;
+  if (d->num_seqs > kMaxPlanSeqs || d->num_pages > kMaxOpsPages || (rows && d->count > kMaxPlanSeqs) ||
+      (int64_t)d->table_width * d->page_size >= (int64_t(1) << 31))
+    return NSA_ERR_UNSUPPORTED;
+  return NSA_OK;
+}
+
+PageOpsParams ops_params(const nsa_page_ops_dims *d, int32_t *status) {
+  PageOpsParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.num_seqs = d->num_seqs;
+  p.page = d->page_size;
+  p.width = d->table_width;
+  p.num_pages = d->num_pages;
+  p.num_free = d->num_free;
+  p.count = d->count;
+  p.status = status;
+  return p;
+}
+
+// All of them there (where `needed`) and 4-byte aligned.
+struct IntArg {
+  const void *ptr;
+  bool needed;
+};
+bool ints_ok(std::initializer_list<IntArg> args) {
+  for (const IntArg &a : args)
+    if ((a.needed && !a.ptr) || !on(a.ptr, 4)) return false;
+  return true;
 }
 
 nsa_status check_kv4(const nsa_kv4_dims *d) {
@@ -129,6 +165,93 @@ nsa_status nsa_page_slots(const nsa_page_dims *dims, const int32_t *block_table,
   p.cu_out = cu;
   p.status = device_status;
   return launched(launch_pages(p, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nsa_status nsa_page_fork(const nsa_page_ops_dims *dims, int32_t *block_table, int32_t *seq_lens,
+                         const int32_t *parents, const int32_t *children, const int32_t *fork_lens,
+                         int32_t *shares, const int32_t *free_pages, const int32_t *free_head,
+                         int32_t *copy_src, int32_t *copy_dst, int32_t *head_out,
+                         int32_t *device_status, nsa_stream_t stream) {
+  nsa_status st = check_ops(dims, true);
+  if (st != NSA_OK) return st;
+  const bool any = dims->count > 0;
+  if (!ints_ok({{block_table, true}, {seq_lens, true}, {parents, any}, {children, any},
+                {fork_lens, false}, {shares, dims->num_pages > 0}, {free_pages, dims->num_free > 0},
+                {free_head, true}, {copy_src, any}, {copy_dst, any}, {head_out, true},
+                {device_status, false}}))
+    return NSA_ERR_INVALID_ARG;
+  PageOpsParams p = ops_params(dims, device_status);
+  p.table = block_table;
+  p.lens = seq_lens;
+  p.rows_from = parents;
+  p.rows_to = children;
+  p.fork_lens = fork_lens;
+  p.shares = shares;
+  p.free_pages = const_cast<int32_t *>(free_pages);   // only read by a fork
+  p.head_in = free_head;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.head_out = head_out;
+  return launched(launch_page_op(PageOp::kFork, p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nsa_status nsa_page_free(const nsa_page_ops_dims *dims, int32_t *block_table, int32_t *seq_lens,
+                         const int32_t *rows, int32_t *shares, int32_t *free_pages,
+                         const int32_t *free_head, int32_t *head_out, int32_t *device_status,
+                         nsa_stream_t stream) {
+  nsa_status st = check_ops(dims, true);
+  if (st != NSA_OK) return st;
+  if (!ints_ok({{block_table, true}, {seq_lens, true}, {rows, dims->count > 0},
+                {shares, dims->num_pages > 0}, {free_pages, dims->num_free > 0}, {free_head, true},
+                {head_out, true}, {device_status, false}}))
+    return NSA_ERR_INVALID_ARG;
+  PageOpsParams p = ops_params(dims, device_status);
+  p.table = block_table;
+  p.lens = seq_lens;
+  p.rows_from = rows;
+  p.shares = shares;
+  p.free_pages = free_pages;
+  p.head_in = free_head;
+  p.head_out = head_out;
+  return launched(launch_page_op(PageOp::kFree, p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nsa_status nsa_page_compact(const nsa_page_ops_dims *dims, const int32_t *block_table,
+                            const int32_t *seq_lens, const int32_t *shares, int32_t *table_out,
+                            int32_t *shares_out, int32_t *free_out, int32_t *copy_src,
+                            int32_t *copy_dst, int32_t *head_out, int32_t *device_status,
+                            nsa_stream_t stream) {
+  nsa_status st = check_ops(dims, false);
+  if (st != NSA_OK) return st;
+  const bool any = dims->count > 0, pages = dims->num_pages > 0;
+  if (!ints_ok({{block_table, true}, {seq_lens, true}, {shares, pages}, {table_out, true},
+                {shares_out, pages}, {free_out, dims->num_free > 0}, {copy_src, any},
+                {copy_dst, any}, {head_out, true}, {device_status, false}}))
+    return NSA_ERR_INVALID_ARG;
+  PageOpsParams p = ops_params(dims, device_status);
+  p.table_in = block_table;
+  p.table = table_out;
+  p.lens = const_cast<int32_t *>(seq_lens);           // only read by a compaction
+  p.shares_in = shares;
+  p.shares = shares_out;
+  p.free_pages = free_out;
+  p.copy_src = copy_src;
+  p.copy_dst = copy_dst;
+  p.head_out = head_out;
+  return launched(launch_page_op(PageOp::kCompact, p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+nsa_status nsa_page_copy(int32_t num_pages, int64_t page_bytes, int32_t count, void *pool,
+                         const int32_t *src, const int32_t *dst, int32_t *device_status,
+                         nsa_stream_t stream) {
+  if (num_pages < 0 || page_bytes < 1 || count < 0) return NSA_ERR_INVALID_ARG;
+  if (page_bytes % 16 || page_bytes >= (int64_t(1) << 40)) return NSA_ERR_UNSUPPORTED;
+  if (count == 0) return NSA_OK;
+  if ((num_pages > 0 && !pool) || !on(pool, 16) ||
+      !ints_ok({{src, true}, {dst, true}, {device_status, false}}))
+    return NSA_ERR_INVALID_ARG;
+  return launched(launch_page_copy(num_pages, page_bytes, count, pool, src, dst, device_status,
+                                   reinterpret_cast<cudaStream_t>(stream)));
 }
 
 nsa_status nsa_kv4_page_bytes(const nsa_kv4_dims *dims, size_t *bytes) {

@@ -794,11 +794,6 @@ __device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int h
     p.lse[(int64_t)hq * p.num_seqs + b] = any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, int rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
 __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -811,10 +806,6 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t a) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
   return v;
-}
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // kWarps warps per segment, in one CTA; kCluster: in each of a cluster's `parts` CTAs.

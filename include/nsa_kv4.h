@@ -1,7 +1,7 @@
 /*
  * nsa_kv4.h -- C ABI of the paged KV cache held in 4 bits: block tables and slot maps
- * built on the GPU, rows written and read back, and the one-step decode that attends
- * to the pages.
+ * built on the GPU, rows of the table forked and freed, pages compacted and copied, rows
+ * of K and V written and read back, and the one-step decode that attends to the pages.
  *
  * Conventions are those of nsa_sel_attn.h: device pointers owned by the caller, calls
  * asynchronous on `stream`, arguments checked before anything is enqueued, no device
@@ -41,7 +41,7 @@ extern "C" {
 
 /* A bit of the device status words of this header, beside those of nsa_sel_attn.h. */
 enum {
-    NSA_DEVERR_NO_PAGES = 8 /* nsa_page_plan: the free list or the slot map is too short */
+    NSA_DEVERR_NO_PAGES = 8 /* the free list, the slot map or a list of copies is too short */
 };
 
 typedef struct {
@@ -88,6 +88,88 @@ NSA_API nsa_status nsa_page_slots(const nsa_page_dims *dims, const int32_t *bloc
                                   const int32_t *start, const int32_t *count,
                                   int32_t *slot_map, int32_t *cu, int32_t *device_status,
                                   nsa_stream_t stream);
+
+/* Forks, frees and compactions.  Beside the block table and the free list (the pages free_pages[
+ * free_head[0]] ... free_pages[num_free - 1] belong to nobody; the entries before them are room)
+ * the caller keeps
+ *   shares       int32 [num_pages]: rows that name a page beyond the first; 0 at the beginning, and
+ *                nsa_page_plan, which opens pages for one row each, needs none of it.
+ * A page named by a row is one of its first ceil(seq_lens / P) entries.  nsa_page_plan writes tokens
+ * into a row's last page where that is partly full, so that only full pages are shared. */
+typedef struct {
+    int32_t num_seqs;    /* B rows of the table, 1 ... 16384 */
+    int32_t page_size;   /* P tokens per page, >= 1 */
+    int32_t table_width; /* block_table columns, >= 1; table_width * P < 2^31 */
+    int32_t num_pages;   /* entries of shares, 0 ... 2^22 */
+    int32_t num_free;    /* entries of free_pages */
+    int32_t count;       /* entries of the row lists (0 ... 16384) or of the lists of copies */
+} nsa_page_ops_dims;
+
+/* Forks: row children[i] becomes a continuation of row parents[i] (int32 [count]) behind its first
+ * n = fork_lens[i] tokens (fork_lens may be NULL: n = seq_lens[parents[i]]).  It gets the parent's
+ * floor(n / P) full pages, whose shares grow by one, and, where n % P > 0, the next page of the free
+ * list, into which (copy_src[i], copy_dst[i]) says what to copy (nsa_page_copy, for each pool that
+ * the table stands for); the pair is -1 where nothing has to be.  Its length becomes n; entries
+ * behind it are left alone.  What the child's row held is forgotten, not freed (nsa_page_free).
+ * A parent may have several children.  head_out int32 [1], which may be free_head, gets the head
+ * advanced by the pages taken.
+ * A fork is refused, which leaves the child's row and length alone and its pair -1,
+ *   with NSA_DEVERR_BAD_INDEX: a row outside the table, a child that is also a parent, or that an
+ *                              earlier entry has named;
+ *   with NSA_DEVERR_BAD_SEQLENS: a length n that is negative or beyond the parent's, or a parent's
+ *                              length beyond the table;
+ *   with NSA_DEVERR_NO_PAGES:  the free list ends before its page (later ones that need a page are
+ *                              then refused too).
+ * A page id outside 0 ... num_pages - 1, from the table or the free list, sets
+ * NSA_DEVERR_BAD_INDEX: the child's entry is -1, or its pair where the copy's source is meant. */
+NSA_API nsa_status nsa_page_fork(const nsa_page_ops_dims *dims, int32_t *block_table,
+                                 int32_t *seq_lens, const int32_t *parents,
+                                 const int32_t *children, const int32_t *fork_lens,
+                                 int32_t *shares, const int32_t *free_pages,
+                                 const int32_t *free_head, int32_t *copy_src, int32_t *copy_dst,
+                                 int32_t *head_out, int32_t *device_status, nsa_stream_t stream);
+
+/* Frees rows (int32 [count]): each of a row's pages loses one owner; those without another go to
+ * the free list, in ascending order, into the entries just before its head (head_out, which may be
+ * free_head, gets the head less their number).  The row's entries become -1, its length 0.
+ * A row outside the table, and one that the list has named before, is passed over with
+ * NSA_DEVERR_BAD_INDEX, a row whose length is negative or beyond the table with
+ * NSA_DEVERR_BAD_SEQLENS.  Page ids outside 0 ... num_pages - 1 are passed over, and a page that more
+ * rows give up than its shares count is freed once, both with NSA_DEVERR_BAD_INDEX.  Where the list
+ * has too few entries before its head (or the head lies outside 0 ... num_free), the smallest ids
+ * (all) are left out of it, with NSA_DEVERR_NO_PAGES. */
+NSA_API nsa_status nsa_page_free(const nsa_page_ops_dims *dims, int32_t *block_table,
+                                 int32_t *seq_lens, const int32_t *rows, int32_t *shares,
+                                 int32_t *free_pages, const int32_t *free_head, int32_t *head_out,
+                                 int32_t *device_status, nsa_stream_t stream);
+
+/* Compacts the pool: with n pages named by the table's rows, those among them with ids from n on
+ * move, in ascending order, to the ids below n that no row names, in ascending order.  copy_src and
+ * copy_dst (int32 [count]) get the moves, -1 behind them; no page is the source of one and the
+ * destination of another, so that nsa_page_copy may make them in any order.  table_out and shares_out,
+ * which may be block_table and shares, get the new ids and counts (0 from n on); the last
+ * num_pages - n entries of free_out get n ... num_pages - 1, those before are left alone; head_out
+ * int32 [1] gets num_free - (num_pages - n).  Pages that no row names count as free: the old free
+ * list is not read.
+ * Where count is less than the moves, or num_free than num_pages - n, NSA_DEVERR_NO_PAGES is set and
+ * nothing changes: table_out and shares_out get their inputs, the lists -1, free_out and head_out are
+ * left alone.  count >= num_pages / 2 always suffices.
+ * Page ids outside 0 ... num_pages - 1 stay, with NSA_DEVERR_BAD_INDEX; a length outside the table
+ * counts as its nearest end, with NSA_DEVERR_BAD_SEQLENS. */
+NSA_API nsa_status nsa_page_compact(const nsa_page_ops_dims *dims, const int32_t *block_table,
+                                    const int32_t *seq_lens, const int32_t *shares,
+                                    int32_t *table_out, int32_t *shares_out, int32_t *free_out,
+                                    int32_t *copy_src, int32_t *copy_dst, int32_t *head_out,
+                                    int32_t *device_status, nsa_stream_t stream);
+
+/* Copies pages of a pool of num_pages records of page_bytes bytes each (all heads of a page; a
+ * multiple of 16, the pool 16-byte aligned): record src[i] to record dst[i], i < count.  Pairs of
+ * two -1 are skipped; others with an id outside the pool too, with NSA_DEVERR_BAD_INDEX.  A page is
+ * the destination of one pair at most, and of none if it is a source: what else is left in it is
+ * not defined. */
+NSA_API nsa_status nsa_page_copy(int32_t num_pages, int64_t page_bytes, int32_t count, void *pool,
+                                 const int32_t *src, const int32_t *dst, int32_t *device_status,
+                                 nsa_stream_t stream);
 
 typedef struct {
     int32_t num_pages; /* pages of the pool; num_pages * page_size < 2^31 */
