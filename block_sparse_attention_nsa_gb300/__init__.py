@@ -10,7 +10,7 @@ Names follow the C ABI in include/nsa_sel_attn.h:
   window_select, fwd_window, bwd_window, gate_combine, gate_combine_bwd,
   compress_kv, cmp_attn_select, profile_enable, profile_collect.
 The 4-bit paged KV cache (include/nsa_kv4.h) is bound in kv4.py and offered here too:
-  page_plan, page_slots, kv4_pool, kv4_append, kv4_read, kv4_decode.
+  page_plan, page_slots, kv4_pool, kv4_append, kv4_read, kv4_decode, kv4_decode_shared.
 The life of its pages is bound in pages.py:
   page_fork, page_free, page_compact, page_copy.
 Rotary positions (include/nsa_rope.h) are bound in rope.py:
@@ -25,7 +25,8 @@ from typing import Optional
 import torch
 
 from .kv4 import (DEVERR_BAD_INDEX, DEVERR_BAD_SEQLENS, DEVERR_NO_PAGES, kv4_append, kv4_decode,
-                  kv4_decode_workspace_size, kv4_pool, kv4_read, page_plan, page_slots)
+                  kv4_decode_shared, kv4_decode_shared_workspace_size, kv4_decode_workspace_size,
+                  kv4_pool, kv4_read, page_plan, page_slots)
 from .kv4 import signatures as _kv4_signatures
 from .pages import page_compact, page_copy, page_fork, page_free
 from .pages import signatures as _pages_signatures
@@ -39,7 +40,8 @@ __all__ = ["Dims", "NsaError", "load", "workspace_size", "index", "index_view", 
            "kernel_names", "make_dims", "LIB_PATH", "page_plan", "page_slots", "kv4_pool",
            "kv4_append", "kv4_read", "kv4_decode", "kv4_decode_workspace_size",
            "DEVERR_BAD_INDEX", "DEVERR_BAD_SEQLENS", "DEVERR_NO_PAGES", "rope_freqs", "rope",
-           "rope_bwd", "page_fork", "page_free", "page_compact", "page_copy"]
+           "rope_bwd", "page_fork", "page_free", "page_compact", "page_copy",
+           "kv4_decode_shared", "kv4_decode_shared_workspace_size"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libnsa_sel.so")

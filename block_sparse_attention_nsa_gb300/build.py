@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnsa_sel.so")
 SOURCES = ["api.cu", "index_build.cu", "fwd.cu", "bwd.cu", "noalloc.cu", "decode.cu", "window.cu",
-           "compress.cu", "pages.cu", "page_ops.cu", "kv4_rows.cu", "kv4_decode.cu", "kv4_api.cu", "rope.cu"]
+           "compress.cu", "pages.cu", "page_ops.cu", "kv4_rows.cu", "kv4_decode.cu", "kv4_shared.cu",
+           "kv4_api.cu", "rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -64,7 +64,16 @@ struct Kv4DecodeParams {
   float *lse;
   int32_t *status;
   void *ws;
+  // behind a shared prefix (kv4_shared.cu): each sequence's first key, and records in the place of
+  // out and lse
+  const int32_t *lo;
+  float *rec;
 };
+
+// A record: the sums of a (sequence, query head), not divided, then its maximum (in the exponent of
+// 2) and sum of weights.
+template <int D>
+constexpr int kRecFloats = D + 4;
 
 // Two fp32 operations in one instruction, each rounded to nearest.
 struct Pair {
@@ -148,5 +157,15 @@ cudaError_t launch_kv4_read(int d, bool fp16, const Kv4RowParams &p, cudaStream_
 size_t kv4_decode_workspace(int d, int g, bool selected);
 int64_t kv4_decode_tiles(const Kv4DecodeParams &p);
 cudaError_t launch_kv4_decode(int d, bool fp16, const Kv4DecodeParams &p, cudaStream_t s);
+cudaError_t launch_kv4_suffix(int d, bool fp16, const Kv4DecodeParams &p, cudaStream_t s);
+
+struct Kv4SharedParams {
+  Kv4DecodeParams dec;               // ws: the suffixes' part of the workspace
+  int num_groups;
+  const int32_t *cu, *prefix;        // [groups + 1], [groups]
+  uint8_t *ws;                       // the rest
+};
+size_t kv4_shared_workspace(int d, int num_seqs, int h_q, int num_groups);
+cudaError_t launch_kv4_shared(int d, bool fp16, const Kv4SharedParams &p, cudaStream_t s);
 
 }  // namespace nsa

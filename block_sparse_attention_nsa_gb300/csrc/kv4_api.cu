@@ -318,12 +318,13 @@ nsa_status nsa_kv4_decode_workspace_size(const nsa_kv4_dims *dims, int32_t num_s
   return NSA_OK;
 }
 
-nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_q,
-                          int32_t table_width, int32_t topk, int32_t window, const void *q,
-                          const void *pool, const int32_t *block_table, const int32_t *seq_lens,
-                          const int32_t *sel_idx, float scale, void *out, float *lse,
-                          int32_t *device_status, void *workspace, size_t workspace_bytes,
-                          nsa_stream_t stream) {
+// Checks of what both decodes take, and their parameters.
+static nsa_status decode_params(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_q,
+                                int32_t table_width, int32_t topk, int32_t window, const void *q,
+                                const void *pool, const int32_t *block_table,
+                                const int32_t *seq_lens, const int32_t *sel_idx, float scale, void *out,
+                                float *lse, int32_t *device_status, void *workspace,
+                                Kv4DecodeParams &p) {
   nsa_status st = check_decode(dims, num_seqs, h_q, topk);
   if (st != NSA_OK) return st;
   if (table_width < 1 || window < 0 || !std::isfinite(scale)) return NSA_ERR_INVALID_ARG;
@@ -334,15 +335,11 @@ nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_
   if (!on(q, 16) || !on(pool, 16) || !on(out, 16) || !on(workspace, 16) || !on(block_table, 4) ||
       !on(seq_lens, 4) || !on(sel_idx, 4) || !on(lse, 4) || !on(device_status, 4))
     return NSA_ERR_INVALID_ARG;
-  const int g = h_q / dims->h_k;
-  const size_t need = kv4_decode_workspace(dims->head_dim, g, topk > 0);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return NSA_ERR_WORKSPACE;
-  Kv4DecodeParams p;
   std::memset(&p, 0, sizeof(p));
   p.num_seqs = num_seqs;
   p.h_q = h_q;
   p.h_k = dims->h_k;
-  p.g = g;
+  p.g = h_q / dims->h_k;
   p.num_pages = dims->num_pages;
   p.page_log2 = log2_of(dims->page_size);
   p.width = table_width;
@@ -358,8 +355,71 @@ nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_
   p.lse = lse;
   p.status = device_status;
   p.ws = workspace;
+  return NSA_OK;
+}
+
+nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_q,
+                          int32_t table_width, int32_t topk, int32_t window, const void *q,
+                          const void *pool, const int32_t *block_table, const int32_t *seq_lens,
+                          const int32_t *sel_idx, float scale, void *out, float *lse,
+                          int32_t *device_status, void *workspace, size_t workspace_bytes,
+                          nsa_stream_t stream) {
+  Kv4DecodeParams p;
+  const nsa_status st =
+      decode_params(dims, num_seqs, h_q, table_width, topk, window, q, pool, block_table, seq_lens,
+                    sel_idx, scale, out, lse, device_status, workspace, p);
+  if (st != NSA_OK) return st;
+  const size_t need = kv4_decode_workspace(dims->head_dim, p.g, topk > 0);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return NSA_ERR_WORKSPACE;
   if (kv4_decode_tiles(p) >= (int64_t(1) << 30)) return NSA_ERR_UNSUPPORTED;
   return launched(launch_kv4_decode(dims->head_dim, dims->dtype == NSA_FP16, p,
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// The workspace: what the sequences' own parts take, then the plan and the partial results.
+static nsa_status check_shared(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_q,
+                               int32_t num_groups, size_t *first, size_t *bytes) {
+  const nsa_status st = check_decode(dims, num_seqs, h_q, 0);
+  if (st != NSA_OK) return st;
+  if (num_groups < 1) return NSA_ERR_INVALID_ARG;
+  if (num_groups > (1 << 20)) return NSA_ERR_UNSUPPORTED;
+  *first = (kv4_decode_workspace(dims->head_dim, h_q / dims->h_k, false) + 255) / 256 * 256;
+  *bytes = *first + kv4_shared_workspace(dims->head_dim, num_seqs, h_q, num_groups);
+  return NSA_OK;
+}
+
+nsa_status nsa_kv4_decode_shared_workspace_size(const nsa_kv4_dims *dims, int32_t num_seqs,
+                                                int32_t h_q, int32_t num_groups, size_t *bytes) {
+  size_t first, all;
+  const nsa_status st = check_shared(dims, num_seqs, h_q, num_groups, &first, &all);
+  if (st != NSA_OK) return st;
+  if (!bytes) return NSA_ERR_INVALID_ARG;
+  *bytes = all;
+  return NSA_OK;
+}
+
+nsa_status nsa_kv4_decode_shared(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_q,
+                                 int32_t table_width, int32_t num_groups, const void *q,
+                                 const void *pool, const int32_t *block_table,
+                                 const int32_t *seq_lens, const int32_t *cu_groups,
+                                 const int32_t *prefix_lens, float scale, void *out, float *lse,
+                                 int32_t *device_status, void *workspace, size_t workspace_bytes,
+                                 nsa_stream_t stream) {
+  Kv4SharedParams p;
+  size_t first, need;
+  nsa_status st = check_shared(dims, num_seqs, h_q, num_groups, &first, &need);
+  if (st == NSA_OK)
+    st = decode_params(dims, num_seqs, h_q, table_width, 0, 0, q, pool, block_table, seq_lens, nullptr,
+                       scale, out, lse, device_status, workspace, p.dec);
+  if (st != NSA_OK) return st;
+  if (!ints_ok({{cu_groups, true}, {prefix_lens, true}})) return NSA_ERR_INVALID_ARG;
+  if (!workspace || workspace_bytes < need) return NSA_ERR_WORKSPACE;
+  if (kv4_decode_tiles(p.dec) >= (int64_t(1) << 30)) return NSA_ERR_UNSUPPORTED;
+  p.num_groups = num_groups;
+  p.cu = cu_groups;
+  p.prefix = prefix_lens;
+  p.ws = static_cast<uint8_t *>(workspace) + first;
+  return launched(launch_kv4_shared(dims->head_dim, dims->dtype == NSA_FP16, p,
                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -588,13 +588,15 @@ __device__ __forceinline__ int seq_len(const Kv4DecodeParams &p, int b, int32_t 
   if (raw != len) err |= NSA_DEVERR_BAD_SEQLENS;
   return len;
 }
-__device__ __forceinline__ int seq_lo(const Kv4DecodeParams &p, int len) {
+template <bool kSuffix>
+__device__ __forceinline__ int seq_lo(const Kv4DecodeParams &p, int b, int len) {
+  if (kSuffix) return min(p.lo[b], len);
   return p.window > 0 && len > p.window ? len - p.window : 0;
 }
 
 // Fills a segment's tiles.  With a selection: the kept blocks, valid, first of their value,
 // with a page in the pool (64 words of scratch in shared memory bring them together).
-template <bool kSel>
+template <bool kSel, bool kSuffix>
 __device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg, uint8_t *scratch,
                                              int lane, int32_t &err) {
   int blk = -1;
@@ -602,9 +604,10 @@ __device__ __forceinline__ void open_segment(const Kv4DecodeParams &p, K4Seg &sg
     blk = p.sel[((int64_t)sg.h * p.num_seqs + sg.b) * p.topk + lane];
   int32_t ignore = 0;        // reported once, where the lengths are first read
   sg.len = seq_len(p, sg.b, ignore);
-  sg.lo = seq_lo(p, sg.len);
+  sg.lo = seq_lo<kSuffix>(p, sg.b, sg.len);
   sg.first = sg.lo >> 5;
   sg.tiles = ((sg.len + 31) >> 5) - sg.first;
+  if (kSuffix && sg.lo == sg.len) sg.tiles = 0;   // the tile at the prefix' end holds no key of its own
   if (kSel) {
     const int nblk = (sg.len + (1 << p.page_log2) - 1) >> p.page_log2;
     if (lane < p.topk && (blk < -1 || blk >= nblk)) err |= NSA_DEVERR_BAD_INDEX;
@@ -781,10 +784,16 @@ __device__ __forceinline__ void leave_out(float *area, int lane, const K4State<D
   }
 }
 
-// Final values of dimensions dim ... dim + 3 of query head hq.
-template <int D, bool kFp16>
+// Final values of dimensions dim ... dim + 3 of query head hq; or (kSuffix) its record.
+template <int D, bool kFp16, bool kSuffix = false>
 __device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int hq, int dim, float4 x,
                                           float M, float l) {
+  if constexpr (kSuffix) {
+    float *rec = p.rec + ((int64_t)b * p.h_q + hq) * kRecFloats<D>;
+    *reinterpret_cast<float4 *>(rec + dim) = x;
+    if (dim == 0) *reinterpret_cast<float2 *>(rec + D) = make_float2(M, l);
+    return;
+  }
   const bool any = l != 0.f;                        // a NaN sum stays one
   const float inv = any ? __fdividef(1.f, l) : 0.f;
   const int64_t row = (int64_t)b * p.h_q + hq;
@@ -825,7 +834,7 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps<D> / kWarps)
   after_previous();
   K4RawQuery<D> raw;
   fetch_query<D>(p, sg, lane, raw);
-  open_segment<kSel>(p, sg, smem + warp * K4<D>::kRing, lane, err);
+  open_segment<kSel, false>(p, sg, smem + warp * K4<D>::kRing, lane, err);
   const int first = rank * kWarps + warp;
   K4Stream<D, kFp16, kSel> st(p, sg, first, max(0, (sg.tiles - first + step - 1) / step), step,
                               smem + warp * K4<D>::kRing, true, lane);
@@ -925,8 +934,9 @@ __global__ void __launch_bounds__(kWarps * 32, kSmWarps<D> / kWarps)
 
 // Tiles that a sequence's segments count as: what they have, at least one, so that an empty
 // one's output is written too, and kOver.
-__device__ __forceinline__ int counted_tiles(const Kv4DecodeParams &p, int len) {
-  return max(((len + 31) >> 5) - (seq_lo(p, len) >> 5), 1) + kOver;
+template <bool kSuffix>
+__device__ __forceinline__ int counted_tiles(const Kv4DecodeParams &p, int b, int len) {
+  return max(((len + 31) >> 5) - (seq_lo<kSuffix>(p, b, len) >> 5), 1) + kOver;
 }
 
 __device__ __forceinline__ K4Split *splits_of(const Kv4DecodeParams &p) {
@@ -952,7 +962,7 @@ __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
 }
 
 // Equal runs of the batch's counted tiles.
-template <int D, bool kFp16>
+template <int D, bool kFp16, bool kSuffix>
 __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
     kv4_run_kernel(Kv4DecodeParams p, int units) {
   constexpr int kWarps = K4<D>::kRunWarps, kThreads = K4<D>::kRunThreads;
@@ -969,7 +979,7 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
   const int b0 = min(tid * per_thread, p.num_seqs), b1 = min(b0 + per_thread, p.num_seqs);
   int32_t err = 0, ignore = 0;
   int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += counted_tiles(p, seq_len(p, b, err));
+  for (int b = b0; b < b1; ++b) mine += counted_tiles<kSuffix>(p, b, seq_len(p, b, err));
   if (blockIdx.x == 0 && err) raise(p.status, err);
   err = 0;
   pre[tid] = warp_incl_sum(mine * units, lane);
@@ -992,7 +1002,8 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
     if (per_thread == 1) return;
     while (b < p.num_seqs) {               // 32 sequences at a time
       const int n = b + lane < p.num_seqs
-                        ? counted_tiles(p, seq_len(p, b + lane, ignore)) * units : 0;
+                        ? counted_tiles<kSuffix>(p, b + lane, seq_len(p, b + lane, ignore)) * units
+                        : 0;
       const int in = warp_incl_sum(n, lane);
       const uint32_t past = __ballot_sync(0xffffffffu, v < base + in);
       const int hit = past ? __ffs(past) - 1 : 31;
@@ -1021,7 +1032,7 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
   while (at < stop) {
     K4Seg sg = {};
     sg.b = b;
-    if (unit <= 0) nt = counted_tiles(p, seq_len(p, b, ignore));
+    if (unit <= 0) nt = counted_tiles<kSuffix>(p, b, seq_len(p, b, ignore));
     if (unit < 0) unit = (at - base) / nt;
     set_unit(p, unit, sg);
     const int seg0 = base + unit * nt;
@@ -1030,7 +1041,7 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
     if (v1 > kOver) {
       K4RawQuery<D> raw;
       fetch_query<D>(p, sg, lane, raw);
-      open_segment<false>(p, sg, ring, lane, err);
+      open_segment<false, kSuffix>(p, sg, ring, lane, err);
       const int t0 = max(0, v0 - kOver), t1 = min(v1 - kOver, sg.tiles);
       K4Stream<D, kFp16, false> st(p, sg, t0, max(0, t1 - t0), 1, ring, !(left & kKeep), lane);
       st.start(err);
@@ -1060,7 +1071,8 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
         const float4 o = *reinterpret_cast<const float4 *>(
             area + (head >> 1) * K4<D>::kHeadPair + (head & 1) * D + dim);
         const float4 v = ml[1][warp][head >> 1];
-        write_out<D, kFp16>(p, b, sg.q0 + head, dim, o, head & 1 ? v.z : v.x, head & 1 ? v.w : v.y);
+        write_out<D, kFp16, kSuffix>(p, b, sg.q0 + head, dim, o, head & 1 ? v.z : v.x,
+                                     head & 1 ? v.w : v.y);
       }
       __syncwarp();                        // read before the ring is filled again
     }
@@ -1166,7 +1178,7 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
         dst[1] = make_float2(x.z, x.w);
         if (dim == 0) *reinterpret_cast<float2 *>(part + sg.g * D + 2 * head) = make_float2(M, l);
       } else {
-        write_out<D, kFp16>(p, sg.b, sg.q0 + head, dim, x, M, l);
+        write_out<D, kFp16, kSuffix>(p, sg.b, sg.q0 + head, dim, x, M, l);
       }
     }
   }
@@ -1176,7 +1188,7 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
 // second part and the following CTAs' first ones.  One CTA per (split, head): its warps take
 // the parts in turn, eight in flight.
 constexpr int kMergeThreads = 256;
-template <int D, bool kFp16>
+template <int D, bool kFp16, bool kSuffix>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParams p, int units) {
   constexpr int kWarps = kMergeThreads / 32, E = D / 32;
   __shared__ __align__(16) float acc[kWarps][D];
@@ -1250,7 +1262,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParam
       u.z = fmaf(f, o.z, u.z);
       u.w = fmaf(f, o.w, u.w);
     }
-    write_out<D, kFp16>(p, sg.b, sg.q0 + head, 4 * tid, u, M, l);
+    write_out<D, kFp16, kSuffix>(p, sg.b, sg.q0 + head, 4 * tid, u, M, l);
   }
 }
 
@@ -1335,6 +1347,19 @@ static bool seg_better(int64_t segs, int64_t most, int ctas, int sms) {
   return 4.2 + 0.125 * most / ctas * on_sm < 8.9 + 0.125 * segs * most / sms;
 }
 
+template <int D, bool kFp16, bool kSuffix>
+static cudaError_t run_runs(const Kv4DecodeParams &p, int units, int sms, cudaStream_t s) {
+  const int ctas = min(sms * 2, kK4MaxCtas);               // resident at once
+  auto *kernel = kv4_run_kernel<D, kFp16, kSuffix>;
+  constexpr int threads = K4<D>::kRunThreads, smem = K4<D>::kRunWarps * K4<D>::kRing;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_kv4(kernel, dim3(ctas), threads, smem, 1, s, p, units);
+  if (e != cudaSuccess) return e;
+  return launch_kv4(kv4_merge_kernel<D, kFp16, kSuffix>, dim3(ctas, min(p.g, kK4Heads)), kMergeThreads, 0,
+                    1, s, p, units);
+}
+
 template <int D, bool kFp16, bool kSel>
 static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
   int dev = 0;
@@ -1365,15 +1390,7 @@ static cudaError_t run_decode4(const Kv4DecodeParams &p, cudaStream_t s) {
       default: return run_segs<D, kFp16, kSel, kHalf>(p, units, 1, s);
     }
   }
-  const int ctas = min(sms * 2, kK4MaxCtas);               // resident at once
-  auto *kernel = kv4_run_kernel<D, kFp16>;
-  constexpr int threads = K4<D>::kRunThreads, smem = K4<D>::kRunWarps * K4<D>::kRing;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  e = launch_kv4(kernel, dim3(ctas), threads, smem, 1, s, p, units);
-  if (e != cudaSuccess) return e;
-  return launch_kv4(kv4_merge_kernel<D, kFp16>, dim3(ctas, min(p.g, kK4Heads)), kMergeThreads, 0, 1,
-                    s, p, units);
+  return run_runs<D, kFp16, false>(p, units, sms, s);
 }
 
 template <int D, bool kFp16>
@@ -1384,6 +1401,19 @@ static cudaError_t run_decode4_sel(const Kv4DecodeParams &p, cudaStream_t s) {
 cudaError_t launch_kv4_decode(int d, bool fp16, const Kv4DecodeParams &p, cudaStream_t s) {
   if (d == 64) return fp16 ? run_decode4_sel<64, true>(p, s) : run_decode4_sel<64, false>(p, s);
   return fp16 ? run_decode4_sel<128, true>(p, s) : run_decode4_sel<128, false>(p, s);
+}
+
+template <int D, bool kFp16>
+static cudaError_t run_suffix(const Kv4DecodeParams &p, cudaStream_t s) {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return run_runs<D, kFp16, true>(p, p.h_k * head_parts(p.g), sm_count(dev), s);
+}
+
+cudaError_t launch_kv4_suffix(int d, bool fp16, const Kv4DecodeParams &p, cudaStream_t s) {
+  if (d == 64) return fp16 ? run_suffix<64, true>(p, s) : run_suffix<64, false>(p, s);
+  return fp16 ? run_suffix<128, true>(p, s) : run_suffix<128, false>(p, s);
 }
 
 }  // namespace nsa

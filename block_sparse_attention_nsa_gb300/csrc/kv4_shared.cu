@@ -1,0 +1,841 @@
+// kv4_shared.cu -- one-step decode over the 4-bit pages for sequences that share a prefix.
+//
+// The sequences of a group have the same first tokens, in the same pages.  Softmax over a sequence's
+// keys splits at the prefix' end into two sums that are joined by their maxima:
+//   out = (sum_prefix w v + sum_own w v) / (sum_prefix w + sum_own w),   w = exp(S - max S).
+// The prefix' part is a product of all the group's query rows with the same keys, done once per 128
+// rows on the tensor cores; each sequence's own part is kv4_decode.cu's, from the prefix' end on.
+//
+// Prefix kernel (tcgen05).  Rows of a KV head's tile are (sequence, query head) pairs, M = 128; 64
+// keys a block.  Scores need the exactness of fp32 (the log-sum-exp is returned in it), so K's codes
+// are operands as whole numbers, c - 8 in fp16, and scales and zeros come after, in fp32:
+//   x = sum_g ks_g A_g + (kz_g + 8 ks_g) Q_g,   A_g = sum over group g of q^ (c - 8),  Q_g = sum q^,
+//   S = x |scale| 2^(ex - 14);  q^ is q times 2^(14 - ex), ex the exponent of its largest magnitude,
+// so that fp16 holds bf16's and fp16's values (what is lost is 2^-38 of the largest).  A_g are
+// accumulators of their own in tensor memory, a group a K-major 64-column block of the operands.
+// Weights are w = 2^(S - m) 2^8 (with their factor those down to 2^-22 of the maximum are normal
+// numbers in fp16).  Two roundings to fp16, of 2^-11 at most each: V's values as they are unpacked, and
+// the weights, for bf16 outputs, whose own rounding is eight times as large.  For fp16 outputs, of
+// the same size, W is the sum of two fp16 numbers: with W in one part the error over a long prefix
+// was 1.66 times that of the output's rounding alone, with two 1.4.  Sums of weights are fp32, of
+// the weights before they are rounded.
+// The maximum m is raised only when a score passes it by 2^4, so that most blocks rescale nothing.
+//
+// Roles of a CTA (one an SM, 14 warps), handing blocks on by mbarriers, every wait bounded:
+//   loader       a block's two record tiles by bulk copies into a ring, page by page of the table;
+//   4 unpackers  codes to the K and V operands (128-byte swizzle; the eight dimensions of a word stay
+//                in the order 0 4 1 5 2 6 3 7 that masking gives, on both sides of the product and
+//                until the output is written), scales and zeros to fp32;
+//   MMA thread   S = Q K^T of block n + 1 ahead of O += W V of block n;
+//   2 x 4 softmax warps   a thread a row; the two warpgroups take every other block, each with its own
+//                maximum, sum and output, joined at the tile's end.  W goes to tensor memory over the
+//                scores it came from.
+// Work: the line of all (tile, block) pairs, tile after tile, in equal runs, one a CTA; where a tile
+// is shared by CTAs each leaves partial rows.  kv4_join_kernel adds them and the own part.
+#include <cmath>
+
+#include "kv4.cuh"
+
+namespace nsa {
+
+constexpr int kShRows = 128;         // query rows of a tile
+constexpr int kShKeys = 64;          // keys of a block
+constexpr int kShStages = 4;         // blocks unpacked ahead
+constexpr int kShRaw = 4;            // blocks copied ahead
+constexpr int kShThreads = 448;
+constexpr int kShMaxCtas = 256;
+constexpr int kShareMin = 2;         // sequences from which a prefix is shared
+constexpr int kSetupThreads = 1024;
+constexpr float kShSlack = 4.f;      // scores may exceed the reference by this much
+constexpr float kShUp = 8.f;         // weights are 2^8 times 2^(S - m)
+constexpr int kShMulTop = 88;        // a score's factor stays below 2^(kShMulTop + 2)
+
+// A group that shares: its first sequence and number of rows per KV head, its blocks and tiles, and
+// what lies before it: (tile, block) pairs, and partial rows.
+struct ShGroup {
+  int32_t seq0, rows, blocks, tiles, keys, pair0, row0, pad;
+};
+struct ShHead {
+  int32_t groups, pairs, per, pad;   // per: pairs of a CTA
+};
+struct ShPlan {
+  ShHead *head;
+  ShGroup *groups;                   // [num_groups]
+  int32_t *lo, *of;                  // [num_seqs]: first own key; group in `groups`, -1: none
+  int32_t *at;                       // [num_groups]: place of a group in `groups`
+  float *rec, *part;                 // records of the own parts, partial rows of the prefixes
+  float2 *part_ml;
+};
+
+static int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+static int64_t partial_rows(int num_seqs, int h_q) {
+  return (int64_t)kShMaxCtas * kShRows + (int64_t)num_seqs * h_q;
+}
+// The plan's places in a workspace, and its bytes.
+static int64_t shared_layout(int d, int num_seqs, int h_q, int num_groups, uint8_t *ws, ShPlan *p) {
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t x = at;
+    at += up16(bytes);
+    return ws + x;
+  };
+  ShPlan q;
+  q.head = reinterpret_cast<ShHead *>(take(sizeof(ShHead)));
+  q.groups = reinterpret_cast<ShGroup *>(take((int64_t)num_groups * sizeof(ShGroup)));
+  q.lo = reinterpret_cast<int32_t *>(take(4 * (int64_t)num_seqs));
+  q.of = reinterpret_cast<int32_t *>(take(4 * (int64_t)num_seqs));
+  q.at = reinterpret_cast<int32_t *>(take(4 * (int64_t)num_groups));
+  q.rec = reinterpret_cast<float *>(take((int64_t)num_seqs * h_q * (d + 4) * 4));
+  q.part_ml = reinterpret_cast<float2 *>(take(partial_rows(num_seqs, h_q) * 8));
+  q.part = reinterpret_cast<float *>(take(partial_rows(num_seqs, h_q) * d * 4));
+  if (p) *p = q;
+  return at;
+}
+
+// ---- setup -----------------------------------------------------------------------------
+// Inclusive prefix over the CTA; total gets the sum.
+__device__ __forceinline__ int setup_incl(int x, int (&part)[32], int &total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  int w = part[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
+  }
+  total = __shfl_sync(0xffffffffu, w, 31);
+  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+  return x + (warp ? before : 0);
+}
+
+// One CTA: groups that share, in order, what lies before each, and each sequence's group and first own
+// key.  A cu_groups out of order shares nothing.
+__global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParams p, ShPlan plan, int ctas,
+                                                                  int least) {
+  __shared__ int part[32];
+  const int tid = threadIdx.x, cap = p.dec.width << p.dec.page_log2;
+  after_previous();
+  int32_t err = 0;
+  for (int i = tid; i < p.num_groups; i += kSetupThreads) {
+    const int a = p.cu[i], b = p.cu[i + 1];
+    if (a < 0 || (i == 0 && a != 0) || b < a || b > p.dec.num_seqs) err |= NSA_DEVERR_BAD_SEQLENS;
+  }
+  const bool ordered = !__syncthreads_or(err);
+  int groups = 0, pairs = 0, rows = 0;
+  for (int i0 = 0; ordered && i0 < p.num_groups; i0 += kSetupThreads) {
+    const int i = i0 + tid;
+    int n = 0, keys = 0, a = 0;
+    if (i < p.num_groups) {
+      a = p.cu[i];
+      n = p.cu[i + 1] - a;
+      keys = p.prefix[i];
+      if (keys < 0 || keys > cap) {
+        err |= NSA_DEVERR_BAD_SEQLENS;
+        keys = 0;
+      }
+    }
+    const bool shares = n >= kShareMin && keys > 0;
+    const int r = shares ? n * p.dec.g : 0, tiles = (r + kShRows - 1) / kShRows;
+    const int blocks = (keys + kShKeys - 1) / kShKeys;
+    int total;
+    const int g = groups + setup_incl(shares, part, total) - shares;
+    groups += total;
+    const int w = tiles * p.dec.h_k * blocks;
+    const int before = pairs + setup_incl(w, part, total) - w;
+    pairs += total;
+    const int row = rows + setup_incl(r * p.dec.h_k, part, total) - r * p.dec.h_k;
+    rows += total;
+    if (shares) plan.groups[g] = ShGroup{a, r, blocks, tiles, keys, before, row, 0};
+    if (i < p.num_groups) plan.at[i] = shares ? g : -1;
+  }
+  if (tid == 0) {
+    const int per = max((pairs + ctas - 1) / ctas, least);
+    *plan.head = ShHead{groups, pairs, per, 0};
+  }
+  if (__syncthreads_or(err) && tid == 0) raise(p.dec.status, NSA_DEVERR_BAD_SEQLENS);
+  for (int b = tid; b < p.dec.num_seqs; b += kSetupThreads) {
+    int g = -1, lo = 0;
+    if (ordered && b < p.cu[p.num_groups]) g = plan.at[upper_index(p.cu, p.num_groups, b)];
+    if (g >= 0) {
+      const int keys = plan.groups[g].keys;
+      // a sequence that ends inside the prefix attends to its own pages alone
+      if (min(max(p.dec.lens[b], 0), cap) >= keys) lo = keys;
+      else g = -1;
+    }
+    plan.lo[b] = lo;
+    plan.of[b] = g;
+  }
+}
+
+// ---- prefix ----------------------------------------------------------------------------
+template <int D>
+struct Sh {
+  using T = Kv4Tile<D>;
+  static constexpr int kG = T::kG;
+  static constexpr uint32_t kOperand = kShKeys * D * 2;        // K or V of a block
+  static constexpr uint32_t kRawBytes = 2 * T::kBytes;
+  static constexpr uint32_t kParBytes = kShKeys * kG * 2 * 4;  // scales and zeros of K
+  static constexpr uint32_t kOffQ = 0;
+  static constexpr uint32_t kOffK = kOffQ + kShRows * D * 2;
+  static constexpr uint32_t kOffV = kOffK + kShStages * kOperand;
+  static constexpr uint32_t kOffRaw = kOffV + kShStages * kOperand;
+  static constexpr uint32_t kOffPar = kOffRaw + kShRaw * kRawBytes;
+  static constexpr uint32_t kBytes = kOffPar + kShStages * kParBytes + 1024;   // + alignment
+  static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffRaw % 1024 == 0, "operands' alignment");
+  static_assert(kOffPar % 16 == 0 && kBytes <= 227 * 1024, "shared memory");
+  static constexpr uint32_t kScores = kG * kShKeys;            // columns of a warpgroup's scores
+  static constexpr uint32_t kCols = 2 * (kScores + D);
+  static_assert(kCols == 512 || kCols == 256, "tensor memory is taken in powers of two");
+};
+
+struct ShShared {
+  uint64_t raw_full[kShRaw], raw_empty[kShRaw], kv_full[kShStages], kv_empty[kShStages];
+  uint64_t q_full, o_free, s_full[2], p_full[2], o_done[2];
+  uint2 seen_raw[kShRaw], seen[kShStages];     // a block's keys that exist, a bit each
+  float2 ml[2][kShRows];                       // of the two warpgroups, at a tile's end
+  float sums[2][kShRows];                      // sums of q^
+  int top[2][kShRows];                         // largest magnitude of a row's part, as bits
+  uint32_t tmem;
+  int fail;
+};
+
+// One tile's blocks in a CTA's run.
+struct ShSpan {
+  int group, h, tile, first, end;              // blocks [first, end)
+  int part;                                    // where its partial rows lie
+};
+// Walks a CTA's run.
+struct ShWalk {
+  const ShGroup *groups;
+  ShGroup g;
+  int group, at, stop, n_groups, cta;
+  __device__ __forceinline__ ShWalk(const ShPlan &plan, int cta_) : groups(plan.groups), cta(cta_) {
+    const ShHead hd = *plan.head;
+    n_groups = hd.groups;
+    at = static_cast<int>(min((int64_t)cta * hd.per, (int64_t)hd.pairs));
+    stop = static_cast<int>(min((int64_t)at + hd.per, (int64_t)hd.pairs));
+    group = 0;
+    if (at < stop) {
+      int lo = 0, hi = n_groups - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (groups[mid].pair0 <= at) lo = mid; else hi = mid - 1;
+      }
+      group = lo;
+      g = groups[group];
+    }
+  }
+  __device__ __forceinline__ bool next(ShSpan &s, int h_k) {
+    if (at >= stop) return false;
+    if (at >= g.pair0 + g.tiles * h_k * g.blocks) g = groups[++group];
+    const int rel = at - g.pair0, tile = rel / g.blocks;        // of the group's h_k * tiles
+    s.group = group;
+    s.h = tile / g.tiles;
+    s.tile = tile - s.h * g.tiles;
+    s.first = rel - tile * g.blocks;
+    s.end = min(g.blocks, s.first + (stop - at));
+    s.part = cta * kShRows + g.row0 + s.h * g.rows + s.tile * kShRows;
+    at += s.end - s.first;
+    return true;
+  }
+};
+
+// Waits that give up after two seconds, once for the CTA (*fail).
+__device__ __forceinline__ bool sh_wait(uint64_t *bar, uint32_t parity, int32_t *status,
+                                        volatile int *fail) {
+  const uint32_t addr = smem_u32(bar);
+  if (mbar_try_wait(addr, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (*fail) return false;
+    if (mbar_try_wait(addr, parity)) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      *fail = 1;
+      raise(status, NSA_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// The codes of a word as fp16 less `off` - 1024: dimensions (0, 4), (1, 5), (2, 6), (3, 7).
+__device__ __forceinline__ uint4 code_halves(uint32_t w, __half2 off) {
+  uint32_t u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t c = (w >> (4 * k) & 0x000f000fu) | 0x64006400u;   // 1024 + c
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&c), off);
+    u[k] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+__device__ __forceinline__ uint32_t scaled(uint32_t c, __half2 s, __half2 z) {
+  const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&c), s, z);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// V's values past fp16's largest, which the rounding of a scale can make of 65504, are held to it.
+__device__ __forceinline__ uint32_t held(uint32_t v) {
+  const __half2 top = __float2half2_rn(65504.f), h = *reinterpret_cast<const __half2 *>(&v);
+  const __half2 x = __hmin2_nan(__hmax2_nan(h, __hneg2(top)), top);
+  return *reinterpret_cast<const uint32_t *>(&x);
+}
+
+template <int D>
+__device__ __forceinline__ void unpack_block(const uint8_t *raw, uint2 seen, uint32_t kdst, uint32_t vdst,
+                                             float *par, int tid) {
+  using T = Kv4Tile<D>;
+  constexpr int G = T::kG;
+  constexpr int kChunks = T::kRow / 16;                        // 16-byte pieces of a row
+  constexpr int kTurns = kShKeys * kChunks / 128;
+  const __half2 k_off = __float2half2_rn(1032.f), v_off = __float2half2_rn(1024.f);
+#pragma unroll
+  for (int u = 0; u < kTurns; ++u) {
+    const int i = u * 128 + tid, key = i / kChunks, q = i % kChunks;
+    const uint8_t *tile = raw + (key >> 5) * T::kBytes;
+    const int row = key & 31;
+    const bool in = (key < 32 ? seen.x : seen.y) >> row & 1;
+    const uint4 k4 = *reinterpret_cast<const uint4 *>(tile + row * T::kRow + q * 16);
+    const uint4 v4 = *reinterpret_cast<const uint4 *>(tile + T::kV + row * T::kRow + q * 16);
+    const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w}, vw[4] = {v4.x, v4.y, v4.z, v4.w};
+    const __half *vs = reinterpret_cast<const __half *>(tile + T::kPar + 2 * T::kArr) + row * G;
+    const __half *vz = vs + T::kArr / 2;
+    const __half zero = __ushort_as_half(0);
+    __half2 s[G], z[G];
+    bool wide = false;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      s[g] = __half2half2(in ? vs[g] : zero);
+      z[g] = __half2half2(in ? vz[g] : zero);
+      wide |= !(fabsf(__low2float(z[g])) + 15.f * __low2float(s[g]) < 65504.f);
+    }
+    const bool any_wide = __any_sync(0xffffffffu, wide);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      // word 4 q + w is dimensions 64 g + 8 j ...
+      const int g = w % G, j = (4 / G) * q + w / G;
+      const uint32_t off = sw128_offset(key, 8 * g + j, kShKeys);
+      sts128(kdst + off, code_halves(kw[w], k_off));
+      uint4 v = code_halves(vw[w], v_off);
+      v = make_uint4(scaled(v.x, s[g], z[g]), scaled(v.y, s[g], z[g]), scaled(v.z, s[g], z[g]),
+                     scaled(v.w, s[g], z[g]));
+      if (any_wide) v = make_uint4(held(v.x), held(v.y), held(v.z), held(v.w));
+      sts128(vdst + off, v);
+    }
+  }
+  if (tid < kShKeys) {                                         // K's scales and zeros of key tid
+    const int row = tid & 31;
+    const uint8_t *tile = raw + (tid >> 5) * T::kBytes + T::kPar;
+    const bool in = (tid < 32 ? seen.x : seen.y) >> row & 1;
+    float *dst = par + (tid >> 1) * (4 * G) + (tid & 1);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float s = in ? __half2float(reinterpret_cast<const __half *>(tile)[row * G + g]) : 0.f;
+      const float z =
+          in ? __half2float(reinterpret_cast<const __half *>(tile + T::kArr)[row * G + g]) : 0.f;
+      dst[2 * g] = s;                                          // [pair][ks_0 x 2, ks_1 x 2, kz_0 x 2, kz_1 x 2]
+      dst[2 * (G + g)] = fmaf(8.f, s, z);
+    }
+  }
+}
+
+template <int D, bool kFp16>
+__global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodeParams p, ShPlan plan) {
+  using S = Sh<D>;
+  using T = Kv4Tile<D>;
+  constexpr int G = S::kG;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ShShared sh;
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int *const fail = &sh.fail;
+  after_previous();
+  if (plan.head->pairs <= (int64_t)blockIdx.x * plan.head->per) return;   // the whole CTA
+  if (warp == 12) tmem_alloc(&sh.tmem, S::kCols);
+  if (tid == 0) {
+    for (int i = 0; i < kShRaw; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 128);
+    }
+    for (int i = 0; i < kShStages; ++i) {
+      mbar_init(&sh.kv_full[i], 128);
+      mbar_init(&sh.kv_empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 256);
+    mbar_init(&sh.o_free, 256);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sh.s_full[w], 1);
+      mbar_init(&sh.p_full[w], 128);
+      mbar_init(&sh.o_done[w], 1);
+    }
+    sh.fail = 0;
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t sQ = smem_u32(smem + S::kOffQ), sK = smem_u32(smem + S::kOffK),
+                 sV = smem_u32(smem + S::kOffV);
+  uint8_t *const raw0 = smem + S::kOffRaw;
+  float *const par0 = reinterpret_cast<float *>(smem + S::kOffPar);
+  ShWalk walk(plan, blockIdx.x);
+  ShSpan sp;
+
+  if (warp == 13) {
+    // ------------------------------ loader ------------------------------
+    int it = 0;
+    int32_t err = 0;
+    while (walk.next(sp, p.h_k)) {
+      const int keys = walk.g.keys;
+      const int32_t *row = p.table + (int64_t)walk.g.seq0 * p.width;
+      int my_page = -1;
+      for (int b = sp.first; b < sp.end; ++b, ++it) {
+        const int n = (b - sp.first) & 15;
+        if (n == 0) {                                          // the pages of the next 32 tiles
+          const int key = b * kShKeys + lane * 32;
+          my_page = -1;
+          if (key < keys && key < sp.end * kShKeys) {
+            my_page = row[key >> p.page_log2];
+            if (my_page < 0 || my_page >= p.num_pages) {
+              my_page = -1;
+              err |= NSA_DEVERR_BAD_INDEX;
+            }
+          }
+        }
+        const int pg[2] = {__shfl_sync(0xffffffffu, my_page, 2 * n),
+                           __shfl_sync(0xffffffffu, my_page, 2 * n + 1)};
+        const int rs = it % kShRaw;
+        if (lane == 0) {
+          if (it >= kShRaw) sh_wait(&sh.raw_empty[rs], ((it / kShRaw) - 1) & 1, p.status, fail);
+          uint32_t seen[2], bytes = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int left = keys - (b * kShKeys + 32 * u);
+            seen[u] = pg[u] < 0 || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
+            if (pg[u] >= 0) bytes += T::kBytes;
+          }
+          sh.seen_raw[rs] = make_uint2(seen[0], seen[1]);
+          if (bytes) mbar_arrive_expect_tx(&sh.raw_full[rs], bytes);
+          else mbar_arrive(&sh.raw_full[rs]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            if (pg[u] < 0) continue;
+            const int key = b * kShKeys + 32 * u, tpl = p.page_log2 - 5;
+            const int64_t tile = (((int64_t)pg[u] * p.h_k + sp.h) << tpl) +
+                                 ((key & ((1 << p.page_log2) - 1)) >> 5);
+            bulk_load(smem_u32(raw0 + rs * S::kRawBytes + u * T::kBytes), p.pool + tile * T::kBytes,
+                      T::kBytes, &sh.raw_full[rs]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    err = __reduce_or_sync(0xffffffffu, err);
+    if (err && lane == 0) raise(p.status, err);
+    // nothing may be in flight when the CTA ends, given up or not
+    if (lane == 0)
+      for (int i = max(0, it - kShRaw); i < it; ++i) {
+        const uint32_t bar = smem_u32(&sh.raw_full[i % kShRaw]);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(bar, (i / kShRaw) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    __syncwarp();
+  } else if (warp >= 8 && warp < 12) {
+    // ----------------------------- unpackers ----------------------------
+    const int t = tid - 256;
+    int it = 0;
+    while (walk.next(sp, p.h_k)) {
+      for (int b = sp.first; b < sp.end; ++b, ++it) {
+        const int rs = it % kShRaw, st = it % kShStages;
+        sh_wait(&sh.raw_full[rs], (it / kShRaw) & 1, p.status, fail);
+        if (it >= kShStages) sh_wait(&sh.kv_empty[st], ((it / kShStages) - 1) & 1, p.status, fail);
+        __syncwarp();
+        const uint2 seen = sh.seen_raw[rs];
+        if (t == 0) sh.seen[st] = seen;
+        unpack_block<D>(raw0 + rs * S::kRawBytes, seen, sK + st * S::kOperand, sV + st * S::kOperand,
+                        par0 + st * (S::kParBytes / 4), t);
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.raw_empty[rs]);
+        mbar_arrive(&sh.kv_full[st]);
+      }
+    }
+  } else if (warp == 12) {
+    // ---------------------------- MMA thread ----------------------------
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc_f16(kShRows, kShKeys, false, false, true);
+      constexpr uint32_t kIdO = idesc_f16(kShRows, D, false, true, true);
+      constexpr uint32_t kHi = sdesc_hi_sw128(1024);
+      const uint32_t lo_q = sdesc_lo_sw128(sQ, 16), lo_k = sdesc_lo_sw128(sK, 16);
+      const uint32_t lo_v = sdesc_lo_sw128(sV, kShKeys * 128);
+      int it = 0, turn = 0, done[2] = {0, 0};
+      for (; walk.next(sp, p.h_k); ++turn) {
+        const int nb = sp.end - sp.first;
+        sh_wait(&sh.q_full, turn & 1, p.status, fail);
+        for (int n = 0; n <= nb; ++n) {
+          if (n < nb) {
+            const int st = (it + n) % kShStages, w = n & 1;
+            sh_wait(&sh.kv_full[st], ((it + n) / kShStages) & 1, p.status, fail);
+            tc_fence_after();
+            const uint32_t ts = tmem + w * S::kScores, bk = lo_k + (st * S::kOperand >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+              mma_f16(ts + (kk >> 2) * kShKeys, sdesc_join(lo_q + (kmajor_step(kShRows, kk) >> 4), kHi),
+                      sdesc_join(bk + (kmajor_step(kShKeys, kk) >> 4), kHi), kIdS, (kk & 3) > 0);
+            mma_commit(&sh.s_full[w]);
+          }
+          if (n > 0) {
+            const int m = n - 1, st = (it + m) % kShStages, w = m & 1;
+            sh_wait(&sh.p_full[w], done[w] & 1, p.status, fail);
+            ++done[w];
+            if (m == 0 && turn > 0) sh_wait(&sh.o_free, (turn - 1) & 1, p.status, fail);
+            tc_fence_after();
+            const uint32_t ts = tmem + w * S::kScores, to = tmem + 2 * S::kScores + w * D;
+            const uint32_t bv = lo_v + (st * S::kOperand >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kShKeys / 16; ++kk)
+              mma_f16_ts(to, ts + kk * 8, sdesc_join(bv + (mnmajor_step(kk) >> 4), kHi), kIdO,
+                         m >= 2 || kk > 0);
+            if (kFp16) {                                       // what the rounding of W has left
+#pragma unroll
+              for (int kk = 0; kk < kShKeys / 16; ++kk)
+                mma_f16_ts(to, ts + kShKeys / 2 + kk * 8,
+                           sdesc_join(bv + (mnmajor_step(kk) >> 4), kHi), kIdO, 1);
+            }
+            mma_commit(&sh.kv_empty[st]);
+            mma_commit(&sh.o_done[w]);
+          }
+        }
+        it += nb;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------ softmax -----------------------------
+    const int w = warp >> 2, row = tid & 127;                  // row: tensor memory lane
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + w * S::kScores + lane_off;
+    const uint32_t to = tmem + 2 * S::kScores + lane_off;
+    constexpr int kHalf = D / 2;                               // dimensions of a row that a thread brings
+    int it = 0, count = 0;
+    while (walk.next(sp, p.h_k)) {
+      const int nb = sp.end - sp.first;
+      // ---- the tile's queries ----
+      const int r = sp.tile * kShRows + row;
+      const bool real = r < walk.g.rows;
+      uint4 q4[kHalf / 8];
+      int64_t qrow = 0;
+      if (real) {
+        const int b = r / p.g;
+        qrow = (int64_t)(walk.g.seq0 + b) * p.h_q + sp.h * p.g + (r - b * p.g);
+      }
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < kHalf / 8; ++i) {
+        q4[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (real)
+          q4[i] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + qrow * D +
+                                                   w * kHalf + i * 8);
+        top = __vmaxu2(__vmaxu2(top, q4[i].x & 0x7fff7fffu), q4[i].y & 0x7fff7fffu);
+        top = __vmaxu2(__vmaxu2(top, q4[i].z & 0x7fff7fffu), q4[i].w & 0x7fff7fffu);
+      }
+      sh.top[w][row] = max(top & 0xffffu, top >> 16);
+      named_bar_sync(1, 256);
+      const uint32_t big = max(sh.top[0][row], sh.top[1][row]);
+      const float mag = unpack2<kFp16>(big).x;
+      const int ex = max(static_cast<int>(__float_as_uint(mag) >> 23) - 127, -100);
+      const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);   // 2^(14 - ex)
+      const float sgn = p.scale < 0.f ? -up : up;
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < kHalf / 8; ++i) {
+        const float2 a = unpack2<kFp16>(q4[i].x), b = unpack2<kFp16>(q4[i].y);
+        const float2 c = unpack2<kFp16>(q4[i].z), e = unpack2<kFp16>(q4[i].w);
+        uint4 o;                                               // dimensions 0 4, 1 5, 2 6, 3 7
+        o.x = pack2<true>(a.x * sgn, c.x * sgn);
+        o.y = pack2<true>(a.y * sgn, c.y * sgn);
+        o.z = pack2<true>(b.x * sgn, e.x * sgn);
+        o.w = pack2<true>(b.y * sgn, e.y * sgn);
+        const float2 f0 = unpack2<true>(o.x), f1 = unpack2<true>(o.y);
+        const float2 f2 = unpack2<true>(o.z), f3 = unpack2<true>(o.w);
+        sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+        sts128(sQ + sw128_offset(row, w * (kHalf / 8) + i, kShRows), o);
+      }
+      sh.sums[w][row] = sum;
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.q_full);
+      named_bar_sync(1, 256);
+      float qs[G];
+      if constexpr (G == 2) {
+        qs[0] = sh.sums[0][row];
+        qs[1] = sh.sums[1][row];
+      } else {
+        qs[0] = sh.sums[0][row] + sh.sums[1][row];
+      }
+      // S = |scale| 2^(ex - 14) x, in the exponent of 2; `over` powers are left out where the factor
+      // could overflow, and put back into the maximum (scores then are equal or far apart)
+      const int over = max(0, static_cast<int>((__float_as_uint(p.scale) & 0x7fffffffu) >> 23) - 127 +
+                                  ex - 14 + 2 - kShMulTop);
+      const float mul = ldexpf(fabsf(p.scale), ex - 14 - over) * 1.4426950408889634f;
+      // ---- its blocks, every other one ----
+      float ref = -INFINITY, thr = -INFINITY;                  // reference (the maximum less 8), when to raise it
+      Pair l(0.f, 0.f);
+      for (int n = w; n < nb; n += 2, ++count) {
+        const int st = (it + n) % kShStages;
+        sh_wait(&sh.kv_full[st], ((it + n) / kShStages) & 1, p.status, fail);   // scales and zeros
+        sh_wait(&sh.s_full[w], count & 1, p.status, fail);
+        tc_fence_after();
+        const float4 *par = reinterpret_cast<const float4 *>(par0 + st * (S::kParBytes / 4));
+        float s[kShKeys];
+#pragma unroll
+        for (int c = 0; c < kShKeys; c += 32) {
+          float a[G][32];
+#pragma unroll
+          for (int g = 0; g < G; ++g) tmem_ld32(ts + g * kShKeys + c, a[g]);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            Pair x;
+            if constexpr (G == 2) {
+              const float4 ks = par[c + j], kz = par[c + j + 1];
+              x = Pair(kz.x, kz.y) * Pair(qs[0], qs[0]);
+              x = fma(Pair(kz.z, kz.w), Pair(qs[1], qs[1]), x);
+              x = fma(Pair(ks.x, ks.y), Pair(a[0][j], a[0][j + 1]), x);
+              x = fma(Pair(ks.z, ks.w), Pair(a[1][j], a[1][j + 1]), x);
+            } else {
+              const float4 k = par[(c + j) / 2];
+              x = fma(Pair(k.x, k.y), Pair(a[0][j], a[0][j + 1]), Pair(k.z, k.w) * Pair(qs[0], qs[0]));
+            }
+            const float2 y = (x * Pair(mul, mul)).get();       // rounded before the reference is taken off
+            s[c + j] = y.x;
+            s[c + j + 1] = y.y;
+          }
+        }
+        const uint2 seen = sh.seen[st];
+        if ((seen.x & seen.y) != ~0u) {
+#pragma unroll
+          for (int j = 0; j < kShKeys; ++j)
+            if (!((j < 32 ? seen.x : seen.y) >> (j & 31) & 1)) s[j] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int j = 4; j < kShKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (__any_sync(0xffffffffu, m > thr)) {
+          float f = 1.f;
+          if (m > thr) {
+            const float next = __fadd_ru(m, -kShUp);           // never lower: weights have to fit fp16
+            f = ex2_approx(ref - next);                        // 0 the first time
+            ref = next;
+            thr = __fadd_rd(m, kShSlack);
+          }
+          l = l * Pair(f, f);
+          if (n >= 2) {                                        // what the blocks before have left
+            sh_wait(&sh.o_done[w], (count - 1) & 1, p.status, fail);
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(to + w * D + c, o);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st16(to + w * D + c, o);
+            }
+          }
+        }
+        const float base = ref == -INFINITY ? 0.f : -ref;      // no key so far: weights of 0
+#pragma unroll
+        for (int c = 0; c < kShKeys; c += 32) {
+          uint32_t pk[16], rest[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float2 e = (Pair(s[c + j], s[c + j + 1]) + Pair(base, base)).get();
+            const float x = ex2_approx(e.x), y = ex2_approx(e.y);
+            l = l + Pair(x, y);
+            pk[j / 2] = pack2<true>(x, y);
+            if (kFp16) {
+              const float2 hi = unpack2<true>(pk[j / 2]);
+              rest[j / 2] = pack2<true>(x - hi.x, y - hi.y);
+            }
+          }
+          tmem_st16(ts + c / 2, pk);
+          if (kFp16) tmem_st16(ts + kShKeys / 2 + c / 2, rest);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.p_full[w]);
+      }
+      it += nb;
+      // ---- the two warpgroups' sums ----
+      if (nb > w) sh_wait(&sh.o_done[w], (count - 1) & 1, p.status, fail);
+      const float2 l2 = l.get();
+      sh.ml[w][row] = make_float2(ref, l2.x + l2.y);
+      named_bar_sync(1, 256);
+      tc_fence_after();
+      const float2 m0 = sh.ml[0][row];
+      const float2 m1 = nb > 1 ? sh.ml[1][row] : make_float2(-INFINITY, 0.f);
+      const float M = fmaxf(m0.x, m1.x);
+      const float f0 = m0.y != 0.f ? ex2_approx(m0.x - M) : 0.f;
+      const float f1 = m1.y != 0.f ? ex2_approx(m1.x - M) : 0.f;
+      float *dst = plan.part + ((int64_t)sp.part + row) * D + w * kHalf;
+#pragma unroll 1
+      for (int c = 0; c < kHalf; c += 16) {
+        uint32_t x[16], y[16];
+        tmem_ld16(to + w * kHalf + c, x);
+        if (nb > 1) tmem_ld16(to + D + w * kHalf + c, y);
+        float o[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          o[j] = m0.y != 0.f ? __uint_as_float(x[j]) * f0 : 0.f;
+          if (nb > 1 && m1.y != 0.f) o[j] = fmaf(__uint_as_float(y[j]), f1, o[j]);
+        }
+        if (real) {
+#pragma unroll
+          for (int j = 0; j < 16; j += 8) {                    // back in the order of the dimensions
+            *reinterpret_cast<float4 *>(dst + c + j) = make_float4(o[j], o[j + 2], o[j + 4], o[j + 6]);
+            *reinterpret_cast<float4 *>(dst + c + j + 4) =
+                make_float4(o[j + 1], o[j + 3], o[j + 5], o[j + 7]);
+          }
+        }
+      }
+      if (real && w == 0)
+        plan.part_ml[sp.part + row] =
+            make_float2(ldexpf(M, over), f0 * m0.y + (nb > 1 ? f1 * m1.y : 0.f));
+      tc_fence_before();
+      mbar_arrive(&sh.o_free);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, S::kCols);
+}
+
+// ---- join ------------------------------------------------------------------------------
+// A warp a (sequence, query head): its record and, where its sequence shares a prefix, the partial rows
+// of the CTAs that its tile went through.
+constexpr int kJoinThreads = 256;
+template <int D, bool kFp16>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4DecodeParams p, ShPlan plan) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int64_t wid = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  if (wid >= (int64_t)p.num_seqs * p.h_q) return;
+  after_previous();
+  const int b = static_cast<int>(wid / p.h_q), hq = static_cast<int>(wid - (int64_t)b * p.h_q);
+  const float *rec = plan.rec + wid * kRecFloats<D>;
+  float2 ml = *reinterpret_cast<const float2 *>(rec + D);
+  float M = ml.x, l = ml.y, x[E];
+  auto row = [&](const float *src, float (&v)[E]) {
+    const float2 *s = reinterpret_cast<const float2 *>(src + lane * E);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const float2 y = s[e];
+      v[2 * e] = y.x;
+      v[2 * e + 1] = y.y;
+    }
+  };
+  row(rec, x);
+  const int gi = plan.of[b];
+  if (gi >= 0) {
+    const ShGroup g = plan.groups[gi];
+    const int h = hq / p.g, r = (b - g.seq0) * p.g + hq - h * p.g, tile = r / kShRows;
+    const int pair0 = g.pair0 + (h * g.tiles + tile) * g.blocks, per = plan.head->per;
+    const int c0 = pair0 / per, c1 = (pair0 + g.blocks - 1) / per;
+    const int64_t at = (int64_t)g.row0 + h * g.rows + r;
+    for (int c = c0; c <= c1; c += 4) {
+      float2 v[4];
+      float o[4][E];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        v[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+        if (c + u <= c1) {
+          const int64_t i = (int64_t)(c + u) * kShRows + at;
+          v[u] = plan.part_ml[i];
+          row(plan.part + i * D, o[u]);
+        }
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) top = fmaxf(top, v[u].x);
+      const float old = l != 0.f ? ex2_approx(M - top) : 0.f;
+      l *= old;
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] *= old;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float f = v[u].y != 0.f ? ex2_approx(v[u].x - top) : 0.f;
+        l = fmaf(f, v[u].y, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = fmaf(f, o[u][e], x[e]);
+      }
+      M = top;
+    }
+  }
+  const bool any = l != 0.f;                                   // a NaN sum stays one
+  const float inv = any ? __fdividef(1.f, l) : 0.f;
+  uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + wid * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) out[e] = pack2<kFp16>(x[2 * e] * inv, x[2 * e + 1] * inv);
+  if (lane == 0)
+    p.lse[(int64_t)hq * p.num_seqs + b] = any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
+// ---- launches ----------------------------------------------------------------------------
+size_t kv4_shared_workspace(int d, int num_seqs, int h_q, int num_groups) {
+  return static_cast<size_t>(shared_layout(d, num_seqs, h_q, num_groups, nullptr, nullptr));
+}
+
+template <int D, bool kFp16>
+static cudaError_t run_shared(const Kv4SharedParams &p, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  ShPlan plan;
+  shared_layout(D, p.dec.num_seqs, p.dec.h_q, p.num_groups, p.ws, &plan);
+  const int ctas = sms < kShMaxCtas ? sms : kShMaxCtas;
+  e = launch_kv4(kv4_share_kernel, dim3(1), kSetupThreads, 0, 1, s, p, plan, ctas, 4);
+  if (e != cudaSuccess) return e;
+  auto *kernel = kv4_prefix_kernel<D, kFp16>;
+  // more than half of an SM's: one CTA each, as its tensor memory allows
+  constexpr int smem = Sh<D>::kBytes > 120 * 1024 ? Sh<D>::kBytes : 120 * 1024;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_kv4(kernel, dim3(static_cast<unsigned>(ctas)), kShThreads, smem, 1, s, p.dec, plan);
+  if (e != cudaSuccess) return e;
+  Kv4DecodeParams own = p.dec;
+  own.lo = plan.lo;
+  own.rec = plan.rec;
+  e = launch_kv4_suffix(D, kFp16, own, s);
+  if (e != cudaSuccess) return e;
+  const int64_t warps = (int64_t)p.dec.num_seqs * p.dec.h_q, per = kJoinThreads / 32;
+  return launch_kv4(kv4_join_kernel<D, kFp16>, dim3(static_cast<unsigned>((warps + per - 1) / per)),
+                    kJoinThreads, 0, 1, s, p.dec, plan);
+}
+
+cudaError_t launch_kv4_shared(int d, bool fp16, const Kv4SharedParams &p, cudaStream_t s) {
+  if (d == 64) return fp16 ? run_shared<64, true>(p, s) : run_shared<64, false>(p, s);
+  return fp16 ? run_shared<128, true>(p, s) : run_shared<128, false>(p, s);
+}
+
+}  // namespace nsa

@@ -15,8 +15,8 @@ from typing import Optional
 import torch
 
 __all__ = ["page_plan", "page_slots", "kv4_pool", "kv4_append", "kv4_read", "kv4_decode",
-           "kv4_decode_workspace_size", "DEVERR_BAD_INDEX", "DEVERR_BAD_SEQLENS",
-           "DEVERR_NO_PAGES"]
+           "kv4_decode_workspace_size", "kv4_decode_shared", "kv4_decode_shared_workspace_size",
+           "DEVERR_BAD_INDEX", "DEVERR_BAD_SEQLENS", "DEVERR_NO_PAGES"]
 
 DEVERR_BAD_INDEX, DEVERR_BAD_SEQLENS, DEVERR_NO_PAGES = 1, 2, 8
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
@@ -47,6 +47,9 @@ def signatures():
         "nsa_kv4_decode": (st, [kd, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, f32, vp, vp, vp,
                                 vp, sz, vp]),
         "nsa_kv4_decode_workspace_size": (st, [kd, i32, i32, i32, psz]),
+        "nsa_kv4_decode_shared": (st, [kd, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, f32, vp, vp,
+                                       vp, vp, sz, vp]),
+        "nsa_kv4_decode_shared_workspace_size": (st, [kd, i32, i32, i32, psz]),
     }
 
 
@@ -365,4 +368,71 @@ def kv4_decode(q, pool, block_table, seq_lens, scale: float, sel_idx=None, windo
         _raw(stream, dev))
     if code:
         _fail(code, "kv4_decode")
+    return out, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _shared_workspace(dims_key, num_seqs, h_q, num_groups):
+    _held((num_seqs, h_q, num_groups), "kv4_decode_shared")
+    size = ctypes.c_size_t()
+    code = _lib().nsa_kv4_decode_shared_workspace_size(_kv4_dims(*dims_key), num_seqs, h_q, num_groups,
+                                                       ctypes.byref(size))
+    if code:
+        _fail(code, "kv4_decode_shared_workspace_size")
+    return size.value
+
+
+def kv4_decode_shared_workspace_size(num_pages: int, page_size: int, h_k: int, head_dim: int,
+                                     num_seqs: int, h_q: int, num_groups: int) -> int:
+    """Workspace bytes of kv4_decode_shared."""
+    return _shared_workspace((num_pages, page_size, h_k, head_dim, 0), num_seqs, h_q, num_groups)
+
+
+def kv4_decode_shared(q, pool, block_table, seq_lens, scale: float, cu_groups, prefix_lens, out=None,
+                      lse=None, workspace: Optional[torch.Tensor] = None, device_status=None,
+                      stream=None):
+    """kv4_decode of everything cached, for sequences that share prefixes: group i is sequences
+    cu_groups[i] ... cu_groups[i + 1] - 1 (cu_groups int32 [G + 1]; those behind the last group
+    share nothing), whose first prefix_lens[i] tokens (int32 [G]) are the same and are read once,
+    from the first one's pages.  Returns out [B, h_q, d] and lse float32 [h_q, B].  workspace:
+    uint8, at least kv4_decode_shared_workspace_size bytes; allocated here when None."""
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
+        raise ValueError("q [B, h_q, d] expected")
+    b, h_q, d = shape
+    dims, dev = _pool_dims(pool, d, dtype, "kv4_decode_shared")
+    if not q.is_contiguous() or q.get_device() != dev:
+        _check("q", q, dtype, shape, dev)
+    rows, width = block_table.shape
+    if rows != b:
+        raise ValueError(f"block_table of {rows} rows for {b} sequences")
+    groups = prefix_lens.numel()
+    _ints("block_table", block_table, b * width, dev)
+    _ints("seq_lens", seq_lens, b, dev)
+    _ints("prefix_lens", prefix_lens, groups, dev)
+    _ints("cu_groups", cu_groups, groups + 1, dev)
+    if out is None:
+        out = _empty(shape, dtype, dev, stream)
+    else:
+        _check("out", out, dtype, shape, dev)
+    if lse is None:
+        lse = _empty((h_q, b), torch.float32, dev, stream)
+    else:
+        _check("lse", lse, torch.float32, (h_q, b), dev)
+    if width >> 31 or b >> 31 or groups >> 31:
+        _fail(2, "kv4_decode_shared: sizes beyond 32 bits")
+    if workspace is None:
+        need = _shared_workspace((dims.num_pages, dims.page_size, dims.h_k, d, dims.dtype), b, h_q,
+                                 groups)
+        workspace = _empty((need,), torch.uint8, dev, stream)
+    elif (workspace.dtype is not torch.uint8 or not workspace.is_contiguous()
+          or workspace.get_device() != dev):
+        _check("workspace", workspace, torch.uint8, workspace.shape, dev)
+    code = _lib().nsa_kv4_decode_shared(
+        dims, b, h_q, width, groups, q.data_ptr(), pool.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), cu_groups.data_ptr(), prefix_lens.data_ptr(), scale, out.data_ptr(),
+        lse.data_ptr(), None if device_status is None else _status(device_status, dev),
+        workspace.data_ptr(), workspace.numel(), _raw(stream, dev))
+    if code:
+        _fail(code, "kv4_decode_shared")
     return out, lse

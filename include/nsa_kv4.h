@@ -228,6 +228,28 @@ NSA_API nsa_status nsa_kv4_decode(const nsa_kv4_dims *dims, int32_t num_seqs, in
 NSA_API nsa_status nsa_kv4_decode_workspace_size(const nsa_kv4_dims *dims, int32_t num_seqs,
                                                  int32_t h_q, int32_t topk, size_t *bytes);
 
+/* nsa_kv4_decode without a selection or a window, for a batch whose sequences share prefixes: group i
+ * is sequences cu_groups[i] ... cu_groups[i + 1] - 1 (cu_groups int32 [num_groups + 1], from 0 on,
+ * non-decreasing, num_seqs at most; sequences behind the last group share nothing), whose first
+ * prefix_lens[i] tokens (int32 [num_groups], any number) are the same.  They are read from the pages of
+ * the group's first sequence, once for the group; what lies behind them from each sequence's own.
+ * The result is nsa_kv4_decode's for tables that hold the same tokens (nsa_page_fork makes such).
+ * A sequence that is shorter than its group's prefix attends to its own pages alone.
+ *   Arguments and errors are nsa_kv4_decode's; in addition a cu_groups out of order (nothing is shared
+ * then) and a prefix that is negative or above table_width * P (that group shares nothing) set
+ * NSA_DEVERR_BAD_SEQLENS, and a device wait that gave up NSA_DEVERR_TIMEOUT (outputs are then not
+ * defined).  num_groups is 1 ... 2^20. */
+NSA_API nsa_status nsa_kv4_decode_shared(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_q,
+                                         int32_t table_width, int32_t num_groups, const void *q,
+                                         const void *pool, const int32_t *block_table,
+                                         const int32_t *seq_lens, const int32_t *cu_groups,
+                                         const int32_t *prefix_lens, float scale, void *out,
+                                         float *lse, int32_t *device_status, void *workspace,
+                                         size_t workspace_bytes, nsa_stream_t stream);
+NSA_API nsa_status nsa_kv4_decode_shared_workspace_size(const nsa_kv4_dims *dims, int32_t num_seqs,
+                                                        int32_t h_q, int32_t num_groups,
+                                                        size_t *bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,249 @@
+"""The decode over shared prefixes against the fp64 oracle, which knows nothing of sharing."""
+import numpy as np
+import pytest
+import torch
+
+from kv4_helpers import DTYPES
+from oracle import kv4
+from shared_helpers import check_shared, make_shared
+
+pytestmark = pytest.mark.gpu
+
+
+def _dev(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).cuda()
+
+
+def _run(groups, page, h_k, g, d, dtype, seed, alone=(), scale=None, width=None, mags=(1.0,), q=None,
+         some=None):
+    import block_sparse_attention_nsa_gb300 as nsa
+    pool, table, lens, cu, prefix = make_shared(groups, page, h_k, d, seed, alone, width, mags)
+    dt = DTYPES[dtype]
+    if q is None:
+        q = torch.randn(len(lens), h_k * g, d, generator=torch.Generator().manual_seed(seed)).to(dt)
+    scale = d ** -0.5 if scale is None else scale
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), scale, _dev(cu),
+                                     _dev(prefix), device_status=status)
+    assert int(status.item()) == 0
+    rows = np.arange(len(lens)) if some is None else np.asarray(some)
+    ref = kv4.attend(q[rows].double().numpy(), pool, table[rows], lens[rows], page, scale)
+    check_shared(out[rows], lse[:, rows], ref, dt)
+    return out, ref
+
+
+@pytest.mark.parametrize("d,page,h_k,g,dtype", [(128, 64, 1, 4, "bf16"), (64, 32, 2, 1, "fp16")])
+def test_two_of_one_prompt(d, page, h_k, g, dtype):
+    _run([(64, (70, 65))], page, h_k, g, d, dtype, 1)
+
+
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 63, 64, 65, 127, 128, 129, 191, 193, 257, 511, 513])
+def test_prefixes_around_blocks(n):
+    _run([(n, (n + 1, n + 40, n))], 64, 1, 4, 128, "bf16", n)
+    _run([(n, (n + 3, n))], 32, 2, 1, 64, "fp16", n)
+    _run([(n, (n, n + 1, n + 130, n + 64))], 128, 1, 3, 128, "fp16", n)
+
+
+@pytest.mark.parametrize("d,page,h_k,g,dtype", [(128, 64, 2, 4, "bf16"), (128, 64, 1, 16, "fp16"),
+                                                (64, 32, 3, 1, "fp16"), (128, 128, 2, 8, "bf16"),
+                                                (64, 128, 1, 7, "bf16"), (128, 32, 1, 12, "fp16"),
+                                                (64, 64, 2, 9, "bf16")])
+def test_groups_of_all_kinds(d, page, h_k, g, dtype):
+    """Groups of one sequence and of none, a prefix of nothing, sequences that end inside the prefix
+    or at its end, empty ones, and sequences behind the last group."""
+    groups = [(300, (420, 300, 301, 999)), (200, (260,)), (77, ()), (0, (50, 60)),
+              (500, (600, 130, 0, 499, 500)), (64, (64, 64))]
+    _run(groups, page, h_k, g, d, dtype, 10 * d + page + g, alone=(5, 0, 333))
+
+
+@pytest.mark.parametrize("n,g,dtype", [(31, 4, "bf16"), (33, 4, "bf16"), (40, 16, "fp16"), (9, 15, "fp16"),
+                                       (128, 1, "bf16"), (129, 1, "fp16"), (300, 1, "bf16")])
+def test_rows_around_tiles(n, g, dtype):
+    rng = np.random.default_rng(n)
+    own = rng.integers(0, 50, n)
+    some = sorted(set([0, 1, n // 2, n - 2, n - 1]) | set(rng.integers(0, n, 6).tolist()))
+    _run([(200, tuple(200 + own))], 64, 2, g, 64, dtype, n, some=some)
+    _run([(130, tuple(130 + own))], 32, 1, g, 128, dtype, n + 1, some=some)
+
+
+def test_long_prefixes():
+    """Runs that cross tiles, heads and groups; partial rows of many CTAs to join."""
+    own = tuple(20011 + 3 * i for i in range(70))
+    _run([(20011, own)], 64, 3, 4, 128, "bf16", 3, some=(0, 1, 31, 32, 69))
+    _run([(9000, tuple(9000 + i for i in range(33))), (4001, (4100, 4001, 4050))], 128, 2, 8, 64, "fp16", 4,
+         some=(0, 15, 16, 32, 33, 34, 35))
+    many = [(int(p), tuple(int(p) + np.arange(k))) for p, k in
+            zip(np.random.default_rng(5).integers(1, 900, 60), [2, 3, 5, 1, 9, 2] * 10)]
+    _run(many, 32, 2, 2, 64, "bf16", 5, width=200)
+
+
+@pytest.mark.parametrize("d,page", [(64, 128), (128, 64)])
+def test_long_fp16_loses_little(d, page):
+    """Weights and values rounded to fp16 add two errors of the output's own size, at most half of
+    it together."""
+    lens = (30011, 30030, 30500)
+    out, ref = _run([(30011, lens)], page, 1, 2, d, "fp16", 77)
+    rounding = np.linalg.norm(ref[0].astype(np.float16) - ref[0])
+    assert np.linalg.norm(out.double().cpu().numpy() - ref[0]) <= 1.5 * rounding
+
+
+def test_spread_of_scores_and_magnitudes():
+    groups = [(500, (520, 600, 501)), (64, (90, 64))]
+    _run(groups, 64, 2, 4, 128, "bf16", 21, scale=2.0)
+    _run(groups, 64, 2, 4, 128, "fp16", 22, scale=-0.5)
+    _run(groups, 64, 1, 8, 128, "fp16", 23, scale=1e-3, mags=(2.0 ** -9, 0.1, 8.0))
+    _run(groups, 32, 1, 2, 64, "bf16", 24, scale=0.0, mags=(2.0 ** -8, 16.0))
+    q = torch.randn(5, 6, 128, generator=torch.Generator().manual_seed(0))
+    q *= torch.tensor([1.0, 1e-20, 1e4, 0.0, 1e-3, 300.0]).view(1, 6, 1)
+    _run(groups, 64, 1, 6, 128, "bf16", 25, scale=1e-4, q=q.to(torch.bfloat16))
+
+
+def test_rising_scores():
+    """Keys that grow along the prefix: the reference is raised again and again."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, d, n = 64, 128, 3000
+    rng = np.random.default_rng(1)
+    u = rng.standard_normal(d).astype(np.float32)
+    pool, table, lens, cu, prefix = make_shared([(n, (n + 9, n, n + 70))], page, 1, d, 2)
+    code, scale, zero = kv4.unpack(pool, page, d)
+    for t in range(n):
+        pg, at = table[0, t // page], t % page
+        c, s, z = kv4.quantise(u * (t / n * 8) + 0.1 * rng.standard_normal(d).astype(np.float32))
+        code[pg, 0, 0, at], scale[pg, 0, 0, at], zero[pg, 0, 0, at] = c, s, z
+    pool2 = kv4.pack(code, scale, zero)
+    table[1:, :n // page] = table[0, :n // page]
+    if n % page:
+        for b in (1, 2):
+            a, z_ = table[0, n // page], table[b, n // page]
+            for arr in (code, scale, zero):
+                arr[z_, :, :, :n % page] = arr[a, :, :, :n % page]
+        pool2 = kv4.pack(code, scale, zero)
+    for dtype, size in ((torch.bfloat16, 0.3), (torch.float16, 3.0)):
+        q = (torch.from_numpy(u)[None, None] * size + torch.randn(3, 2, d,
+             generator=torch.Generator().manual_seed(3))).to(dtype)
+        out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool2), _dev(table), _dev(lens), d ** -0.5,
+                                         _dev(cu), _dev(prefix))
+        check_shared(out, lse, kv4.attend(q.double().numpy(), pool2, table, lens, page, d ** -0.5), dtype)
+
+
+@pytest.mark.parametrize("size,scale", [(2.0 ** 100, 2.0 ** -101), (2.0 ** -90, 2.0 ** 90), (1.0, 2.0 ** 40),
+                                        (2.0 ** 114, 1.0)])
+def test_largest_queries_and_scales(size, scale):
+    """Factors past fp32's comfort; weights are those of the largest score alone where scores are
+    huge."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    pool, table, lens, cu, prefix = make_shared([(300, (320, 300, 400))], 64, 1, 128, 31)
+    q = (torch.randn(3, 2, 128, generator=torch.Generator().manual_seed(1)) * size).to(torch.bfloat16)
+    got = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), scale, _dev(cu), _dev(prefix))
+    ref = kv4.attend(q.double().numpy(), pool, table, lens, 64, scale)
+    assert got[0].isfinite().all()
+    if np.abs(ref[1]).max() < 1e30:
+        check_shared(*got, ref, torch.bfloat16)
+    else:
+        tol = 2.0 ** -8 * np.abs(ref[0]) + 2.0 ** -9 * ref[3] + 1e-6
+        assert (np.abs(got[0].double().cpu().numpy() - ref[0]) <= tol).all()
+
+
+def test_bad_pages_and_nan_rows():
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d = 32, 2, 4, 128
+    pool, table, lens, cu, prefix = make_shared([(300, (320, 300, 400)), (64, (64, 90))], page, h_k, d, 41)
+    q = torch.randn(5, h_k * g, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    # pages of the prefix that are none: their keys are left out, for all of the group
+    t = table.copy()
+    t[:3, 2], t[:3, 5], t[3:, 0] = -1, pool.shape[0], -9
+    out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(t), _dev(lens), 0.1, _dev(cu), _dev(prefix),
+                                     device_status=status)
+    assert int(status.item()) == nsa.DEVERR_BAD_INDEX
+    check_shared(out, lse, kv4.attend(q.double().numpy(), pool, t, lens, page, 0.1), torch.bfloat16)
+    # all of a prefix
+    t[:3, :9] = -1
+    out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(t), _dev(lens), 0.1, _dev(cu), _dev(prefix))
+    check_shared(out, lse, kv4.attend(q.double().numpy(), pool, t, lens, page, 0.1), torch.bfloat16)
+    # a NaN query stays in its row
+    ref = kv4.attend(q.double().numpy(), pool, table, lens, page, 0.1)
+    bad = q.clone()
+    bad[1, 5, 3] = float("nan")
+    out, lse = nsa.kv4_decode_shared(bad.cuda(), _dev(pool), _dev(table), _dev(lens), 0.1, _dev(cu),
+                                     _dev(prefix))
+    assert out[1, 5].isnan().all() and lse[5, 1].isnan()
+    out[1, 5], lse[5, 1] = torch.from_numpy(ref[0][1, 5]).to(out), float(ref[1][5, 1])
+    check_shared(out, lse, ref, torch.bfloat16)
+
+
+def test_malformed_groups():
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, d = 32, 64
+    pool, table, lens, cu, prefix = make_shared([(100, (120, 100, 130)), (64, (64, 90))], page, 1, d, 51)
+    q = torch.randn(5, 2, d, generator=torch.Generator().manual_seed(1)).half()
+    ref = kv4.attend(q.double().numpy(), pool, table, lens, page, 0.1)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for c, p in (((0, 3, 6), prefix), ((1, 3, 5), prefix), ((0, 3, 2), prefix), ((0, -1, 5), prefix),
+                 (cu, (-1, 64)), (cu, (100, 10 ** 6)), (cu, (100, table.shape[1] * page + 1))):
+        out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), 0.1,
+                                         _dev(np.int32(c)), _dev(np.int32(p)), device_status=status.zero_())
+        assert int(status.item()) == nsa.DEVERR_BAD_SEQLENS, (c, p)
+        check_shared(out, lse, ref, torch.float16)
+    n = lens.copy()
+    n[1], n[4] = -3, 10 ** 6
+    out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(n), 0.1, _dev(cu), _dev(prefix),
+                                     device_status=status.zero_())
+    assert int(status.item()) & nsa.DEVERR_BAD_SEQLENS
+    assert (out[1] == 0).all() and lse[:, 1].isneginf().all()
+
+
+def test_streams_graphs_and_dirty_workspaces():
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d = 64, 2, 4, 128
+    sets = []
+    for seed in range(3):
+        pool, table, lens, cu, prefix = make_shared([(700, (720, 700, 900, 701)), (64, (64, 90))], page, h_k,
+                                                    d, 61 + seed, width=40)
+        q = torch.randn(6, h_k * g, d, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
+        sets.append([x.cuda() if torch.is_tensor(x) else _dev(x) for x in (q, pool, table, lens, cu, prefix)])
+    def call(s, **kw):
+        q, pool, table, lens, cu, prefix = s
+        return nsa.kv4_decode_shared(q, pool, table, lens, 0.1, cu, prefix, **kw)
+    want = [call(s) for s in sets]
+    torch.cuda.synchronize()
+    need = nsa.kv4_decode_shared_workspace_size(sets[0][1].shape[0], page, h_k, d, 6, h_k * g, 2)
+    dirty = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    for s, w in zip(sets, want):
+        got = call(s, workspace=dirty)
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = [call(s, stream=st) for s, st in zip(sets, streams)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) for a, b in zip(got, want))
+    inputs = [x.clone() for x in sets[0]]
+    out, lse = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(inputs, out=out, lse=lse, workspace=dirty)
+    for i in (1, 2, 0, 1):
+        for a, b in zip(inputs, sets[i]):
+            if a.shape == b.shape:
+                a.copy_(b)
+        graph.replay()
+        again = call([a if a.shape == b.shape else b for a, b in zip(inputs, sets[i])])
+        assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
+def test_refusals_of_python():
+    import block_sparse_attention_nsa_gb300 as nsa
+    pool, table, lens, cu, prefix = [_dev(x) for x in make_shared([(64, (70, 65))], 64, 1, 128, 1)]
+    q = torch.zeros(2, 4, 128, dtype=torch.bfloat16, device="cuda")
+    args = (pool, table, lens, 0.1)
+    with pytest.raises(ValueError):
+        nsa.kv4_decode_shared(q, *args, cu[:-1], prefix)
+    with pytest.raises(ValueError):
+        nsa.kv4_decode_shared(q, *args, cu, prefix.long())
+    with pytest.raises(nsa.NsaError) as e:
+        nsa.kv4_decode_shared(q, *args, cu, prefix, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == 3
+    with pytest.raises(nsa.NsaError):
+        nsa.kv4_decode_shared(q, *args, cu[:1], prefix[:0])
+    with pytest.raises(nsa.NsaError):
+        nsa.kv4_decode_shared(torch.zeros(2, 17, 128, dtype=torch.bfloat16, device="cuda"), *args, cu, prefix)

@@ -68,3 +68,30 @@ def test_python_refuses_cpu_tensors(lib):
         nsa.page_compact(x, x[0], 4, x[0], x[0])
     with pytest.raises(ValueError):
         nsa.page_copy(x, one, one)
+
+
+def test_shared_decode_refusals(lib):
+    import ctypes
+
+    from block_sparse_attention_nsa_gb300.kv4 import Kv4Dims
+    base = dict(num_pages=100, page_size=64, h_k=2, head_dim=128, dtype=0)
+
+    def call(b=2, h_q=8, width=4, groups=1, q=FAKE, pool=FAKE, table=FAKE, lens=FAKE, cu=FAKE, pre=FAKE,
+             scale=0.1, out=FAKE, lse=FAKE, st=None, ws=FAKE, size=1 << 40, **kw):
+        return lib.nsa_kv4_decode_shared(Kv4Dims(**{**base, **kw}), b, h_q, width, groups, q, pool, table,
+                                         lens, cu, pre, scale, out, lse, st, ws, size, None)
+    for kw in (dict(b=0), dict(h_q=3), dict(width=0), dict(groups=0), dict(scale=float("nan")), dict(q=None),
+               dict(pool=None), dict(table=None), dict(lens=None), dict(cu=None), dict(pre=None),
+               dict(out=None), dict(lse=None), dict(q=FAKE + 8), dict(cu=FAKE + 2), dict(pre=FAKE + 1),
+               dict(ws=FAKE + 8), dict(st=FAKE + 2), dict(h_k=0)):
+        assert call(**kw) == 1, kw
+    for kw in (dict(h_q=34), dict(width=1 << 26), dict(b=1 << 28), dict(groups=(1 << 20) + 1),
+               dict(b=1 << 10, width=1 << 18), dict(head_dim=256), dict(page_size=16)):
+        assert call(**kw) == 2, kw
+    assert call(ws=None, size=0) == 3 and call(size=1024) == 3
+    size = ctypes.c_size_t()
+    f = lib.nsa_kv4_decode_shared_workspace_size
+    assert f(Kv4Dims(**base), 2, 8, 1, ctypes.byref(size)) == 0 and size.value > 0
+    assert call(size=size.value - 1) == 3
+    assert f(Kv4Dims(**base), 2, 8, 0, ctypes.byref(size)) == 1
+    assert f(Kv4Dims(**base), 2, 8, 1, None) == 1
