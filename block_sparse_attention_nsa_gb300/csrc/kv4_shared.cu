@@ -7,12 +7,15 @@
 // rows on the tensor cores; each sequence's own part is kv4_decode.cu's, from the prefix' end on.
 //
 // Prefix kernel (tcgen05).  Rows of a KV head's tile are (sequence, query head) pairs, M = 128; 64
-// keys a block.  Scores need the exactness of fp32 (the log-sum-exp is returned in it), so K's codes
-// are operands as whole numbers, c - 8 in fp16, and scales and zeros come after, in fp32:
-//   x = sum_g ks_g A_g + (kz_g + 8 ks_g) Q_g,   A_g = sum over group g of q^ (c - 8),  Q_g = sum q^,
-//   S = x |scale| 2^(ex - 14);  q^ is q times 2^(14 - ex), ex the exponent of its largest magnitude,
-// so that fp16 holds bf16's and fp16's values (what is lost is 2^-38 of the largest).  A_g are
-// accumulators of their own in tensor memory, a group a K-major 64-column block of the operands.
+// keys a block.  The scores' sums are the tensor core's alone, as exact as fp32 products (their
+// log-sum-exp is returned in fp32).  With q^ = q 2^(5 - ex), ex the exponent of a row's largest
+// magnitude (in fp16 it loses 2^-30 of that), and k = c s + z in a group of dimensions,
+//   q^ . k = sum_j q^_j (c_j - 8) s_hi + sum_j q^_j (c_j - 8) s_lo + Q z + 8 Q s,   Q = sum_j q^_j:
+// s_hi is s without its last three bits, so that both products with c - 8 (four bits and a sign) are
+// exact in fp16; Q and 8 Q are three fp16 numbers each, against z and s in 12 of the 16 columns of
+// one more step.  S = |scale| 2^(ex - 5) q^ . k.  (Codes as operands and scales afterwards, in fp32,
+// want both groups' accumulators apart and four numbers a key from shared memory for every thread:
+// 3190 cycles a block, where this takes XXX.)
 // Weights are w = 2^(S - m) 2^8 (with their factor those down to 2^-22 of the maximum are normal
 // numbers in fp16).  Two roundings to fp16, of 2^-11 at most each: V's values as they are unpacked, and
 // the weights, for bf16 outputs, whose own rounding is eight times as large.  For fp16 outputs, of
@@ -21,15 +24,17 @@
 // the weights before they are rounded.
 // The maximum m is raised only when a score passes it by 2^4, so that most blocks rescale nothing.
 //
-// Roles of a CTA (one an SM, 14 warps), handing blocks on by mbarriers, every wait bounded:
+// Roles of a CTA (one an SM, 20 warps), handing blocks on by mbarriers, every wait bounded:
 //   loader       a block's two record tiles by bulk copies into a ring, page by page of the table;
-//   4 unpackers  codes to the K and V operands (128-byte swizzle; the eight dimensions of a word stay
-//                in the order 0 4 1 5 2 6 3 7 that masking gives, on both sides of the product and
-//                until the output is written), scales and zeros to fp32;
-//   MMA thread   S = Q K^T of block n + 1 ahead of O += W V of block n;
-//   2 x 4 softmax warps   a thread a row; the two warpgroups take every other block, each with its own
-//                maximum, sum and output, joined at the tile's end.  W goes to tensor memory over the
-//                scores it came from.
+//   2 x 4 unpackers  codes, scales and zeros to the K and V operands (128-byte swizzle; the eight
+//                dimensions of a word stay in the order 0 4 1 5 2 6 3 7 that masking gives, on both
+//                sides of the product and until the output is written);
+//   2 MMA threads    S = Q K^T, then O += W V, with Q and W from tensor memory: only K and V are read
+//                from shared memory, whose bandwidth the two products would else fill;
+//   2 x 4 softmax warps   a thread a row.
+// Unpackers, MMA thread and softmax warps of either half take every other block, with a maximum, sum
+// and output of their own, joined at the tile's end; while one half is between its products the
+// other's run.  W goes to tensor memory over the scores it came from.
 // Work: the line of all (tile, block) pairs, tile after tile, in equal runs, one a CTA; where a tile
 // is shared by CTAs each leaves partial rows.  kv4_join_kernel adds them and the own part.
 #include <cmath>
@@ -40,15 +45,17 @@ namespace nsa {
 
 constexpr int kShRows = 128;         // query rows of a tile
 constexpr int kShKeys = 64;          // keys of a block
-constexpr int kShStages = 4;         // blocks unpacked ahead
-constexpr int kShRaw = 4;            // blocks copied ahead
-constexpr int kShThreads = 448;
+// Blocks of each half (every other one of a tile) that are copied ahead, and unpacked: K's for the
+// next product beside those in use; V's follow the product that frees the place.
+constexpr int kShRaw = 2, kShK = 2;
+constexpr int kShThreads = 640;
 constexpr int kShMaxCtas = 256;
 constexpr int kShareMin = 2;         // sequences from which a prefix is shared
 constexpr int kSetupThreads = 1024;
 constexpr float kShSlack = 4.f;      // scores may exceed the reference by this much
 constexpr float kShUp = 8.f;         // weights are 2^8 times 2^(S - m)
-constexpr int kShMulTop = 88;        // a score's factor stays below 2^(kShMulTop + 2)
+constexpr int kShQTop = 5;           // exponent of a row's largest q^
+constexpr int kShMulTop = 92;        // a score's factor stays below 2^(kShMulTop + 2), scores in its unit below 2^30
 
 // A group that shares: its first sequence and number of rows per KV head, its blocks and tiles, and
 // what lies before it: (tile, block) pairs, and partial rows.
@@ -179,27 +186,28 @@ template <int D>
 struct Sh {
   using T = Kv4Tile<D>;
   static constexpr int kG = T::kG;
-  static constexpr uint32_t kOperand = kShKeys * D * 2;        // K or V of a block
+  static constexpr uint32_t kOperand = kShKeys * D * 2;        // V of a block, and each part of K
   static constexpr uint32_t kRawBytes = 2 * T::kBytes;
-  static constexpr uint32_t kParBytes = kShKeys * kG * 2 * 4;  // scales and zeros of K
-  static constexpr uint32_t kOffQ = 0;
-  static constexpr uint32_t kOffK = kOffQ + kShRows * D * 2;
-  static constexpr uint32_t kOffV = kOffK + kShStages * kOperand;
-  static constexpr uint32_t kOffRaw = kOffV + kShStages * kOperand;
-  static constexpr uint32_t kOffPar = kOffRaw + kShRaw * kRawBytes;
-  static constexpr uint32_t kBytes = kOffPar + kShStages * kParBytes + 1024;   // + alignment
-  static_assert(kOffK % 1024 == 0 && kOffV % 1024 == 0 && kOffRaw % 1024 == 0, "operands' alignment");
-  static_assert(kOffPar % 16 == 0 && kBytes <= 227 * 1024, "shared memory");
-  static constexpr uint32_t kScores = kG * kShKeys;            // columns of a warpgroup's scores
-  static constexpr uint32_t kCols = 2 * (kScores + D);
-  static_assert(kCols == 512 || kCols == 256, "tensor memory is taken in powers of two");
+  static constexpr uint32_t kOffK = 0;
+  static constexpr uint32_t kOffV = kOffK + 2 * kShK * 2 * kOperand;
+  static constexpr uint32_t kOffZ = kOffV + 2 * kOperand;      // 16 columns of z and s a stage of K
+  static constexpr uint32_t kOffRaw = kOffZ + kShKeys * 128;
+  static constexpr uint32_t kBytes = kOffRaw + 2 * kShRaw * kRawBytes + 1024;   // + alignment
+  static_assert(2 * kShK <= 4, "a 128-byte row holds four stages' columns");
+  static_assert(kOffV % 1024 == 0 && kOffZ % 1024 == 0 && kOffRaw % 1024 == 0, "operands' alignment");
+  static_assert(kBytes <= 226 * 1024, "shared memory");
+  // columns of tensor memory: scores of both halves, outputs of both, Q, its sums
+  static constexpr uint32_t kS = 0, kO = 2 * kShKeys, kQ = kO + 2 * D, kSums = kQ + D / 2;
+  static constexpr uint32_t kCols = 512;
+  static_assert(kSums + 8 <= kCols, "tensor memory");
 };
 
 struct ShShared {
-  uint64_t raw_full[kShRaw], raw_empty[kShRaw], kv_full[kShStages], kv_empty[kShStages];
+  // of half w: stages w * kShRaw ..., w * kShK ...; of V one
+  uint64_t raw_full[2 * kShRaw], raw_empty[2 * kShRaw], k_full[2 * kShK], k_empty[2 * kShK], v_full[2];
   uint64_t q_full, o_free, s_full[2], p_full[2], o_done[2];
-  uint2 seen_raw[kShRaw], seen[kShStages];     // a block's keys that exist, a bit each
-  float2 ml[2][kShRows];                       // of the two warpgroups, at a tile's end
+  uint2 seen[2 * kShRaw];                      // a block's keys that exist, a bit each
+  float2 ml[2][kShRows];                       // of the two halves, at a tile's end
   float sums[2][kShRows];                      // sums of q^
   int top[2][kShRows];                         // largest magnitude of a row's part, as bits
   uint32_t tmem;
@@ -276,82 +284,149 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
 }
 
 // The codes of a word as fp16 less `off` - 1024: dimensions (0, 4), (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ uint4 code_halves(uint32_t w, __half2 off) {
-  uint32_t u[4];
+__device__ __forceinline__ void code_halves(uint32_t w, __half2 off, __half2 (&c)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t c = (w >> (4 * k) & 0x000f000fu) | 0x64006400u;   // 1024 + c
-    const __half2 h = __hsub2(*reinterpret_cast<const __half2 *>(&c), off);
-    u[k] = *reinterpret_cast<const uint32_t *>(&h);
+    const uint32_t u = (w >> (4 * k) & 0x000f000fu) | 0x64006400u;   // 1024 + c
+    c[k] = __hsub2(*reinterpret_cast<const __half2 *>(&u), off);
   }
-  return make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ uint32_t scaled(uint32_t c, __half2 s, __half2 z) {
-  const __half2 h = __hfma2(*reinterpret_cast<const __half2 *>(&c), s, z);
-  return *reinterpret_cast<const uint32_t *>(&h);
+__device__ __forceinline__ void sts_halves(uint32_t a, const __half2 (&h)[4]) {
+  const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
+  sts128(a, make_uint4(u[0], u[1], u[2], u[3]));
 }
 // V's values past fp16's largest, which the rounding of a scale can make of 65504, are held to it.
-__device__ __forceinline__ uint32_t held(uint32_t v) {
-  const __half2 top = __float2half2_rn(65504.f), h = *reinterpret_cast<const __half2 *>(&v);
-  const __half2 x = __hmin2_nan(__hmax2_nan(h, __hneg2(top)), top);
-  return *reinterpret_cast<const uint32_t *>(&x);
+__device__ __forceinline__ __half2 held(__half2 h) {
+  const __half2 top = __float2half2_rn(65504.f);
+  return __hmin2_nan(__hmax2_nan(h, __hneg2(top)), top);
+}
+// s less its last three bits, at most 8128: eight times it fits fp16 (scales reach 8736).
+__device__ __forceinline__ __half2 upper(__half2 s) {
+  const uint32_t u = *reinterpret_cast<const uint32_t *>(&s) & 0xfff8fff8u;
+  return __hmin2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(8128.f));
+}
+
+// A thread's places in a block: turn u takes 16 bytes, q of them, of a key's row.
+template <int D>
+struct ShPlace {
+  static constexpr int kChunks = Kv4Tile<D>::kRow / 16;        // 16-byte pieces of a row
+  static constexpr int kTurns = kShKeys * kChunks / 128;
+  int key, q, row;
+  const uint8_t *tile;
+  bool in;
+  __device__ __forceinline__ ShPlace(const uint8_t *raw, uint2 seen, int u, int t) {
+    const int i = u * 128 + t;
+    key = i / kChunks;
+    q = i % kChunks;
+    row = key & 31;
+    tile = raw + (key >> 5) * Kv4Tile<D>::kBytes;
+    in = (key < 32 ? seen.x : seen.y) >> row & 1;
+  }
+  // entry `which` of the four arrays (K scale, K zero, V scale, V zero), 0 for a key that is not there
+  __device__ __forceinline__ __half2 par(int which, int g) const {
+    const __half x = reinterpret_cast<const __half *>(tile + Kv4Tile<D>::kPar + which * Kv4Tile<D>::kArr)
+        [row * Kv4Tile<D>::kG + g];
+    return __half2half2(in ? x : __ushort_as_half(0));
+  }
+  // of word 4 q + w: its group, and where its dimensions lie in an operand
+  __device__ __forceinline__ uint32_t at(int w) const {
+    constexpr int G = Kv4Tile<D>::kG;
+    return sw128_offset(key, 8 * (w % G) + (4 / G) * q + w / G, kShKeys);
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void unpack_k(const uint8_t *raw, uint2 seen, uint32_t kdst, uint32_t zdst,
+                                         int stage, int t) {
+  using T = Kv4Tile<D>;
+  using P = ShPlace<D>;
+  constexpr int G = T::kG;
+  const __half2 off = __float2half2_rn(1032.f);
+#pragma unroll
+  for (int u = 0; u < P::kTurns; ++u) {
+    const P p(raw, seen, u, t);
+    const uint4 k4 = *reinterpret_cast<const uint4 *>(p.tile + p.row * T::kRow + p.q * 16);
+    const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+    __half2 hi[G], lo[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const __half2 s = p.par(0, g);
+      hi[g] = upper(s);
+      lo[g] = __hsub2(s, hi[g]);
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      __half2 c[4], x[4], y[4];
+      code_halves(kw[w], off, c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[k] = __hmul2(c[k], hi[w % G]);
+        y[k] = __hmul2(c[k], lo[w % G]);
+      }
+      sts_halves(kdst + p.at(w), x);
+      sts_halves(kdst + Sh<D>::kOperand + p.at(w), y);
+    }
+  }
+  if (t < kShKeys) {                                           // z z z s s s of each group; 0, or -inf: no key
+    const int row = t & 31;
+    const uint8_t *par = raw + (t >> 5) * T::kBytes + T::kPar;
+    const bool in = (t < 32 ? seen.x : seen.y) >> row & 1;
+    uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const uint32_t s = in ? reinterpret_cast<const uint16_t *>(par)[row * G + g] : 0u;
+      const uint32_t z = in ? reinterpret_cast<const uint16_t *>(par + T::kArr)[row * G + g] : 0u;
+      v[3 * g] = z | z << 16;
+      v[3 * g + 1] = z | s << 16;
+      v[3 * g + 2] = s | s << 16;
+    }
+    v[6] = in ? 0u : 0xfc00u;
+    sts128(zdst + sw128_offset(t, 2 * stage, kShKeys), make_uint4(v[0], v[1], v[2], v[3]));
+    sts128(zdst + sw128_offset(t, 2 * stage + 1, kShKeys), make_uint4(v[4], v[5], v[6], v[7]));
+  }
 }
 
 template <int D>
-__device__ __forceinline__ void unpack_block(const uint8_t *raw, uint2 seen, uint32_t kdst, uint32_t vdst,
-                                             float *par, int tid) {
+__device__ __forceinline__ void unpack_v(const uint8_t *raw, uint2 seen, uint32_t vdst, int t) {
   using T = Kv4Tile<D>;
+  using P = ShPlace<D>;
   constexpr int G = T::kG;
-  constexpr int kChunks = T::kRow / 16;                        // 16-byte pieces of a row
-  constexpr int kTurns = kShKeys * kChunks / 128;
-  const __half2 k_off = __float2half2_rn(1032.f), v_off = __float2half2_rn(1024.f);
+  const __half2 off = __float2half2_rn(1024.f);
 #pragma unroll
-  for (int u = 0; u < kTurns; ++u) {
-    const int i = u * 128 + tid, key = i / kChunks, q = i % kChunks;
-    const uint8_t *tile = raw + (key >> 5) * T::kBytes;
-    const int row = key & 31;
-    const bool in = (key < 32 ? seen.x : seen.y) >> row & 1;
-    const uint4 k4 = *reinterpret_cast<const uint4 *>(tile + row * T::kRow + q * 16);
-    const uint4 v4 = *reinterpret_cast<const uint4 *>(tile + T::kV + row * T::kRow + q * 16);
-    const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w}, vw[4] = {v4.x, v4.y, v4.z, v4.w};
-    const __half *vs = reinterpret_cast<const __half *>(tile + T::kPar + 2 * T::kArr) + row * G;
-    const __half *vz = vs + T::kArr / 2;
-    const __half zero = __ushort_as_half(0);
+  for (int u = 0; u < P::kTurns; ++u) {
+    const P p(raw, seen, u, t);
+    const uint4 v4 = *reinterpret_cast<const uint4 *>(p.tile + T::kV + p.row * T::kRow + p.q * 16);
+    const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
     __half2 s[G], z[G];
     bool wide = false;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      s[g] = __half2half2(in ? vs[g] : zero);
-      z[g] = __half2half2(in ? vz[g] : zero);
+      s[g] = p.par(2, g);
+      z[g] = p.par(3, g);
       wide |= !(fabsf(__low2float(z[g])) + 15.f * __low2float(s[g]) < 65504.f);
     }
     const bool any_wide = __any_sync(0xffffffffu, wide);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      // word 4 q + w is dimensions 64 g + 8 j ...
-      const int g = w % G, j = (4 / G) * q + w / G;
-      const uint32_t off = sw128_offset(key, 8 * g + j, kShKeys);
-      sts128(kdst + off, code_halves(kw[w], k_off));
-      uint4 v = code_halves(vw[w], v_off);
-      v = make_uint4(scaled(v.x, s[g], z[g]), scaled(v.y, s[g], z[g]), scaled(v.z, s[g], z[g]),
-                     scaled(v.w, s[g], z[g]));
-      if (any_wide) v = make_uint4(held(v.x), held(v.y), held(v.z), held(v.w));
-      sts128(vdst + off, v);
+      __half2 c[4];
+      code_halves(vw[w], off, c);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = __hfma2(c[k], s[w % G], z[w % G]);
+      if (any_wide) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = held(c[k]);
+      }
+      sts_halves(vdst + p.at(w), c);
     }
   }
-  if (tid < kShKeys) {                                         // K's scales and zeros of key tid
-    const int row = tid & 31;
-    const uint8_t *tile = raw + (tid >> 5) * T::kBytes + T::kPar;
-    const bool in = (tid < 32 ? seen.x : seen.y) >> row & 1;
-    float *dst = par + (tid >> 1) * (4 * G) + (tid & 1);
+}
+
+// A number as three fp16 ones.
+__device__ __forceinline__ void three_parts(float x, __half (&h)[3]) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const float s = in ? __half2float(reinterpret_cast<const __half *>(tile)[row * G + g]) : 0.f;
-      const float z =
-          in ? __half2float(reinterpret_cast<const __half *>(tile + T::kArr)[row * G + g]) : 0.f;
-      dst[2 * g] = s;                                          // [pair][ks_0 x 2, ks_1 x 2, kz_0 x 2, kz_1 x 2]
-      dst[2 * (G + g)] = fmaf(8.f, s, z);
-    }
+  for (int i = 0; i < 3; ++i) {
+    h[i] = __float2half_rn(x);
+    x -= __half2float(h[i]);
   }
 }
 
@@ -368,19 +443,20 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
   volatile int *const fail = &sh.fail;
   after_previous();
   if (plan.head->pairs <= (int64_t)blockIdx.x * plan.head->per) return;   // the whole CTA
-  if (warp == 12) tmem_alloc(&sh.tmem, S::kCols);
+  if (warp == 19) tmem_alloc(&sh.tmem, S::kCols);
   if (tid == 0) {
-    for (int i = 0; i < kShRaw; ++i) {
+    for (int i = 0; i < 2 * kShRaw; ++i) {
       mbar_init(&sh.raw_full[i], 1);
       mbar_init(&sh.raw_empty[i], 128);
     }
-    for (int i = 0; i < kShStages; ++i) {
-      mbar_init(&sh.kv_full[i], 128);
-      mbar_init(&sh.kv_empty[i], 1);
+    for (int i = 0; i < 2 * kShK; ++i) {
+      mbar_init(&sh.k_full[i], 128);
+      mbar_init(&sh.k_empty[i], 1);
     }
     mbar_init(&sh.q_full, 256);
     mbar_init(&sh.o_free, 256);
     for (int w = 0; w < 2; ++w) {
+      mbar_init(&sh.v_full[w], 128);
       mbar_init(&sh.s_full[w], 1);
       mbar_init(&sh.p_full[w], 128);
       mbar_init(&sh.o_done[w], 1);
@@ -392,23 +468,22 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const uint32_t sQ = smem_u32(smem + S::kOffQ), sK = smem_u32(smem + S::kOffK),
-                 sV = smem_u32(smem + S::kOffV);
+  const uint32_t sK = smem_u32(smem + S::kOffK), sV = smem_u32(smem + S::kOffV),
+                 sZ = smem_u32(smem + S::kOffZ);
   uint8_t *const raw0 = smem + S::kOffRaw;
-  float *const par0 = reinterpret_cast<float *>(smem + S::kOffPar);
   ShWalk walk(plan, blockIdx.x);
   ShSpan sp;
 
-  if (warp == 13) {
+  if (warp == 18) {
     // ------------------------------ loader ------------------------------
-    int it = 0;
+    int count[2] = {0, 0};                                     // blocks of each half
     int32_t err = 0;
     while (walk.next(sp, p.h_k)) {
       const int keys = walk.g.keys;
       const int32_t *row = p.table + (int64_t)walk.g.seq0 * p.width;
       int my_page = -1;
-      for (int b = sp.first; b < sp.end; ++b, ++it) {
-        const int n = (b - sp.first) & 15;
+      for (int b = sp.first; b < sp.end; ++b) {
+        const int n = (b - sp.first) & 15, w = n & 1, c = w ? count[1]++ : count[0]++;
         if (n == 0) {                                          // the pages of the next 32 tiles
           const int key = b * kShKeys + lane * 32;
           my_page = -1;
@@ -422,9 +497,9 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
         }
         const int pg[2] = {__shfl_sync(0xffffffffu, my_page, 2 * n),
                            __shfl_sync(0xffffffffu, my_page, 2 * n + 1)};
-        const int rs = it % kShRaw;
+        const int rs = w * kShRaw + c % kShRaw;
         if (lane == 0) {
-          if (it >= kShRaw) sh_wait(&sh.raw_empty[rs], ((it / kShRaw) - 1) & 1, p.status, fail);
+          if (c >= kShRaw) sh_wait(&sh.raw_empty[rs], ((c / kShRaw) - 1) & 1, p.status, fail);
           uint32_t seen[2], bytes = 0;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
@@ -432,7 +507,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
             seen[u] = pg[u] < 0 || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
             if (pg[u] >= 0) bytes += T::kBytes;
           }
-          sh.seen_raw[rs] = make_uint2(seen[0], seen[1]);
+          sh.seen[rs] = make_uint2(seen[0], seen[1]);
           if (bytes) mbar_arrive_expect_tx(&sh.raw_full[rs], bytes);
           else mbar_arrive(&sh.raw_full[rs]);
 #pragma unroll
@@ -452,90 +527,95 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
     if (err && lane == 0) raise(p.status, err);
     // nothing may be in flight when the CTA ends, given up or not
     if (lane == 0)
-      for (int i = max(0, it - kShRaw); i < it; ++i) {
-        const uint32_t bar = smem_u32(&sh.raw_full[i % kShRaw]);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(bar, (i / kShRaw) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      for (int w = 0; w < 2; ++w)
+        for (int c = max(0, count[w] - kShRaw); c < count[w]; ++c) {
+          const uint32_t bar = smem_u32(&sh.raw_full[w * kShRaw + c % kShRaw]);
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(bar, (c / kShRaw) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+          }
         }
-      }
     __syncwarp();
-  } else if (warp >= 8 && warp < 12) {
+  } else if (warp >= 8 && warp < 16) {
     // ----------------------------- unpackers ----------------------------
-    const int t = tid - 256;
-    int it = 0;
+    const int w = (warp - 8) >> 2, t = tid & 127;
+    int c = 0;                                                 // blocks of this half so far
     while (walk.next(sp, p.h_k)) {
-      for (int b = sp.first; b < sp.end; ++b, ++it) {
-        const int rs = it % kShRaw, st = it % kShStages;
-        sh_wait(&sh.raw_full[rs], (it / kShRaw) & 1, p.status, fail);
-        if (it >= kShStages) sh_wait(&sh.kv_empty[st], ((it / kShStages) - 1) & 1, p.status, fail);
+      for (int n = w; n < sp.end - sp.first; n += 2, ++c) {
+        const int rs = w * kShRaw + c % kShRaw, ks = w * kShK + c % kShK;
+        sh_wait(&sh.raw_full[rs], (c / kShRaw) & 1, p.status, fail);
+        if (c >= kShK) sh_wait(&sh.k_empty[ks], ((c / kShK) - 1) & 1, p.status, fail);
         __syncwarp();
-        const uint2 seen = sh.seen_raw[rs];
-        if (t == 0) sh.seen[st] = seen;
-        unpack_block<D>(raw0 + rs * S::kRawBytes, seen, sK + st * S::kOperand, sV + st * S::kOperand,
-                        par0 + st * (S::kParBytes / 4), t);
+        const uint2 seen = sh.seen[rs];
+        const uint8_t *raw = raw0 + rs * S::kRawBytes;
+        unpack_k<D>(raw, seen, sK + ks * 2 * S::kOperand, sZ, ks, t);
         fence_proxy_async_smem();
+        mbar_arrive(&sh.k_full[ks]);
+        if (c > 0) sh_wait(&sh.o_done[w], (c - 1) & 1, p.status, fail);
+        __syncwarp();
+        unpack_v<D>(raw, seen, sV + w * S::kOperand, t);
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.v_full[w]);
         mbar_arrive(&sh.raw_empty[rs]);
-        mbar_arrive(&sh.kv_full[st]);
       }
     }
-  } else if (warp == 12) {
-    // ---------------------------- MMA thread ----------------------------
+  } else if (warp == 16 || warp == 17) {
+    // ---------------------------- MMA threads ---------------------------
     if (lane == 0) {
       constexpr uint32_t kIdS = idesc_f16(kShRows, kShKeys, false, false, true);
       constexpr uint32_t kIdO = idesc_f16(kShRows, D, false, true, true);
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);
-      const uint32_t lo_q = sdesc_lo_sw128(sQ, 16), lo_k = sdesc_lo_sw128(sK, 16);
-      const uint32_t lo_v = sdesc_lo_sw128(sV, kShKeys * 128);
-      int it = 0, turn = 0, done[2] = {0, 0};
+      const int w = warp - 16;
+      const uint32_t lo_k = sdesc_lo_sw128(sK, 16), lo_z = sdesc_lo_sw128(sZ, 16);
+      const uint32_t bv = sdesc_lo_sw128(sV + w * S::kOperand, kShKeys * 128);
+      const uint32_t ts = tmem + S::kS + w * kShKeys, to = tmem + S::kO + w * D;
+      const uint32_t tq = tmem + S::kQ, tsum = tmem + S::kSums;
+      int turn = 0, c = 0;
       for (; walk.next(sp, p.h_k); ++turn) {
         const int nb = sp.end - sp.first;
         sh_wait(&sh.q_full, turn & 1, p.status, fail);
-        for (int n = 0; n <= nb; ++n) {
-          if (n < nb) {
-            const int st = (it + n) % kShStages, w = n & 1;
-            sh_wait(&sh.kv_full[st], ((it + n) / kShStages) & 1, p.status, fail);
-            tc_fence_after();
-            const uint32_t ts = tmem + w * S::kScores, bk = lo_k + (st * S::kOperand >> 4);
+        for (int n = w; n < nb; n += 2, ++c) {
+          const int ks = w * kShK + c % kShK;
+          const uint32_t bk = lo_k + ks * (2 * S::kOperand >> 4), bz = lo_z + ks * (32 >> 4);
+          sh_wait(&sh.k_full[ks], (c / kShK) & 1, p.status, fail);
+          tc_fence_after();
+          // smallest parts first: each step cuts the sum so far towards zero
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              mma_f16(ts + (kk >> 2) * kShKeys, sdesc_join(lo_q + (kmajor_step(kShRows, kk) >> 4), kHi),
-                      sdesc_join(bk + (kmajor_step(kShKeys, kk) >> 4), kHi), kIdS, (kk & 3) > 0);
-            mma_commit(&sh.s_full[w]);
-          }
-          if (n > 0) {
-            const int m = n - 1, st = (it + m) % kShStages, w = m & 1;
-            sh_wait(&sh.p_full[w], done[w] & 1, p.status, fail);
-            ++done[w];
-            if (m == 0 && turn > 0) sh_wait(&sh.o_free, (turn - 1) & 1, p.status, fail);
-            tc_fence_after();
-            const uint32_t ts = tmem + w * S::kScores, to = tmem + 2 * S::kScores + w * D;
-            const uint32_t bv = lo_v + (st * S::kOperand >> 4);
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16_ts(ts, tq + kk * 8,
+                       sdesc_join(bk + ((S::kOperand + kmajor_step(kShKeys, kk)) >> 4), kHi), kIdS, kk > 0);
+          mma_f16_ts(ts, tsum, sdesc_join(bz, kHi), kIdS, 1);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16_ts(ts, tq + kk * 8, sdesc_join(bk + (kmajor_step(kShKeys, kk) >> 4), kHi), kIdS, 1);
+          mma_commit(&sh.s_full[w]);
+          mma_commit(&sh.k_empty[ks]);
+          sh_wait(&sh.v_full[w], c & 1, p.status, fail);
+          sh_wait(&sh.p_full[w], c & 1, p.status, fail);
+          if (n == w && turn > 0) sh_wait(&sh.o_free, (turn - 1) & 1, p.status, fail);
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < kShKeys / 16; ++kk)
+            mma_f16_ts(to, ts + kk * 8, sdesc_join(bv + (mnmajor_step(kk) >> 4), kHi), kIdO,
+                       n >= 2 || kk > 0);
+          if (kFp16) {                                         // what the rounding of W has left
 #pragma unroll
             for (int kk = 0; kk < kShKeys / 16; ++kk)
-              mma_f16_ts(to, ts + kk * 8, sdesc_join(bv + (mnmajor_step(kk) >> 4), kHi), kIdO,
-                         m >= 2 || kk > 0);
-            if (kFp16) {                                       // what the rounding of W has left
-#pragma unroll
-              for (int kk = 0; kk < kShKeys / 16; ++kk)
-                mma_f16_ts(to, ts + kShKeys / 2 + kk * 8,
-                           sdesc_join(bv + (mnmajor_step(kk) >> 4), kHi), kIdO, 1);
-            }
-            mma_commit(&sh.kv_empty[st]);
-            mma_commit(&sh.o_done[w]);
+              mma_f16_ts(to, ts + kShKeys / 2 + kk * 8, sdesc_join(bv + (mnmajor_step(kk) >> 4), kHi),
+                         kIdO, 1);
           }
+          mma_commit(&sh.o_done[w]);                           // V's place is free, too
         }
-        it += nb;
       }
     }
     __syncwarp();
-  } else {
+  } else if (warp < 8) {
     // ------------------------------ softmax -----------------------------
     const int w = warp >> 2, row = tid & 127;                  // row: tensor memory lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + w * S::kScores + lane_off;
-    const uint32_t to = tmem + 2 * S::kScores + lane_off;
+    const uint32_t ts = tmem + S::kS + w * kShKeys + lane_off;
+    const uint32_t to = tmem + S::kO + lane_off;
     constexpr int kHalf = D / 2;                               // dimensions of a row that a thread brings
-    int it = 0, count = 0;
+    int count = 0;
     while (walk.next(sp, p.h_k)) {
       const int nb = sp.end - sp.first;
       // ---- the tile's queries ----
@@ -562,89 +642,83 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
       const uint32_t big = max(sh.top[0][row], sh.top[1][row]);
       const float mag = unpack2<kFp16>(big).x;
       const int ex = max(static_cast<int>(__float_as_uint(mag) >> 23) - 127, -100);
-      const float up = __uint_as_float(static_cast<uint32_t>(14 - ex + 127) << 23);   // 2^(14 - ex)
+      const float up = __uint_as_float(static_cast<uint32_t>(kShQTop - ex + 127) << 23);   // 2^(5 - ex)
       const float sgn = p.scale < 0.f ? -up : up;
       float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < kHalf / 8; ++i) {
-        const float2 a = unpack2<kFp16>(q4[i].x), b = unpack2<kFp16>(q4[i].y);
-        const float2 c = unpack2<kFp16>(q4[i].z), e = unpack2<kFp16>(q4[i].w);
-        uint4 o;                                               // dimensions 0 4, 1 5, 2 6, 3 7
-        o.x = pack2<true>(a.x * sgn, c.x * sgn);
-        o.y = pack2<true>(a.y * sgn, c.y * sgn);
-        o.z = pack2<true>(b.x * sgn, e.x * sgn);
-        o.w = pack2<true>(b.y * sgn, e.y * sgn);
-        const float2 f0 = unpack2<true>(o.x), f1 = unpack2<true>(o.y);
-        const float2 f2 = unpack2<true>(o.z), f3 = unpack2<true>(o.w);
-        sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
-        sts128(sQ + sw128_offset(row, w * (kHalf / 8) + i, kShRows), o);
+      for (int i = 0; i < kHalf / 8; i += 4) {
+        uint32_t o[16];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 a = unpack2<kFp16>(q4[i + j].x), b = unpack2<kFp16>(q4[i + j].y);
+          const float2 c = unpack2<kFp16>(q4[i + j].z), e = unpack2<kFp16>(q4[i + j].w);
+          o[4 * j] = pack2<true>(a.x * sgn, c.x * sgn);        // dimensions 0 4, 1 5, 2 6, 3 7
+          o[4 * j + 1] = pack2<true>(a.y * sgn, c.y * sgn);
+          o[4 * j + 2] = pack2<true>(b.x * sgn, e.x * sgn);
+          o[4 * j + 3] = pack2<true>(b.y * sgn, e.y * sgn);
+          const float2 f0 = unpack2<true>(o[4 * j]), f1 = unpack2<true>(o[4 * j + 1]);
+          const float2 f2 = unpack2<true>(o[4 * j + 2]), f3 = unpack2<true>(o[4 * j + 3]);
+          sum += ((f0.x + f0.y) + (f1.x + f1.y)) + ((f2.x + f2.y) + (f3.x + f3.y));
+        }
+        tmem_st16(tmem + S::kQ + lane_off + w * (kHalf / 2) + i * 4, o);
       }
       sh.sums[w][row] = sum;
-      fence_proxy_async_smem();
-      mbar_arrive(&sh.q_full);
       named_bar_sync(1, 256);
-      float qs[G];
-      if constexpr (G == 2) {
-        qs[0] = sh.sums[0][row];
-        qs[1] = sh.sums[1][row];
-      } else {
-        qs[0] = sh.sums[0][row] + sh.sums[1][row];
+      if (w == 0) {
+        // Q and 8 Q of each group, in three parts each, against z and s; 1 against the mask
+        float qs[2] = {sh.sums[0][row], sh.sums[1][row]};
+        if (G == 1) qs[0] += qs[1];
+        uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          __half a[3], b[3];
+          three_parts(qs[g], a);
+          three_parts(8.f * qs[g], b);
+          const __half2 x = __halves2half2(a[0], a[1]), y = __halves2half2(a[2], b[0]),
+                        z = __halves2half2(b[1], b[2]);
+          o[3 * g] = *reinterpret_cast<const uint32_t *>(&x);
+          o[3 * g + 1] = *reinterpret_cast<const uint32_t *>(&y);
+          o[3 * g + 2] = *reinterpret_cast<const uint32_t *>(&z);
+        }
+        o[6] = 0x3c00u;
+        tmem_st8(tmem + S::kSums + lane_off, o);
       }
-      // S = |scale| 2^(ex - 14) x, in the exponent of 2; `over` powers are left out where the factor
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh.q_full);
+      // S = |scale| 2^(ex - 5) x, in the exponent of 2; `over` powers are left out where the factor
       // could overflow, and put back into the maximum (scores then are equal or far apart)
       const int over = max(0, static_cast<int>((__float_as_uint(p.scale) & 0x7fffffffu) >> 23) - 127 +
-                                  ex - 14 + 2 - kShMulTop);
-      const float mul = ldexpf(fabsf(p.scale), ex - 14 - over) * 1.4426950408889634f;
+                                  ex - kShQTop + 2 - kShMulTop);
+      // (a factor of 0 would make NaN of the mask's -inf: the least one leaves scores of 0)
+      const float mul =
+          fmaxf(ldexpf(fabsf(p.scale), ex - kShQTop - over) * 1.4426950408889634f, 1.17549435e-38f);
       // ---- its blocks, every other one ----
-      float ref = -INFINITY, thr = -INFINITY;                  // reference (the maximum less 8), when to raise it
+      // Differences are taken before the factor: between scores they are exact or nearly so, whatever
+      // the scores' size, and weights stay within fp16 however a product rounds.
+      float ref = -INFINITY, thr = -INFINITY;                  // the reference score, and when to raise it
+      const float slack = __fdividef(kShSlack, mul);
       Pair l(0.f, 0.f);
       for (int n = w; n < nb; n += 2, ++count) {
-        const int st = (it + n) % kShStages;
-        sh_wait(&sh.kv_full[st], ((it + n) / kShStages) & 1, p.status, fail);   // scales and zeros
         sh_wait(&sh.s_full[w], count & 1, p.status, fail);
         tc_fence_after();
-        const float4 *par = reinterpret_cast<const float4 *>(par0 + st * (S::kParBytes / 4));
-        float s[kShKeys];
+        // 32 scores at a time, once for the maximum and once for the weights: all 64 do not fit
+        // beside what the rest takes of 96 registers
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < kShKeys; c += 32) {
-          float a[G][32];
+          float x[32];
+          tmem_ld32(ts + c, x);
 #pragma unroll
-          for (int g = 0; g < G; ++g) tmem_ld32(ts + g * kShKeys + c, a[g]);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            Pair x;
-            if constexpr (G == 2) {
-              const float4 ks = par[c + j], kz = par[c + j + 1];
-              x = Pair(kz.x, kz.y) * Pair(qs[0], qs[0]);
-              x = fma(Pair(kz.z, kz.w), Pair(qs[1], qs[1]), x);
-              x = fma(Pair(ks.x, ks.y), Pair(a[0][j], a[0][j + 1]), x);
-              x = fma(Pair(ks.z, ks.w), Pair(a[1][j], a[1][j + 1]), x);
-            } else {
-              const float4 k = par[(c + j) / 2];
-              x = fma(Pair(k.x, k.y), Pair(a[0][j], a[0][j + 1]), Pair(k.z, k.w) * Pair(qs[0], qs[0]));
-            }
-            const float2 y = (x * Pair(mul, mul)).get();       // rounded before the reference is taken off
-            s[c + j] = y.x;
-            s[c + j + 1] = y.y;
-          }
+          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
         }
-        const uint2 seen = sh.seen[st];
-        if ((seen.x & seen.y) != ~0u) {
-#pragma unroll
-          for (int j = 0; j < kShKeys; ++j)
-            if (!((j < 32 ? seen.x : seen.y) >> (j & 31) & 1)) s[j] = -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int j = 4; j < kShKeys; ++j) mx[j & 3] = fmaxf(mx[j & 3], s[j]);
         const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         if (__any_sync(0xffffffffu, m > thr)) {
           float f = 1.f;
           if (m > thr) {
-            const float next = __fadd_ru(m, -kShUp);           // never lower: weights have to fit fp16
-            f = ex2_approx(ref - next);                        // 0 the first time
-            ref = next;
-            thr = __fadd_rd(m, kShSlack);
+            f = ex2_approx((ref - m) * mul);                   // 0 the first time
+            ref = m;
+            thr = __fadd_rd(m, slack);
           }
           l = l * Pair(f, f);
           if (n >= 2) {                                        // what the blocks before have left
@@ -661,39 +735,46 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
           }
         }
         const float base = ref == -INFINITY ? 0.f : -ref;      // no key so far: weights of 0
+        uint32_t rest[2][16];
 #pragma unroll
         for (int c = 0; c < kShKeys; c += 32) {
-          uint32_t pk[16], rest[16];
+          float s[32];
+          tmem_ld32(ts + c, s);
+          uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const float2 e = (Pair(s[c + j], s[c + j + 1]) + Pair(base, base)).get();
-            const float x = ex2_approx(e.x), y = ex2_approx(e.y);
-            l = l + Pair(x, y);
-            pk[j / 2] = pack2<true>(x, y);
+            const Pair d = Pair(s[j], s[j + 1]) + Pair(base, base);
+            const float2 e = fma(d, Pair(mul, mul), Pair(kShUp, kShUp)).get();
+            const float a = ex2_approx(e.x), b = ex2_approx(e.y);
+            l = l + Pair(a, b);
+            pk[j / 2] = pack2<true>(a, b);
             if (kFp16) {
               const float2 hi = unpack2<true>(pk[j / 2]);
-              rest[j / 2] = pack2<true>(x - hi.x, y - hi.y);
+              rest[c / 32][j / 2] = pack2<true>(a - hi.x, b - hi.y);
             }
           }
-          tmem_st16(ts + c / 2, pk);
-          if (kFp16) tmem_st16(ts + kShKeys / 2 + c / 2, rest);
+          tmem_st16(ts + c / 2, pk);                           // over scores that have been read
+        }
+        if (kFp16) {
+          tmem_st16(ts + kShKeys / 2, rest[0]);
+          tmem_st16(ts + kShKeys / 2 + 16, rest[1]);
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&sh.p_full[w]);
       }
-      it += nb;
-      // ---- the two warpgroups' sums ----
+      // ---- the two halves' sums ----
       if (nb > w) sh_wait(&sh.o_done[w], (count - 1) & 1, p.status, fail);
       const float2 l2 = l.get();
-      sh.ml[w][row] = make_float2(ref, l2.x + l2.y);
+      sh.ml[w][row] = make_float2(ref * mul, l2.x + l2.y);
       named_bar_sync(1, 256);
       tc_fence_after();
       const float2 m0 = sh.ml[0][row];
       const float2 m1 = nb > 1 ? sh.ml[1][row] : make_float2(-INFINITY, 0.f);
       const float M = fmaxf(m0.x, m1.x);
-      const float f0 = m0.y != 0.f ? ex2_approx(m0.x - M) : 0.f;
-      const float f1 = m1.y != 0.f ? ex2_approx(m1.x - M) : 0.f;
+      constexpr float kDown = 1.f / 256.f;                     // 2^-kShUp
+      const float f0 = m0.y != 0.f ? ex2_approx(m0.x - M) * kDown : 0.f;
+      const float f1 = m1.y != 0.f ? ex2_approx(m1.x - M) * kDown : 0.f;
       float *dst = plan.part + ((int64_t)sp.part + row) * D + w * kHalf;
 #pragma unroll 1
       for (int c = 0; c < kHalf; c += 16) {
@@ -725,7 +806,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12) tmem_dealloc(tmem, S::kCols);
+  if (warp == 19) tmem_dealloc(tmem, S::kCols);
 }
 
 // ---- join ------------------------------------------------------------------------------
