@@ -70,8 +70,26 @@ struct Kv4DecodeParams {
   float *rec;
 };
 
+// Of the run kernel (kv4_decode.cu): query heads of a segment at most, CTAs at most, and where the parts
+// of a segment that begins in CTA i and ends in another lie.
+constexpr int kK4Heads = 8;
+constexpr int kK4MaxCtas = 320;
+struct K4Split {
+  int32_t seg, parts;   // parts 0: no segment of this CTA continues in the next
+};
+// Partial result i: O [heads][D] (not divided by l), then (m, l) per head.
+__host__ __device__ constexpr int part_floats(int d, int g) {
+  return (g < kK4Heads ? g : kK4Heads) * (d + 2);
+}
+template <int D>
+__device__ __forceinline__ float *part_of(const Kv4DecodeParams &p, int i) {
+  return reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + kK4MaxCtas * sizeof(K4Split)) +
+         (int64_t)i * part_floats(D, p.g);
+}
+
 // A record: the sums of a (sequence, query head), not divided, then its maximum (in the exponent of
-// 2) and sum of weights.
+// 2) and sum of weights; or, as whole numbers, 0, 0, the CTA in which its segment begins, and how many
+// parts there are: that CTA's second and the following ones' first.
 template <int D>
 constexpr int kRecFloats = D + 4;
 

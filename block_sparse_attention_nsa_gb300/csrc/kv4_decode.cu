@@ -68,10 +68,8 @@ namespace nsa {
 // 16 blocks: 12.9 -> 11.7 us; 8 x 64K in full: 59.8 -> 57.0).  At d = 64 126 registers do.
 template <int D>
 constexpr int kSmWarps = D == 128 ? 12 : 16;
-constexpr int kK4Heads = 8;          // query heads of a segment at most
 constexpr int kStages = 3;           // tiles of a warp's ring
 constexpr int kOver = 4;             // tiles that a segment's start counts as
-constexpr int kK4MaxCtas = 320;      // CTAs of the run kernel at most
 constexpr float kSlack = 2.f;        // scores may exceed the reference maximum by this much
 constexpr float kMiddle = 7.5f;      // of the codes
 // Where sums need no centre.  What they lose grows with a warp's tiles and, next to what is left of
@@ -94,11 +92,6 @@ struct K4 {
   static constexpr int kKept = (kStages - 1) * T::kBytes;
   static constexpr int kRunWarps = kSmWarps<D> / 2, kRunThreads = kRunWarps * 32;   // two CTAs an SM
   static_assert(kK4Heads / 2 * kHeadPair * 4 <= T::kBytes, "a stage holds an area");
-};
-
-// Where the parts of a segment that begins in CTA i and ends in another lie.
-struct K4Split {
-  int32_t seg, parts;   // parts 0: no segment of this CTA continues in the next
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -791,7 +784,7 @@ __device__ __forceinline__ void write_out(const Kv4DecodeParams &p, int b, int h
   if constexpr (kSuffix) {
     float *rec = p.rec + ((int64_t)b * p.h_q + hq) * kRecFloats<D>;
     *reinterpret_cast<float4 *>(rec + dim) = x;
-    if (dim == 0) *reinterpret_cast<float2 *>(rec + D) = make_float2(M, l);
+    if (dim == 0) *reinterpret_cast<float4 *>(rec + D) = make_float4(M, l, 0.f, 0.f);
     return;
   }
   const bool any = l != 0.f;                        // a NaN sum stays one
@@ -942,16 +935,6 @@ __device__ __forceinline__ int counted_tiles(const Kv4DecodeParams &p, int b, in
 __device__ __forceinline__ K4Split *splits_of(const Kv4DecodeParams &p) {
   return static_cast<K4Split *>(p.ws);
 }
-// Partial result i: O [heads][D] (not divided by l), then (m, l) per head.
-__host__ __device__ constexpr int part_floats(int d, int g) {
-  return (g < kK4Heads ? g : kK4Heads) * (d + 2);
-}
-template <int D>
-__device__ __forceinline__ float *part_of(const Kv4DecodeParams &p, int i) {
-  return reinterpret_cast<float *>(static_cast<uint8_t *>(p.ws) + kK4MaxCtas * sizeof(K4Split)) +
-         (int64_t)i * part_floats(D, p.g);
-}
-
 __device__ __forceinline__ int warp_incl_sum(int x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -1085,7 +1068,7 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
   err = __reduce_or_sync(0xffffffffu, err);
   if (err && lane == 0) raise(p.status, err);
   if (lane == 0) flags[warp] = left;
-  if (tid == 0) splits_of(p)[blockIdx.x] = K4Split{0, 0};
+  if (!kSuffix && tid == 0) splits_of(p)[blockIdx.x] = K4Split{0, 0};
   __syncthreads();
   // ---- join the parts of segments that cross warps ----
   // A group is a segment's parts in this CTA: the last part of warp `open` (-1: the segment
@@ -1148,9 +1131,9 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
     float *part = nullptr;
     if (open < 0) part = part_of<D>(p, 2 * blockIdx.x);
     else if (on) part = part_of<D>(p, 2 * blockIdx.x + 1);
-    if (open >= 0 && on && th == 0)
-      splits_of(p)[blockIdx.x] = K4Split{
-          sg.b * units + who.y, (who.z - 1) / per - static_cast<int>(blockIdx.x) + 1};
+    const int cta = blockIdx.x, parts = (who.z - 1) / per - cta + 1;   // where the segment began here
+    if (!kSuffix && open >= 0 && on && th == 0)
+      splits_of(p)[cta] = K4Split{sg.b * units + who.y, parts};
 #pragma unroll 1
     for (int i = th; i < sg.g * (D / 4); i += nth) {
       const int head = i / (D / 4), dim = 4 * (i % (D / 4));
@@ -1176,7 +1159,13 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
         float2 *dst = reinterpret_cast<float2 *>(part + head * D + dim);
         dst[0] = make_float2(x.x, x.y);
         dst[1] = make_float2(x.z, x.w);
-        if (dim == 0) *reinterpret_cast<float2 *>(part + sg.g * D + 2 * head) = make_float2(M, l);
+        if (dim == 0) {
+          *reinterpret_cast<float2 *>(part + sg.g * D + 2 * head) = make_float2(M, l);
+          if (kSuffix && open >= 0) {      // the record says where the parts lie
+            float *rec = p.rec + ((int64_t)sg.b * p.h_q + sg.q0 + head) * kRecFloats<D>;
+            *reinterpret_cast<int4 *>(rec + D) = make_int4(0, 0, cta, parts);
+          }
+        }
       } else {
         write_out<D, kFp16, kSuffix>(p, sg.b, sg.q0 + head, dim, x, M, l);
       }
@@ -1188,7 +1177,7 @@ __global__ void __launch_bounds__(K4<D>::kRunThreads, 2)
 // second part and the following CTAs' first ones.  One CTA per (split, head): its warps take
 // the parts in turn, eight in flight.
 constexpr int kMergeThreads = 256;
-template <int D, bool kFp16, bool kSuffix>
+template <int D, bool kFp16>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParams p, int units) {
   constexpr int kWarps = kMergeThreads / 32, E = D / 32;
   __shared__ __align__(16) float acc[kWarps][D];
@@ -1262,7 +1251,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4DecodeParam
       u.z = fmaf(f, o.z, u.z);
       u.w = fmaf(f, o.w, u.w);
     }
-    write_out<D, kFp16, kSuffix>(p, sg.b, sg.q0 + head, 4 * tid, u, M, l);
+    write_out<D, kFp16>(p, sg.b, sg.q0 + head, 4 * tid, u, M, l);
   }
 }
 
@@ -1355,8 +1344,8 @@ static cudaError_t run_runs(const Kv4DecodeParams &p, int units, int sms, cudaSt
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   e = launch_kv4(kernel, dim3(ctas), threads, smem, 1, s, p, units);
-  if (e != cudaSuccess) return e;
-  return launch_kv4(kv4_merge_kernel<D, kFp16, kSuffix>, dim3(ctas, min(p.g, kK4Heads)), kMergeThreads, 0,
+  if (e != cudaSuccess || kSuffix) return e;   // records and parts are joined elsewhere
+  return launch_kv4(kv4_merge_kernel<D, kFp16>, dim3(ctas, min(p.g, kK4Heads)), kMergeThreads, 0,
                     1, s, p, units);
 }
 

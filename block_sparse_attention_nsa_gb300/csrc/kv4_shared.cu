@@ -50,7 +50,7 @@ constexpr int kShKeys = 64;          // keys of a block
 constexpr int kShRaw = 2, kShK = 2;
 constexpr int kShThreads = 640;
 constexpr int kShMaxCtas = 256;
-constexpr int kShareMin = 2;         // sequences from which a prefix is shared
+constexpr int kShOver = 8;           // blocks that a tile's start and end count as
 constexpr int kSetupThreads = 1024;
 constexpr float kShSlack = 4.f;      // scores may exceed the reference by this much
 constexpr float kShUp = 8.f;         // weights are 2^8 times 2^(S - m)
@@ -58,12 +58,13 @@ constexpr int kShQTop = 5;           // exponent of a row's largest q^
 constexpr int kShMulTop = 92;        // a score's factor stays below 2^(kShMulTop + 2), scores in its unit below 2^30
 
 // A group that shares: its first sequence and number of rows per KV head, its blocks and tiles, and
-// what lies before it: (tile, block) pairs, and partial rows.
+// what lies before it: counted blocks (kShOver a tile more than there are), and partial rows.
 struct ShGroup {
   int32_t seq0, rows, blocks, tiles, keys, pair0, row0, pad;
+  __device__ __forceinline__ int counted() const { return blocks + kShOver; }
 };
 struct ShHead {
-  int32_t groups, pairs, per, pad;   // per: pairs of a CTA
+  int32_t groups, pairs, per, pad;   // counted blocks; of them a CTA's
 };
 struct ShPlan {
   ShHead *head;
@@ -122,17 +123,31 @@ __device__ __forceinline__ int setup_incl(int x, int (&part)[32], int &total) {
   return x + (warp ? before : 0);
 }
 
+// Shared or not?  In units of 25 ns of an SM's time: a tile of 128 rows takes about 240 and 24 a block
+// of 64 keys; the sequences' own passes over the prefix take 5 a tile of 32 keys each.
+__device__ __forceinline__ bool worth_sharing(int n, int g, int keys) {
+  const int64_t own = (int64_t)n * (g > kK4Heads ? 2 : 1) * ((keys + 31) / 32) * 5;
+  const int64_t tiles = ((int64_t)n * g + kShRows - 1) / kShRows;
+  return n > 1 && own > tiles * (240 + 24 * (int64_t)((keys + kShKeys - 1) / kShKeys));
+}
+
 // One CTA: groups that share, in order, what lies before each, and each sequence's group and first own
 // key.  A cu_groups out of order shares nothing.
+constexpr int kSetupGroups = 1024;   // up to as many the groups' numbers stay in shared memory
 __global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParams p, ShPlan plan, int ctas,
                                                                   int least) {
-  __shared__ int part[32];
+  __shared__ int part[32], s_cu[kSetupGroups + 1], s_at[kSetupGroups], s_keys[kSetupGroups];
   const int tid = threadIdx.x, cap = p.dec.width << p.dec.page_log2;
+  const bool few = p.num_groups <= kSetupGroups;
   after_previous();
   int32_t err = 0;
   for (int i = tid; i < p.num_groups; i += kSetupThreads) {
     const int a = p.cu[i], b = p.cu[i + 1];
     if (a < 0 || (i == 0 && a != 0) || b < a || b > p.dec.num_seqs) err |= NSA_DEVERR_BAD_SEQLENS;
+    if (few) {
+      s_cu[i] = a;
+      s_cu[i + 1] = b;               // the neighbour writes the same
+    }
   }
   const bool ordered = !__syncthreads_or(err);
   int groups = 0, pairs = 0, rows = 0;
@@ -148,33 +163,43 @@ __global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParam
         keys = 0;
       }
     }
-    const bool shares = n >= kShareMin && keys > 0;
+    const bool shares = keys > 0 && worth_sharing(n, p.dec.g, keys);
     const int r = shares ? n * p.dec.g : 0, tiles = (r + kShRows - 1) / kShRows;
     const int blocks = (keys + kShKeys - 1) / kShKeys;
     int total;
     const int g = groups + setup_incl(shares, part, total) - shares;
     groups += total;
-    const int w = tiles * p.dec.h_k * blocks;
+    const int w = tiles * p.dec.h_k * (blocks + kShOver);
     const int before = pairs + setup_incl(w, part, total) - w;
     pairs += total;
     const int row = rows + setup_incl(r * p.dec.h_k, part, total) - r * p.dec.h_k;
     rows += total;
     if (shares) plan.groups[g] = ShGroup{a, r, blocks, tiles, keys, before, row, 0};
-    if (i < p.num_groups) plan.at[i] = shares ? g : -1;
+    if (i < p.num_groups) {
+      if (few) {
+        s_at[i] = shares ? g : -1;
+        s_keys[i] = keys;
+      } else {
+        plan.at[i] = shares ? g : -1;
+      }
+    }
   }
-  if (tid == 0) {
-    const int per = max((pairs + ctas - 1) / ctas, least);
-    *plan.head = ShHead{groups, pairs, per, 0};
-  }
+  if (tid == 0) *plan.head = ShHead{groups, pairs, max((pairs + ctas - 1) / ctas, least), 0};
   if (__syncthreads_or(err) && tid == 0) raise(p.dec.status, NSA_DEVERR_BAD_SEQLENS);
   for (int b = tid; b < p.dec.num_seqs; b += kSetupThreads) {
     int g = -1, lo = 0;
-    if (ordered && b < p.cu[p.num_groups]) g = plan.at[upper_index(p.cu, p.num_groups, b)];
-    if (g >= 0) {
-      const int keys = plan.groups[g].keys;
-      // a sequence that ends inside the prefix attends to its own pages alone
-      if (min(max(p.dec.lens[b], 0), cap) >= keys) lo = keys;
-      else g = -1;
+    if (ordered && groups > 0) {
+      const int32_t *cu = few ? s_cu : p.cu;
+      if (b < cu[p.num_groups]) {
+        const int i = upper_index(cu, p.num_groups, b);
+        g = few ? s_at[i] : plan.at[i];
+        if (g >= 0) {
+          const int keys = few ? s_keys[i] : plan.groups[g].keys;
+          // a sequence that ends inside the prefix attends to its own pages alone
+          if (min(max(p.dec.lens[b], 0), cap) >= keys) lo = keys;
+          else g = -1;
+        }
+      }
     }
     plan.lo[b] = lo;
     plan.of[b] = g;
@@ -216,8 +241,8 @@ struct ShShared {
 
 // One tile's blocks in a CTA's run.
 struct ShSpan {
-  int group, h, tile, first, end;              // blocks [first, end)
-  int part;                                    // where its partial rows lie
+  int h, tile, first, end;                     // blocks [first, end)
+  int rows, part;                              // its rows, and where its partial rows lie
 };
 // Walks a CTA's run.
 struct ShWalk {
@@ -241,17 +266,21 @@ struct ShWalk {
     }
   }
   __device__ __forceinline__ bool next(ShSpan &s, int h_k) {
-    if (at >= stop) return false;
-    if (at >= g.pair0 + g.tiles * h_k * g.blocks) g = groups[++group];
-    const int rel = at - g.pair0, tile = rel / g.blocks;        // of the group's h_k * tiles
-    s.group = group;
-    s.h = tile / g.tiles;
-    s.tile = tile - s.h * g.tiles;
-    s.first = rel - tile * g.blocks;
-    s.end = min(g.blocks, s.first + (stop - at));
-    s.part = cta * kShRows + g.row0 + s.h * g.rows + s.tile * kShRows;
-    at += s.end - s.first;
-    return true;
+    while (at < stop) {
+      if (at >= g.pair0 + g.tiles * h_k * g.counted()) g = groups[++group];
+      const int rel = at - g.pair0, tile = rel / g.counted();   // of the group's h_k * tiles
+      const int v0 = rel - tile * g.counted(), v1 = min(g.counted(), v0 + (stop - at));
+      at += v1 - v0;
+      s.first = max(0, v0 - kShOver);
+      s.end = v1 - kShOver;
+      if (s.end <= s.first) continue;
+      s.h = tile / g.tiles;
+      s.tile = tile - s.h * g.tiles;
+      s.rows = min(kShRows, g.rows - s.tile * kShRows);
+      s.part = cta * kShRows + g.row0 + s.h * g.rows + s.tile * kShRows;
+      return true;
+    }
+    return false;
   }
 };
 
@@ -620,7 +649,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
       const int nb = sp.end - sp.first;
       // ---- the tile's queries ----
       const int r = sp.tile * kShRows + row;
-      const bool real = r < walk.g.rows;
+      const bool real = row < sp.rows;
       uint4 q4[kHalf / 8];
       int64_t qrow = 0;
       if (real) {
@@ -775,7 +804,8 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
       constexpr float kDown = 1.f / 256.f;                     // 2^-kShUp
       const float f0 = m0.y != 0.f ? ex2_approx(m0.x - M) * kDown : 0.f;
       const float f1 = m1.y != 0.f ? ex2_approx(m1.x - M) * kDown : 0.f;
-      float *dst = plan.part + ((int64_t)sp.part + row) * D + w * kHalf;
+      // four dimensions of all rows, then the next four: whole lines are written
+      float4 *dst = reinterpret_cast<float4 *>(plan.part) + (int64_t)sp.part * (D / 4) + row;
 #pragma unroll 1
       for (int c = 0; c < kHalf; c += 16) {
         uint32_t x[16], y[16];
@@ -790,9 +820,9 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
         if (real) {
 #pragma unroll
           for (int j = 0; j < 16; j += 8) {                    // back in the order of the dimensions
-            *reinterpret_cast<float4 *>(dst + c + j) = make_float4(o[j], o[j + 2], o[j + 4], o[j + 6]);
-            *reinterpret_cast<float4 *>(dst + c + j + 4) =
-                make_float4(o[j + 1], o[j + 3], o[j + 5], o[j + 7]);
+            const int at = (w * kHalf + c + j) / 4;
+            dst[at * sp.rows] = make_float4(o[j], o[j + 2], o[j + 4], o[j + 6]);
+            dst[(at + 1) * sp.rows] = make_float4(o[j + 1], o[j + 3], o[j + 5], o[j + 7]);
           }
         }
       }
@@ -810,75 +840,99 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
 }
 
 // ---- join ------------------------------------------------------------------------------
-// A warp a (sequence, query head): its record and, where its sequence shares a prefix, the partial rows
-// of the CTAs that its tile went through.
-constexpr int kJoinThreads = 256;
+// A CTA takes eight rows of a KV head (neighbouring (sequence, query head) pairs), a thread four
+// dimensions of one: the parts of its sequence's own keys and, where a prefix is shared, the partial
+// rows of the CTAs that its tile went through, four in flight.
+constexpr int kJoinRows = 8;
 template <int D, bool kFp16>
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(Kv4DecodeParams p, ShPlan plan) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t wid = (int64_t)blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
-  if (wid >= (int64_t)p.num_seqs * p.h_q) return;
+__global__ void __launch_bounds__(kJoinRows * D / 4) kv4_join_kernel(Kv4DecodeParams p, ShPlan plan) {
+  const int row8 = threadIdx.x % kJoinRows, at = threadIdx.x / kJoinRows;   // dimensions 4 at ...
+  const int64_t rows = (int64_t)p.num_seqs * p.g, per_head = (rows + kJoinRows - 1) / kJoinRows;
+  const int h = static_cast<int>(blockIdx.x / per_head);
+  const int64_t i = (blockIdx.x - h * per_head) * kJoinRows + row8;
   after_previous();
-  const int b = static_cast<int>(wid / p.h_q), hq = static_cast<int>(wid - (int64_t)b * p.h_q);
-  const float *rec = plan.rec + wid * kRecFloats<D>;
-  float2 ml = *reinterpret_cast<const float2 *>(rec + D);
-  float M = ml.x, l = ml.y, x[E];
-  auto row = [&](const float *src, float (&v)[E]) {
-    const float2 *s = reinterpret_cast<const float2 *>(src + lane * E);
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      const float2 y = s[e];
-      v[2 * e] = y.x;
-      v[2 * e + 1] = y.y;
-    }
-  };
-  row(rec, x);
+  if (i >= rows) return;
+  const int b = static_cast<int>(i / p.g), j = static_cast<int>(i - (int64_t)b * p.g);
+  const int64_t out_row = (int64_t)b * p.h_q + h * p.g + j;
+  const float *rec = plan.rec + out_row * kRecFloats<D>;
+  const int4 tail = *reinterpret_cast<const int4 *>(rec + D);
   const int gi = plan.of[b];
-  if (gi >= 0) {
-    const ShGroup g = plan.groups[gi];
-    const int h = hq / p.g, r = (b - g.seq0) * p.g + hq - h * p.g, tile = r / kShRows;
-    const int pair0 = g.pair0 + (h * g.tiles + tile) * g.blocks, per = plan.head->per;
-    const int c0 = pair0 / per, c1 = (pair0 + g.blocks - 1) / per;
-    const int64_t at = (int64_t)g.row0 + h * g.rows + r;
-    for (int c = c0; c <= c1; c += 4) {
-      float2 v[4];
-      float o[4][E];
+  float M = -INFINITY, l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float2 (&v)[4], const float4 (&o)[4]) {
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) top = fmaxf(top, v[u].x);
+    const float old = l != 0.f ? ex2_approx(M - top) : 0.f;
+    l *= old;
+    x.x *= old;
+    x.y *= old;
+    x.z *= old;
+    x.w *= old;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (v[u].y == 0.f) continue;                             // no keys, or no part
+      const float f = ex2_approx(v[u].x - top);
+      l = fmaf(f, v[u].y, l);
+      x.x = fmaf(f, o[u].x, x.x);
+      x.y = fmaf(f, o[u].y, x.y);
+      x.z = fmaf(f, o[u].z, x.z);
+      x.w = fmaf(f, o[u].w, x.w);
+    }
+    M = top;
+  };
+  float2 v[4];
+  float4 o[4];
+  if (tail.w == 0) {
+    M = __int_as_float(tail.x);
+    l = __int_as_float(tail.y);
+    x = *reinterpret_cast<const float4 *>(rec + 4 * at);
+  } else {
+    const int head = j % kK4Heads, heads = min(kK4Heads, p.g - (j - head));
+    for (int k = 0; k < tail.w; k += 4) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         v[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[u][e] = 0.f;
-        if (c + u <= c1) {
-          const int64_t i = (int64_t)(c + u) * kShRows + at;
-          v[u] = plan.part_ml[i];
-          row(plan.part + i * D, o[u]);
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k + u < tail.w) {
+          const float *part = part_of<D>(p, k + u == 0 ? 2 * tail.z + 1 : 2 * (tail.z + k + u));
+          v[u] = *reinterpret_cast<const float2 *>(part + heads * D + 2 * head);
+          const float2 *src = reinterpret_cast<const float2 *>(part + head * D + 4 * at);
+          const float2 y = src[0], z = src[1];
+          o[u] = make_float4(y.x, y.y, z.x, z.y);
         }
       }
-      float top = M;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) top = fmaxf(top, v[u].x);
-      const float old = l != 0.f ? ex2_approx(M - top) : 0.f;
-      l *= old;
-#pragma unroll
-      for (int e = 0; e < E; ++e) x[e] *= old;
+      add(v, o);
+    }
+  }
+  if (gi >= 0) {
+    const ShGroup g = plan.groups[gi];
+    const int r = (b - g.seq0) * p.g + j, tile = r / kShRows, in = r - tile * kShRows;
+    const int n = min(kShRows, g.rows - tile * kShRows);
+    const int t0 = g.pair0 + (h * g.tiles + tile) * g.counted() + kShOver, per = plan.head->per;
+    const int c0 = t0 / per, c1 = (t0 + g.blocks - 1) / per;
+    const int64_t base = (int64_t)g.row0 + h * g.rows + tile * kShRows;
+    const float4 *parts = reinterpret_cast<const float4 *>(plan.part);
+    for (int c = c0; c <= c1; c += 4) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const float f = v[u].y != 0.f ? ex2_approx(v[u].x - top) : 0.f;
-        l = fmaf(f, v[u].y, l);
-#pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = fmaf(f, o[u][e], x[e]);
+        v[u] = make_float2(-INFINITY, 0.f);
+        o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c + u <= c1) {
+          const int64_t k = (int64_t)(c + u) * kShRows + base;
+          v[u] = plan.part_ml[k + in];
+          o[u] = parts[k * (D / 4) + at * n + in];
+        }
       }
-      M = top;
+      add(v, o);
     }
   }
   const bool any = l != 0.f;                                   // a NaN sum stays one
   const float inv = any ? __fdividef(1.f, l) : 0.f;
-  uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(p.out) + wid * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E / 2; ++e) out[e] = pack2<kFp16>(x[2 * e] * inv, x[2 * e + 1] * inv);
-  if (lane == 0)
-    p.lse[(int64_t)hq * p.num_seqs + b] = any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  reinterpret_cast<uint2 *>(p.out)[out_row * (D / 4) + at] =
+      make_uint2(pack2<kFp16>(x.x * inv, x.y * inv), pack2<kFp16>(x.z * inv, x.w * inv));
+  if (at == 0)
+    p.lse[(int64_t)(h * p.g + j) * p.num_seqs + b] = any ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 // ---- launches ----------------------------------------------------------------------------
@@ -895,7 +949,7 @@ static cudaError_t run_shared(const Kv4SharedParams &p, cudaStream_t s) {
   ShPlan plan;
   shared_layout(D, p.dec.num_seqs, p.dec.h_q, p.num_groups, p.ws, &plan);
   const int ctas = sms < kShMaxCtas ? sms : kShMaxCtas;
-  e = launch_kv4(kv4_share_kernel, dim3(1), kSetupThreads, 0, 1, s, p, plan, ctas, 4);
+  e = launch_kv4(kv4_share_kernel, dim3(1), kSetupThreads, 0, 1, s, p, plan, ctas, kShOver + 4);
   if (e != cudaSuccess) return e;
   auto *kernel = kv4_prefix_kernel<D, kFp16>;
   // more than half of an SM's: one CTA each, as its tensor memory allows
@@ -909,9 +963,10 @@ static cudaError_t run_shared(const Kv4SharedParams &p, cudaStream_t s) {
   own.rec = plan.rec;
   e = launch_kv4_suffix(D, kFp16, own, s);
   if (e != cudaSuccess) return e;
-  const int64_t warps = (int64_t)p.dec.num_seqs * p.dec.h_q, per = kJoinThreads / 32;
-  return launch_kv4(kv4_join_kernel<D, kFp16>, dim3(static_cast<unsigned>((warps + per - 1) / per)),
-                    kJoinThreads, 0, 1, s, p.dec, plan);
+  const int64_t rows = (int64_t)p.dec.num_seqs * p.dec.g;
+  const int64_t joins = p.dec.h_k * ((rows + kJoinRows - 1) / kJoinRows);
+  return launch_kv4(kv4_join_kernel<D, kFp16>, dim3(static_cast<unsigned>(joins)), kJoinRows * D / 4, 0, 1, s,
+                    p.dec, plan);
 }
 
 cudaError_t launch_kv4_shared(int d, bool fp16, const Kv4SharedParams &p, cudaStream_t s) {

@@ -247,3 +247,181 @@ def test_refusals_of_python():
         nsa.kv4_decode_shared(q, *args, cu[:1], prefix[:0])
     with pytest.raises(nsa.NsaError):
         nsa.kv4_decode_shared(torch.zeros(2, 17, 128, dtype=torch.bfloat16, device="cuda"), *args, cu, prefix)
+
+
+# ---- groups that are large enough to be shared whatever their prefix -----------------------
+def _members(n, prefix, seed, most=40):
+    """n sequences behind a prefix, some of nothing but it."""
+    own = np.random.default_rng(seed).integers(0, most, n)
+    own[::7] = 0
+    return tuple(int(prefix + x) for x in own)
+
+
+@pytest.mark.parametrize("prefix", [1, 2, 31, 32, 33, 63, 64, 65, 95, 127, 128, 129, 191, 193, 257, 511, 513])
+def test_shared_prefixes_around_blocks(prefix):
+    some = (0, 1, 7, 30, 59, 69)
+    _run([(prefix, _members(70, prefix, 1))], 64, 1, 1, 128, "bf16", prefix, some=some)
+    _run([(prefix, _members(70, prefix, 2))], 32, 2, 1, 64, "fp16", prefix, some=some)
+    _run([(prefix + 32, _members(70, prefix + 32, 3))], 128, 1, 3, 128, "fp16", prefix, some=some)
+
+
+@pytest.mark.parametrize("d,page,h_k,g,dtype", [(128, 64, 3, 1, "bf16"), (64, 32, 2, 2, "fp16"),
+                                                (128, 128, 1, 16, "fp16"), (64, 64, 2, 9, "bf16"),
+                                                (128, 32, 2, 5, "bf16")])
+def test_shared_and_unshared_groups_together(d, page, h_k, g, dtype):
+    """Large groups between small ones, members that end inside the prefix, empty ones, tiles that
+    are partly full, sequences behind the last group."""
+    a, b = list(_members(75, 300, 4)), list(_members(130, 129, 5))
+    a[3], a[4], b[0], b[129] = 299, 0, 129, 64
+    groups = [(40, (50, 41)), (300, tuple(a)), (77, ()), (129, tuple(b)), (600, (700,))]
+    _run(groups, page, h_k, g, d, dtype, 7 * d + g, alone=(5, 0, 333),
+         some=(0, 1, 2, 3, 5, 6, 40, 76, 77, 78, 140, 205, 206, 207, 208, 209, 210))
+
+
+def test_shared_many_groups():
+    groups = [(int(p), _members(60, int(p), i, 9)) for i, p in
+              enumerate(np.random.default_rng(1).integers(1, 200, 25))]
+    _run(groups, 32, 2, 1, 64, "bf16", 11, some=tuple(range(0, 1500, 53)))
+
+
+def test_shared_spread_of_scores_and_largest_queries():
+    groups = [(200, _members(60, 200, 1))]
+    some = (0, 7, 33, 59)
+    _run(groups, 64, 2, 1, 128, "bf16", 21, scale=2.0, some=some)
+    _run(groups, 64, 1, 2, 128, "fp16", 22, scale=-0.5, some=some)
+    _run(groups, 64, 1, 1, 128, "fp16", 23, scale=1e-3, mags=(2.0 ** -9, 0.1, 8.0), some=some)
+    _run(groups, 32, 1, 2, 64, "bf16", 24, scale=0.0, mags=(2.0 ** -8, 16.0), some=some)
+    q = torch.randn(60, 6, 128, generator=torch.Generator().manual_seed(0))
+    q *= torch.tensor([1.0, 1e-20, 1e4, 0.0, 1e-3, 300.0]).view(1, 6, 1)
+    _run(groups, 64, 1, 6, 128, "bf16", 25, scale=1e-4, q=q.to(torch.bfloat16), some=some)
+    for size, scale in ((2.0 ** 100, 2.0 ** -101), (2.0 ** -90, 2.0 ** 90)):
+        q = torch.randn(60, 1, 128, generator=torch.Generator().manual_seed(1)) * size
+        _run(groups, 64, 1, 1, 128, "bf16", 26, scale=scale, q=q.to(torch.bfloat16), some=some)
+
+
+@pytest.mark.parametrize("size,scale", [(1.0, 2.0 ** 25), (1.0, 2.0 ** 40), (2.0 ** 114, 1.0)])
+def test_shared_huge_scores(size, scale):
+    """Scores whose neighbours in fp32 are further apart than an exponential tells: the largest
+    takes it all, unless two are that close."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    pool, table, lens, cu, prefix = make_shared([(300, _members(60, 300, 1))], 64, 1, 128, 31)
+    q = (torch.randn(60, 1, 128, generator=torch.Generator().manual_seed(1)) * size).to(torch.bfloat16)
+    out, _ = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), scale, _dev(cu), _dev(prefix))
+    ref = kv4.attend(q.double().numpy(), pool, table, lens, 64, scale)
+    assert out.isfinite().all()
+    tol = 2.0 ** -8 * np.abs(ref[0]) + 2.0 ** -9 * ref[3] + 1e-6
+    assert (np.abs(out.double().cpu().numpy() - ref[0]) <= tol).all()
+
+
+def test_shared_rising_scores():
+    """Keys that grow along the prefix: the reference is raised again and again, in both halves."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, d, n = 64, 128, 1984
+    rng = np.random.default_rng(1)
+    u = rng.standard_normal(d).astype(np.float32)
+    pool, table, lens, cu, prefix = make_shared([(n, _members(60, n, 2))], page, 1, d, 2)
+    code, scale, zero = kv4.unpack(pool, page, d)
+    for t in range(n):
+        pg, at = table[0, t // page], t % page
+        c, s, z = kv4.quantise(u * (t / n * 8) + 0.1 * rng.standard_normal(d).astype(np.float32))
+        code[pg, 0, 0, at], scale[pg, 0, 0, at], zero[pg, 0, 0, at] = c, s, z
+    pool = kv4.pack(code, scale, zero)
+    for dtype, size in ((torch.bfloat16, 0.3), (torch.float16, 3.0)):
+        q = (torch.from_numpy(u)[None, None] * size + torch.randn(60, 1, d,
+             generator=torch.Generator().manual_seed(3))).to(dtype)
+        out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), d ** -0.5,
+                                         _dev(cu), _dev(prefix))
+        check_shared(out, lse, kv4.attend(q.double().numpy(), pool, table, lens, page, d ** -0.5), dtype)
+
+
+def test_shared_bad_pages_and_nan_rows():
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d = 32, 1, 2, 128
+    pool, table, lens, cu, prefix = make_shared([(300, _members(60, 300, 1)), (64, _members(60, 64, 2))], page,
+                                                h_k, d, 41)
+    q = torch.randn(120, g, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    def call(q, t):
+        return nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(t), _dev(lens), 0.1, _dev(cu), _dev(prefix),
+                                     device_status=status.zero_())
+    t = table.copy()
+    t[:60, 2], t[:60, 5], t[60:, 0] = -1, pool.shape[0], -9
+    out, lse = call(q, t)
+    assert int(status.item()) == nsa.DEVERR_BAD_INDEX
+    check_shared(out, lse, kv4.attend(q.double().numpy(), pool, t, lens, page, 0.1), torch.bfloat16)
+    t[:60, :9] = -1
+    out, lse = call(q, t)
+    check_shared(out, lse, kv4.attend(q.double().numpy(), pool, t, lens, page, 0.1), torch.bfloat16)
+    ref = kv4.attend(q.double().numpy(), pool, table, lens, page, 0.1)
+    bad = q.clone()
+    bad[17, 1, 3], bad[18, 0, 5] = float("nan"), float("inf")
+    out, lse = call(bad, table)
+    for b, j in ((17, 1), (18, 0)):
+        assert out[b, j].isnan().all() and lse[j, b].isnan()
+        out[b, j], lse[j, b] = torch.from_numpy(ref[0][b, j]).to(out), float(ref[1][j, b])
+    check_shared(out, lse, ref, torch.bfloat16)
+    # a NaN in a cached group of the prefix reaches all of its sequences and nothing else
+    code, scale, zero = kv4.unpack(pool, page, d)
+    zero[table[0, 3], 0, 1, 7, 0] = np.float16("nan")
+    out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(kv4.pack(code, scale, zero)), _dev(table), _dev(lens), 0.1,
+                                     _dev(cu), _dev(prefix))
+    assert out[:60, :, :64].isnan().all() and out[:60, :, 64:].isfinite().all() and out[60:].isfinite().all()
+
+
+def test_shared_largest_values():
+    """Keys and values at fp16's ends, whose scales are the largest there are."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, d, n = 32, 64, 100
+    pool, table, lens, cu, prefix = make_shared([(n, _members(60, n, 2))], page, 1, d, 2)
+    code, scale, zero = kv4.unpack(pool, page, d)
+    rng = np.random.default_rng(3)
+    for t in range(0, n - 10, 3):
+        for w in (0, 1):
+            x = rng.choice([-65504.0, 65504.0, 100.0, -3e4], d).astype(np.float32)
+            x[:2] = -65504, 65504
+            pg, at = table[0, t // page], t % page
+            code[pg, 0, w, at], scale[pg, 0, w, at], zero[pg, 0, w, at] = kv4.quantise(x)
+    pool = kv4.pack(code, scale, zero)
+    q = (torch.randn(60, 1, d, generator=torch.Generator().manual_seed(1)) * 1e-5).half()
+    out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), 1.0, _dev(cu), _dev(prefix))
+    r = kv4.attend(q.double().numpy(), pool, table, lens, page, 1.0)
+    fits = np.abs(r[0]) < 65000
+    got = out.double().cpu().numpy()
+    # values past 65504 (by up to 32) are held to it: half a step of fp16
+    tol = 2.0 ** -10 * np.abs(r[0]) + 2.0 ** -9 * r[3] + 2.0 ** -16 * r[2][..., None] * r[3]
+    assert (np.abs(got - r[0])[fits] <= tol[fits]).all() and np.isfinite(lse.cpu().numpy()).all()
+
+
+def test_shared_graph_and_dirty_workspace():
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, g, d = 64, 2, 2, 128
+    sets = []
+    for seed in range(3):
+        pool, table, lens, cu, prefix = make_shared(
+            [(700, _members(60, 700, 9)), (130, _members(40 + 20 * (seed == 1), 130, 9)),
+             (64, _members(20 - 20 * (seed == 1), 64, 9))], page, h_k, d, 61 + seed, width=20)
+        q = torch.randn(120, h_k * g, d, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
+        sets.append([x.cuda() if torch.is_tensor(x) else _dev(x) for x in (q, pool, table, lens, cu, prefix)])
+    pages = max(s[1].shape[0] for s in sets)
+    for s in sets:
+        s[1] = torch.cat([s[1], s[1][:1].expand(pages - s[1].shape[0], -1, -1)]).contiguous()
+    def call(s, **kw):
+        q, pool, table, lens, cu, prefix = s
+        return nsa.kv4_decode_shared(q, pool, table, lens, 0.1, cu, prefix, **kw)
+    want = [call(s) for s in sets]
+    dirty = torch.full((nsa.kv4_decode_shared_workspace_size(pages, page, h_k, d, 120, h_k * g, 3),), 255,
+                       dtype=torch.uint8, device="cuda")
+    for s, w in zip(sets, want):
+        got = call(s, workspace=dirty)
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+    inputs = [x.clone() for x in sets[0]]
+    out, lse = torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(inputs, out=out, lse=lse, workspace=dirty)
+    for i in (1, 2, 0, 1):
+        for a, b in zip(inputs, sets[i]):
+            a.copy_(b)
+        dirty.fill_(254 - i)
+        graph.replay()
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
