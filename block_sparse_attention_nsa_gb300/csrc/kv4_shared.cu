@@ -6,16 +6,16 @@
 // The prefix' part is a product of all the group's query rows with the same keys, done once per 128
 // rows on the tensor cores; each sequence's own part is kv4_decode.cu's, from the prefix' end on.
 //
-// Prefix kernel (tcgen05).  Rows of a KV head's tile are (sequence, query head) pairs, M = 128; 64
+// Prefix kernel (tcgen05).  Rows of a KV head's tile are (sequence, query head) pairs, M = 128; 128
 // keys a block.  The scores' sums are the tensor core's alone, as exact as fp32 products (their
 // log-sum-exp is returned in fp32).  With q^ = q 2^(5 - ex), ex the exponent of a row's largest
 // magnitude (in fp16 it loses 2^-30 of that), and k = c s + z in a group of dimensions,
 //   q^ . k = sum_j q^_j (c_j - 8) s_hi + sum_j q^_j (c_j - 8) s_lo + Q z + 8 Q s,   Q = sum_j q^_j:
 // s_hi is s without its last three bits, so that both products with c - 8 (four bits and a sign) are
 // exact in fp16; Q and 8 Q are three fp16 numbers each, against z and s in 12 of the 16 columns of
-// one more step.  S = |scale| 2^(ex - 5) q^ . k.  (Codes as operands and scales afterwards, in fp32,
-// want both groups' accumulators apart and four numbers a key from shared memory for every thread:
-// 3190 cycles a block, where this takes XXX.)
+// one more step; a 13th has the mask.  S = |scale| 2^(ex - 5) q^ . k.  (Codes as operands, with scales
+// and zeros taken in fp32 afterwards, want both groups' accumulators apart and four numbers a key from
+// shared memory for every thread: 3190 cycles for 64 keys.)
 // Weights are w = 2^(S - m) 2^8 (with their factor those down to 2^-22 of the maximum are normal
 // numbers in fp16).  Two roundings to fp16, of 2^-11 at most each: V's values as they are unpacked, and
 // the weights, for bf16 outputs, whose own rounding is eight times as large.  For fp16 outputs, of
@@ -25,16 +25,17 @@
 // The maximum m is raised only when a score passes it by 2^4, so that most blocks rescale nothing.
 //
 // Roles of a CTA (one an SM, 20 warps), handing blocks on by mbarriers, every wait bounded:
-//   loader       a block's two record tiles by bulk copies into a ring, page by page of the table;
-//   2 x 4 unpackers  codes, scales and zeros to the K and V operands (128-byte swizzle; the eight
+//   loader       a block's record tiles by bulk copies into a ring, page by page of the table;
+//   8 unpackers  codes, scales and zeros to the K and V operands (128-byte swizzle; the eight
 //                dimensions of a word stay in the order 0 4 1 5 2 6 3 7 that masking gives, on both
 //                sides of the product and until the output is written);
-//   2 MMA threads    S = Q K^T, then O += W V, with Q and W from tensor memory: only K and V are read
-//                from shared memory, whose bandwidth the two products would else fill;
-//   2 x 4 softmax warps   a thread a row.
-// Unpackers, MMA thread and softmax warps of either half take every other block, with a maximum, sum
-// and output of their own, joined at the tile's end; while one half is between its products the
-// other's run.  W goes to tensor memory over the scores it came from.
+//   MMA thread   S = Q K^T of block n + 1 into one of two score buffers, then O += W V of block n.  Q
+//                and W come from tensor memory, so that only K and V are read from shared memory.
+//                Steps of N = 128 in one chain take about 70 cycles each, half of that a key what
+//                steps of 64 do, and only one output fits beside two buffers of 128 scores;
+//   2 x 4 softmax warps   a thread a row and half of a block's keys.  Both halves share the output
+//                and so the reference m: one barrier a block tells them whether any row raises it.
+//                W goes to tensor memory over the scores it came from.
 // Work: the line of all (tile, block) pairs, tile after tile, in equal runs, one a CTA; where a tile
 // is shared by CTAs each leaves partial rows.  kv4_join_kernel adds them and the own part.
 #include <cmath>
@@ -44,13 +45,14 @@
 namespace nsa {
 
 constexpr int kShRows = 128;         // query rows of a tile
-constexpr int kShKeys = 64;          // keys of a block
-// Blocks of each half (every other one of a tile) that are copied ahead, and unpacked: K's for the
-// next product beside those in use; V's follow the product that frees the place.
+constexpr int kShKeys = 128;         // keys of a block
+constexpr int kShTiles = kShKeys / kKv4Tile;
+// Blocks copied, and unpacked, ahead: K's for the next product beside those in use; V's follow the
+// product that frees their place.
 constexpr int kShRaw = 2, kShK = 2;
 constexpr int kShThreads = 640;
 constexpr int kShMaxCtas = 256;
-constexpr int kShOver = 8;           // blocks that a tile's start and end count as
+constexpr int kShOver = 6;           // blocks that a tile's start and end count as
 constexpr int kSetupThreads = 1024;
 constexpr float kShSlack = 4.f;      // scores may exceed the reference by this much
 constexpr float kShUp = 8.f;         // weights are 2^8 times 2^(S - m)
@@ -123,12 +125,12 @@ __device__ __forceinline__ int setup_incl(int x, int (&part)[32], int &total) {
   return x + (warp ? before : 0);
 }
 
-// Shared or not?  In units of 25 ns of an SM's time: a tile of 128 rows takes about 240 and 24 a block
-// of 64 keys; the sequences' own passes over the prefix take 5 a tile of 32 keys each.
+// Shared or not?  In units of 25 ns of an SM's time: a tile of 128 rows takes about 240 and 40 a block
+// of 128 keys; the sequences' own passes over the prefix take 5 a tile of 32 keys each.
 __device__ __forceinline__ bool worth_sharing(int n, int g, int keys) {
   const int64_t own = (int64_t)n * (g > kK4Heads ? 2 : 1) * ((keys + 31) / 32) * 5;
   const int64_t tiles = ((int64_t)n * g + kShRows - 1) / kShRows;
-  return n > 1 && own > tiles * (240 + 24 * (int64_t)((keys + kShKeys - 1) / kShKeys));
+  return n > 1 && own > tiles * (240 + 40 * (int64_t)((keys + kShKeys - 1) / kShKeys));
 }
 
 // One CTA: groups that share, in order, what lies before each, and each sequence's group and first own
@@ -212,29 +214,29 @@ struct Sh {
   using T = Kv4Tile<D>;
   static constexpr int kG = T::kG;
   static constexpr uint32_t kOperand = kShKeys * D * 2;        // V of a block, and each part of K
-  static constexpr uint32_t kRawBytes = 2 * T::kBytes;
+  // K or V of a block as it is stored: of each record tile the codes, then scales and zeros
+  static constexpr uint32_t kHalfTile = T::kV + 2 * T::kArr, kRawBytes = kShTiles * kHalfTile;
   static constexpr uint32_t kOffK = 0;
-  static constexpr uint32_t kOffV = kOffK + 2 * kShK * 2 * kOperand;
-  static constexpr uint32_t kOffZ = kOffV + 2 * kOperand;      // 16 columns of z and s a stage of K
+  static constexpr uint32_t kOffV = kOffK + kShK * 2 * kOperand;
+  static constexpr uint32_t kOffZ = kOffV + kOperand;          // 16 columns of z and s a stage of K
   static constexpr uint32_t kOffRaw = kOffZ + kShKeys * 128;
   static constexpr uint32_t kBytes = kOffRaw + 2 * kShRaw * kRawBytes + 1024;   // + alignment
-  static_assert(2 * kShK <= 4, "a 128-byte row holds four stages' columns");
+  static_assert(kShK <= 4, "a 128-byte row holds four stages' columns");
   static_assert(kOffV % 1024 == 0 && kOffZ % 1024 == 0 && kOffRaw % 1024 == 0, "operands' alignment");
   static_assert(kBytes <= 226 * 1024, "shared memory");
-  // columns of tensor memory: scores of both halves, outputs of both, Q, its sums
-  static constexpr uint32_t kS = 0, kO = 2 * kShKeys, kQ = kO + 2 * D, kSums = kQ + D / 2;
+  // columns of tensor memory: two blocks' scores, the output, Q, its sums
+  static constexpr uint32_t kS = 0, kO = 2 * kShKeys, kQ = kO + D, kSums = kQ + D / 2;
   static constexpr uint32_t kCols = 512;
   static_assert(kSums + 8 <= kCols, "tensor memory");
 };
 
 struct ShShared {
-  // of half w: stages w * kShRaw ..., w * kShK ...; of V one
-  uint64_t raw_full[2 * kShRaw], raw_empty[2 * kShRaw], k_full[2 * kShK], k_empty[2 * kShK], v_full[2];
-  uint64_t q_full, o_free, s_full[2], p_full[2], o_done[2];
-  uint2 seen[2 * kShRaw];                      // a block's keys that exist, a bit each
-  float2 ml[2][kShRows];                       // of the two halves, at a tile's end
-  float sums[2][kShRows];                      // sums of q^
-  int top[2][kShRows];                         // largest magnitude of a row's part, as bits
+  uint64_t raw_full[2][kShRaw], raw_empty[2][kShRaw], k_full[kShK], k_empty[kShK], v_full;   // raw: K's, V's
+  uint64_t q_full, o_free, s_full[2], p_full[2], o_done;
+  uint32_t seen[2][kShRaw][kShTiles];          // a block's keys that exist, a bit each
+  float sums[2][kShRows];                      // of each half of a row: sums of q^; of weights
+  float most[2][kShRows];                      // largest scores
+  int top[2][kShRows];                         // largest magnitudes of q, as bits
   uint32_t tmem;
   int fail;
 };
@@ -307,9 +309,23 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+// In order with the other asm statements (barriers among them), but loads may pass it: the places that
+// these stores write are not read by ordinary loads.
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+}
+// Whether any of the softmax threads says so; a barrier for them all.
+__device__ __forceinline__ bool any_of_256(int id, bool mine) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.or.pred q, %2, 256, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(any)
+      : "r"(mine ? 1u : 0u), "r"(id)
+      : "memory");
+  return any != 0;
 }
 
 // The codes of a word as fp16 less `off` - 1024: dimensions (0, 4), (1, 5), (2, 6), (3, 7).
@@ -335,119 +351,114 @@ __device__ __forceinline__ __half2 upper(__half2 s) {
   return __hmin2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(8128.f));
 }
 
-// A thread's places in a block: turn u takes 16 bytes, q of them, of a key's row.
+// What the unpackers' thread t (of 256) brings of a block: in turn u 16 bytes, q of them, of the row of a
+// key, and that row's scales or zeros (0 for a key that is not there).  All of it is loaded before any
+// of it is worked on.
 template <int D>
-struct ShPlace {
-  static constexpr int kChunks = Kv4Tile<D>::kRow / 16;        // 16-byte pieces of a row
-  static constexpr int kTurns = kShKeys * kChunks / 128;
-  int key, q, row;
-  const uint8_t *tile;
-  bool in;
-  __device__ __forceinline__ ShPlace(const uint8_t *raw, uint2 seen, int u, int t) {
-    const int i = u * 128 + t;
-    key = i / kChunks;
-    q = i % kChunks;
-    row = key & 31;
-    tile = raw + (key >> 5) * Kv4Tile<D>::kBytes;
-    in = (key < 32 ? seen.x : seen.y) >> row & 1;
+struct ShPiece {
+  using T = Kv4Tile<D>;
+  static constexpr int kG = T::kG, kChunks = T::kRow / 16, kTurns = kShKeys * kChunks / 256;
+  uint32_t w[kTurns][4];
+  __half2 s[kTurns][kG], z[kTurns][kG];
+  __device__ __forceinline__ static int key(int u, int t) { return (u * 256 + t) / kChunks; }
+  __device__ __forceinline__ ShPiece(const uint8_t *raw, const uint32_t (&seen)[kShTiles], int t) {
+#pragma unroll
+    for (int u = 0; u < kTurns; ++u) {
+      const int k = key(u, t), row = k & 31, q = t % kChunks;
+      const uint8_t *tile = raw + (k >> 5) * Sh<D>::kHalfTile;
+      const uint4 x = *reinterpret_cast<const uint4 *>(tile + row * T::kRow + q * 16);
+      w[u][0] = x.x;
+      w[u][1] = x.y;
+      w[u][2] = x.z;
+      w[u][3] = x.w;
+      const __half *par = reinterpret_cast<const __half *>(tile + T::kV) + row * kG;
+      const bool in = seen[k >> 5] >> row & 1;
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        s[u][g] = __half2half2(in ? par[g] : __ushort_as_half(0));
+        z[u][g] = __half2half2(in ? par[T::kArr / 2 + g] : __ushort_as_half(0));
+      }
+    }
   }
-  // entry `which` of the four arrays (K scale, K zero, V scale, V zero), 0 for a key that is not there
-  __device__ __forceinline__ __half2 par(int which, int g) const {
-    const __half x = reinterpret_cast<const __half *>(tile + Kv4Tile<D>::kPar + which * Kv4Tile<D>::kArr)
-        [row * Kv4Tile<D>::kG + g];
-    return __half2half2(in ? x : __ushort_as_half(0));
-  }
-  // of word 4 q + w: its group, and where its dimensions lie in an operand
-  __device__ __forceinline__ uint32_t at(int w) const {
-    constexpr int G = Kv4Tile<D>::kG;
-    return sw128_offset(key, 8 * (w % G) + (4 / G) * q + w / G, kShKeys);
+  // word 4 q + i of turn u is group i % kG's; where its dimensions lie in an operand
+  __device__ __forceinline__ static uint32_t at(int u, int i, int t) {
+    return sw128_offset(key(u, t), 8 * (i % kG) + (4 / kG) * (t % kChunks) + i / kG, kShKeys);
   }
 };
 
 template <int D>
-__device__ __forceinline__ void unpack_k(const uint8_t *raw, uint2 seen, uint32_t kdst, uint32_t zdst,
-                                         int stage, int t) {
-  using T = Kv4Tile<D>;
-  using P = ShPlace<D>;
-  constexpr int G = T::kG;
+__device__ __forceinline__ void unpack_k(const uint8_t *raw, const uint32_t (&seen)[kShTiles], uint32_t kdst,
+                                         uint32_t zdst, int stage, int t) {
+  using P = ShPiece<D>;
+  constexpr int G = P::kG;
   const __half2 off = __float2half2_rn(1032.f);
+  const P p(raw, seen, t);
 #pragma unroll
   for (int u = 0; u < P::kTurns; ++u) {
-    const P p(raw, seen, u, t);
-    const uint4 k4 = *reinterpret_cast<const uint4 *>(p.tile + p.row * T::kRow + p.q * 16);
-    const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
     __half2 hi[G], lo[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const __half2 s = p.par(0, g);
-      hi[g] = upper(s);
-      lo[g] = __hsub2(s, hi[g]);
+      hi[g] = upper(p.s[u][g]);
+      lo[g] = __hsub2(p.s[u][g], hi[g]);
     }
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+    for (int i = 0; i < 4; ++i) {
       __half2 c[4], x[4], y[4];
-      code_halves(kw[w], off, c);
+      code_halves(p.w[u][i], off, c);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        x[k] = __hmul2(c[k], hi[w % G]);
-        y[k] = __hmul2(c[k], lo[w % G]);
+        x[k] = __hmul2(c[k], hi[i % G]);
+        y[k] = __hmul2(c[k], lo[i % G]);
       }
-      sts_halves(kdst + p.at(w), x);
-      sts_halves(kdst + Sh<D>::kOperand + p.at(w), y);
+      sts_halves(kdst + P::at(u, i, t), x);
+      sts_halves(kdst + Sh<D>::kOperand + P::at(u, i, t), y);
     }
-  }
-  if (t < kShKeys) {                                           // z z z s s s of each group; 0, or -inf: no key
-    const int row = t & 31;
-    const uint8_t *par = raw + (t >> 5) * T::kBytes + T::kPar;
-    const bool in = (t < 32 ? seen.x : seen.y) >> row & 1;
-    uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    // the first thread of a row: z z z s s s of each group; 0, or -inf: no key
+    if (t % P::kChunks == 0) {
+      const int key = P::key(u, t);
+      uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const uint32_t s = in ? reinterpret_cast<const uint16_t *>(par)[row * G + g] : 0u;
-      const uint32_t z = in ? reinterpret_cast<const uint16_t *>(par + T::kArr)[row * G + g] : 0u;
-      v[3 * g] = z | z << 16;
-      v[3 * g + 1] = z | s << 16;
-      v[3 * g + 2] = s | s << 16;
+      for (int g = 0; g < G; ++g) {
+        const __half2 zs = __lows2half2(p.z[u][g], p.s[u][g]);
+        v[3 * g] = *reinterpret_cast<const uint32_t *>(&p.z[u][g]);
+        v[3 * g + 1] = *reinterpret_cast<const uint32_t *>(&zs);
+        v[3 * g + 2] = *reinterpret_cast<const uint32_t *>(&p.s[u][g]);
+      }
+      v[6] = seen[key >> 5] >> (key & 31) & 1 ? 0u : 0xfc00u;
+      sts128(zdst + sw128_offset(key, 2 * stage, kShKeys), make_uint4(v[0], v[1], v[2], v[3]));
+      sts128(zdst + sw128_offset(key, 2 * stage + 1, kShKeys), make_uint4(v[4], v[5], v[6], v[7]));
     }
-    v[6] = in ? 0u : 0xfc00u;
-    sts128(zdst + sw128_offset(t, 2 * stage, kShKeys), make_uint4(v[0], v[1], v[2], v[3]));
-    sts128(zdst + sw128_offset(t, 2 * stage + 1, kShKeys), make_uint4(v[4], v[5], v[6], v[7]));
   }
 }
 
 template <int D>
-__device__ __forceinline__ void unpack_v(const uint8_t *raw, uint2 seen, uint32_t vdst, int t) {
-  using T = Kv4Tile<D>;
-  using P = ShPlace<D>;
-  constexpr int G = T::kG;
+__device__ __forceinline__ void unpack_v(const uint8_t *raw, const uint32_t (&seen)[kShTiles], uint32_t vdst,
+                                         int t) {
+  using P = ShPiece<D>;
+  constexpr int G = P::kG;
   const __half2 off = __float2half2_rn(1024.f);
+  const P p(raw, seen, t);
+  bool wide = false;
 #pragma unroll
-  for (int u = 0; u < P::kTurns; ++u) {
-    const P p(raw, seen, u, t);
-    const uint4 v4 = *reinterpret_cast<const uint4 *>(p.tile + T::kV + p.row * T::kRow + p.q * 16);
-    const uint32_t vw[4] = {v4.x, v4.y, v4.z, v4.w};
-    __half2 s[G], z[G];
-    bool wide = false;
+  for (int u = 0; u < P::kTurns; ++u)
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      s[g] = p.par(2, g);
-      z[g] = p.par(3, g);
-      wide |= !(fabsf(__low2float(z[g])) + 15.f * __low2float(s[g]) < 65504.f);
-    }
-    const bool any_wide = __any_sync(0xffffffffu, wide);
+    for (int g = 0; g < G; ++g)
+      wide |= !(fabsf(__low2float(p.z[u][g])) + 15.f * __low2float(p.s[u][g]) < 65504.f);
+  const bool any_wide = __any_sync(0xffffffffu, wide);
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
+  for (int u = 0; u < P::kTurns; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       __half2 c[4];
-      code_halves(vw[w], off, c);
+      code_halves(p.w[u][i], off, c);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) c[k] = __hfma2(c[k], s[w % G], z[w % G]);
+      for (int k = 0; k < 4; ++k) c[k] = __hfma2(c[k], p.s[u][i % G], p.z[u][i % G]);
       if (any_wide) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) c[k] = held(c[k]);
       }
-      sts_halves(vdst + p.at(w), c);
+      sts_halves(vdst + P::at(u, i, t), c);
     }
-  }
 }
 
 // A number as three fp16 ones.
@@ -475,20 +486,20 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
   if (warp == 19) tmem_alloc(&sh.tmem, S::kCols);
   if (tid == 0) {
     for (int i = 0; i < 2 * kShRaw; ++i) {
-      mbar_init(&sh.raw_full[i], 1);
-      mbar_init(&sh.raw_empty[i], 128);
+      mbar_init(&sh.raw_full[0][i], 1);
+      mbar_init(&sh.raw_empty[0][i], 256);
     }
-    for (int i = 0; i < 2 * kShK; ++i) {
-      mbar_init(&sh.k_full[i], 128);
+    for (int i = 0; i < kShK; ++i) {
+      mbar_init(&sh.k_full[i], 256);
       mbar_init(&sh.k_empty[i], 1);
     }
+    mbar_init(&sh.v_full, 256);
     mbar_init(&sh.q_full, 256);
     mbar_init(&sh.o_free, 256);
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&sh.v_full[w], 128);
-      mbar_init(&sh.s_full[w], 1);
-      mbar_init(&sh.p_full[w], 128);
-      mbar_init(&sh.o_done[w], 1);
+    mbar_init(&sh.o_done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.p_full[i], 256);
     }
     sh.fail = 0;
     fence_mbar_init();
@@ -505,16 +516,16 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
 
   if (warp == 18) {
     // ------------------------------ loader ------------------------------
-    int count[2] = {0, 0};                                     // blocks of each half
+    int it = 0;
     int32_t err = 0;
     while (walk.next(sp, p.h_k)) {
       const int keys = walk.g.keys;
       const int32_t *row = p.table + (int64_t)walk.g.seq0 * p.width;
       int my_page = -1;
-      for (int b = sp.first; b < sp.end; ++b) {
-        const int n = (b - sp.first) & 15, w = n & 1, c = w ? count[1]++ : count[0]++;
-        if (n == 0) {                                          // the pages of the next 32 tiles
-          const int key = b * kShKeys + lane * 32;
+      for (int b = sp.first; b < sp.end; ++b, ++it) {
+        const int n = (b - sp.first) % (32 / kShTiles);
+        if (n == 0) {                                          // the pages of the next 32 record tiles
+          const int key = b * kShKeys + lane * kKv4Tile;
           my_page = -1;
           if (key < keys && key < sp.end * kShKeys) {
             my_page = row[key >> p.page_log2];
@@ -524,116 +535,127 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
             }
           }
         }
-        const int pg[2] = {__shfl_sync(0xffffffffu, my_page, 2 * n),
-                           __shfl_sync(0xffffffffu, my_page, 2 * n + 1)};
-        const int rs = w * kShRaw + c % kShRaw;
-        if (lane == 0) {
-          if (c >= kShRaw) sh_wait(&sh.raw_empty[rs], ((c / kShRaw) - 1) & 1, p.status, fail);
-          uint32_t seen[2], bytes = 0;
+        // lane u < kShTiles brings the block's record tile u: its K, then its V
+        const int pg = __shfl_sync(0xffffffffu, my_page, (n * kShTiles + lane) & 31);
+        const int rs = it % kShRaw, key = b * kShKeys + lane * kKv4Tile, left = keys - key;
+        const bool mine = lane < kShTiles && pg >= 0;
+        const int tiles = __popc(__ballot_sync(0xffffffffu, mine));
+        const int tpl = p.page_log2 - 5;
+        const uint8_t *src = p.pool + ((((int64_t)pg * p.h_k + sp.h) << tpl) +
+                                       ((key & ((1 << p.page_log2) - 1)) >> 5)) * T::kBytes;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int left = keys - (b * kShKeys + 32 * u);
-            seen[u] = pg[u] < 0 || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
-            if (pg[u] >= 0) bytes += T::kBytes;
+        for (int v = 0; v < 2; ++v) {
+          if (it >= kShRaw) sh_wait(&sh.raw_empty[v][rs], ((it / kShRaw) - 1) & 1, p.status, fail);
+          __syncwarp();
+          if (lane < kShTiles)
+            sh.seen[v][rs][lane] = !mine || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
+          __syncwarp();
+          if (lane == 0) {
+            if (tiles) mbar_arrive_expect_tx(&sh.raw_full[v][rs], tiles * S::kHalfTile);
+            else mbar_arrive(&sh.raw_full[v][rs]);
           }
-          sh.seen[rs] = make_uint2(seen[0], seen[1]);
-          if (bytes) mbar_arrive_expect_tx(&sh.raw_full[rs], bytes);
-          else mbar_arrive(&sh.raw_full[rs]);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            if (pg[u] < 0) continue;
-            const int key = b * kShKeys + 32 * u, tpl = p.page_log2 - 5;
-            const int64_t tile = (((int64_t)pg[u] * p.h_k + sp.h) << tpl) +
-                                 ((key & ((1 << p.page_log2) - 1)) >> 5);
-            bulk_load(smem_u32(raw0 + rs * S::kRawBytes + u * T::kBytes), p.pool + tile * T::kBytes,
-                      T::kBytes, &sh.raw_full[rs]);
+          __syncwarp();
+          if (mine) {
+            const uint32_t dst = smem_u32(raw0 + (v * kShRaw + rs) * S::kRawBytes + lane * S::kHalfTile);
+            bulk_load(dst, src + v * T::kV, T::kV, &sh.raw_full[v][rs]);
+            bulk_load(dst + T::kV, src + T::kPar + v * 2 * T::kArr, 2 * T::kArr, &sh.raw_full[v][rs]);
           }
         }
-        __syncwarp();
       }
     }
     err = __reduce_or_sync(0xffffffffu, err);
     if (err && lane == 0) raise(p.status, err);
     // nothing may be in flight when the CTA ends, given up or not
-    if (lane == 0)
-      for (int w = 0; w < 2; ++w)
-        for (int c = max(0, count[w] - kShRaw); c < count[w]; ++c) {
-          const uint32_t bar = smem_u32(&sh.raw_full[w * kShRaw + c % kShRaw]);
-          const uint64_t t0 = globaltimer_ns();
-          while (!mbar_try_wait(bar, (c / kShRaw) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
-          }
+    if (lane < 2)
+      for (int i = max(0, it - kShRaw); i < it; ++i) {
+        const uint32_t bar = smem_u32(&sh.raw_full[lane][i % kShRaw]);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(bar, (i / kShRaw) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
+      }
     __syncwarp();
   } else if (warp >= 8 && warp < 16) {
     // ----------------------------- unpackers ----------------------------
-    const int w = (warp - 8) >> 2, t = tid & 127;
-    int c = 0;                                                 // blocks of this half so far
-    while (walk.next(sp, p.h_k)) {
-      for (int n = w; n < sp.end - sp.first; n += 2, ++c) {
-        const int rs = w * kShRaw + c % kShRaw, ks = w * kShK + c % kShK;
-        sh_wait(&sh.raw_full[rs], (c / kShRaw) & 1, p.status, fail);
-        if (c >= kShK) sh_wait(&sh.k_empty[ks], ((c / kShK) - 1) & 1, p.status, fail);
-        __syncwarp();
-        const uint2 seen = sh.seen[rs];
-        const uint8_t *raw = raw0 + rs * S::kRawBytes;
-        unpack_k<D>(raw, seen, sK + ks * 2 * S::kOperand, sZ, ks, t);
-        fence_proxy_async_smem();
-        mbar_arrive(&sh.k_full[ks]);
-        if (c > 0) sh_wait(&sh.o_done[w], (c - 1) & 1, p.status, fail);
-        __syncwarp();
-        unpack_v<D>(raw, seen, sV + w * S::kOperand, t);
-        fence_proxy_async_smem();
-        mbar_arrive(&sh.v_full[w]);
-        mbar_arrive(&sh.raw_empty[rs]);
+    // K of a block, then V of the one before it, whose place the product before that frees
+    const int t = tid - 256;
+    int it = 0;
+    auto k_of = [&](int i) {
+      const int rs = i % kShRaw, ks = i % kShK;
+      sh_wait(&sh.raw_full[0][rs], (i / kShRaw) & 1, p.status, fail);
+      if (i >= kShK) sh_wait(&sh.k_empty[ks], ((i / kShK) - 1) & 1, p.status, fail);
+      __syncwarp();
+      unpack_k<D>(raw0 + rs * S::kRawBytes, sh.seen[0][rs], sK + ks * 2 * S::kOperand, sZ, ks, t);
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.k_full[ks]);
+      mbar_arrive(&sh.raw_empty[0][rs]);
+    };
+    auto v_of = [&](int i) {
+      const int rs = i % kShRaw;
+      sh_wait(&sh.raw_full[1][rs], (i / kShRaw) & 1, p.status, fail);
+      if (i > 0) sh_wait(&sh.o_done, (i - 1) & 1, p.status, fail);
+      __syncwarp();
+      unpack_v<D>(raw0 + (kShRaw + rs) * S::kRawBytes, sh.seen[1][rs], sV, t);
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.v_full);
+      mbar_arrive(&sh.raw_empty[1][rs]);
+    };
+    while (walk.next(sp, p.h_k))
+      for (int b = sp.first; b < sp.end; ++b, ++it) {
+        k_of(it);
+        if (it > 0) v_of(it - 1);
       }
-    }
-  } else if (warp == 16 || warp == 17) {
-    // ---------------------------- MMA threads ---------------------------
+    if (it > 0) v_of(it - 1);
+  } else if (warp == 16) {
+    // ---------------------------- MMA thread ----------------------------
     if (lane == 0) {
       constexpr uint32_t kIdS = idesc_f16(kShRows, kShKeys, false, false, true);
       constexpr uint32_t kIdO = idesc_f16(kShRows, D, false, true, true);
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);
-      const int w = warp - 16;
       const uint32_t lo_k = sdesc_lo_sw128(sK, 16), lo_z = sdesc_lo_sw128(sZ, 16);
-      const uint32_t bv = sdesc_lo_sw128(sV + w * S::kOperand, kShKeys * 128);
-      const uint32_t ts = tmem + S::kS + w * kShKeys, to = tmem + S::kO + w * D;
-      const uint32_t tq = tmem + S::kQ, tsum = tmem + S::kSums;
-      int turn = 0, c = 0;
-      for (; walk.next(sp, p.h_k); ++turn) {
-        const int nb = sp.end - sp.first;
-        sh_wait(&sh.q_full, turn & 1, p.status, fail);
-        for (int n = w; n < nb; n += 2, ++c) {
-          const int ks = w * kShK + c % kShK;
-          const uint32_t bk = lo_k + ks * (2 * S::kOperand >> 4), bz = lo_z + ks * (32 >> 4);
-          sh_wait(&sh.k_full[ks], (c / kShK) & 1, p.status, fail);
-          tc_fence_after();
-          // smallest parts first: each step cuts the sum so far towards zero
+      const uint32_t lo_v = sdesc_lo_sw128(sV, kShKeys * 128);
+      const uint32_t to = tmem + S::kO, tq = tmem + S::kQ, tsum = tmem + S::kSums;
+      int it = 0;
+      auto scores = [&](int i) {
+        const int ks = i % kShK;
+        const uint32_t ts = tmem + S::kS + (i & 1) * kShKeys;
+        const uint32_t bk = lo_k + ks * (2 * S::kOperand >> 4), bz = lo_z + ks * (32 >> 4);
+        sh_wait(&sh.k_full[ks], (i / kShK) & 1, p.status, fail);
+        tc_fence_after();
+        // smallest parts first: each step cuts the sum so far towards zero
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16_ts(ts, tq + kk * 8,
-                       sdesc_join(bk + ((S::kOperand + kmajor_step(kShKeys, kk)) >> 4), kHi), kIdS, kk > 0);
-          mma_f16_ts(ts, tsum, sdesc_join(bz, kHi), kIdS, 1);
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ts(ts, tq + kk * 8,
+                     sdesc_join(bk + ((S::kOperand + kmajor_step(kShKeys, kk)) >> 4), kHi), kIdS, kk > 0);
+        mma_f16_ts(ts, tsum, sdesc_join(bz, kHi), kIdS, 1);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16_ts(ts, tq + kk * 8, sdesc_join(bk + (kmajor_step(kShKeys, kk) >> 4), kHi), kIdS, 1);
-          mma_commit(&sh.s_full[w]);
-          mma_commit(&sh.k_empty[ks]);
-          sh_wait(&sh.v_full[w], c & 1, p.status, fail);
-          sh_wait(&sh.p_full[w], c & 1, p.status, fail);
-          if (n == w && turn > 0) sh_wait(&sh.o_free, (turn - 1) & 1, p.status, fail);
-          tc_fence_after();
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_f16_ts(ts, tq + kk * 8, sdesc_join(bk + (kmajor_step(kShKeys, kk) >> 4), kHi), kIdS, 1);
+        mma_commit(&sh.s_full[i & 1]);
+        mma_commit(&sh.k_empty[ks]);
+      };
+      auto output = [&](int i, bool add) {
+        const uint32_t ts = tmem + S::kS + (i & 1) * kShKeys;
+        sh_wait(&sh.v_full, i & 1, p.status, fail);
+        sh_wait(&sh.p_full[i & 1], (i >> 1) & 1, p.status, fail);
+        tc_fence_after();
+        // weights of a half's keys lie over its scores, in fp16 the rest of them behind
+#pragma unroll
+        for (int part = 0; part < (kFp16 ? 2 : 1); ++part)
 #pragma unroll
           for (int kk = 0; kk < kShKeys / 16; ++kk)
-            mma_f16_ts(to, ts + kk * 8, sdesc_join(bv + (mnmajor_step(kk) >> 4), kHi), kIdO,
-                       n >= 2 || kk > 0);
-          if (kFp16) {                                         // what the rounding of W has left
-#pragma unroll
-            for (int kk = 0; kk < kShKeys / 16; ++kk)
-              mma_f16_ts(to, ts + kShKeys / 2 + kk * 8, sdesc_join(bv + (mnmajor_step(kk) >> 4), kHi),
-                         kIdO, 1);
-          }
-          mma_commit(&sh.o_done[w]);                           // V's place is free, too
+            mma_f16_ts(to, ts + (kk >> 2) * 64 + part * 32 + (kk & 3) * 8,
+                       sdesc_join(lo_v + (mnmajor_step(kk) >> 4), kHi), kIdO, add || part > 0 || kk > 0);
+        mma_commit(&sh.o_done);
+      };
+      for (int turn = 0; walk.next(sp, p.h_k); ++turn) {
+        const int nb = sp.end - sp.first;
+        sh_wait(&sh.q_full, turn & 1, p.status, fail);
+        for (int n = 0; n <= nb; ++n) {
+          if (n < nb) scores(it + n);
+          if (n == 1 && turn > 0) sh_wait(&sh.o_free, (turn - 1) & 1, p.status, fail);
+          if (n > 0) output(it + n - 1, n > 1);
         }
+        it += nb;
       }
     }
     __syncwarp();
@@ -641,10 +663,10 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
     // ------------------------------ softmax -----------------------------
     const int w = warp >> 2, row = tid & 127;                  // row: tensor memory lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + S::kS + w * kShKeys + lane_off;
-    const uint32_t to = tmem + S::kO + lane_off;
-    constexpr int kHalf = D / 2;                               // dimensions of a row that a thread brings
-    int count = 0;
+    const uint32_t to = tmem + S::kO + lane_off + w * (D / 2);
+    constexpr int kHalf = D / 2;                               // dimensions of a row that are a thread's
+    constexpr int kMine = kShKeys / 2;                         // keys of a block that are
+    int it = 0;
     while (walk.next(sp, p.h_k)) {
       const int nb = sp.end - sp.first;
       // ---- the tile's queries ----
@@ -722,27 +744,31 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
       // (a factor of 0 would make NaN of the mask's -inf: the least one leaves scores of 0)
       const float mul =
           fmaxf(ldexpf(fabsf(p.scale), ex - kShQTop - over) * 1.4426950408889634f, 1.17549435e-38f);
-      // ---- its blocks, every other one ----
+      // ---- its blocks ----
       // Differences are taken before the factor: between scores they are exact or nearly so, whatever
       // the scores' size, and weights stay within fp16 however a product rounds.
       float ref = -INFINITY, thr = -INFINITY;                  // the reference score, and when to raise it
       const float slack = __fdividef(kShSlack, mul);
       Pair l(0.f, 0.f);
-      for (int n = w; n < nb; n += 2, ++count) {
-        sh_wait(&sh.s_full[w], count & 1, p.status, fail);
+      for (int n = 0; n < nb; ++n, ++it) {
+        const uint32_t ts = tmem + S::kS + (it & 1) * kShKeys + w * kMine + lane_off;
+        sh_wait(&sh.s_full[it & 1], (it >> 1) & 1, p.status, fail);
         tc_fence_after();
         // 32 scores at a time, once for the maximum and once for the weights: all 64 do not fit
         // beside what the rest takes of 96 registers
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < kShKeys; c += 32) {
+        for (int c = 0; c < kMine; c += 32) {
           float x[32];
           tmem_ld32(ts + c, x);
 #pragma unroll
           for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
         }
-        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        if (__any_sync(0xffffffffu, m > thr)) {
+        float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (any_of_256(2, m > thr)) {                          // rare behind the first blocks
+          sh.most[w][row] = m;
+          named_bar_sync(1, 256);
+          m = fmaxf(sh.most[0][row], sh.most[1][row]);
           float f = 1.f;
           if (m > thr) {
             f = ex2_approx((ref - m) * mul);                   // 0 the first time
@@ -750,23 +776,23 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
             thr = __fadd_rd(m, slack);
           }
           l = l * Pair(f, f);
-          if (n >= 2) {                                        // what the blocks before have left
-            sh_wait(&sh.o_done[w], (count - 1) & 1, p.status, fail);
+          if (n > 0) {                                         // what the blocks before have left
+            sh_wait(&sh.o_done, (it - 1) & 1, p.status, fail);
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 0; c < kHalf; c += 16) {
               uint32_t o[16];
-              tmem_ld16(to + w * D + c, o);
+              tmem_ld16(to + c, o);
 #pragma unroll
               for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st16(to + w * D + c, o);
+              tmem_st16(to + c, o);
             }
           }
         }
         const float base = ref == -INFINITY ? 0.f : -ref;      // no key so far: weights of 0
         uint32_t rest[2][16];
 #pragma unroll
-        for (int c = 0; c < kShKeys; c += 32) {
+        for (int c = 0; c < kMine; c += 32) {
           float s[32];
           tmem_ld32(ts + c, s);
           uint32_t pk[16];
@@ -785,38 +811,31 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
           tmem_st16(ts + c / 2, pk);                           // over scores that have been read
         }
         if (kFp16) {
-          tmem_st16(ts + kShKeys / 2, rest[0]);
-          tmem_st16(ts + kShKeys / 2 + 16, rest[1]);
+          tmem_st16(ts + kMine / 2, rest[0]);
+          tmem_st16(ts + kMine / 2 + 16, rest[1]);
         }
+        // every phase of o_done is waited for, one after the other: a parity tells only the last two apart
+        if (it > 0) sh_wait(&sh.o_done, (it - 1) & 1, p.status, fail);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&sh.p_full[w]);
+        mbar_arrive(&sh.p_full[it & 1]);
       }
-      // ---- the two halves' sums ----
-      if (nb > w) sh_wait(&sh.o_done[w], (count - 1) & 1, p.status, fail);
+      // ---- the tile's sums ----
       const float2 l2 = l.get();
-      sh.ml[w][row] = make_float2(ref * mul, l2.x + l2.y);
+      sh.sums[w][row] = l2.x + l2.y;
+      sh_wait(&sh.o_done, (it - 1) & 1, p.status, fail);
       named_bar_sync(1, 256);
       tc_fence_after();
-      const float2 m0 = sh.ml[0][row];
-      const float2 m1 = nb > 1 ? sh.ml[1][row] : make_float2(-INFINITY, 0.f);
-      const float M = fmaxf(m0.x, m1.x);
       constexpr float kDown = 1.f / 256.f;                     // 2^-kShUp
-      const float f0 = m0.y != 0.f ? ex2_approx(m0.x - M) * kDown : 0.f;
-      const float f1 = m1.y != 0.f ? ex2_approx(m1.x - M) * kDown : 0.f;
       // four dimensions of all rows, then the next four: whole lines are written
       float4 *dst = reinterpret_cast<float4 *>(plan.part) + (int64_t)sp.part * (D / 4) + row;
 #pragma unroll 1
       for (int c = 0; c < kHalf; c += 16) {
-        uint32_t x[16], y[16];
-        tmem_ld16(to + w * kHalf + c, x);
-        if (nb > 1) tmem_ld16(to + D + w * kHalf + c, y);
+        uint32_t x[16];
+        tmem_ld16(to + c, x);
         float o[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          o[j] = m0.y != 0.f ? __uint_as_float(x[j]) * f0 : 0.f;
-          if (nb > 1 && m1.y != 0.f) o[j] = fmaf(__uint_as_float(y[j]), f1, o[j]);
-        }
+        for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(x[j]) * kDown;
         if (real) {
 #pragma unroll
           for (int j = 0; j < 16; j += 8) {                    // back in the order of the dimensions
@@ -828,7 +847,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
       }
       if (real && w == 0)
         plan.part_ml[sp.part + row] =
-            make_float2(ldexpf(M, over), f0 * m0.y + (nb > 1 ? f1 * m1.y : 0.f));
+            make_float2(ldexpf(ref * mul, over), (sh.sums[0][row] + sh.sums[1][row]) * kDown);
       tc_fence_before();
       mbar_arrive(&sh.o_free);
     }
