@@ -175,6 +175,7 @@ cudaError_t launch_kv4_read(int d, bool fp16, const Kv4RowParams &p, cudaStream_
 size_t kv4_decode_workspace(int d, int g, bool selected);
 int64_t kv4_decode_tiles(const Kv4DecodeParams &p);
 cudaError_t launch_kv4_decode(int d, bool fp16, const Kv4DecodeParams &p, cudaStream_t s);
+double kv4_decode_estimate(const Kv4DecodeParams &p);
 cudaError_t launch_kv4_suffix(int d, bool fp16, const Kv4DecodeParams &p, cudaStream_t s);
 
 struct Kv4SharedParams {

@@ -1331,9 +1331,24 @@ static int seg_ctas(int64_t segs, int64_t most, int sms) {
 // 12.8 / 16.5, 64 x 2048 18.6 / 26.2, 64 x 4096 31.3 / 38.0 (the one of these where the estimate
 // takes the slower); ragged up to that length 8 x 4096 8.2 / 9.9, 64 x 2048 14.0 / 12.5, 64 x 4096
 // 24.5 / 14.2.
-static bool seg_better(int64_t segs, int64_t most, int ctas, int sms) {
+static double seg_time(int64_t segs, int64_t most, int ctas, int sms) {
   const int64_t on_sm = (segs * ctas + sms - 1) / sms;
-  return 4.2 + 0.125 * most / ctas * on_sm < 8.9 + 0.125 * segs * most / sms;
+  return 4.2 + 0.125 * most / ctas * on_sm;
+}
+static double runs_time(int64_t segs, int64_t most, int sms) { return 8.9 + 0.125 * segs * most / sms; }
+static bool seg_better(int64_t segs, int64_t most, int ctas, int sms) {
+  return seg_time(segs, most, ctas, sms) < runs_time(segs, most, sms);
+}
+
+// Microseconds of a call without a selection or a window, at the longest that the table allows.
+double kv4_decode_estimate(const Kv4DecodeParams &p) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0.;
+  const int sms = sm_count(dev);
+  const int64_t most = ((int64_t)p.width << p.page_log2) / kKv4Tile;
+  const int64_t segs = (int64_t)p.num_seqs * p.h_k * head_parts(p.g);
+  const double seg = seg_time(segs, most, seg_ctas(segs, most, sms), sms), runs = runs_time(segs, most, sms);
+  return seg < runs ? seg : runs;
 }
 
 template <int D, bool kFp16, bool kSuffix>

@@ -52,8 +52,7 @@ constexpr int kShTiles = kShKeys / kKv4Tile;
 constexpr int kShRaw = 2, kShK = 2;
 constexpr int kShThreads = 640;
 constexpr int kShMaxCtas = 256;
-constexpr int kShOver = 6;           // blocks that a tile's start and end count as
-constexpr int kSetupThreads = 1024;
+constexpr int kShOver = 2;           // blocks that a tile's start and end count as
 constexpr float kShSlack = 4.f;      // scores may exceed the reference by this much
 constexpr float kShUp = 8.f;         // weights are 2^8 times 2^(S - m)
 constexpr int kShQTop = 5;           // exponent of a row's largest q^
@@ -102,8 +101,12 @@ static int64_t shared_layout(int d, int num_seqs, int h_q, int num_groups, uint8
   return at;
 }
 
-// ---- setup -----------------------------------------------------------------------------
-// Inclusive prefix over the CTA; total gets the sum.
+// ---- the plan --------------------------------------------------------------------------
+constexpr int kSetupThreads = 1024;
+constexpr int kShOwnPlan = 256;      // groups up to which every CTA of the prefix kernel plans for itself
+
+// Inclusive prefix over a CTA of kWarps warps; total gets the sum.
+template <int kWarps>
 __device__ __forceinline__ int setup_incl(int x, int (&part)[32], int &total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -114,7 +117,7 @@ __device__ __forceinline__ int setup_incl(int x, int (&part)[32], int &total) {
   __syncthreads();
   if (lane == 31) part[warp] = x;
   __syncthreads();
-  int w = part[lane];
+  int w = lane < kWarps ? part[lane] : 0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, w, o);
@@ -125,38 +128,34 @@ __device__ __forceinline__ int setup_incl(int x, int (&part)[32], int &total) {
   return x + (warp ? before : 0);
 }
 
-// Shared or not?  In units of 25 ns of an SM's time: a tile of 128 rows takes about 240 and 40 a block
+// Shared or not?  In units of 25 ns of an SM's time: a tile of 128 rows takes about 240 and 72 a block
 // of 128 keys; the sequences' own passes over the prefix take 5 a tile of 32 keys each.
 __device__ __forceinline__ bool worth_sharing(int n, int g, int keys) {
   const int64_t own = (int64_t)n * (g > kK4Heads ? 2 : 1) * ((keys + 31) / 32) * 5;
   const int64_t tiles = ((int64_t)n * g + kShRows - 1) / kShRows;
-  return n > 1 && own > tiles * (240 + 40 * (int64_t)((keys + kShKeys - 1) / kShKeys));
+  return n > 1 && own > tiles * (240 + 72 * (int64_t)((keys + kShKeys - 1) / kShKeys));
 }
 
-// One CTA: groups that share, in order, what lies before each, and each sequence's group and first own
-// key.  A cu_groups out of order shares nothing.
-constexpr int kSetupGroups = 1024;   // up to as many the groups' numbers stay in shared memory
-__global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParams p, ShPlan plan, int ctas,
-                                                                  int least) {
-  __shared__ int part[32], s_cu[kSetupGroups + 1], s_at[kSetupGroups], s_keys[kSetupGroups];
-  const int tid = threadIdx.x, cap = p.dec.width << p.dec.page_log2;
-  const bool few = p.num_groups <= kSetupGroups;
-  after_previous();
-  int32_t err = 0;
-  for (int i = tid; i < p.num_groups; i += kSetupThreads) {
+// By a CTA of kThreads: groups that share, in order, with what lies before each, into `groups`, and of
+// every group whether it is ordered and its place there (-1: none) into `at`.  A cu_groups out of order
+// shares nothing.  Returns the head (per: CTAs have equal runs, of a block at least).
+template <int kThreads>
+__device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *groups, int32_t *at, int ctas,
+                                            int (&part)[32], int32_t &err) {
+  constexpr int kWarps = kThreads / 32;
+  const int cap = p.dec.width << p.dec.page_log2;
+  bool bad = false;
+  for (int i = threadIdx.x; i < p.num_groups; i += kThreads) {
     const int a = p.cu[i], b = p.cu[i + 1];
-    if (a < 0 || (i == 0 && a != 0) || b < a || b > p.dec.num_seqs) err |= NSA_DEVERR_BAD_SEQLENS;
-    if (few) {
-      s_cu[i] = a;
-      s_cu[i + 1] = b;               // the neighbour writes the same
-    }
+    bad |= a < 0 || (i == 0 && a != 0) || b < a || b > p.dec.num_seqs;
   }
-  const bool ordered = !__syncthreads_or(err);
-  int groups = 0, pairs = 0, rows = 0;
-  for (int i0 = 0; ordered && i0 < p.num_groups; i0 += kSetupThreads) {
-    const int i = i0 + tid;
+  const bool ordered = !__syncthreads_or(bad);
+  if (!ordered) err |= NSA_DEVERR_BAD_SEQLENS;
+  int count = 0, pairs = 0, rows = 0;
+  for (int i0 = 0; i0 < p.num_groups; i0 += kThreads) {
+    const int i = i0 + threadIdx.x;
     int n = 0, keys = 0, a = 0;
-    if (i < p.num_groups) {
+    if (ordered && i < p.num_groups) {
       a = p.cu[i];
       n = p.cu[i + 1] - a;
       keys = p.prefix[i];
@@ -169,43 +168,48 @@ __global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParam
     const int r = shares ? n * p.dec.g : 0, tiles = (r + kShRows - 1) / kShRows;
     const int blocks = (keys + kShKeys - 1) / kShKeys;
     int total;
-    const int g = groups + setup_incl(shares, part, total) - shares;
-    groups += total;
+    const int g = count + setup_incl<kWarps>(shares, part, total) - shares;
+    if (i < p.num_groups) at[i] = shares ? g : -1;
+    if (total == 0) continue;                                  // the same for all threads
+    count += total;
     const int w = tiles * p.dec.h_k * (blocks + kShOver);
-    const int before = pairs + setup_incl(w, part, total) - w;
+    const int before = pairs + setup_incl<kWarps>(w, part, total) - w;
     pairs += total;
-    const int row = rows + setup_incl(r * p.dec.h_k, part, total) - r * p.dec.h_k;
+    const int row = rows + setup_incl<kWarps>(r * p.dec.h_k, part, total) - r * p.dec.h_k;
     rows += total;
-    if (shares) plan.groups[g] = ShGroup{a, r, blocks, tiles, keys, before, row, 0};
-    if (i < p.num_groups) {
-      if (few) {
-        s_at[i] = shares ? g : -1;
-        s_keys[i] = keys;
-      } else {
-        plan.at[i] = shares ? g : -1;
-      }
+    if (shares) groups[g] = ShGroup{a, r, blocks, tiles, keys, before, row, 0};
+  }
+  __syncthreads();
+  return ShHead{count, pairs, max((pairs + ctas - 1) / ctas, kShOver + 1), 0};
+}
+
+// Sequence b's group among those that share, and its first own key.  One that ends inside the prefix
+// attends to its own pages alone.
+__device__ __forceinline__ void place_sequence(const Kv4SharedParams &p, const ShPlan &plan, const ShHead &head,
+                                               const ShGroup *groups, const int32_t *at, int b) {
+  int g = -1, lo = 0;
+  if (head.groups > 0 && b < p.cu[p.num_groups]) {
+    g = at[upper_index(p.cu, p.num_groups, b)];
+    if (g >= 0) {
+      const int keys = groups[g].keys, cap = p.dec.width << p.dec.page_log2;
+      if (min(max(p.dec.lens[b], 0), cap) >= keys) lo = keys;
+      else g = -1;
     }
   }
-  if (tid == 0) *plan.head = ShHead{groups, pairs, max((pairs + ctas - 1) / ctas, least), 0};
-  if (__syncthreads_or(err) && tid == 0) raise(p.dec.status, NSA_DEVERR_BAD_SEQLENS);
-  for (int b = tid; b < p.dec.num_seqs; b += kSetupThreads) {
-    int g = -1, lo = 0;
-    if (ordered && groups > 0) {
-      const int32_t *cu = few ? s_cu : p.cu;
-      if (b < cu[p.num_groups]) {
-        const int i = upper_index(cu, p.num_groups, b);
-        g = few ? s_at[i] : plan.at[i];
-        if (g >= 0) {
-          const int keys = few ? s_keys[i] : plan.groups[g].keys;
-          // a sequence that ends inside the prefix attends to its own pages alone
-          if (min(max(p.dec.lens[b], 0), cap) >= keys) lo = keys;
-          else g = -1;
-        }
-      }
-    }
-    plan.lo[b] = lo;
-    plan.of[b] = g;
-  }
+  plan.lo[b] = lo;
+  plan.of[b] = g;
+}
+
+// For more groups than the prefix kernel's CTAs plan themselves.
+__global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParams p, ShPlan plan, int ctas) {
+  __shared__ int part[32];
+  after_previous();
+  int32_t err = 0;
+  const ShHead head = make_plan<kSetupThreads>(p, plan.groups, plan.at, ctas, part, err);
+  if (__syncthreads_or(err) && threadIdx.x == 0) raise(p.dec.status, NSA_DEVERR_BAD_SEQLENS);
+  if (threadIdx.x == 0) *plan.head = head;
+  for (int b = threadIdx.x; b < p.dec.num_seqs; b += kSetupThreads)
+    place_sequence(p, plan, head, plan.groups, plan.at, b);
 }
 
 // ---- prefix ----------------------------------------------------------------------------
@@ -223,7 +227,7 @@ struct Sh {
   static constexpr uint32_t kBytes = kOffRaw + 2 * kShRaw * kRawBytes + 1024;   // + alignment
   static_assert(kShK <= 4, "a 128-byte row holds four stages' columns");
   static_assert(kOffV % 1024 == 0 && kOffZ % 1024 == 0 && kOffRaw % 1024 == 0, "operands' alignment");
-  static_assert(kBytes <= 226 * 1024, "shared memory");
+  static_assert(kBytes <= 214 * 1024, "shared memory, with 13 KB of barriers and the plan");
   // columns of tensor memory: two blocks' scores, the output, Q, its sums
   static constexpr uint32_t kS = 0, kO = 2 * kShKeys, kQ = kO + D, kSums = kQ + D / 2;
   static constexpr uint32_t kCols = 512;
@@ -239,6 +243,8 @@ struct ShShared {
   int top[2][kShRows];                         // largest magnitudes of q, as bits
   uint32_t tmem;
   int fail;
+  int part[32], at[kShOwnPlan];                // of the plan
+  ShGroup groups[kShOwnPlan];
 };
 
 // One tile's blocks in a CTA's run.
@@ -251,8 +257,8 @@ struct ShWalk {
   const ShGroup *groups;
   ShGroup g;
   int group, at, stop, n_groups, cta;
-  __device__ __forceinline__ ShWalk(const ShPlan &plan, int cta_) : groups(plan.groups), cta(cta_) {
-    const ShHead hd = *plan.head;
+  __device__ __forceinline__ ShWalk(const ShHead &hd, const ShGroup *groups_, int cta_)
+      : groups(groups_), cta(cta_) {
     n_groups = hd.groups;
     at = static_cast<int>(min((int64_t)cta * hd.per, (int64_t)hd.pairs));
     stop = static_cast<int>(min((int64_t)at + hd.per, (int64_t)hd.pairs));
@@ -471,7 +477,8 @@ __device__ __forceinline__ void three_parts(float x, __half (&h)[3]) {
 }
 
 template <int D, bool kFp16>
-__global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodeParams p, ShPlan plan) {
+__global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_constant__ Kv4SharedParams sp_,
+                                                                   ShPlan plan) {
   using S = Sh<D>;
   using T = Kv4Tile<D>;
   constexpr int G = S::kG;
@@ -481,8 +488,26 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
                                               ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int *const fail = &sh.fail;
+  const Kv4DecodeParams &p = sp_.dec;
   after_previous();
-  if (plan.head->pairs <= (int64_t)blockIdx.x * plan.head->per) return;   // the whole CTA
+  const bool own_plan = sp_.num_groups <= kShOwnPlan;
+  ShHead head;
+  if (own_plan) {
+    // every CTA plans; the first one leaves the plan, and each a share of the sequences' places, to
+    // the kernels behind
+    int32_t err = 0;
+    head = make_plan<kShThreads>(sp_, sh.groups, sh.at, gridDim.x, sh.part, err);
+    for (int64_t b = (int64_t)blockIdx.x * kShThreads + tid; b < p.num_seqs; b += (int64_t)gridDim.x * kShThreads)
+      place_sequence(sp_, plan, head, sh.groups, sh.at, static_cast<int>(b));
+    if (blockIdx.x == 0) {
+      if (err) raise(p.status, err);
+      if (tid == 0) *plan.head = head;
+      for (int i = tid; i < head.groups; i += kShThreads) plan.groups[i] = sh.groups[i];
+    }
+  } else {
+    head = *plan.head;
+  }
+  if (head.pairs <= (int64_t)blockIdx.x * head.per) return;    // the whole CTA
   if (warp == 19) tmem_alloc(&sh.tmem, S::kCols);
   if (tid == 0) {
     for (int i = 0; i < 2 * kShRaw; ++i) {
@@ -511,7 +536,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(Kv4DecodePara
   const uint32_t sK = smem_u32(smem + S::kOffK), sV = smem_u32(smem + S::kOffV),
                  sZ = smem_u32(smem + S::kOffZ);
   uint8_t *const raw0 = smem + S::kOffRaw;
-  ShWalk walk(plan, blockIdx.x);
+  ShWalk walk(head, own_plan ? sh.groups : plan.groups, blockIdx.x);
   ShSpan sp;
 
   if (warp == 18) {
@@ -968,14 +993,16 @@ static cudaError_t run_shared(const Kv4SharedParams &p, cudaStream_t s) {
   ShPlan plan;
   shared_layout(D, p.dec.num_seqs, p.dec.h_q, p.num_groups, p.ws, &plan);
   const int ctas = sms < kShMaxCtas ? sms : kShMaxCtas;
-  e = launch_kv4(kv4_share_kernel, dim3(1), kSetupThreads, 0, 1, s, p, plan, ctas, kShOver + 4);
-  if (e != cudaSuccess) return e;
+  if (p.num_groups > kShOwnPlan) {
+    e = launch_kv4(kv4_share_kernel, dim3(1), kSetupThreads, 0, 1, s, p, plan, ctas);
+    if (e != cudaSuccess) return e;
+  }
   auto *kernel = kv4_prefix_kernel<D, kFp16>;
   // more than half of an SM's: one CTA each, as its tensor memory allows
   constexpr int smem = Sh<D>::kBytes > 120 * 1024 ? Sh<D>::kBytes : 120 * 1024;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_kv4(kernel, dim3(static_cast<unsigned>(ctas)), kShThreads, smem, 1, s, p.dec, plan);
+  e = launch_kv4(kernel, dim3(static_cast<unsigned>(ctas)), kShThreads, smem, 1, s, p, plan);
   if (e != cudaSuccess) return e;
   Kv4DecodeParams own = p.dec;
   own.lo = plan.lo;
@@ -988,7 +1015,13 @@ static cudaError_t run_shared(const Kv4SharedParams &p, cudaStream_t s) {
                     p.dec, plan);
 }
 
+// A batch small enough, by the bounds that the host knows, goes the way of kv4_decode: three kernels
+// that plan, share and join take about 20 us for the least of work (4 sequences behind 517 tokens: 14
+// us against 7, 30 of up to 900: 17 against 10).
+constexpr double kShLeastUs = 20.;
+
 cudaError_t launch_kv4_shared(int d, bool fp16, const Kv4SharedParams &p, cudaStream_t s) {
+  if (kv4_decode_estimate(p.dec) < kShLeastUs) return launch_kv4_decode(d, fp16, p.dec, s);
   if (d == 64) return fp16 ? run_shared<64, true>(p, s) : run_shared<64, false>(p, s);
   return fp16 ? run_shared<128, true>(p, s) : run_shared<128, false>(p, s);
 }

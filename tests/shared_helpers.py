@@ -68,3 +68,14 @@ def check_shared(out, lse, ref, dtype):
         def numpy(self):
             return moved.numpy()
     check_decode(_Wide(), lse, ref, dtype)
+
+
+def wide(table, page, segs):
+    """The table with room for far longer sequences than it has: a batch for which, by the sizes that
+    the host knows, sharing may pay (segs: sequences times KV heads, twice for more than 8 query
+    heads each)."""
+    tiles = max(1100, 16000 // segs)
+    cols = -(-tiles * 32 // page)
+    out = np.full((table.shape[0], max(cols, table.shape[1])), -1, np.int32)
+    out[:, :table.shape[1]] = table
+    return out

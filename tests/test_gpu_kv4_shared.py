@@ -5,7 +5,7 @@ import torch
 
 from kv4_helpers import DTYPES
 from oracle import kv4
-from shared_helpers import check_shared, make_shared
+from shared_helpers import check_shared, make_shared, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -23,12 +23,14 @@ def _run(groups, page, h_k, g, d, dtype, seed, alone=(), scale=None, width=None,
         q = torch.randn(len(lens), h_k * g, d, generator=torch.Generator().manual_seed(seed)).to(dt)
     scale = d ** -0.5 if scale is None else scale
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), scale, _dev(cu),
-                                     _dev(prefix), device_status=status)
-    assert int(status.item()) == 0
     rows = np.arange(len(lens)) if some is None else np.asarray(some)
     ref = kv4.attend(q[rows].double().numpy(), pool, table[rows], lens[rows], page, scale)
-    check_shared(out[rows], lse[:, rows], ref, dt)
+    # as it is, and with a table that leaves the choice to the device
+    for t in (table, wide(table, page, len(lens) * h_k)):
+        out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(t), _dev(lens), scale, _dev(cu),
+                                         _dev(prefix), device_status=status)
+        assert int(status.item()) == 0
+        check_shared(out[rows], lse[:, rows], ref, dt)
     return out, ref
 
 
@@ -118,6 +120,7 @@ def test_rising_scores():
             for arr in (code, scale, zero):
                 arr[z_, :, :, :n % page] = arr[a, :, :, :n % page]
         pool2 = kv4.pack(code, scale, zero)
+    table = wide(table, page, 3)
     for dtype, size in ((torch.bfloat16, 0.3), (torch.float16, 3.0)):
         q = (torch.from_numpy(u)[None, None] * size + torch.randn(3, 2, d,
              generator=torch.Generator().manual_seed(3))).to(dtype)
@@ -133,6 +136,7 @@ def test_largest_queries_and_scales(size, scale):
     huge."""
     import block_sparse_attention_nsa_gb300 as nsa
     pool, table, lens, cu, prefix = make_shared([(300, (320, 300, 400))], 64, 1, 128, 31)
+    table = wide(table, 64, 3)
     q = (torch.randn(3, 2, 128, generator=torch.Generator().manual_seed(1)) * size).to(torch.bfloat16)
     got = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), scale, _dev(cu), _dev(prefix))
     ref = kv4.attend(q.double().numpy(), pool, table, lens, 64, scale)
@@ -148,6 +152,7 @@ def test_bad_pages_and_nan_rows():
     import block_sparse_attention_nsa_gb300 as nsa
     page, h_k, g, d = 32, 2, 4, 128
     pool, table, lens, cu, prefix = make_shared([(300, (320, 300, 400)), (64, (64, 90))], page, h_k, d, 41)
+    table = wide(table, page, 5 * h_k)
     q = torch.randn(5, h_k * g, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     # pages of the prefix that are none: their keys are left out, for all of the group
@@ -176,17 +181,18 @@ def test_malformed_groups():
     import block_sparse_attention_nsa_gb300 as nsa
     page, d = 32, 64
     pool, table, lens, cu, prefix = make_shared([(100, (120, 100, 130)), (64, (64, 90))], page, 1, d, 51)
+    table = wide(table, page, 5)
     q = torch.randn(5, 2, d, generator=torch.Generator().manual_seed(1)).half()
     ref = kv4.attend(q.double().numpy(), pool, table, lens, page, 0.1)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     for c, p in (((0, 3, 6), prefix), ((1, 3, 5), prefix), ((0, 3, 2), prefix), ((0, -1, 5), prefix),
-                 (cu, (-1, 64)), (cu, (100, 10 ** 6)), (cu, (100, table.shape[1] * page + 1))):
+                 (cu, (-1, 64)), (cu, (100, 10 ** 7)), (cu, (100, table.shape[1] * page + 1))):
         out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), 0.1,
                                          _dev(np.int32(c)), _dev(np.int32(p)), device_status=status.zero_())
         assert int(status.item()) == nsa.DEVERR_BAD_SEQLENS, (c, p)
         check_shared(out, lse, ref, torch.float16)
     n = lens.copy()
-    n[1], n[4] = -3, 10 ** 6
+    n[1], n[4] = -3, 10 ** 7
     out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(n), 0.1, _dev(cu), _dev(prefix),
                                      device_status=status.zero_())
     assert int(status.item()) & nsa.DEVERR_BAD_SEQLENS
@@ -200,6 +206,7 @@ def test_streams_graphs_and_dirty_workspaces():
     for seed in range(3):
         pool, table, lens, cu, prefix = make_shared([(700, (720, 700, 900, 701)), (64, (64, 90))], page, h_k,
                                                     d, 61 + seed, width=40)
+        table = wide(table, page, 6 * h_k)
         q = torch.randn(6, h_k * g, d, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
         sets.append([x.cuda() if torch.is_tensor(x) else _dev(x) for x in (q, pool, table, lens, cu, prefix)])
     def call(s, **kw):
@@ -278,6 +285,14 @@ def test_shared_and_unshared_groups_together(d, page, h_k, g, dtype):
          some=(0, 1, 2, 3, 5, 6, 40, 76, 77, 78, 140, 205, 206, 207, 208, 209, 210))
 
 
+def test_shared_more_groups_than_a_cta_plans():
+    groups = [(int(p), _members(int(n), int(p), i, 5)) for i, (p, n) in enumerate(zip(
+        np.random.default_rng(1).integers(1, 60, 300), np.random.default_rng(2).integers(0, 4, 300)))]
+    groups[100], groups[299] = (200, _members(90, 200, 7)), (70, _members(100, 70, 8))
+    n = sum(len(g[1]) for g in groups)
+    _run(groups, 32, 1, 1, 64, "bf16", 12, alone=(9, 40), some=tuple(range(0, n + 2, 41)) + (n, n + 1))
+
+
 def test_shared_many_groups():
     groups = [(int(p), _members(60, int(p), i, 9)) for i, p in
               enumerate(np.random.default_rng(1).integers(1, 200, 25))]
@@ -305,6 +320,7 @@ def test_shared_huge_scores(size, scale):
     takes it all, unless two are that close."""
     import block_sparse_attention_nsa_gb300 as nsa
     pool, table, lens, cu, prefix = make_shared([(300, _members(60, 300, 1))], 64, 1, 128, 31)
+    table = wide(table, 64, 60)
     q = (torch.randn(60, 1, 128, generator=torch.Generator().manual_seed(1)) * size).to(torch.bfloat16)
     out, _ = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), scale, _dev(cu), _dev(prefix))
     ref = kv4.attend(q.double().numpy(), pool, table, lens, 64, scale)
@@ -320,6 +336,7 @@ def test_shared_rising_scores():
     rng = np.random.default_rng(1)
     u = rng.standard_normal(d).astype(np.float32)
     pool, table, lens, cu, prefix = make_shared([(n, _members(60, n, 2))], page, 1, d, 2)
+    table = wide(table, page, 60)
     code, scale, zero = kv4.unpack(pool, page, d)
     for t in range(n):
         pg, at = table[0, t // page], t % page
@@ -339,6 +356,7 @@ def test_shared_bad_pages_and_nan_rows():
     page, h_k, g, d = 32, 1, 2, 128
     pool, table, lens, cu, prefix = make_shared([(300, _members(60, 300, 1)), (64, _members(60, 64, 2))], page,
                                                 h_k, d, 41)
+    table = wide(table, page, 120)
     q = torch.randn(120, g, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     def call(q, t):
@@ -373,6 +391,7 @@ def test_shared_largest_values():
     import block_sparse_attention_nsa_gb300 as nsa
     page, d, n = 32, 64, 100
     pool, table, lens, cu, prefix = make_shared([(n, _members(60, n, 2))], page, 1, d, 2)
+    table = wide(table, page, 60)
     code, scale, zero = kv4.unpack(pool, page, d)
     rng = np.random.default_rng(3)
     for t in range(0, n - 10, 3):
@@ -400,6 +419,7 @@ def test_shared_graph_and_dirty_workspace():
         pool, table, lens, cu, prefix = make_shared(
             [(700, _members(60, 700, 9)), (130, _members(40 + 20 * (seed == 1), 130, 9)),
              (64, _members(20 - 20 * (seed == 1), 64, 9))], page, h_k, d, 61 + seed, width=20)
+        table = wide(table, page, 120 * h_k)
         q = torch.randn(120, h_k * g, d, generator=torch.Generator().manual_seed(seed)).to(torch.bfloat16)
         sets.append([x.cuda() if torch.is_tensor(x) else _dev(x) for x in (q, pool, table, lens, cu, prefix)])
     pages = max(s[1].shape[0] for s in sets)
