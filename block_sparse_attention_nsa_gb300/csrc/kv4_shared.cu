@@ -39,6 +39,8 @@
 // Work: the line of all (tile, block) pairs, tile after tile, in equal runs, one a CTA; where a tile
 // is shared by CTAs each leaves partial rows.  kv4_join_kernel adds them and the own part.
 #include <cmath>
+#include <type_traits>
+#include <utility>
 
 #include "kv4.cuh"
 
@@ -317,8 +319,10 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 }
 // In order with the other asm statements (barriers among them), but loads may pass it: the places that
 // these stores write are not read by ordinary loads.
+template <int kOffset = 0>
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+  asm volatile("st.shared.v4.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w), "n"(kOffset));
 }
 // Whether any of the softmax threads says so; a barrier for them all.
 __device__ __forceinline__ bool any_of_256(int id, bool mine) {
@@ -334,17 +338,20 @@ __device__ __forceinline__ bool any_of_256(int id, bool mine) {
   return any != 0;
 }
 
-// The codes of a word as fp16 less `off` - 1024: dimensions (0, 4), (1, 5), (2, 6), (3, 7).
-__device__ __forceinline__ void code_halves(uint32_t w, __half2 off, __half2 (&c)[4]) {
+// The codes of a word less `off`, as fp16: dimensions (0, 4), (1, 5), (2, 6), (3, 7).  A code in the
+// lowest bits of 1024's or in bits 4 to 7 of 64's is added to it.
+__device__ __forceinline__ void code_halves(uint32_t w, float off, __half2 (&c)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t u = (w >> (4 * k) & 0x000f000fu) | 0x64006400u;   // 1024 + c
-    c[k] = __hsub2(*reinterpret_cast<const __half2 *>(&u), off);
+    const uint32_t x = k & 2 ? w >> 8 : w;
+    const uint32_t u = k & 1 ? (x & 0x00f000f0u) | 0x54005400u : (x & 0x000f000fu) | 0x64006400u;
+    c[k] = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn((k & 1 ? 64.f : 1024.f) + off));
   }
 }
+template <int kOffset>
 __device__ __forceinline__ void sts_halves(uint32_t a, const __half2 (&h)[4]) {
   const uint32_t *u = reinterpret_cast<const uint32_t *>(h);
-  sts128(a, make_uint4(u[0], u[1], u[2], u[3]));
+  sts128<kOffset>(a, make_uint4(u[0], u[1], u[2], u[3]));
 }
 // V's values past fp16's largest, which the rounding of a scale can make of 65504, are held to it.
 __device__ __forceinline__ __half2 held(__half2 h) {
@@ -386,41 +393,51 @@ struct ShPiece {
       }
     }
   }
-  // word 4 q + i of turn u is group i % kG's; where its dimensions lie in an operand
-  __device__ __forceinline__ static uint32_t at(int u, int i, int t) {
-    return sw128_offset(key(u, t), 8 * (i % kG) + (4 / kG) * (t % kChunks) + i / kG, kShKeys);
+  // Word 4 q + i is group i % kG's, its dimensions' chunk there (4 / kG) q + i / kG: in an operand it lies
+  // at (first(t) ^ flip(i)) + step(u, i), whatever the operand's start, a multiple of 1024.
+  __device__ __forceinline__ static uint32_t first(int t) {
+    return sw128_offset(key(0, t), (4 / kG) * (t % kChunks), kShKeys);
   }
+  static constexpr uint32_t flip(int i) { return static_cast<uint32_t>(i / kG) << 4; }
+  static constexpr int step(int u, int i) { return (i % kG) * kShKeys * 128 + u * (256 / kChunks) * 128; }
 };
+
+// f(u, i) for all turns and words, with both known to the compiler.
+template <typename F, int... kI>
+__device__ __forceinline__ void each_word(F &&f, std::integer_sequence<int, kI...>) {
+  (f(std::integral_constant<int, kI / 4>{}, std::integral_constant<int, kI % 4>{}), ...);
+}
 
 template <int D>
 __device__ __forceinline__ void unpack_k(const uint8_t *raw, const uint32_t (&seen)[kShTiles], uint32_t kdst,
-                                         uint32_t zdst, int stage, int t) {
+                                         uint32_t zdst, int stage, int t, uint32_t first) {
   using P = ShPiece<D>;
   constexpr int G = P::kG;
-  const __half2 off = __float2half2_rn(1032.f);
   const P p(raw, seen, t);
+  __half2 hi[P::kTurns][G], lo[P::kTurns][G];
 #pragma unroll
-  for (int u = 0; u < P::kTurns; ++u) {
-    __half2 hi[G], lo[G];
+  for (int u = 0; u < P::kTurns; ++u)
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      hi[g] = upper(p.s[u][g]);
-      lo[g] = __hsub2(p.s[u][g], hi[g]);
+      hi[u][g] = upper(p.s[u][g]);
+      lo[u][g] = __hsub2(p.s[u][g], hi[u][g]);
     }
+  each_word([&](auto u, auto i) {
+    __half2 c[4], x[4], y[4];
+    code_halves(p.w[u][i], 8.f, c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __half2 c[4], x[4], y[4];
-      code_halves(p.w[u][i], off, c);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[k] = __hmul2(c[k], hi[i % G]);
-        y[k] = __hmul2(c[k], lo[i % G]);
-      }
-      sts_halves(kdst + P::at(u, i, t), x);
-      sts_halves(kdst + Sh<D>::kOperand + P::at(u, i, t), y);
+    for (int k = 0; k < 4; ++k) {
+      x[k] = __hmul2(c[k], hi[u][i % G]);
+      y[k] = __hmul2(c[k], lo[u][i % G]);
     }
-    // the first thread of a row: z z z s s s of each group; 0, or -inf: no key
-    if (t % P::kChunks == 0) {
+    const uint32_t a = (kdst + first) ^ P::flip(i);
+    sts_halves<P::step(u, i)>(a, x);
+    sts_halves<P::step(u, i) + static_cast<int>(Sh<D>::kOperand)>(a, y);
+  }, std::make_integer_sequence<int, 4 * P::kTurns>{});
+  // the first thread of a row: z z z s s s of each group; 0, or -inf: no key
+  if (t % P::kChunks == 0) {
+#pragma unroll
+    for (int u = 0; u < P::kTurns; ++u) {
       const int key = P::key(u, t);
       uint32_t v[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
 #pragma unroll
@@ -439,10 +456,9 @@ __device__ __forceinline__ void unpack_k(const uint8_t *raw, const uint32_t (&se
 
 template <int D>
 __device__ __forceinline__ void unpack_v(const uint8_t *raw, const uint32_t (&seen)[kShTiles], uint32_t vdst,
-                                         int t) {
+                                         int t, uint32_t first) {
   using P = ShPiece<D>;
   constexpr int G = P::kG;
-  const __half2 off = __float2half2_rn(1024.f);
   const P p(raw, seen, t);
   bool wide = false;
 #pragma unroll
@@ -451,20 +467,23 @@ __device__ __forceinline__ void unpack_v(const uint8_t *raw, const uint32_t (&se
     for (int g = 0; g < G; ++g)
       wide |= !(fabsf(__low2float(p.z[u][g])) + 15.f * __low2float(p.s[u][g]) < 65504.f);
   const bool any_wide = __any_sync(0xffffffffu, wide);
+  each_word([&](auto u, auto i) {
+    __half2 c[4];
+    code_halves(p.w[u][i], 0.f, c);
 #pragma unroll
-  for (int u = 0; u < P::kTurns; ++u)
+    for (int k = 0; k < 4; ++k) c[k] = __hfma2(c[k], p.s[u][i % G], p.z[u][i % G]);
+    if (any_wide) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __half2 c[4];
-      code_halves(p.w[u][i], off, c);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) c[k] = __hfma2(c[k], p.s[u][i % G], p.z[u][i % G]);
-      if (any_wide) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = held(c[k]);
-      }
-      sts_halves(vdst + P::at(u, i, t), c);
+      for (int k = 0; k < 4; ++k) c[k] = held(c[k]);
     }
+    sts_halves<P::step(u, i)>((vdst + first) ^ P::flip(i), c);
+  }, std::make_integer_sequence<int, 4 * P::kTurns>{});
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
 }
 
 // A number as three fp16 ones.
@@ -603,13 +622,14 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     // ----------------------------- unpackers ----------------------------
     // K of a block, then V of the one before it, whose place the product before that frees
     const int t = tid - 256;
+    const uint32_t first = ShPiece<D>::first(t);
     int it = 0;
     auto k_of = [&](int i) {
       const int rs = i % kShRaw, ks = i % kShK;
       sh_wait(&sh.raw_full[0][rs], (i / kShRaw) & 1, p.status, fail);
       if (i >= kShK) sh_wait(&sh.k_empty[ks], ((i / kShK) - 1) & 1, p.status, fail);
       __syncwarp();
-      unpack_k<D>(raw0 + rs * S::kRawBytes, sh.seen[0][rs], sK + ks * 2 * S::kOperand, sZ, ks, t);
+      unpack_k<D>(raw0 + rs * S::kRawBytes, sh.seen[0][rs], sK + ks * 2 * S::kOperand, sZ, ks, t, first);
       fence_proxy_async_smem();
       mbar_arrive(&sh.k_full[ks]);
       mbar_arrive(&sh.raw_empty[0][rs]);
@@ -619,7 +639,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
       sh_wait(&sh.raw_full[1][rs], (i / kShRaw) & 1, p.status, fail);
       if (i > 0) sh_wait(&sh.o_done, (i - 1) & 1, p.status, fail);
       __syncwarp();
-      unpack_v<D>(raw0 + (kShRaw + rs) * S::kRawBytes, sh.seen[1][rs], sV, t);
+      unpack_v<D>(raw0 + (kShRaw + rs) * S::kRawBytes, sh.seen[1][rs], sV, t, first);
       fence_proxy_async_smem();
       mbar_arrive(&sh.v_full);
       mbar_arrive(&sh.raw_empty[1][rs]);
@@ -781,15 +801,15 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         tc_fence_after();
         // 32 scores at a time, once for the maximum and once for the weights: all 64 do not fit
         // beside what the rest takes of 96 registers
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < kMine; c += 32) {
           float x[32];
           tmem_ld32(ts + c, x);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], x[j]);
+          for (int j = 0; j < 32; j += 2) mx[j >> 1 & 1] = max3(mx[j >> 1 & 1], x[j], x[j + 1]);
         }
-        float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        float m = fmaxf(mx[0], mx[1]);
         if (any_of_256(2, m > thr)) {                          // rare behind the first blocks
           sh.most[w][row] = m;
           named_bar_sync(1, 256);
