@@ -165,6 +165,13 @@ inline cudaError_t launch_kv4(void (*kernel)(P...), dim3 grid, int threads, size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// CTAs of a wide cluster of this kernel: sixteen, which it has to be allowed and a GPU may have no room
+// for, or eight.  smem: the most dynamic shared memory that any of its calls takes (the limit is the
+// kernel's, and another host thread may be between its own and its launch).
+constexpr int kWideCluster = 16;
+enum WideKernel { kWidePlan, kWideSlots, kWideFork, kWideFree, kWideCompact, kWideKernels };
+cudaError_t wide_cluster(WideKernel which, const void *kernel, int threads, size_t smem, int *ctas);
+
 cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s);
 enum class PageOp { kFork, kFree, kCompact };
 cudaError_t launch_page_op(PageOp op, const PageOpsParams &p, cudaStream_t s);

@@ -802,7 +802,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         // 32 scores at a time, once for the maximum and once for the weights: all 64 do not fit
         // beside what the rest takes of 96 registers
         float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kMine; c += 32) {
           float x[32];
           tmem_ld32(ts + c, x);
@@ -836,7 +836,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         }
         const float base = ref == -INFINITY ? 0.f : -ref;      // no key so far: weights of 0
         uint32_t rest[2][16];
-#pragma unroll
+#pragma unroll (kFp16 ? 2 : 1)
         for (int c = 0; c < kMine; c += 32) {
           float s[32];
           tmem_ld32(ts + c, s);

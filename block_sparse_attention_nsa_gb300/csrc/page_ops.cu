@@ -6,7 +6,7 @@
 // scans: a fork's free page is the head plus the forks before it that need one; pages that are
 // freed, moved or filled are taken in ascending order from a bitmap of all pages.
 //
-// A few bytes per page: latency counts.  One launch of one CTA, or of a cluster of eight that split
+// A few bytes per page: latency counts.  One launch of one CTA, or of a cluster of sixteen that split
 // the rows (a warp a row) and the bitmap (a slice of pages a CTA, set through distributed shared
 // memory); a cluster barrier between the steps.  page_copy moves bytes, bound by HBM.
 #include "kv4.cuh"
@@ -14,7 +14,6 @@
 namespace nsa {
 
 constexpr int kOpsThreads = 1024, kOpsWarps = kOpsThreads / 32;
-constexpr int kOpsCluster = 8;
 
 // Inclusive prefix over the CTA's threads; total gets the sum.  All threads take part.
 __device__ __forceinline__ int cta_incl(int x, int (&part)[kOpsWarps], int &total) {
@@ -222,40 +221,59 @@ __global__ void __launch_bounds__(kOpsThreads) page_free_kernel(PageOpsParams p,
   const PageBits map{smem_u32(bits), words};
   for (int w = tid; w < words; w += kOpsThreads) bits[w] = 0;
   after_previous();
-  first_owners(owner, p.rows_from, p.count, p.num_seqs);
+  constexpr int kNone = INT32_MIN;
+  const int first_i = rank * kOpsWarps + (tid >> 5), step = ncta * kOpsWarps;
+  int r_l = kNone, len_l = 0;
+  auto look = [&](int k0) {
+    const int64_t i = first_i + (int64_t)(k0 + lane) * step;
+    r_l = i < p.count ? p.rows_from[i] : kNone;
+    if (r_l == kNone && i < p.count) r_l = -1;
+    len_l = r_l >= 0 && r_l < p.num_seqs ? p.lens[r_l] : 0;
+  };
+  look(0);
   const int head = *p.head_in;
+  first_owners(owner, p.rows_from, p.count, p.num_seqs);
   cluster_sync();                          // every slice is clear; owner is complete
   int32_t err = 0;
-  for (int i = rank * kOpsWarps + (tid >> 5); i < p.count; i += ncta * kOpsWarps) {
-    const int r = p.rows_from[i];
-    if (r < 0 || r >= p.num_seqs || owner[r] != i) {
-      err |= NSA_DEVERR_BAD_INDEX;
-      continue;
-    }
-    const int len = p.lens[r];
-    int32_t bad = 0;
-    const int pages = row_pages(p, len, bad);
-    err |= bad;
-    if (bad) continue;                     // the row is left alone
-    int32_t *row = p.table + (int64_t)r * p.width;
-    for (int j0 = 0; j0 < pages; j0 += 128) {
-      int pg[4], had[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) pg[u] = j0 + u * 32 + lane < pages ? row[j0 + u * 32 + lane] : -2;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        had[u] = 1;
-        if (pg[u] >= 0 && pg[u] < p.num_pages) had[u] = atomicSub(&p.shares[pg[u]], 1);
-        else if (pg[u] != -2 || j0 + u * 32 + lane < pages) err |= NSA_DEVERR_BAD_INDEX;
-        if (j0 + u * 32 + lane < pages) row[j0 + u * 32 + lane] = -1;
+  // lane k has looked up the k-th of the warp's next 32 rows
+  for (int k0 = 0; first_i + (int64_t)k0 * step < p.count; k0 += 32) {
+    if (k0) look(k0);
+    int row_l = 0, pages_l = 0;
+    if (r_l != kNone) {
+      int32_t bad = 0;
+      if (r_l < 0 || r_l >= p.num_seqs || owner[r_l] != first_i + (k0 + lane) * step) {
+        bad = NSA_DEVERR_BAD_INDEX;
+      } else {
+        pages_l = row_pages(p, len_l, bad);
+        row_l = r_l;
+        if (!bad) p.lens[r_l] = 0;
       }
+      if (bad) pages_l = 0;                // passed over: left alone
+      err |= bad;
+    }
+    const int turns = static_cast<int>(min((int64_t)32, (p.count - first_i - (int64_t)k0 * step + step - 1) / step));
+    for (int k = 0; k < turns; ++k) {
+      const int pages = __shfl_sync(0xffffffffu, pages_l, k);
+      int32_t *row = p.table + (int64_t)__shfl_sync(0xffffffffu, row_l, k) * p.width;
+      for (int j0 = lane; j0 < pages; j0 += 128) {
+        int pg[4], had[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (had[u] == 0) map.set(pg[u]);
-        if (had[u] < 0) err |= NSA_DEVERR_BAD_INDEX;   // more rows named it than were counted
+        for (int u = 0; u < 4; ++u) pg[u] = j0 + u * 32 < pages ? row[j0 + u * 32] : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          had[u] = 1;
+          if (j0 + u * 32 >= pages) continue;
+          if (pg[u] >= 0 && pg[u] < p.num_pages) had[u] = atomicSub(&p.shares[pg[u]], 1);
+          else err |= NSA_DEVERR_BAD_INDEX;
+          row[j0 + u * 32] = -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (had[u] == 0) map.set(pg[u]);
+          if (had[u] < 0) err |= NSA_DEVERR_BAD_INDEX;   // more rows named it than were counted
+        }
       }
     }
-    if (lane == 0) p.lens[r] = 0;
   }
   cluster_sync();
   const int slice = count_words(bits, before, words, part);
@@ -360,16 +378,29 @@ __global__ void __launch_bounds__(kOpsThreads) page_compact_kernel(PageOpsParams
     }
   }
   const bool apart = p.table != p.table_in;
+  constexpr int kAtOnce = 8;
   for (int r = rank * kOpsWarps + (tid >> 5); r < p.num_seqs; r += ncta * kOpsWarps) {
     int32_t again = 0;                                 // reported above
     const int pages = row_pages(p, p.lens[r], again);
     const int32_t *row = p.table_in + (int64_t)r * p.width;
     int32_t *out = p.table + (int64_t)r * p.width;
-    for (int j = lane; j < (apart ? p.width : pages); j += 32) {
-      const int pg = row[j];
-      const bool moved = fits && j < pages && pg >= live && pg < p.num_pages;
-      if (moved) out[j] = p.copy_dst[below(pg) - stay];
-      else if (apart) out[j] = pg;
+    const int end = apart ? p.width : pages;
+    for (int j0 = lane; j0 < end; j0 += 32 * kAtOnce) {   // the steps of kAtOnce lookups side by side
+      int pg[kAtOnce], to[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) pg[u] = j0 + 32 * u < end ? row[j0 + 32 * u] : -1;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const bool moved = fits && j0 + 32 * u < pages && pg[u] >= live && pg[u] < p.num_pages;
+        to[u] = moved ? below(pg[u]) - stay : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) to[u] = to[u] >= 0 ? p.copy_dst[to[u]] : -1;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        if (to[u] >= 0) out[j0 + 32 * u] = to[u];
+        else if (apart && j0 + 32 * u < end) out[j0 + 32 * u] = pg[u];
+      }
     }
   }
   report(p, err);
@@ -425,36 +456,39 @@ __global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(int num_pages, 
 }
 
 // ---- launches ----------------------------------------------------------------------------
-// One CTA where the rows have few entries and the pages a small bitmap, else a cluster of eight.
-static int ops_ctas(int64_t entries, int num_pages) {
-  return entries <= 4096 && num_pages <= 65536 ? 1 : kOpsCluster;
-}
-
-template <typename... A>
-static cudaError_t run_op(void (*kernel)(A...), size_t smem, size_t most, int ctas, cudaStream_t s,
-                          A... args) {
-  if (smem > 40 * 1024) {                  // the largest call's, whatever this one's (pages.cu)
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(most));
-    if (e != cudaSuccess) return e;
-  }
-  return launch_kv4(kernel, dim3(static_cast<unsigned>(ctas)), kOpsThreads, smem, ctas, s, args...);
+// One CTA where the rows have few entries and the pages a small bitmap, else a wide cluster.  smem(ctas):
+// what the call takes, most: what the largest does.
+template <typename S, typename... P, typename... A>
+static cudaError_t run_op(void (*kernel)(P...), WideKernel which, int64_t entries, int num_pages, S &&smem,
+                          size_t most, cudaStream_t s, A &&...args_of) {
+  int ctas = 1;
+  cudaError_t e = cudaSuccess;
+  if (entries > 4096 || num_pages > 65536)
+    e = wide_cluster(which, reinterpret_cast<const void *>(kernel), kOpsThreads, most, &ctas);
+  else if (smem(1) > 40 * 1024)            // the limit is the kernel's (pages.cu)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+  if (e != cudaSuccess) return e;
+  return launch_kv4(kernel, dim3(static_cast<unsigned>(ctas)), kOpsThreads, smem(ctas), ctas, s, args_of(ctas)...);
 }
 
 cudaError_t launch_page_op(PageOp op, const PageOpsParams &p, cudaStream_t s) {
-  constexpr size_t kRows = kMaxPlanSeqs, kWords = kMaxOpsPages / 32 / kOpsCluster;
-  if (op == PageOp::kFork) {
-    const int ctas = ops_ctas((int64_t)p.count * p.width, 0);
-    const size_t smem = 4 * (p.num_seqs + 2 * (size_t)p.count + (p.num_seqs + 31) / 32);
-    return run_op(page_fork_kernel, smem, 4 * (3 * kRows + kRows / 32), ctas, s, p);
+  // of the largest calls, with a cluster of eight
+  constexpr size_t kRows = kMaxPlanSeqs, kWords = kMaxOpsPages / 32 / 8 + 1;
+  auto same = [&](int) { return p; };
+  auto words = [&](int ctas) { return (p.num_pages / 32 + ctas) / ctas; };   // a word past the last page, too
+  switch (op) {
+    case PageOp::kFork:
+      return run_op(page_fork_kernel, kWideFork, (int64_t)p.count * p.width, 0,
+                    [&](int) { return 4 * (p.num_seqs + 2 * (size_t)p.count + (p.num_seqs + 31) / 32); },
+                    4 * (3 * kRows + kRows / 32), s, same);
+    case PageOp::kFree:
+      return run_op(page_free_kernel, kWideFree, (int64_t)p.count * p.width, p.num_pages,
+                    [&](int ctas) { return 8 * (size_t)words(ctas) + 4 * (size_t)p.num_seqs; },
+                    8 * kWords + 4 * kRows, s, same, words);
+    default:
+      return run_op(page_compact_kernel, kWideCompact, (int64_t)p.num_seqs * p.width, p.num_pages,
+                    [&](int ctas) { return 8 * (size_t)words(ctas); }, 8 * kWords, s, same, words);
   }
-  const bool free = op == PageOp::kFree;
-  const int ctas = ops_ctas((int64_t)(free ? p.count : p.num_seqs) * p.width, p.num_pages);
-  const int words = (p.num_pages / 32 + ctas) / ctas;   // a word past the last page, too
-  const size_t most = 8 * (kWords + 1);
-  if (!free) return run_op(page_compact_kernel, 8 * (size_t)words, most, ctas, s, p, words);
-  return run_op(page_free_kernel, 8 * (size_t)words + 4 * (size_t)p.num_seqs, most + 4 * kRows, ctas, s,
-                p, words);
 }
 
 cudaError_t launch_page_copy(int num_pages, int64_t page_bytes, int n, void *pool, const int32_t *src,

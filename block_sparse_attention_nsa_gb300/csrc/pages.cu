@@ -11,16 +11,17 @@
 // A few bytes per request and slot: what counts is latency.  One launch: every CTA scans
 // all requests for itself (offsets kept in shared memory, so that a slot's request is
 // found there by bisection) and fills its share of the slots.  Up to 4096 slots one CTA
-// does it all; above, a cluster of eight shares the slots (64 decode steps 4.4 us, 1000 mixed
+// does it all; above, a cluster of sixteen shares the slots (64 decode steps 4.4 us, 1000 mixed
 // requests with 42K slots 7.1 us in a CUDA graph, launch included).  The outputs that may be the
 // inputs' own arrays (seq_lens = ctx_lens, head_out = free_head) are written by the first
 // CTA behind a cluster barrier that every CTA reaches after its last read of them.
+#include <atomic>
+
 #include "kv4.cuh"
 
 namespace nsa {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCluster = 8;
 constexpr int kPlanOneCta = 4096;   // slots up to which one CTA fills the map
 
 __device__ __forceinline__ int64_t warp_incl(int64_t x, int lane) {
@@ -157,19 +158,51 @@ __global__ void __launch_bounds__(kPlanThreads) page_kernel(PageParams p) {
   }
 }
 
+cudaError_t wide_cluster(WideKernel which, const void *kernel, int threads, size_t smem, int *ctas) {
+  static std::atomic<int> known[kWideKernels][64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  const bool keep = dev >= 0 && dev < 64;
+  *ctas = keep ? known[which][dev].load(std::memory_order_relaxed) : 0;
+  if (*ctas) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kWideCluster);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = kWideCluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();                    // none, then
+    clusters = 0;
+  }
+  *ctas = clusters > 0 ? kWideCluster : 8;
+  if (keep) known[which][dev].store(*ctas, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s) {
   auto *kernel = plan ? page_kernel<true> : page_kernel<false>;
   const size_t smem = (3 * static_cast<size_t>(p.num_seqs) + 1) * sizeof(int32_t);
-  if (smem > 40 * 1024) {
+  constexpr size_t kMost = (3 * static_cast<size_t>(kMaxPlanSeqs) + 1) * sizeof(int32_t);
+  int ctas = 1;
+  cudaError_t e = cudaSuccess;
+  if (p.max_slots > kPlanOneCta) {
+    e = wide_cluster(plan ? kWidePlan : kWideSlots, reinterpret_cast<const void *>(kernel), kPlanThreads,
+                     kMost, &ctas);
+  } else if (smem > 40 * 1024) {
     // the largest plan's, whatever this one's: the limit is the kernel's, and another host thread may
     // be between its own and its launch
-    constexpr int kMost = (3 * kMaxPlanSeqs + 1) * static_cast<int>(sizeof(int32_t));
-    cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
   }
-  const bool one = p.max_slots <= kPlanOneCta;
-  const int ctas = one ? 1 : kPlanCluster;
+  if (e != cudaSuccess) return e;
   return launch_kv4(kernel, dim3(ctas), kPlanThreads, smem, ctas, s, p);
 }
 
