@@ -219,39 +219,40 @@ bool apart(int64_t n, int64_t ts, int64_t h, int64_t hs, int64_t d) {
   return n1 <= 1 || s1 >= span;
 }
 
-nsa_status tensor(const nsa_rope_dims *d, int heads, const nsa_rope_in *in, const nsa_rope_out *out,
-                  RopeTensor &x, bool &copy) {
+struct RopeArg {
+  const void *data;
+  int64_t ts, hs;
+};
+
+nsa_status tensor(const nsa_rope_dims *d, int heads, const RopeArg &in, const RopeArg &out, RopeTensor &x,
+                  bool &copy) {
   std::memset(&x, 0, sizeof(x));
   copy = false;
   if (heads == 0) return NSA_OK;
-  if (!in || !out) return NSA_ERR_INVALID_ARG;
-  if (!in->data || !out->data) return NSA_ERR_INVALID_ARG;
-  const int64_t strides[4] = {in->token_stride, in->head_stride, out->token_stride, out->head_stride};
-  for (int64_t v : strides) {
+  if (!in.data || !out.data) return NSA_ERR_INVALID_ARG;
+  for (int64_t v : {in.ts, in.hs, out.ts, out.hs}) {
     if (v % 8) return NSA_ERR_INVALID_ARG;
     if (v <= -(int64_t(1) << 40) || v >= (int64_t(1) << 40)) return NSA_ERR_UNSUPPORTED;
   }
-  if (!on(in->data, 16) || !on(out->data, 16)) return NSA_ERR_INVALID_ARG;
-  if (!apart(d->num_tokens, out->token_stride, heads, out->head_stride, d->head_dim))
+  if (!on(in.data, 16) || !on(out.data, 16)) return NSA_ERR_INVALID_ARG;
+  if (!apart(d->num_tokens, out.ts, heads, out.hs, d->head_dim)) return NSA_ERR_INVALID_ARG;
+  const bool same = in.data == out.data;
+  if (same && ((d->num_tokens > 1 && in.ts != out.ts) || (heads > 1 && in.hs != out.hs)))
     return NSA_ERR_INVALID_ARG;
-  const bool same = in->data == out->data;
-  if (same && ((d->num_tokens > 1 && in->token_stride != out->token_stride) ||
-               (heads > 1 && in->head_stride != out->head_stride)))
-    return NSA_ERR_INVALID_ARG;
-  x.in = static_cast<const uint16_t *>(in->data);
-  x.out = static_cast<uint16_t *>(out->data);
-  x.its = in->token_stride;
-  x.ihs = in->head_stride;
-  x.ots = out->token_stride;
-  x.ohs = out->head_stride;
+  x.in = static_cast<const uint16_t *>(in.data);
+  x.out = static_cast<uint16_t *>(const_cast<void *>(out.data));
+  x.its = in.ts;
+  x.ihs = in.hs;
+  x.ots = out.ts;
+  x.ohs = out.hs;
   copy = !same && d->rot_dim < d->head_dim;
   return NSA_OK;
 }
 
-nsa_status run_rope(const nsa_rope_dims *dims, const nsa_rope_in *q, const nsa_rope_in *k,
-                    const uint64_t *freqs, const int32_t *positions, const int32_t *cu,
-                    const int32_t *start, float mscale, float sign, const nsa_rope_out *q_out,
-                    const nsa_rope_out *k_out, int32_t *status, nsa_stream_t stream) {
+nsa_status run_rope(const nsa_rope_dims *dims, const RopeArg &q, const RopeArg &k, const uint64_t *freqs,
+                    const int32_t *positions, const int32_t *cu, const int32_t *start, float mscale,
+                    float sign, const RopeArg &q_out, const RopeArg &k_out, int32_t *status,
+                    nsa_stream_t stream) {
   if (!dims) return NSA_ERR_INVALID_ARG;
   const nsa_rope_dims d = *dims;
   if (d.num_tokens < 0 || d.h_q < 0 || d.h_k < 0 || d.h_q + (int64_t)d.h_k < 1 || d.head_dim < 1 ||
@@ -329,21 +330,30 @@ nsa_status nsa_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double 
   return NSA_OK;
 }
 
-nsa_status nsa_rope(const nsa_rope_dims *dims, const nsa_rope_in *q, const nsa_rope_in *k,
-                    const uint64_t *freqs, const int32_t *positions, const int32_t *cu_seqlens,
-                    const int32_t *start, float mscale, const nsa_rope_out *q_out,
-                    const nsa_rope_out *k_out, int32_t *device_status, nsa_stream_t stream) {
-  return run_rope(dims, q, k, freqs, positions, cu_seqlens, start, mscale, 1.f, q_out, k_out,
-                  device_status, stream);
+nsa_status nsa_rope(const nsa_rope_dims *dims, const void *q, int64_t q_token_stride,
+                    int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                    int64_t k_head_stride, const uint64_t *freqs, const int32_t *positions,
+                    const int32_t *cu_seqlens, const int32_t *start, float mscale, void *q_out,
+                    int64_t q_out_token_stride, int64_t q_out_head_stride, void *k_out,
+                    int64_t k_out_token_stride, int64_t k_out_head_stride, int32_t *device_status,
+                    nsa_stream_t stream) {
+  return run_rope(dims, {q, q_token_stride, q_head_stride}, {k, k_token_stride, k_head_stride}, freqs,
+                  positions, cu_seqlens, start, mscale, 1.f,
+                  {q_out, q_out_token_stride, q_out_head_stride},
+                  {k_out, k_out_token_stride, k_out_head_stride}, device_status, stream);
 }
 
-nsa_status nsa_rope_bwd(const nsa_rope_dims *dims, const nsa_rope_in *dq_out,
-                        const nsa_rope_in *dk_out, const uint64_t *freqs, const int32_t *positions,
-                        const int32_t *cu_seqlens, const int32_t *start, float mscale,
-                        const nsa_rope_out *dq, const nsa_rope_out *dk, int32_t *device_status,
+nsa_status nsa_rope_bwd(const nsa_rope_dims *dims, const void *dq_out, int64_t dq_out_token_stride,
+                        int64_t dq_out_head_stride, const void *dk_out, int64_t dk_out_token_stride,
+                        int64_t dk_out_head_stride, const uint64_t *freqs, const int32_t *positions,
+                        const int32_t *cu_seqlens, const int32_t *start, float mscale, void *dq,
+                        int64_t dq_token_stride, int64_t dq_head_stride, void *dk,
+                        int64_t dk_token_stride, int64_t dk_head_stride, int32_t *device_status,
                         nsa_stream_t stream) {
-  return run_rope(dims, dq_out, dk_out, freqs, positions, cu_seqlens, start, mscale, -1.f, dq, dk,
-                  device_status, stream);
+  return run_rope(dims, {dq_out, dq_out_token_stride, dq_out_head_stride},
+                  {dk_out, dk_out_token_stride, dk_out_head_stride}, freqs, positions, cu_seqlens, start,
+                  mscale, -1.f, {dq, dq_token_stride, dq_head_stride},
+                  {dk, dk_token_stride, dk_head_stride}, device_status, stream);
 }
 
 }  // extern "C"

@@ -86,9 +86,9 @@ def _kv4_dims(*sizes):
     return Kv4Dims(*_held(sizes, "kv4 dims"))
 
 
-_current_device = torch.cuda.current_device
-# The current stream's handle without a Stream object around it; builds of
-# torch without CUDA do not have this name.
+# The current device's index and stream handle without what torch.cuda puts around them (a tensor on a
+# CUDA device has set CUDA up); builds of torch without CUDA do not have these names.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 

@@ -24,16 +24,11 @@ class RopeDims(ctypes.Structure):
                                               "interleaved", "num_seqs", "dtype")]
 
 
-class RopeTensor(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
-                ("head_stride", ctypes.c_int64)]
-
-
 def signatures():
     """ctypes result and argument types of the library's functions."""
     vp, i32, f64, st = ctypes.c_void_p, ctypes.c_int32, ctypes.c_double, ctypes.c_int
-    rt = ctypes.POINTER(RopeTensor)
-    call = (st, [ctypes.POINTER(RopeDims), rt, rt, vp, vp, vp, vp, ctypes.c_float, rt, rt, vp, vp])
+    rt = [vp, ctypes.c_int64, ctypes.c_int64]
+    call = (st, [ctypes.POINTER(RopeDims), *rt, *rt, vp, vp, vp, vp, ctypes.c_float, *rt, *rt, vp, vp])
     return {
         "nsa_rope_freqs": (st, [i32, f64, i32, f64, f64, f64, f64, vp]),
         "nsa_rope": call,
@@ -64,15 +59,18 @@ def _rope_dims(*sizes):
     return RopeDims(*_held(sizes, "rope dims"))
 
 
-def _tensor(name, t, shape, dtype, dev):
-    """t [N, heads, d] as strides and a pointer; its last dimension has to be contiguous."""
-    strides = t.stride()
-    if (t.shape != shape or t.dtype is not dtype or t.get_device() != dev
-            or (strides[2] != 1 and shape[2] != 1)):
-        raise ValueError(f"{name}: a {dtype} tensor {tuple(shape)} on device {dev} with a contiguous "
-                         f"last dimension expected, got {t.dtype} {tuple(t.shape)}, strides "
-                         f"{strides}, on {t.device}")
-    return RopeTensor(t.data_ptr(), strides[0], strides[1])
+def _tensor(name, t, n, heads, d, dtype, dev):
+    """Pointer and strides of t [n, heads, d], whose last dimension has to be contiguous."""
+    shape, strides = t.shape, t.stride()
+    if (len(shape) != 3 or shape[0] != n or shape[1] != heads or shape[2] != d or strides[2] != 1
+            or t.dtype is not dtype or t.get_device() != dev):
+        raise ValueError(f"{name}: a {dtype} tensor {(n, heads, d)} on device {dev} with a contiguous last "
+                         f"dimension expected, got {t.dtype} {tuple(shape)}, strides {strides}, on {t.device}")
+    return t.data_ptr(), strides[0], strides[1]
+
+
+_NONE = (None, 0, 0)
+_i64 = torch.int64
 
 
 def _run(where, call, q, k, freqs, positions, cu_seqlens, start, interleaved, mscale, q_out, k_out,
@@ -80,48 +78,43 @@ def _run(where, call, q, k, freqs, positions, cu_seqlens, start, interleaved, ms
     first = k if q is None else q
     if first is None:
         raise ValueError("q or k expected")
-    shape, dtype = first.shape, first.dtype
-    if len(shape) != 3:
+    if first.dim() != 3:
         raise ValueError("q and k [N, heads, d] expected")
-    dev = _device(first)
-    n, _, d = shape
+    n, h, d = first.shape
+    dtype, dev = first.dtype, _device(first)
     code = _DTYPES.get(dtype)
     if code is None:
         _fail(2, f"{where}: dtype {dtype}")
-    heads, ins, outs = [], [], []
-    new = []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            if y is not None:
-                raise ValueError(f"{name}: an output without its input")
-            heads.append(0)
-            ins.append(None)
-            outs.append(None)
-            new.append(None)
-            continue
-        if x.dim() != 3:
-            raise ValueError("q and k [N, heads, d] expected")
-        h = x.shape[1]
-        want = (n, h, d)
-        heads.append(h)
-        ins.append(_tensor(name, x, want, dtype, dev))
-        if y is None:
-            y = _empty(want, dtype, dev, stream)
-        outs.append(_tensor(f"{name}'s output", y, want, dtype, dev))
-        new.append(y)
-    pairs = freqs.numel()
-    if (freqs.dtype is not torch.int64 or freqs.get_device() != dev or not freqs.is_contiguous()
-            or freqs.dim() != 1):
+    h_q = h_k = 0
+    q_in = k_in = q_to = k_to = _NONE
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q: an output without its input")
+    else:
+        h_q = h
+        q_in = _tensor("q", q, n, h_q, d, dtype, dev)
+        if q_out is None:
+            q_out = _empty((n, h_q, d), dtype, dev, stream)
+        q_to = _tensor("q's output", q_out, n, h_q, d, dtype, dev)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k: an output without its input")
+    else:
+        h_k = k.shape[1] if k.dim() == 3 else -1
+        k_in = _tensor("k", k, n, h_k, d, dtype, dev)
+        if k_out is None:
+            k_out = _empty((n, h_k, d), dtype, dev, stream)
+        k_to = _tensor("k's output", k_out, n, h_k, d, dtype, dev)
+    if (freqs.dtype is not _i64 or freqs.dim() != 1 or freqs.get_device() != dev
+            or not freqs.is_contiguous()):
         raise ValueError("freqs: the int64 tensor that rope_freqs makes expected, on the tensors' device")
     seqs, pos, cu, at = 0, None, None, None
-    if (positions is None) == (cu_seqlens is None):
-        raise ValueError("either positions or cu_seqlens expected")
     if positions is not None:
-        if start is not None:
-            raise ValueError("start goes with cu_seqlens")
+        if cu_seqlens is not None or start is not None:
+            raise ValueError("either positions, or cu_seqlens and start")
         _ints("positions", positions, n, dev)
         pos = positions.data_ptr()
-    else:
+    elif cu_seqlens is not None:
         seqs = cu_seqlens.numel() - 1
         if seqs < 1:
             raise ValueError("cu_seqlens: at least two entries expected")
@@ -130,13 +123,15 @@ def _run(where, call, q, k, freqs, positions, cu_seqlens, start, interleaved, ms
         if start is not None:
             _ints("start", start, seqs, dev)
             at = start.data_ptr()
-    status = getattr(_lib(), call)(
-        _rope_dims(n, heads[0], heads[1], d, 2 * pairs, 1 if interleaved else 0, seqs, code), ins[0],
-        ins[1], freqs.data_ptr(), pos, cu, at, mscale, outs[0], outs[1],
+    else:
+        raise ValueError("positions or cu_seqlens expected")
+    status = call(
+        _rope_dims(n, h_q, h_k, d, 2 * freqs.numel(), 1 if interleaved else 0, seqs, code), *q_in, *k_in,
+        freqs.data_ptr(), pos, cu, at, mscale, *q_to, *k_to,
         None if device_status is None else _status(device_status, dev), _raw(stream, dev))
     if status:
         _fail(status, where)
-    return new[0], new[1]
+    return q_out, k_out
 
 
 def rope(q, k, freqs, positions=None, cu_seqlens=None, start=None, interleaved: bool = False,
@@ -147,7 +142,7 @@ def rope(q, k, freqs, positions=None, cu_seqlens=None, start=None, interleaved: 
     Positions: int32 [N], or those of a packed batch by cu_seqlens int32 [S + 1], counted from
     start int32 [S] (None: 0) in each sequence; rows behind the last sequence are left as they are.
     q_out and k_out may be q and k.  Returns q_out, k_out."""
-    return _run("rope", "nsa_rope", q, k, freqs, positions, cu_seqlens, start, interleaved, mscale,
+    return _run("rope", _lib().nsa_rope, q, k, freqs, positions, cu_seqlens, start, interleaved, mscale,
                 q_out, k_out, device_status, stream)
 
 
@@ -156,5 +151,5 @@ def rope_bwd(dq_out, dk_out, freqs, positions=None, cu_seqlens=None, start=None,
              device_status=None, stream=None):
     """The gradients of rope's q and k from those of its outputs (dq_in and dk_in may be dq_out and
     dk_out).  Returns dq_in, dk_in."""
-    return _run("rope_bwd", "nsa_rope_bwd", dq_out, dk_out, freqs, positions, cu_seqlens, start,
+    return _run("rope_bwd", _lib().nsa_rope_bwd, dq_out, dk_out, freqs, positions, cu_seqlens, start,
                 interleaved, mscale, dq_in, dk_in, device_status, stream)

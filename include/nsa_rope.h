@@ -51,18 +51,9 @@ typedef struct {
     int32_t dtype;       /* nsa_dtype of q, k and the outputs */
 } nsa_rope_dims;
 
-/* A tensor [N, heads, head_dim]: strides in elements, the last dimension contiguous.  The pointer
- * is 16-byte aligned and the strides are multiples of 8. */
-typedef struct {
-    const void *data;
-    int64_t token_stride, head_stride;
-} nsa_rope_in;
-typedef struct {
-    void *data;
-    int64_t token_stride, head_stride;
-} nsa_rope_out;
-
-/* q and k to q_out and k_out.  An output may be its own input (the same pointer and strides); apart
+/* q and k to q_out and k_out: [N, heads, head_dim] each, with a stride in elements from token to token
+ * and one from head to head (multiples of 8), the last dimension contiguous, the pointer 16-byte
+ * aligned.  An output may be its own input (the same pointer and strides); apart
  * from that outputs overlap neither inputs nor each other, nor do an output's own rows.
  * Positions: positions[t], int32 [N] (negative ones turn backwards); or, where it is NULL, those
  * of a packed batch: cu_seqlens int32 [num_seqs + 1], token t of sequence s has position
@@ -71,19 +62,24 @@ typedef struct {
  * sequence, which sets NSA_DEVERR_BAD_SEQLENS in *device_status (may be NULL).
  * freqs: uint64 [rot_dim / 2], as nsa_rope_freqs makes them, 8-byte aligned.  mscale is finite.
  * num_tokens * (h_q + h_k) has to stay below 2^31. */
-NSA_API nsa_status nsa_rope(const nsa_rope_dims *dims, const nsa_rope_in *q, const nsa_rope_in *k,
-                            const uint64_t *freqs, const int32_t *positions,
+NSA_API nsa_status nsa_rope(const nsa_rope_dims *dims, const void *q, int64_t q_token_stride,
+                            int64_t q_head_stride, const void *k, int64_t k_token_stride,
+                            int64_t k_head_stride, const uint64_t *freqs, const int32_t *positions,
                             const int32_t *cu_seqlens, const int32_t *start, float mscale,
-                            const nsa_rope_out *q_out, const nsa_rope_out *k_out,
+                            void *q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                            void *k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
                             int32_t *device_status, nsa_stream_t stream);
 
 /* The gradient: from the gradients of q_out and k_out to those of q and k, the same rules. */
-NSA_API nsa_status nsa_rope_bwd(const nsa_rope_dims *dims, const nsa_rope_in *dq_out,
-                                const nsa_rope_in *dk_out, const uint64_t *freqs,
+NSA_API nsa_status nsa_rope_bwd(const nsa_rope_dims *dims, const void *dq_out,
+                                int64_t dq_out_token_stride, int64_t dq_out_head_stride,
+                                const void *dk_out, int64_t dk_out_token_stride,
+                                int64_t dk_out_head_stride, const uint64_t *freqs,
                                 const int32_t *positions, const int32_t *cu_seqlens,
-                                const int32_t *start, float mscale, const nsa_rope_out *dq,
-                                const nsa_rope_out *dk, int32_t *device_status,
-                                nsa_stream_t stream);
+                                const int32_t *start, float mscale, void *dq,
+                                int64_t dq_token_stride, int64_t dq_head_stride, void *dk,
+                                int64_t dk_token_stride, int64_t dk_head_stride,
+                                int32_t *device_status, nsa_stream_t stream);
 
 #ifdef __cplusplus
 }

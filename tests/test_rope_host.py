@@ -58,22 +58,20 @@ def test_freqs_refusals(lib):
 
 
 def test_refusals(lib):
-    from block_sparse_attention_nsa_gb300.rope import RopeDims, RopeTensor
+    from block_sparse_attention_nsa_gb300.rope import RopeDims
     base = dict(num_tokens=4, h_q=4, h_k=2, head_dim=128, rot_dim=64, interleaved=0, num_seqs=0,
                 dtype=0)
     def call(q=(FAKE, 512, 128), k=(FAKE, 256, 128), qo=(2 * FAKE, 512, 128), ko=(3 * FAKE, 256, 128),
              freqs=FAKE, pos=FAKE, cu=None, start=None, mscale=1.0, status=None, bwd=False, **kw):
-        t = [None if x is None else RopeTensor(*x) for x in (q, k, qo, ko)]
         f = lib.nsa_rope_bwd if bwd else lib.nsa_rope
-        return f(RopeDims(**{**base, **kw}), t[0], t[1], freqs, pos, cu, start, mscale, t[2], t[3],
-                 status, None)
+        return f(RopeDims(**{**base, **kw}), *q, *k, freqs, pos, cu, start, mscale, *qo, *ko, status, None)
     inf = float("inf")
     for bwd in (False, True):
         for kw in (dict(num_tokens=-1), dict(h_q=-1), dict(h_q=0, h_k=0), dict(rot_dim=0),
                    dict(rot_dim=144), dict(interleaved=2), dict(mscale=inf), dict(freqs=None),
                    dict(pos=None), dict(cu=FAKE), dict(num_seqs=1), dict(start=FAKE),
                    dict(pos=None, cu=FAKE), dict(freqs=FAKE + 4), dict(pos=FAKE + 2),
-                   dict(status=FAKE + 1), dict(q=None), dict(ko=None), dict(q=(None, 512, 128)),
+                   dict(status=FAKE + 1), dict(ko=(None, 256, 128)), dict(q=(None, 512, 128)),
                    dict(q=(FAKE + 8, 512, 128)), dict(k=(FAKE, 260, 128)), dict(k=(FAKE, 256, 4)),
                    dict(qo=(2 * FAKE + 2, 512, 128)),
                    # an output's rows overlap
@@ -88,7 +86,7 @@ def test_refusals(lib):
             assert call(bwd=bwd, **kw) == 2, kw
         # no rows: nothing to do, whatever the pointers
         assert call(bwd=bwd, num_tokens=0) == 0
-        assert call(bwd=bwd, num_tokens=0, h_k=0, k=None, ko=None) == 0
+        assert call(bwd=bwd, num_tokens=0, h_k=0, k=(None, 0, 0), ko=(None, 0, 0)) == 0
 
 
 def test_python_refusals(lib):
