@@ -28,16 +28,30 @@
 //   loader       a block's record tiles by bulk copies into a ring, page by page of the table;
 //   8 unpackers  codes, scales and zeros to the K and V operands (128-byte swizzle; the eight
 //                dimensions of a word stay in the order 0 4 1 5 2 6 3 7 that masking gives, on both
-//                sides of the product and until the output is written);
-//   MMA thread   S = Q K^T of block n + 1 into one of two score buffers, then O += W V of block n.  Q
+//                sides of the product and until the output is written).  Where there is room for two
+//                blocks' V, half the warps take every second block: a warp waits on the latency of
+//                what it does, and has half the barriers a block (181 us to 169, 256 behind 32K);
+//   MMA warp     S = Q K^T of block n + 1 into one of two score buffers, then O += W V of block n.  Q
 //                and W come from tensor memory, so that only K and V are read from shared memory.
-//                Steps of N = 128 in one chain take about 70 cycles each, half of that a key what
-//                steps of 64 do, and only one output fits beside two buffers of 128 scores;
+//                A step of N = 128 takes the tensor core 64 cycles (one of 64 takes 48, and only one
+//                output fits beside two buffers of 128 scores); the 25 of a block took one thread
+//                2800 cycles to issue, its operands moved to uniform registers each time, on a
+//                scheduler that it shares with four other warps.  So the whole warp runs the loop with
+//                operands the same in all lanes, and one lane issues: 212 us to 181;
 //   2 x 4 softmax warps   a thread a row and half of a block's keys.  Both halves share the output
 //                and so the reference m: one barrier a block tells them whether any row raises it.
 //                W goes to tensor memory over the scores it came from.
-// Work: the line of all (tile, block) pairs, tile after tile, in equal runs, one a CTA; where a tile
-// is shared by CTAs each leaves partial rows.  kv4_join_kernel adds them and the own part.
+// Two CTAs as a pair (D = 128, more than 128 rows a group on average): M = 256, a CTA's softmax on 128
+// of the rows, and each unpacks half of a block's K and one group of V's dimensions, which the tensor
+// cores of both read.  The CTA of rank 0 issues for both; arrivals on what it waits for go to its
+// barriers, commits to both CTAs'.  (Those arrivals need no release at the cluster's scope: what they
+// report is shared memory behind a proxy fence, or tensor memory behind a wait, of the CTA's own; with
+// it an arrival took 900 cycles.)  At D = 64 half of V's dimensions would be half a swizzle row.
+// A block takes about 2300 cycles in a pair and 3350 alone, against 1600 of the tensor core's.  Alone
+// the unpackers are the longest; in a pair no role is busy all the time, each waits on the others'
+// latencies.
+// Work: the line of all (tile, block) pairs, tile after tile, in equal runs, one a CTA or pair; where a
+// tile is shared by runs each leaves partial rows.  kv4_join_kernel adds them and the own part.
 #include <cmath>
 #include <type_traits>
 #include <utility>
@@ -49,9 +63,6 @@ namespace nsa {
 constexpr int kShRows = 128;         // query rows of a tile
 constexpr int kShKeys = 128;         // keys of a block
 constexpr int kShTiles = kShKeys / kKv4Tile;
-// Blocks copied, and unpacked, ahead: K's for the next product beside those in use; V's follow the
-// product that frees their place.
-constexpr int kShRaw = 2, kShK = 2;
 constexpr int kShThreads = 640;
 constexpr int kShMaxCtas = 256;
 constexpr int kShOver = 2;           // blocks that a tile's start and end count as
@@ -67,7 +78,7 @@ struct ShGroup {
   __device__ __forceinline__ int counted() const { return blocks + kShOver; }
 };
 struct ShHead {
-  int32_t groups, pairs, per, pad;   // counted blocks; of them a CTA's
+  int32_t groups, pairs, per, rows_log2;   // counted blocks; of them a CTA's (a pair's); rows of a tile
 };
 struct ShPlan {
   ShHead *head;
@@ -131,11 +142,13 @@ __device__ __forceinline__ int setup_incl(int x, int (&part)[32], int &total) {
 }
 
 // Shared or not?  In units of 25 ns of an SM's time: a tile of 128 rows takes about 240 and 72 a block
-// of 128 keys; the sequences' own passes over the prefix take 5 a tile of 32 keys each.
-__device__ __forceinline__ bool worth_sharing(int n, int g, int keys) {
+// of 128 keys, one of 256 rows, of a pair, twice 240 and 50; the sequences' own passes over the prefix
+// take 5 a tile of 32 keys each.
+__device__ __forceinline__ bool worth_sharing(int n, int g, int keys, int rows_log2) {
   const int64_t own = (int64_t)n * (g > kK4Heads ? 2 : 1) * ((keys + 31) / 32) * 5;
-  const int64_t tiles = ((int64_t)n * g + kShRows - 1) / kShRows;
-  return n > 1 && own > tiles * (240 + 72 * (int64_t)((keys + kShKeys - 1) / kShKeys));
+  const int64_t tiles = ((int64_t)n * g + (1 << rows_log2) - 1) >> rows_log2;
+  const int64_t blocks = (keys + kShKeys - 1) / kShKeys;
+  return n > 1 && own > tiles * ((1 << rows_log2) == kShRows ? 240 + 72 * blocks : 480 + 100 * blocks);
 }
 
 // By a CTA of kThreads: groups that share, in order, with what lies before each, into `groups`, and of
@@ -143,7 +156,7 @@ __device__ __forceinline__ bool worth_sharing(int n, int g, int keys) {
 // shares nothing.  Returns the head (per: CTAs have equal runs, of a block at least).
 template <int kThreads>
 __device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *groups, int32_t *at, int ctas,
-                                            int (&part)[32], int32_t &err) {
+                                            int rows_log2, int (&part)[32], int32_t &err) {
   constexpr int kWarps = kThreads / 32;
   const int cap = p.dec.width << p.dec.page_log2;
   bool bad = false;
@@ -166,8 +179,8 @@ __device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *g
         keys = 0;
       }
     }
-    const bool shares = keys > 0 && worth_sharing(n, p.dec.g, keys);
-    const int r = shares ? n * p.dec.g : 0, tiles = (r + kShRows - 1) / kShRows;
+    const bool shares = keys > 0 && worth_sharing(n, p.dec.g, keys, rows_log2);
+    const int r = shares ? n * p.dec.g : 0, tiles = (r + (1 << rows_log2) - 1) >> rows_log2;
     const int blocks = (keys + kShKeys - 1) / kShKeys;
     int total;
     const int g = count + setup_incl<kWarps>(shares, part, total) - shares;
@@ -182,7 +195,7 @@ __device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *g
     if (shares) groups[g] = ShGroup{a, r, blocks, tiles, keys, before, row, 0};
   }
   __syncthreads();
-  return ShHead{count, pairs, max((pairs + ctas - 1) / ctas, kShOver + 1), 0};
+  return ShHead{count, pairs, max((pairs + ctas - 1) / ctas, kShOver + 1), rows_log2};
 }
 
 // Sequence b's group among those that share, and its first own key.  One that ends inside the prefix
@@ -203,11 +216,12 @@ __device__ __forceinline__ void place_sequence(const Kv4SharedParams &p, const S
 }
 
 // For more groups than the prefix kernel's CTAs plan themselves.
-__global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParams p, ShPlan plan, int ctas) {
+__global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParams p, ShPlan plan, int ctas,
+                                                                int rows_log2) {
   __shared__ int part[32];
   after_previous();
   int32_t err = 0;
-  const ShHead head = make_plan<kSetupThreads>(p, plan.groups, plan.at, ctas, part, err);
+  const ShHead head = make_plan<kSetupThreads>(p, plan.groups, plan.at, ctas, rows_log2, part, err);
   if (__syncthreads_or(err) && threadIdx.x == 0) raise(p.dec.status, NSA_DEVERR_BAD_SEQLENS);
   if (threadIdx.x == 0) *plan.head = head;
   for (int b = threadIdx.x; b < p.dec.num_seqs; b += kSetupThreads)
@@ -215,19 +229,28 @@ __global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParam
 }
 
 // ---- prefix ----------------------------------------------------------------------------
-template <int D>
+template <int D, bool kPair>
 struct Sh {
   using T = Kv4Tile<D>;
   static constexpr int kG = T::kG;
-  static constexpr uint32_t kOperand = kShKeys * D * 2;        // V of a block, and each part of K
+  // Blocks copied ahead; K and V unpacked.  A set of unpackers uses stages of its own, phase by phase: a
+  // parity tells only the last two phases apart.
+  static constexpr int kSets = kPair || D == 64 ? 2 : 1;       // of unpackers, which take blocks in turn
+  static constexpr int kUnpackers = 256 / kSets;
+  static constexpr int kRaw = kPair ? 4 : 2, kK = 2, kV = kSets;
+  static_assert(kRaw % kSets == 0 && kK % kSets == 0, "stages of its own");
+  static constexpr int kKeys = kPair ? kShKeys / 2 : kShKeys;  // of a block's K, a CTA's
+  static constexpr int kTiles = kKeys / kKv4Tile;
+  static constexpr uint32_t kPartK = kKeys * D * 2;            // each part of K
+  static constexpr uint32_t kPartV = kShKeys * (kPair ? D / 2 : D) * 2;
   // K or V of a block as it is stored: of each record tile the codes, then scales and zeros
   static constexpr uint32_t kHalfTile = T::kV + 2 * T::kArr, kRawBytes = kShTiles * kHalfTile;
   static constexpr uint32_t kOffK = 0;
-  static constexpr uint32_t kOffV = kOffK + kShK * 2 * kOperand;
-  static constexpr uint32_t kOffZ = kOffV + kOperand;          // 16 columns of z and s a stage of K
-  static constexpr uint32_t kOffRaw = kOffZ + kShKeys * 128;
-  static constexpr uint32_t kBytes = kOffRaw + 2 * kShRaw * kRawBytes + 1024;   // + alignment
-  static_assert(kShK <= 4, "a 128-byte row holds four stages' columns");
+  static constexpr uint32_t kOffV = kOffK + kK * 2 * kPartK;
+  static constexpr uint32_t kOffZ = kOffV + kV * kPartV;       // 16 columns of z and s a stage of K
+  static constexpr uint32_t kOffRaw = kOffZ + kKeys * 128;
+  static constexpr uint32_t kBytes = kOffRaw + 2 * kRaw * kRawBytes + 1024;   // + alignment
+  static_assert(kK <= 4, "a 128-byte row holds four stages' columns");
   static_assert(kOffV % 1024 == 0 && kOffZ % 1024 == 0 && kOffRaw % 1024 == 0, "operands' alignment");
   static_assert(kBytes <= 214 * 1024, "shared memory, with 13 KB of barriers and the plan");
   // columns of tensor memory: two blocks' scores, the output, Q, its sums
@@ -236,10 +259,11 @@ struct Sh {
   static_assert(kSums + 8 <= kCols, "tensor memory");
 };
 
+template <int kRaw, int kK, int kV>
 struct ShShared {
-  uint64_t raw_full[2][kShRaw], raw_empty[2][kShRaw], k_full[kShK], k_empty[kShK], v_full;   // raw: K's, V's
+  uint64_t raw_full[2][kRaw], raw_empty[2][kRaw], k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];   // raw: K's, V's
   uint64_t q_full, o_free, s_full[2], p_full[2], o_done;
-  uint32_t seen[2][kShRaw][kShTiles];          // a block's keys that exist, a bit each
+  uint32_t seen[2][kRaw][kShTiles];            // a block's keys that exist, a bit each
   float sums[2][kShRows];                      // of each half of a row: sums of q^; of weights
   float most[2][kShRows];                      // largest scores
   int top[2][kShRows];                         // largest magnitudes of q, as bits
@@ -255,6 +279,7 @@ struct ShSpan {
   int rows, part;                              // its rows, and where its partial rows lie
 };
 // Walks a CTA's run.
+template <int kRows>                            // of a tile
 struct ShWalk {
   const ShGroup *groups;
   ShGroup g;
@@ -286,8 +311,8 @@ struct ShWalk {
       if (s.end <= s.first) continue;
       s.h = tile / g.tiles;
       s.tile = tile - s.h * g.tiles;
-      s.rows = min(kShRows, g.rows - s.tile * kShRows);
-      s.part = cta * kShRows + g.row0 + s.h * g.rows + s.tile * kShRows;
+      s.rows = min(kRows, g.rows - s.tile * kRows);
+      s.part = cta * kRows + g.row0 + s.h * g.rows + s.tile * kRows;
       return true;
     }
     return false;
@@ -309,6 +334,18 @@ __device__ __forceinline__ bool sh_wait(uint64_t *bar, uint32_t parity, int32_t 
       return false;
     }
   }
+}
+
+// A warp arrives at the barrier of the CTA that issues the products, with what its threads did before.
+template <bool kPair>
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) != 0) return;
+  if constexpr (kPair)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_cta(smem_u32(bar), 0))
+                 : "memory");
+  else
+    mbar_arrive(bar);
 }
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -336,6 +373,28 @@ __device__ __forceinline__ bool any_of_256(int id, bool mine) {
       : "r"(mine ? 1u : 0u), "r"(id)
       : "memory");
   return any != 0;
+}
+
+// By a whole warp, with the same operands in all lanes, so that they stay in uniform registers; the one
+// with `one` issues.
+template <bool kPair>
+__device__ __forceinline__ void sh_mma(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add, uint32_t one) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(one)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(one)
+        : "memory");
 }
 
 // The codes of a word less `off`, as fp16: dimensions (0, 4), (1, 5), (2, 6), (3, 7).  A code in the
@@ -367,18 +426,18 @@ __device__ __forceinline__ __half2 upper(__half2 s) {
 // What the unpackers' thread t (of 256) brings of a block: in turn u 16 bytes, q of them, of the row of a
 // key, and that row's scales or zeros (0 for a key that is not there).  All of it is loaded before any
 // of it is worked on.
-template <int D>
+template <int D, int kKeys, int kThreads>       // keys of the block, or of a part of it
 struct ShPiece {
   using T = Kv4Tile<D>;
-  static constexpr int kG = T::kG, kChunks = T::kRow / 16, kTurns = kShKeys * kChunks / 256;
+  static constexpr int kG = T::kG, kChunks = T::kRow / 16, kTurns = kKeys * kChunks / kThreads;
   uint32_t w[kTurns][4];
   __half2 s[kTurns][kG], z[kTurns][kG];
-  __device__ __forceinline__ static int key(int u, int t) { return (u * 256 + t) / kChunks; }
+  __device__ __forceinline__ static int key(int u, int t) { return (u * kThreads + t) / kChunks; }
   __device__ __forceinline__ ShPiece(const uint8_t *raw, const uint32_t (&seen)[kShTiles], int t) {
 #pragma unroll
     for (int u = 0; u < kTurns; ++u) {
       const int k = key(u, t), row = k & 31, q = t % kChunks;
-      const uint8_t *tile = raw + (k >> 5) * Sh<D>::kHalfTile;
+      const uint8_t *tile = raw + (k >> 5) * Sh<D, false>::kHalfTile;
       const uint4 x = *reinterpret_cast<const uint4 *>(tile + row * T::kRow + q * 16);
       w[u][0] = x.x;
       w[u][1] = x.y;
@@ -396,10 +455,10 @@ struct ShPiece {
   // Word 4 q + i is group i % kG's, its dimensions' chunk there (4 / kG) q + i / kG: in an operand it lies
   // at (first(t) ^ flip(i)) + step(u, i), whatever the operand's start, a multiple of 1024.
   __device__ __forceinline__ static uint32_t first(int t) {
-    return sw128_offset(key(0, t), (4 / kG) * (t % kChunks), kShKeys);
+    return sw128_offset(key(0, t), (4 / kG) * (t % kChunks), kKeys);
   }
   static constexpr uint32_t flip(int i) { return static_cast<uint32_t>(i / kG) << 4; }
-  static constexpr int step(int u, int i) { return (i % kG) * kShKeys * 128 + u * (256 / kChunks) * 128; }
+  static constexpr int step(int u, int i) { return (i % kG) * kKeys * 128 + u * (kThreads / kChunks) * 128; }
 };
 
 // f(u, i) for all turns and words, with both known to the compiler.
@@ -408,10 +467,10 @@ __device__ __forceinline__ void each_word(F &&f, std::integer_sequence<int, kI..
   (f(std::integral_constant<int, kI / 4>{}, std::integral_constant<int, kI % 4>{}), ...);
 }
 
-template <int D>
+template <int D, int kKeys, int kThreads>
 __device__ __forceinline__ void unpack_k(const uint8_t *raw, const uint32_t (&seen)[kShTiles], uint32_t kdst,
                                          uint32_t zdst, int stage, int t, uint32_t first) {
-  using P = ShPiece<D>;
+  using P = ShPiece<D, kKeys, kThreads>;
   constexpr int G = P::kG;
   const P p(raw, seen, t);
   __half2 hi[P::kTurns][G], lo[P::kTurns][G];
@@ -432,7 +491,7 @@ __device__ __forceinline__ void unpack_k(const uint8_t *raw, const uint32_t (&se
     }
     const uint32_t a = (kdst + first) ^ P::flip(i);
     sts_halves<P::step(u, i)>(a, x);
-    sts_halves<P::step(u, i) + static_cast<int>(Sh<D>::kOperand)>(a, y);
+    sts_halves<P::step(u, i) + kKeys * D * 2>(a, y);
   }, std::make_integer_sequence<int, 4 * P::kTurns>{});
   // the first thread of a row: z z z s s s of each group; 0, or -inf: no key
   if (t % P::kChunks == 0) {
@@ -448,18 +507,45 @@ __device__ __forceinline__ void unpack_k(const uint8_t *raw, const uint32_t (&se
         v[3 * g + 2] = *reinterpret_cast<const uint32_t *>(&p.s[u][g]);
       }
       v[6] = seen[key >> 5] >> (key & 31) & 1 ? 0u : 0xfc00u;
-      sts128(zdst + sw128_offset(key, 2 * stage, kShKeys), make_uint4(v[0], v[1], v[2], v[3]));
-      sts128(zdst + sw128_offset(key, 2 * stage + 1, kShKeys), make_uint4(v[4], v[5], v[6], v[7]));
+      sts128(zdst + sw128_offset(key, 2 * stage, kKeys), make_uint4(v[0], v[1], v[2], v[3]));
+      sts128(zdst + sw128_offset(key, 2 * stage + 1, kKeys), make_uint4(v[4], v[5], v[6], v[7]));
     }
   }
 }
 
-template <int D>
+// kPair: group `rank` of the dimensions alone, every second word.
+template <int D, bool kPair, int kThreads>
 __device__ __forceinline__ void unpack_v(const uint8_t *raw, const uint32_t (&seen)[kShTiles], uint32_t vdst,
-                                         int t, uint32_t first) {
-  using P = ShPiece<D>;
+                                         int t, uint32_t first, int rank) {
+  using P = ShPiece<D, kShKeys, kThreads>;
   constexpr int G = P::kG;
   const P p(raw, seen, t);
+  if constexpr (kPair) {
+    static_assert(G == 2, "a CTA of a pair has a group of V's dimensions");
+    __half2 s[P::kTurns], z[P::kTurns];
+    bool big = false;
+#pragma unroll
+    for (int u = 0; u < P::kTurns; ++u) {
+      s[u] = rank ? p.s[u][G - 1] : p.s[u][0];
+      z[u] = rank ? p.z[u][G - 1] : p.z[u][0];
+      big |= !(fabsf(__low2float(z[u])) + 15.f * __low2float(s[u]) < 65504.f);
+    }
+    const bool any_big = __any_sync(0xffffffffu, big);
+    each_word([&](auto u, auto i) {
+      if constexpr (i % G == 0) {
+        __half2 c[4];
+        code_halves(rank ? p.w[u][i + 1] : p.w[u][i], 0.f, c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = __hfma2(c[k], s[u], z[u]);
+        if (any_big) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) c[k] = held(c[k]);
+        }
+        sts_halves<P::step(u, i)>((vdst + first) ^ P::flip(i), c);
+      }
+    }, std::make_integer_sequence<int, 4 * P::kTurns>{});
+    return;
+  }
   bool wide = false;
 #pragma unroll
   for (int u = 0; u < P::kTurns; ++u)
@@ -495,19 +581,22 @@ __device__ __forceinline__ void three_parts(float x, __half (&h)[3]) {
   }
 }
 
-template <int D, bool kFp16>
+template <int D, bool kFp16, bool kPair>
 __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_constant__ Kv4SharedParams sp_,
                                                                    ShPlan plan) {
-  using S = Sh<D>;
+  using S = Sh<D, kPair>;
+  constexpr int kShRaw = S::kRaw, kShK = S::kK, kShV = S::kV, kCtas = kPair ? 2 : 1;
+  constexpr int kTileRows = kShRows * kCtas;                   // of a tile, 128 of them a CTA's
   using T = Kv4Tile<D>;
   constexpr int G = S::kG;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ ShShared sh;
+  __shared__ ShShared<kShRaw, kShK, kShV> sh;
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int *const fail = &sh.fail;
   const Kv4DecodeParams &p = sp_.dec;
+  const int rank = kPair ? blockIdx.x & 1 : 0, unit = blockIdx.x / kCtas;   // a unit walks one run
   after_previous();
   const bool own_plan = sp_.num_groups <= kShOwnPlan;
   ShHead head;
@@ -515,7 +604,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     // every CTA plans; the first one leaves the plan, and each a share of the sequences' places, to
     // the kernels behind
     int32_t err = 0;
-    head = make_plan<kShThreads>(sp_, sh.groups, sh.at, gridDim.x, sh.part, err);
+    head = make_plan<kShThreads>(sp_, sh.groups, sh.at, gridDim.x / kCtas, kPair ? 8 : 7, sh.part, err);
     for (int64_t b = (int64_t)blockIdx.x * kShThreads + tid; b < p.num_seqs; b += (int64_t)gridDim.x * kShThreads)
       place_sequence(sp_, plan, head, sh.groups, sh.at, static_cast<int>(b));
     if (blockIdx.x == 0) {
@@ -526,36 +615,40 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
   } else {
     head = *plan.head;
   }
-  if (head.pairs <= (int64_t)blockIdx.x * head.per) return;    // the whole CTA
-  if (warp == 19) tmem_alloc(&sh.tmem, S::kCols);
+  if (head.pairs <= (int64_t)unit * head.per) return;          // the whole unit
+  if (warp == 19) tmem_alloc<kPair>(&sh.tmem, S::kCols);
   if (tid == 0) {
     for (int i = 0; i < 2 * kShRaw; ++i) {
       mbar_init(&sh.raw_full[0][i], 1);
-      mbar_init(&sh.raw_empty[0][i], 256);
+      mbar_init(&sh.raw_empty[0][i], S::kUnpackers);
     }
     for (int i = 0; i < kShK; ++i) {
-      mbar_init(&sh.k_full[i], 256);
+      mbar_init(&sh.k_full[i], S::kUnpackers / 32 * kCtas);
       mbar_init(&sh.k_empty[i], 1);
     }
-    mbar_init(&sh.v_full, 256);
-    mbar_init(&sh.q_full, 256);
-    mbar_init(&sh.o_free, 256);
+    for (int i = 0; i < kShV; ++i) {
+      mbar_init(&sh.v_full[i], S::kUnpackers / 32 * kCtas);
+      mbar_init(&sh.v_empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 8 * kCtas);
+    mbar_init(&sh.o_free, 8 * kCtas);
     mbar_init(&sh.o_done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 256);
+      mbar_init(&sh.p_full[i], 8 * kCtas);
     }
     sh.fail = 0;
     fence_mbar_init();
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t sK = smem_u32(smem + S::kOffK), sV = smem_u32(smem + S::kOffV),
                  sZ = smem_u32(smem + S::kOffZ);
   uint8_t *const raw0 = smem + S::kOffRaw;
-  ShWalk walk(head, own_plan ? sh.groups : plan.groups, blockIdx.x);
+  ShWalk<kTileRows> walk(head, own_plan ? sh.groups : plan.groups, unit);
   ShSpan sp;
 
   if (warp == 18) {
@@ -582,17 +675,19 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         // lane u < kShTiles brings the block's record tile u: its K, then its V
         const int pg = __shfl_sync(0xffffffffu, my_page, (n * kShTiles + lane) & 31);
         const int rs = it % kShRaw, key = b * kShKeys + lane * kKv4Tile, left = keys - key;
-        const bool mine = lane < kShTiles && pg >= 0;
-        const int tiles = __popc(__ballot_sync(0xffffffffu, mine));
+        const bool there = lane < kShTiles && pg >= 0;
         const int tpl = p.page_log2 - 5;
         const uint8_t *src = p.pool + ((((int64_t)pg * p.h_k + sp.h) << tpl) +
                                        ((key & ((1 << p.page_log2) - 1)) >> 5)) * T::kBytes;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
+          // of K a CTA brings its own keys
+          const int at = lane - (v ? 0 : rank * S::kTiles);
+          const bool in = at >= 0 && at < (v ? kShTiles : S::kTiles), mine = there && in;
+          const int tiles = __popc(__ballot_sync(0xffffffffu, mine));
           if (it >= kShRaw) sh_wait(&sh.raw_empty[v][rs], ((it / kShRaw) - 1) & 1, p.status, fail);
           __syncwarp();
-          if (lane < kShTiles)
-            sh.seen[v][rs][lane] = !mine || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
+          if (in) sh.seen[v][rs][at] = !mine || left <= 0 ? 0u : left >= 32 ? ~0u : (1u << left) - 1u;
           __syncwarp();
           if (lane == 0) {
             if (tiles) mbar_arrive_expect_tx(&sh.raw_full[v][rs], tiles * S::kHalfTile);
@@ -600,7 +695,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
           }
           __syncwarp();
           if (mine) {
-            const uint32_t dst = smem_u32(raw0 + (v * kShRaw + rs) * S::kRawBytes + lane * S::kHalfTile);
+            const uint32_t dst = smem_u32(raw0 + (v * kShRaw + rs) * S::kRawBytes + at * S::kHalfTile);
             bulk_load(dst, src + v * T::kV, T::kV, &sh.raw_full[v][rs]);
             bulk_load(dst + T::kV, src + T::kPar + v * 2 * T::kArr, 2 * T::kArr, &sh.raw_full[v][rs]);
           }
@@ -620,80 +715,91 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     __syncwarp();
   } else if (warp >= 8 && warp < 16) {
     // ----------------------------- unpackers ----------------------------
-    // K of a block, then V of the one before it, whose place the product before that frees
-    const int t = tid - 256;
-    const uint32_t first = ShPiece<D>::first(t);
+    // K of a block, then its V, or with one place for V that of the block before, which the product
+    // before that frees
+    constexpr int kMine = S::kUnpackers;
+    const int t = (tid - 256) % kMine, set = (tid - 256) / kMine;
+    const uint32_t first_k = ShPiece<D, S::kKeys, kMine>::first(t), first_v = ShPiece<D, kShKeys, kMine>::first(t);
     int it = 0;
     auto k_of = [&](int i) {
       const int rs = i % kShRaw, ks = i % kShK;
       sh_wait(&sh.raw_full[0][rs], (i / kShRaw) & 1, p.status, fail);
       if (i >= kShK) sh_wait(&sh.k_empty[ks], ((i / kShK) - 1) & 1, p.status, fail);
       __syncwarp();
-      unpack_k<D>(raw0 + rs * S::kRawBytes, sh.seen[0][rs], sK + ks * 2 * S::kOperand, sZ, ks, t, first);
+      unpack_k<D, S::kKeys, kMine>(raw0 + rs * S::kRawBytes, sh.seen[0][rs], sK + ks * 2 * S::kPartK, sZ, ks, t, first_k);
       fence_proxy_async_smem();
-      mbar_arrive(&sh.k_full[ks]);
+      warp_arrive<kPair>(&sh.k_full[ks]);
       mbar_arrive(&sh.raw_empty[0][rs]);
     };
     auto v_of = [&](int i) {
-      const int rs = i % kShRaw;
+      const int rs = i % kShRaw, vs = i % kShV;
       sh_wait(&sh.raw_full[1][rs], (i / kShRaw) & 1, p.status, fail);
-      if (i > 0) sh_wait(&sh.o_done, (i - 1) & 1, p.status, fail);
+      if (i >= kShV) sh_wait(&sh.v_empty[vs], ((i / kShV) - 1) & 1, p.status, fail);
       __syncwarp();
-      unpack_v<D>(raw0 + (kShRaw + rs) * S::kRawBytes, sh.seen[1][rs], sV, t, first);
+      unpack_v<D, kPair, kMine>(raw0 + (kShRaw + rs) * S::kRawBytes, sh.seen[1][rs], sV + vs * S::kPartV, t, first_v, rank);
       fence_proxy_async_smem();
-      mbar_arrive(&sh.v_full);
+      warp_arrive<kPair>(&sh.v_full[vs]);
       mbar_arrive(&sh.raw_empty[1][rs]);
     };
     while (walk.next(sp, p.h_k))
       for (int b = sp.first; b < sp.end; ++b, ++it) {
+        if (it % S::kSets != set) continue;
         k_of(it);
-        if (it > 0) v_of(it - 1);
+        if (S::kSets > 1) v_of(it);
+        else if (it > 0) v_of(it - 1);
       }
-    if (it > 0) v_of(it - 1);
+    if (S::kSets == 1 && it > 0) v_of(it - 1);
   } else if (warp == 16) {
-    // ---------------------------- MMA thread ----------------------------
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc_f16(kShRows, kShKeys, false, false, true);
-      constexpr uint32_t kIdO = idesc_f16(kShRows, D, false, true, true);
+    // ----------------------------- MMA warp -----------------------------
+    if (rank == 0) {
+      uint32_t one;
+      asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}\n" : "=r"(one));
+      auto same = [](uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); };
+      const uint32_t tmem_u = same(tmem);
+      constexpr uint32_t kIdS = idesc_f16(kTileRows, kShKeys, false, false, true);
+      constexpr uint32_t kIdO = idesc_f16(kTileRows, D, false, true, true);
       constexpr uint32_t kHi = sdesc_hi_sw128(1024);
-      const uint32_t lo_k = sdesc_lo_sw128(sK, 16), lo_z = sdesc_lo_sw128(sZ, 16);
-      const uint32_t lo_v = sdesc_lo_sw128(sV, kShKeys * 128);
-      const uint32_t to = tmem + S::kO, tq = tmem + S::kQ, tsum = tmem + S::kSums;
+      const uint32_t lo_k = same(sdesc_lo_sw128(sK, 16)), lo_z = same(sdesc_lo_sw128(sZ, 16));
+      const uint32_t lo_v = same(sdesc_lo_sw128(sV, kShKeys * 128));
+      const uint32_t to = tmem_u + S::kO, tq = tmem_u + S::kQ, tsum = tmem_u + S::kSums;
       int it = 0;
       auto scores = [&](int i) {
         const int ks = i % kShK;
-        const uint32_t ts = tmem + S::kS + (i & 1) * kShKeys;
-        const uint32_t bk = lo_k + ks * (2 * S::kOperand >> 4), bz = lo_z + ks * (32 >> 4);
+        const uint32_t ts = tmem_u + S::kS + (i & 1) * kShKeys;
+        const uint32_t bk = lo_k + ks * (2 * S::kPartK >> 4), bz = lo_z + ks * (32 >> 4);
         sh_wait(&sh.k_full[ks], (i / kShK) & 1, p.status, fail);
         tc_fence_after();
         // smallest parts first: each step cuts the sum so far towards zero
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_f16_ts(ts, tq + kk * 8,
-                     sdesc_join(bk + ((S::kOperand + kmajor_step(kShKeys, kk)) >> 4), kHi), kIdS, kk > 0);
-        mma_f16_ts(ts, tsum, sdesc_join(bz, kHi), kIdS, 1);
+          sh_mma<kPair>(ts, tq + kk * 8,
+                            sdesc_join(bk + ((S::kPartK + kmajor_step(S::kKeys, kk)) >> 4), kHi), kIdS, kk > 0, one);
+        sh_mma<kPair>(ts, tsum, sdesc_join(bz, kHi), kIdS, 1, one);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          mma_f16_ts(ts, tq + kk * 8, sdesc_join(bk + (kmajor_step(kShKeys, kk) >> 4), kHi), kIdS, 1);
-        mma_commit(&sh.s_full[i & 1]);
-        mma_commit(&sh.k_empty[ks]);
+          sh_mma<kPair>(ts, tq + kk * 8, sdesc_join(bk + (kmajor_step(S::kKeys, kk) >> 4), kHi), kIdS, 1, one);
+        if (one) mma_commit<kPair>(&sh.s_full[i & 1]);
+        if (one) mma_commit<kPair>(&sh.k_empty[ks]);
       };
       auto output = [&](int i, bool add) {
-        const uint32_t ts = tmem + S::kS + (i & 1) * kShKeys;
-        sh_wait(&sh.v_full, i & 1, p.status, fail);
+        const uint32_t ts = tmem_u + S::kS + (i & 1) * kShKeys;
+        const int vs = i % kShV;
+        sh_wait(&sh.v_full[vs], (i / kShV) & 1, p.status, fail);
         sh_wait(&sh.p_full[i & 1], (i >> 1) & 1, p.status, fail);
         tc_fence_after();
-        // weights of a half's keys lie over its scores, in fp16 the rest of them behind
+        // weights of 32 keys lie over their scores, in fp16 the rest of them behind
 #pragma unroll
         for (int part = 0; part < (kFp16 ? 2 : 1); ++part)
 #pragma unroll
           for (int kk = 0; kk < kShKeys / 16; ++kk)
-            mma_f16_ts(to, ts + (kk >> 2) * 64 + part * 32 + (kk & 3) * 8,
-                       sdesc_join(lo_v + (mnmajor_step(kk) >> 4), kHi), kIdO, add || part > 0 || kk > 0);
-        mma_commit(&sh.o_done);
+            sh_mma<kPair>(to, ts + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
+                              sdesc_join(lo_v + ((vs * S::kPartV + mnmajor_step(kk)) >> 4), kHi), kIdO,
+                              add || part > 0 || kk > 0, one);
+        if (one) mma_commit<kPair>(&sh.o_done);
+        if (one) mma_commit<kPair>(&sh.v_empty[vs]);
       };
       for (int turn = 0; walk.next(sp, p.h_k); ++turn) {
-        const int nb = sp.end - sp.first;
+        const int nb = same(sp.end - sp.first);
         sh_wait(&sh.q_full, turn & 1, p.status, fail);
         for (int n = 0; n <= nb; ++n) {
           if (n < nb) scores(it + n);
@@ -706,7 +812,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------ softmax -----------------------------
-    const int w = warp >> 2, row = tid & 127;                  // row: tensor memory lane
+    const int w = warp >> 2, row = tid & 127, in_tile = row + rank * kShRows;   // row: tensor memory lane
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t to = tmem + S::kO + lane_off + w * (D / 2);
     constexpr int kHalf = D / 2;                               // dimensions of a row that are a thread's
@@ -715,8 +821,8 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     while (walk.next(sp, p.h_k)) {
       const int nb = sp.end - sp.first;
       // ---- the tile's queries ----
-      const int r = sp.tile * kShRows + row;
-      const bool real = row < sp.rows;
+      const int r = sp.tile * kTileRows + in_tile;
+      const bool real = in_tile < sp.rows;
       uint4 q4[kHalf / 8];
       int64_t qrow = 0;
       if (real) {
@@ -781,7 +887,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
       }
       tmem_wait_st();
       tc_fence_before();
-      mbar_arrive(&sh.q_full);
+      warp_arrive<kPair>(&sh.q_full);
       // S = |scale| 2^(ex - 5) x, in the exponent of 2; `over` powers are left out where the factor
       // could overflow, and put back into the maximum (scores then are equal or far apart)
       const int over = max(0, static_cast<int>((__float_as_uint(p.scale) & 0x7fffffffu) >> 23) - 127 +
@@ -799,10 +905,10 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         const uint32_t ts = tmem + S::kS + (it & 1) * kShKeys + w * kMine + lane_off;
         sh_wait(&sh.s_full[it & 1], (it >> 1) & 1, p.status, fail);
         tc_fence_after();
-        // 32 scores at a time, once for the maximum and once for the weights: all 64 do not fit
-        // beside what the rest takes of 96 registers
+        // twice from tensor memory, for the maximum and, 32 at a time, for the weights: 64 scores do
+        // not stay in 96 registers
         float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < kMine; c += 32) {
           float x[32];
           tmem_ld32(ts + c, x);
@@ -835,12 +941,11 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
           }
         }
         const float base = ref == -INFINITY ? 0.f : -ref;      // no key so far: weights of 0
-        uint32_t rest[2][16];
-#pragma unroll (kFp16 ? 2 : 1)
+#pragma unroll 1
         for (int c = 0; c < kMine; c += 32) {
           float s[32];
           tmem_ld32(ts + c, s);
-          uint32_t pk[16];
+          uint32_t pk[16], rest[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
             const Pair d = Pair(s[j], s[j + 1]) + Pair(base, base);
@@ -850,20 +955,17 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
             pk[j / 2] = pack2<true>(a, b);
             if (kFp16) {
               const float2 hi = unpack2<true>(pk[j / 2]);
-              rest[c / 32][j / 2] = pack2<true>(a - hi.x, b - hi.y);
+              rest[j / 2] = pack2<true>(a - hi.x, b - hi.y);
             }
           }
-          tmem_st16(ts + c / 2, pk);                           // over scores that have been read
-        }
-        if (kFp16) {
-          tmem_st16(ts + kMine / 2, rest[0]);
-          tmem_st16(ts + kMine / 2 + 16, rest[1]);
+          tmem_st16(ts + c, pk);                               // over the scores that have been read
+          if (kFp16) tmem_st16(ts + c + 16, rest);
         }
         // every phase of o_done is waited for, one after the other: a parity tells only the last two apart
         if (it > 0) sh_wait(&sh.o_done, (it - 1) & 1, p.status, fail);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&sh.p_full[it & 1]);
+        warp_arrive<kPair>(&sh.p_full[it & 1]);
       }
       // ---- the tile's sums ----
       const float2 l2 = l.get();
@@ -873,7 +975,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
       tc_fence_after();
       constexpr float kDown = 1.f / 256.f;                     // 2^-kShUp
       // four dimensions of all rows, then the next four: whole lines are written
-      float4 *dst = reinterpret_cast<float4 *>(plan.part) + (int64_t)sp.part * (D / 4) + row;
+      float4 *dst = reinterpret_cast<float4 *>(plan.part) + (int64_t)sp.part * (D / 4) + in_tile;
 #pragma unroll 1
       for (int c = 0; c < kHalf; c += 16) {
         uint32_t x[16];
@@ -891,16 +993,17 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         }
       }
       if (real && w == 0)
-        plan.part_ml[sp.part + row] =
+        plan.part_ml[sp.part + in_tile] =
             make_float2(ldexpf(ref * mul, over), (sh.sums[0][row] + sh.sums[1][row]) * kDown);
       tc_fence_before();
-      mbar_arrive(&sh.o_free);
+      warp_arrive<kPair>(&sh.o_free);
     }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) cluster_sync();
+  else __syncthreads();
   tc_fence_after();
-  if (warp == 19) tmem_dealloc(tmem, S::kCols);
+  if (warp == 19) tmem_dealloc<kPair>(tmem, S::kCols);
 }
 
 // ---- join ------------------------------------------------------------------------------
@@ -971,11 +1074,12 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) kv4_join_kernel(Kv4DecodePa
   }
   if (gi >= 0) {
     const ShGroup g = plan.groups[gi];
-    const int r = (b - g.seq0) * p.g + j, tile = r / kShRows, in = r - tile * kShRows;
-    const int n = min(kShRows, g.rows - tile * kShRows);
-    const int t0 = g.pair0 + (h * g.tiles + tile) * g.counted() + kShOver, per = plan.head->per;
+    const int per = plan.head->per, log2 = plan.head->rows_log2;
+    const int r = (b - g.seq0) * p.g + j, tile = r >> log2, in = r - (tile << log2);
+    const int n = min(1 << log2, g.rows - (tile << log2));
+    const int t0 = g.pair0 + (h * g.tiles + tile) * g.counted() + kShOver;
     const int c0 = t0 / per, c1 = (t0 + g.blocks - 1) / per;
-    const int64_t base = (int64_t)g.row0 + h * g.rows + tile * kShRows;
+    const int64_t base = (int64_t)g.row0 + h * g.rows + (tile << log2);
     const float4 *parts = reinterpret_cast<const float4 *>(plan.part);
     for (int c = c0; c <= c1; c += 4) {
 #pragma unroll
@@ -983,7 +1087,7 @@ __global__ void __launch_bounds__(kJoinRows * D / 4) kv4_join_kernel(Kv4DecodePa
         v[u] = make_float2(-INFINITY, 0.f);
         o[u] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (c + u <= c1) {
-          const int64_t k = (int64_t)(c + u) * kShRows + base;
+          const int64_t k = ((int64_t)(c + u) << log2) + base;
           v[u] = plan.part_ml[k + in];
           o[u] = parts[k * (D / 4) + at * n + in];
         }
@@ -1004,7 +1108,7 @@ size_t kv4_shared_workspace(int d, int num_seqs, int h_q, int num_groups) {
   return static_cast<size_t>(shared_layout(d, num_seqs, h_q, num_groups, nullptr, nullptr));
 }
 
-template <int D, bool kFp16>
+template <int D, bool kFp16, bool kPair>
 static cudaError_t run_shared(const Kv4SharedParams &p, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -1012,17 +1116,17 @@ static cudaError_t run_shared(const Kv4SharedParams &p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   ShPlan plan;
   shared_layout(D, p.dec.num_seqs, p.dec.h_q, p.num_groups, p.ws, &plan);
-  const int ctas = sms < kShMaxCtas ? sms : kShMaxCtas;
+  const int units = (sms < kShMaxCtas ? sms : kShMaxCtas) / (kPair ? 2 : 1), ctas = units * (kPair ? 2 : 1);
   if (p.num_groups > kShOwnPlan) {
-    e = launch_kv4(kv4_share_kernel, dim3(1), kSetupThreads, 0, 1, s, p, plan, ctas);
+    e = launch_kv4(kv4_share_kernel, dim3(1), kSetupThreads, 0, 1, s, p, plan, units, kPair ? 8 : 7);
     if (e != cudaSuccess) return e;
   }
-  auto *kernel = kv4_prefix_kernel<D, kFp16>;
+  auto *kernel = kv4_prefix_kernel<D, kFp16, kPair>;
   // more than half of an SM's: one CTA each, as its tensor memory allows
-  constexpr int smem = Sh<D>::kBytes > 120 * 1024 ? Sh<D>::kBytes : 120 * 1024;
+  constexpr int smem = Sh<D, kPair>::kBytes > 120 * 1024 ? Sh<D, kPair>::kBytes : 120 * 1024;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_kv4(kernel, dim3(static_cast<unsigned>(ctas)), kShThreads, smem, 1, s, p, plan);
+  e = launch_kv4(kernel, dim3(static_cast<unsigned>(ctas)), kShThreads, smem, kPair ? 2 : 1, s, p, plan);
   if (e != cudaSuccess) return e;
   Kv4DecodeParams own = p.dec;
   own.lo = plan.lo;
@@ -1042,8 +1146,12 @@ constexpr double kShLeastUs = 20.;
 
 cudaError_t launch_kv4_shared(int d, bool fp16, const Kv4SharedParams &p, cudaStream_t s) {
   if (kv4_decode_estimate(p.dec) < kShLeastUs) return launch_kv4_decode(d, fp16, p.dec, s);
-  if (d == 64) return fp16 ? run_shared<64, true>(p, s) : run_shared<64, false>(p, s);
-  return fp16 ? run_shared<128, true>(p, s) : run_shared<128, false>(p, s);
+  if (d == 64) return fp16 ? run_shared<64, true, false>(p, s) : run_shared<64, false, false>(p, s);
+  // Pairs where a group has more than 128 rows on average (of 8 KV heads behind 16K: 256 rows 42 us
+  // against 48, 512 61 against 72; 96 rows 39 against 35, half of the pair's rows being none)
+  if ((int64_t)p.dec.num_seqs * p.dec.g > (int64_t)kShRows * p.num_groups)
+    return fp16 ? run_shared<128, true, true>(p, s) : run_shared<128, false, true>(p, s);
+  return fp16 ? run_shared<128, true, false>(p, s) : run_shared<128, false, false>(p, s);
 }
 
 }  // namespace nsa

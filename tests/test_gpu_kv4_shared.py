@@ -445,3 +445,27 @@ def test_shared_graph_and_dirty_workspace():
         dirty.fill_(254 - i)
         graph.replay()
         assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,prefix", [(129, 700), (200, 40), (256, 64), (257, 65), (300, 1), (385, 129), (520, 300)])
+def test_shared_more_rows_than_a_tile(rows, prefix, dtype):
+    """Tiles of 256 rows, their second half full, partly full or empty; prefixes that leave the second
+    half of a block's keys empty."""
+    n = -(-rows // 4)
+    rng = np.random.default_rng(rows)
+    own = prefix + rng.integers(0, 90, n)
+    some = sorted(set([0, 1, 31, 32, n - 2, n - 1]) | set(rng.integers(0, n, 5).tolist()))
+    _run([(prefix, tuple(own))], 64, 2, 4, 128, dtype, rows, some=some)
+    # 129 or 131 rows and the like: a group size that does not divide a tile
+    g = 3 if rows % 2 else 5
+    n = -(-rows // g)
+    _run([(prefix, tuple(prefix + rng.integers(0, 90, n))), (70, (90, 75))], 32, 1, g, 128, dtype, rows + 1,
+         some=sorted({0, 42 % n, n - 1, n, n + 1}))
+
+
+def test_shared_tiles_of_two_ctas_cross_runs():
+    """Tiles of 256 rows whose blocks many CTAs share, with scores that rise along the prefix in some."""
+    own = tuple(16000 + i for i in range(75))
+    _run([(16000, own)], 64, 3, 4, 128, "bf16", 41, some=(0, 1, 31, 32, 63, 64, 74), mags=(0.5, 1.0, 4.0))
+    _run([(9000, own[:70]), (3000, own[:40])], 32, 2, 5, 128, "fp16", 42, some=(0, 25, 26, 51, 69, 70, 109))
