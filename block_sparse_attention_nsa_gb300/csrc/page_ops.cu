@@ -7,8 +7,12 @@
 // freed, moved or filled are taken in ascending order from a bitmap of all pages.
 //
 // A few bytes per page: latency counts.  One launch of one CTA, or of a cluster of sixteen that split
-// the rows (a warp a row) and the bitmap (a slice of pages a CTA, set through distributed shared
-// memory); a cluster barrier between the steps.  page_copy moves bytes, bound by HBM.
+// the rows (a warp a row, or a part of one) and the bitmap (a slice of pages a CTA, set through
+// distributed shared memory); a cluster barrier between the steps.  Measured, caches cold: 512 forks of a
+// 64-row prompt's pages and the like 7.5 us, 333 rows of 128 pages freed 12, 30K pages compacted 28: a
+// third of that the marks and lookups in other CTAs' memory, the rest chains of dependent reads, most of
+// them rows and lengths from HBM.  page_copy moves bytes, bound by HBM (238 MB of pages read and
+// written in 70 us: 6.8 TB/s).
 #include "kv4.cuh"
 
 namespace nsa {
@@ -168,9 +172,13 @@ __global__ void __launch_bounds__(kOpsThreads) page_fork_kernel(PageOpsParams p)
 // ---- bitmaps of pages, a slice of them a CTA -----------------------------------------------
 struct PageBits {
   uint32_t base;                           // shared address of the CTA's own words
-  int words;                               // of a slice
+  int words;                               // of a slice, at least 2
+  uint32_t inv;                            // 2^32 / words, rounded up or one more
+  __device__ __forceinline__ PageBits(uint32_t base_, int words_)
+      : base(base_), words(words_), inv(0xffffffffu / words_ + 1) {}
   __device__ __forceinline__ uint32_t addr(int word, int offset) const {
-    const int cta = word / words;
+    // the product is off by word * words at most, less than 2^32 (2^17 words of 2^22 pages in all)
+    const int cta = static_cast<int>(__umulhi(word, inv));
     return in_cta(base + offset + (word - cta * words) * 4, cta);
   }
   __device__ __forceinline__ void set(int page) const {
@@ -199,15 +207,14 @@ __device__ __forceinline__ int count_words(const uint32_t *bits, int *before, in
   }
   return sum;
 }
-// Bits of the slices ahead of this one, and of all, from the CTAs' counts (one shared word each).
+// Bits of the slices ahead of this one, and of all, from the CTAs' counts (one shared word each): a lane
+// reads one, not each thread all of them in turn (sixteen: 4000 cycles).
 __device__ __forceinline__ void cluster_counts(const int *mine, int rank, int ncta, int &ahead,
                                                int &all) {
-  ahead = all = 0;
-  for (int c = 0; c < ncta; ++c) {
-    const int n = static_cast<int>(ld_cluster(in_cta(smem_u32(mine), c)));
-    if (c < rank) ahead += n;
-    all += n;
-  }
+  const int lane = threadIdx.x & 31;
+  const int n = lane < ncta ? static_cast<int>(ld_cluster(in_cta(smem_u32(mine), lane))) : 0;
+  ahead = __reduce_add_sync(0xffffffffu, lane < rank ? n : 0);
+  all = __reduce_add_sync(0xffffffffu, n);
 }
 
 // ---- free --------------------------------------------------------------------------------
@@ -218,7 +225,7 @@ __global__ void __launch_bounds__(kOpsThreads) page_free_kernel(PageOpsParams p,
   int *owner = before + words;                         // [B]
   __shared__ int part[kOpsWarps], mine;
   const int tid = threadIdx.x, lane = tid & 31, rank = blockIdx.x, ncta = gridDim.x;
-  const PageBits map{smem_u32(bits), words};
+  const PageBits map(smem_u32(bits), words);
   for (int w = tid; w < words; w += kOpsThreads) bits[w] = 0;
   after_previous();
   constexpr int kNone = INT32_MIN;
@@ -300,21 +307,38 @@ __global__ void __launch_bounds__(kOpsThreads) page_free_kernel(PageOpsParams p,
 }
 
 // ---- compact -----------------------------------------------------------------------------
+// f(row, pages, first, stride) for every row and class of kChunk-sized pieces of it, a warp each: a long
+// row is shared by up to kSplit warps (500 rows of up to 512 pages, 22K in all: 2.3 us of 31).  Lane k
+// looks up the length of the k-th of a warp's next 32.
+constexpr int kSplit = 4;
+template <int kChunk, typename F>
+__device__ __forceinline__ void each_row(const PageOpsParams &p, int rank, int ncta, int32_t &err, F &&f) {
+  const int lane = threadIdx.x & 31, step = ncta * kOpsWarps;
+  const int split = min(kSplit, (p.width + kChunk - 1) / kChunk), tasks = p.num_seqs * split;
+  for (int t0 = rank * kOpsWarps + (threadIdx.x >> 5); t0 < tasks; t0 += 32 * step) {
+    const int t = t0 + lane * step, part_l = t / p.num_seqs, row_l = t - part_l * p.num_seqs;
+    const int pages_l = t < tasks ? row_pages(p, p.lens[row_l], err) : 0;
+    const int turns = min(32, (tasks - t0 + step - 1) / step);
+    for (int k = 0; k < turns; ++k)
+      f(__shfl_sync(0xffffffffu, row_l, k), __shfl_sync(0xffffffffu, pages_l, k),
+        __shfl_sync(0xffffffffu, part_l, k) * kChunk, split * kChunk);
+  }
+}
+
 __global__ void __launch_bounds__(kOpsThreads) page_compact_kernel(PageOpsParams p, int words) {
   extern __shared__ int32_t sm[];
   uint32_t *bits = reinterpret_cast<uint32_t *>(sm);   // [words] pages in use
   int *before = sm + words;                            // [words] then: of all pages ahead
   __shared__ int part[kOpsWarps], mine;
   const int tid = threadIdx.x, lane = tid & 31, rank = blockIdx.x, ncta = gridDim.x;
-  const PageBits map{smem_u32(bits), words};
+  const PageBits map(smem_u32(bits), words);
   for (int w = tid; w < words; w += kOpsThreads) bits[w] = 0;
   after_previous();
   cluster_sync();
   int32_t err = 0;
-  for (int r = rank * kOpsWarps + (tid >> 5); r < p.num_seqs; r += ncta * kOpsWarps) {
-    const int pages = row_pages(p, p.lens[r], err);
+  each_row<128>(p, rank, ncta, err, [&](int r, int pages, int first, int stride) {
     const int32_t *row = p.table_in + (int64_t)r * p.width;
-    for (int j0 = 0; j0 < pages; j0 += 128) {
+    for (int j0 = first; j0 < pages; j0 += stride) {
       int pg[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) pg[u] = j0 + u * 32 + lane < pages ? row[j0 + u * 32 + lane] : -1;
@@ -324,7 +348,7 @@ __global__ void __launch_bounds__(kOpsThreads) page_compact_kernel(PageOpsParams
         else if (j0 + u * 32 + lane < pages) err |= NSA_DEVERR_BAD_INDEX;
       }
     }
-  }
+  });
   cluster_sync();
   const int slice = count_words(bits, before, words, part);
   if (tid == 0) mine = slice;
@@ -379,13 +403,12 @@ __global__ void __launch_bounds__(kOpsThreads) page_compact_kernel(PageOpsParams
   }
   const bool apart = p.table != p.table_in;
   constexpr int kAtOnce = 8;
-  for (int r = rank * kOpsWarps + (tid >> 5); r < p.num_seqs; r += ncta * kOpsWarps) {
-    int32_t again = 0;                                 // reported above
-    const int pages = row_pages(p, p.lens[r], again);
+  int32_t again = 0;                                   // reported above
+  each_row<32 * kAtOnce>(p, rank, ncta, again, [&](int r, int pages, int first, int stride) {
     const int32_t *row = p.table_in + (int64_t)r * p.width;
     int32_t *out = p.table + (int64_t)r * p.width;
     const int end = apart ? p.width : pages;
-    for (int j0 = lane; j0 < end; j0 += 32 * kAtOnce) {   // the steps of kAtOnce lookups side by side
+    for (int j0 = first + lane; j0 < end; j0 += stride) {   // the steps of kAtOnce lookups side by side
       int pg[kAtOnce], to[kAtOnce];
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) pg[u] = j0 + 32 * u < end ? row[j0 + 32 * u] : -1;
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(kOpsThreads) page_compact_kernel(PageOpsParams
         else if (apart && j0 + 32 * u < end) out[j0 + 32 * u] = pg[u];
       }
     }
-  }
+  });
   report(p, err);
   cluster_sync();                                      // no CTA leaves while its words are read
 }
@@ -475,7 +498,7 @@ cudaError_t launch_page_op(PageOp op, const PageOpsParams &p, cudaStream_t s) {
   // of the largest calls, with a cluster of eight
   constexpr size_t kRows = kMaxPlanSeqs, kWords = kMaxOpsPages / 32 / 8 + 1;
   auto same = [&](int) { return p; };
-  auto words = [&](int ctas) { return (p.num_pages / 32 + ctas) / ctas; };   // a word past the last page, too
+  auto words = [&](int ctas) { return max(2, (p.num_pages / 32 + ctas) / ctas); };   // a word past the last page, too
   switch (op) {
     case PageOp::kFork:
       return run_op(page_fork_kernel, kWideFork, (int64_t)p.count * p.width, 0,
