@@ -8,8 +8,10 @@
 // Every value is read once and written once: HBM bounds it.  A warp takes a token, or a share of its
 // heads where tokens are few.  It works out the token's rot_dim / 2 sines and cosines once, for all
 // heads of q and k, two a lane at rot_dim 128, and keeps them in shared memory; an item is 8 pairs
-// of one head, two 16-byte loads and stores, kBatch items a lane in flight, the first of them loaded
-// ahead of the position's lookup and the sines.
+// of one head, two 16-byte loads and stores, the first of them loaded ahead of the position's lookup and
+// the sines.  A lane has one item at a time: with four in flight, 72 registers and half as many warps
+// on an SM, 64K tokens of 16 + 4 heads of 128 took 110 us a call, now 100 (671 MB: 6.7 TB/s, of a copy's
+// 6.8), and 9001 tokens of 6 + 3 heads of 64 8.4, now 6.6; CTAs of 256 threads in the place of 128: 102.
 #include <cmath>
 #include <cstring>
 
@@ -18,8 +20,7 @@
 
 namespace nsa {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;       // items of a lane in flight
+constexpr int kRopeThreads = 128;
 constexpr int kRopeMaxDim = 512;
 
 struct RopeTensor {
@@ -99,32 +100,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
   const int dh = 32 / units, du = 32 - dh * units;             // 32 items on
   const int item0 = share * p.passes * 32 + lane;
   int head = item0 / units, unit = item0 - head * units;
-  const int head_end = heads;
   const int step = kInter ? 16 : 8;                            // elements from unit to unit
 
-  uint4 a[kRopeBatch], b[kRopeBatch];
-  uint16_t *dst[kRopeBatch];
-  int at[kRopeBatch];                                          // unit, -1: none
-  auto load = [&](int pass0) {
-#pragma unroll
-    for (int j = 0; j < kRopeBatch; ++j) {
-      at[j] = -1;
-      if (pass0 + j < p.passes && head < head_end) {
-        const RopePlace w = rope_place(p, t, head, unit * step);
-        a[j] = *reinterpret_cast<const uint4 *>(w.src);
-        b[j] = *reinterpret_cast<const uint4 *>(w.src + second);
-        dst[j] = w.dst;
-        at[j] = unit;
-      }
-      head += dh;
-      unit += du;
-      if (unit >= units) {
-        unit -= units;
-        ++head;
-      }
-    }
+  uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+  uint16_t *dst = nullptr;
+  auto load = [&]() {
+    if (head >= heads) return;
+    const RopePlace w = rope_place(p, t, head, unit * step);
+    a = *reinterpret_cast<const uint4 *>(w.src);
+    b = *reinterpret_cast<const uint4 *>(w.src + second);
+    dst = w.dst;
   };
-  load(0);
+  load();
 
   long long pos;
   if (p.positions) {
@@ -148,33 +135,36 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
     mine[i] = turn_of(p.freqs[i] * static_cast<unsigned long long>(pos), p.mscale, p.sign);
   __syncwarp();
 
-  for (int pass0 = 0;;) {
-#pragma unroll
-    for (int j = 0; j < kRopeBatch; ++j) {
-      if (at[j] < 0) continue;
-      const float4 *cs = reinterpret_cast<const float4 *>(mine + at[j] * 8);
+  for (int pass = 0;;) {
+    if (head < heads) {
+      const float4 *cs = reinterpret_cast<const float4 *>(mine + unit * 8);
       const float4 c0 = cs[0], c1 = cs[1], c2 = cs[2], c3 = cs[3];
       if (kInter) {
-        a[j].x = turn_pair<kFp16>(a[j].x, c0.x, c0.y);
-        a[j].y = turn_pair<kFp16>(a[j].y, c0.z, c0.w);
-        a[j].z = turn_pair<kFp16>(a[j].z, c1.x, c1.y);
-        a[j].w = turn_pair<kFp16>(a[j].w, c1.z, c1.w);
-        b[j].x = turn_pair<kFp16>(b[j].x, c2.x, c2.y);
-        b[j].y = turn_pair<kFp16>(b[j].y, c2.z, c2.w);
-        b[j].z = turn_pair<kFp16>(b[j].z, c3.x, c3.y);
-        b[j].w = turn_pair<kFp16>(b[j].w, c3.z, c3.w);
+        a.x = turn_pair<kFp16>(a.x, c0.x, c0.y);
+        a.y = turn_pair<kFp16>(a.y, c0.z, c0.w);
+        a.z = turn_pair<kFp16>(a.z, c1.x, c1.y);
+        a.w = turn_pair<kFp16>(a.w, c1.z, c1.w);
+        b.x = turn_pair<kFp16>(b.x, c2.x, c2.y);
+        b.y = turn_pair<kFp16>(b.y, c2.z, c2.w);
+        b.z = turn_pair<kFp16>(b.z, c3.x, c3.y);
+        b.w = turn_pair<kFp16>(b.w, c3.z, c3.w);
       } else {
-        turn_pairs<kFp16>(a[j].x, b[j].x, c0);
-        turn_pairs<kFp16>(a[j].y, b[j].y, c1);
-        turn_pairs<kFp16>(a[j].z, b[j].z, c2);
-        turn_pairs<kFp16>(a[j].w, b[j].w, c3);
+        turn_pairs<kFp16>(a.x, b.x, c0);
+        turn_pairs<kFp16>(a.y, b.y, c1);
+        turn_pairs<kFp16>(a.z, b.z, c2);
+        turn_pairs<kFp16>(a.w, b.w, c3);
       }
-      *reinterpret_cast<uint4 *>(dst[j]) = a[j];
-      *reinterpret_cast<uint4 *>(dst[j] + second) = b[j];
+      *reinterpret_cast<uint4 *>(dst) = a;
+      *reinterpret_cast<uint4 *>(dst + second) = b;
     }
-    pass0 += kRopeBatch;
-    if (pass0 >= p.passes) break;
-    load(pass0);
+    if (++pass >= p.passes) break;
+    head += dh;
+    unit += du;
+    if (unit >= units) {
+      unit -= units;
+      ++head;
+    }
+    load();
   }
   // what is not turned
   if (!p.copy_q && !p.copy_k) return;
@@ -186,11 +176,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
   }
 }
 
-// Warps: a token each; where tokens are fewer than 16 warps an SM, a token's heads are shared
-// between warps, each of which works out the sines for itself.
+// Warps: a token each; where tokens are fewer than the 48 warps that an SM's registers hold, on 152 SMs, a
+// token's heads are shared between warps, each of which works out the sines for itself (to 16 warps
+// only: 3000 tokens of 16 + 4 heads 12 us in the place of 8.4, 1000 5.2 in that of 4.2).
 static cudaError_t launch_rope(RopeParams &p, bool fp16, bool inter, cudaStream_t s) {
   const int64_t items = (int64_t)(p.h_q + p.h_k) * (p.rot / 16);
-  const int64_t passes = (items + 31) / 32, want = 152 * 16;
+  const int64_t passes = (items + 31) / 32, want = 152 * 48;
   int64_t shares = (want + p.n - 1) / p.n;
   if (shares > passes) shares = passes;
   p.passes = static_cast<int>((passes + shares - 1) / shares);
