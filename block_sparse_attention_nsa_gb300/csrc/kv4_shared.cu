@@ -118,27 +118,29 @@ static int64_t shared_layout(int d, int num_seqs, int h_q, int num_groups, uint8
 constexpr int kSetupThreads = 1024;
 constexpr int kShOwnPlan = 256;      // groups up to which every CTA of the prefix kernel plans for itself
 
-// Inclusive prefix over a CTA of kWarps warps; total gets the sum.
+// Inclusive prefixes of three numbers over a CTA of kWarps warps; total gets the sums.
 template <int kWarps>
-__device__ __forceinline__ int setup_incl(int x, int (&part)[32], int &total) {
+__device__ __forceinline__ void setup_incl(int (&x)[3], int (&part)[3][32], int (&total)[3]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  int w = lane < kWarps ? part[lane] : 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += y;
+    for (int k = 0; k < 3; ++k) {
+      const int y = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] += y;
+    }
   }
-  total = __shfl_sync(0xffffffffu, w, 31);
-  const int before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
-  return x + (warp ? before : 0);
+  __syncthreads();                         // the totals of the call before have been read
+  if (lane == 31)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) part[k][warp] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const int w = lane < kWarps ? part[k][lane] : 0;
+    total[k] = static_cast<int>(__reduce_add_sync(0xffffffffu, w));
+    x[k] += static_cast<int>(__reduce_add_sync(0xffffffffu, lane < warp ? w : 0));
+  }
 }
 
 // Shared or not?  In units of 25 ns of an SM's time: a tile of 128 rows takes about 240 and 72 a block
@@ -156,46 +158,48 @@ __device__ __forceinline__ bool worth_sharing(int n, int g, int keys, int rows_l
 // shares nothing.  Returns the head (per: CTAs have equal runs, of a block at least).
 template <int kThreads>
 __device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *groups, int32_t *at, int ctas,
-                                            int rows_log2, int (&part)[32], int32_t &err) {
+                                            int rows_log2, int (&part)[3][32], int32_t &err) {
   constexpr int kWarps = kThreads / 32;
   const int cap = p.dec.width << p.dec.page_log2;
-  bool bad = false;
-  for (int i = threadIdx.x; i < p.num_groups; i += kThreads) {
-    const int a = p.cu[i], b = p.cu[i + 1];
-    bad |= a < 0 || (i == 0 && a != 0) || b < a || b > p.dec.num_seqs;
+  const bool once = p.num_groups <= kThreads;                  // every thread has one group at most
+  auto out_of_order = [&](int i, int a, int b) { return a < 0 || (i == 0 && a != 0) || b < a || b > p.dec.num_seqs; };
+  bool ordered = true;
+  if (!once) {
+    bool bad = false;
+    for (int i = threadIdx.x; i < p.num_groups; i += kThreads) bad |= out_of_order(i, p.cu[i], p.cu[i + 1]);
+    ordered = !__syncthreads_or(bad);
   }
-  const bool ordered = !__syncthreads_or(bad);
-  if (!ordered) err |= NSA_DEVERR_BAD_SEQLENS;
-  int count = 0, pairs = 0, rows = 0;
+  int sum[3] = {0, 0, 0};                                      // groups, counted blocks, rows
   for (int i0 = 0; i0 < p.num_groups; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
     int n = 0, keys = 0, a = 0;
-    if (ordered && i < p.num_groups) {
+    bool bad = false;
+    if (i < p.num_groups) {
       a = p.cu[i];
-      n = p.cu[i + 1] - a;
+      const int b = p.cu[i + 1];
       keys = p.prefix[i];
-      if (keys < 0 || keys > cap) {
-        err |= NSA_DEVERR_BAD_SEQLENS;
-        keys = 0;
-      }
+      bad = out_of_order(i, a, b);
+      n = b - a;
     }
+    if (once) ordered = !__syncthreads_or(bad);
+    if (ordered && (keys < 0 || keys > cap)) err |= NSA_DEVERR_BAD_SEQLENS;
+    if (!ordered || keys < 0 || keys > cap) keys = 0;
     const bool shares = keys > 0 && worth_sharing(n, p.dec.g, keys, rows_log2);
     const int r = shares ? n * p.dec.g : 0, tiles = (r + (1 << rows_log2) - 1) >> rows_log2;
     const int blocks = (keys + kShKeys - 1) / kShKeys;
-    int total;
-    const int g = count + setup_incl<kWarps>(shares, part, total) - shares;
-    if (i < p.num_groups) at[i] = shares ? g : -1;
-    if (total == 0) continue;                                  // the same for all threads
-    count += total;
-    const int w = tiles * p.dec.h_k * (blocks + kShOver);
-    const int before = pairs + setup_incl<kWarps>(w, part, total) - w;
-    pairs += total;
-    const int row = rows + setup_incl<kWarps>(r * p.dec.h_k, part, total) - r * p.dec.h_k;
-    rows += total;
-    if (shares) groups[g] = ShGroup{a, r, blocks, tiles, keys, before, row, 0};
+    const int mine[3] = {shares, tiles * p.dec.h_k * (blocks + kShOver), r * p.dec.h_k};
+    int x[3] = {mine[0], mine[1], mine[2]}, total[3];
+    setup_incl<kWarps>(x, part, total);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) x[k] += sum[k] - mine[k];
+    if (i < p.num_groups) at[i] = shares ? x[0] : -1;
+    if (shares) groups[x[0]] = ShGroup{a, r, blocks, tiles, keys, x[1], x[2], 0};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sum[k] += total[k];
   }
+  if (!ordered) err |= NSA_DEVERR_BAD_SEQLENS;
   __syncthreads();
-  return ShHead{count, pairs, max((pairs + ctas - 1) / ctas, kShOver + 1), rows_log2};
+  return ShHead{sum[0], sum[1], max((sum[1] + ctas - 1) / ctas, kShOver + 1), rows_log2};
 }
 
 // Sequence b's group among those that share, and its first own key.  One that ends inside the prefix
@@ -218,7 +222,7 @@ __device__ __forceinline__ void place_sequence(const Kv4SharedParams &p, const S
 // For more groups than the prefix kernel's CTAs plan themselves.
 __global__ void __launch_bounds__(kSetupThreads) kv4_share_kernel(Kv4SharedParams p, ShPlan plan, int ctas,
                                                                 int rows_log2) {
-  __shared__ int part[32];
+  __shared__ int part[3][32];
   after_previous();
   int32_t err = 0;
   const ShHead head = make_plan<kSetupThreads>(p, plan.groups, plan.at, ctas, rows_log2, part, err);
@@ -269,7 +273,7 @@ struct ShShared {
   int top[2][kShRows];                         // largest magnitudes of q, as bits
   uint32_t tmem;
   int fail;
-  int part[32], at[kShOwnPlan];                // of the plan
+  int part[3][32], at[kShOwnPlan];                // of the plan
   ShGroup groups[kShOwnPlan];
 };
 
@@ -615,7 +619,8 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
   } else {
     head = *plan.head;
   }
-  if (head.pairs <= (int64_t)unit * head.per) return;          // the whole unit
+  if (head.pairs <= (int64_t)unit * head.per) return;
+  // tensor memory and barriers while the kernel before still runs
   if (warp == 19) tmem_alloc<kPair>(&sh.tmem, S::kCols);
   if (tid == 0) {
     for (int i = 0; i < 2 * kShRaw; ++i) {
