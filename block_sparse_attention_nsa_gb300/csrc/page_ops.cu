@@ -8,11 +8,11 @@
 //
 // A few bytes per page: latency counts.  One launch of one CTA, or of a cluster of sixteen that split
 // the rows (a warp a row, or a part of one) and the bitmap (a slice of pages a CTA, set through
-// distributed shared memory); a cluster barrier between the steps.  Measured, caches cold: 512 forks of a
-// 64-row prompt's pages and the like 7.5 us, 333 rows of 128 pages freed 12, 30K pages compacted 28: a
-// third of that the marks and lookups in other CTAs' memory, the rest chains of dependent reads, most of
-// them rows and lengths from HBM.  page_copy moves bytes, bound by HBM (238 MB of pages read and
-// written in 70 us: 6.8 TB/s).
+// distributed shared memory); a cluster barrier between the steps.  Measured, caches cold: 64 rows of up to
+// 128 pages forked eight times each 9 us, those 512 rows freed 12, 333 rows of up to 128 pages freed 13,
+// 500 rows with 22K of 30K pages compacted 27: a third of that are marks and lookups in other CTAs'
+// memory, the rest chains of dependent reads, most of them rows and lengths from HBM.  page_copy moves
+// bytes, bound by HBM (238 MB of pages read and written in 70 us: 6.8 TB/s).
 #include "kv4.cuh"
 
 namespace nsa {

@@ -231,14 +231,18 @@ NSA_API nsa_status nsa_kv4_decode_workspace_size(const nsa_kv4_dims *dims, int32
 /* nsa_kv4_decode without a selection or a window, for a batch whose sequences share prefixes: group i
  * is sequences cu_groups[i] ... cu_groups[i + 1] - 1 (cu_groups int32 [num_groups + 1], from 0 on,
  * non-decreasing, num_seqs at most; sequences behind the last group share nothing), whose first
- * prefix_lens[i] tokens (int32 [num_groups], any number) are the same.  They are read from the pages of
- * the group's first sequence, once for the group; what lies behind them from each sequence's own.
- * The result is nsa_kv4_decode's for tables that hold the same tokens (nsa_page_fork makes such).
- * A sequence that is shorter than its group's prefix attends to its own pages alone.
- *   Arguments and errors are nsa_kv4_decode's; in addition a cu_groups out of order (nothing is shared
- * then) and a prefix that is negative or above table_width * P (that group shares nothing) set
- * NSA_DEVERR_BAD_SEQLENS, and a device wait that gave up NSA_DEVERR_TIMEOUT (outputs are then not
- * defined).  num_groups is 1 ... 2^20. */
+ * prefix_lens[i] tokens (int32 [num_groups], any number) are the same.  Every row of the table names all
+ * of its sequence's pages, those of the prefix too (nsa_page_fork makes such rows), and the first
+ * sequence's row all pages of the prefix.  Where it pays, the prefix is read from the pages of the
+ * group's first sequence, once for the group, and what lies behind it from each sequence's own;
+ * elsewhere (groups of one, short prefixes, and batches that are small by num_seqs, h_q and
+ * table_width * P, which go nsa_kv4_decode's way) each sequence reads its own pages.  The result is
+ * nsa_kv4_decode's.  A sequence that is shorter than its group's prefix attends to its own pages alone.
+ * Products' weights and V are rounded to fp16 in a prefix that is shared.
+ *   Arguments and errors are nsa_kv4_decode's; in addition, where the call looks for what to share, a
+ * cu_groups out of order (nothing is shared then) and a prefix that is negative or above
+ * table_width * P (that group shares nothing) set NSA_DEVERR_BAD_SEQLENS, and a device wait that gave
+ * up NSA_DEVERR_TIMEOUT (outputs are then not defined).  num_groups is 1 ... 2^20. */
 NSA_API nsa_status nsa_kv4_decode_shared(const nsa_kv4_dims *dims, int32_t num_seqs, int32_t h_q,
                                          int32_t table_width, int32_t num_groups, const void *q,
                                          const void *pool, const int32_t *block_table,
