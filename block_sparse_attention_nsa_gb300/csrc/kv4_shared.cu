@@ -73,9 +73,10 @@ constexpr int kShQTop = 5;           // exponent of a row's largest q^
 constexpr int kShMulTop = 92;        // a score's factor stays below 2^(kShMulTop + 2), scores in its unit below 2^30
 
 // A group that shares: its first sequence and number of rows per KV head, its blocks and tiles, and
-// what lies before it: counted blocks (kShOver a tile more than there are), and partial rows.
+// what lies before it: counted blocks (kShOver a tile more than there are), and partial rows.  ended: the
+// first sequence is shorter than the prefix.
 struct ShGroup {
-  int32_t seq0, rows, blocks, tiles, keys, pair0, row0, pad;
+  int32_t seq0, rows, blocks, tiles, keys, pair0, row0, ended;
   __device__ __forceinline__ int counted() const { return blocks + kShOver; }
 };
 struct ShHead {
@@ -173,7 +174,7 @@ __device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *g
   int sum[3] = {0, 0, 0};                                      // groups, counted blocks, rows
   for (int i0 = 0; i0 < p.num_groups; i0 += kThreads) {
     const int i = i0 + threadIdx.x;
-    int n = 0, keys = 0, a = 0;
+    int n = 0, keys = 0, a = 0, len = 0;
     bool bad = false;
     if (i < p.num_groups) {
       a = p.cu[i];
@@ -181,6 +182,7 @@ __device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *g
       keys = p.prefix[i];
       bad = out_of_order(i, a, b);
       n = b - a;
+      if (!bad && n > 0) len = p.dec.lens[a];
     }
     if (once) ordered = !__syncthreads_or(bad);
     if (ordered && (keys < 0 || keys > cap)) err |= NSA_DEVERR_BAD_SEQLENS;
@@ -194,7 +196,7 @@ __device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *g
 #pragma unroll
     for (int k = 0; k < 3; ++k) x[k] += sum[k] - mine[k];
     if (i < p.num_groups) at[i] = shares ? x[0] : -1;
-    if (shares) groups[x[0]] = ShGroup{a, r, blocks, tiles, keys, x[1], x[2], 0};
+    if (shares) groups[x[0]] = ShGroup{a, r, blocks, tiles, keys, x[1], x[2], len < keys};
 #pragma unroll
     for (int k = 0; k < 3; ++k) sum[k] += total[k];
   }
@@ -323,6 +325,17 @@ struct ShWalk {
     return false;
   }
 };
+
+// By a warp: the sequence whose row names a group's prefix, the first that is as long; -1: none is.
+__device__ __forceinline__ int prefix_row(const Kv4DecodeParams &p, const ShGroup &g, int lane) {
+  if (!g.ended) return g.seq0;
+  const int n = g.rows / p.g;
+  for (int i = 1; i < n; i += 32) {
+    const uint32_t has = __ballot_sync(0xffffffffu, i + lane < n && p.lens[g.seq0 + i + lane] >= g.keys);
+    if (has) return g.seq0 + i + __ffs(has) - 1;
+  }
+  return -1;
+}
 
 // Waits that give up after two seconds, once for the CTA (*fail).
 __device__ __forceinline__ bool sh_wait(uint64_t *bar, uint32_t parity, int32_t *status,
@@ -662,8 +675,9 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     int it = 0;
     int32_t err = 0;
     while (walk.next(sp, p.h_k)) {
-      const int keys = walk.g.keys;
-      const int32_t *row = p.table + (int64_t)walk.g.seq0 * p.width;
+      const int src_row = prefix_row(p, walk.g, lane);
+      const int keys = src_row < 0 ? 0 : walk.g.keys;          // 0: no sequence reads what comes of it
+      const int32_t *row = p.table + (int64_t)src_row * p.width;
       int my_page = -1;
       for (int b = sp.first; b < sp.end; ++b, ++it) {
         const int n = (b - sp.first) % (32 / kShTiles);

@@ -232,12 +232,11 @@ NSA_API nsa_status nsa_kv4_decode_workspace_size(const nsa_kv4_dims *dims, int32
  * is sequences cu_groups[i] ... cu_groups[i + 1] - 1 (cu_groups int32 [num_groups + 1], from 0 on,
  * non-decreasing, num_seqs at most; sequences behind the last group share nothing), whose first
  * prefix_lens[i] tokens (int32 [num_groups], any number) are the same.  Every row of the table names all
- * of its sequence's pages, those of the prefix too (nsa_page_fork makes such rows), and the first
- * sequence's row all pages of the prefix.  Where it pays, the prefix is read from the pages of the
- * group's first sequence, once for the group, and what lies behind it from each sequence's own;
- * elsewhere (groups of one, short prefixes, and batches that are small by num_seqs, h_q and
- * table_width * P, which go nsa_kv4_decode's way) each sequence reads its own pages.  The result is
- * nsa_kv4_decode's.  A sequence that is shorter than its group's prefix attends to its own pages alone.
+ * of its sequence's pages, those of the prefix too (nsa_page_fork makes such rows).  Where it pays, the
+ * prefix is read once for the group, from the pages of its first sequence that is as long as it (others
+ * may have ended, nsa_page_free), and what lies behind it from each sequence's own; elsewhere (groups of
+ * one, short prefixes, and batches that are small by num_seqs, h_q and table_width * P, which go
+ * nsa_kv4_decode's way) each sequence reads its own pages.  The result is nsa_kv4_decode's.  A sequence that is shorter than its group's prefix attends to its own pages alone.
  * Products' weights and V are rounded to fp16 in a prefix that is shared.
  *   Arguments and errors are nsa_kv4_decode's; in addition, where the call looks for what to share, a
  * cu_groups out of order (nothing is shared then) and a prefix that is negative or above

@@ -469,3 +469,34 @@ def test_shared_tiles_of_two_ctas_cross_runs():
     own = tuple(16000 + i for i in range(75))
     _run([(16000, own)], 64, 3, 4, 128, "bf16", 41, some=(0, 1, 31, 32, 63, 64, 74), mags=(0.5, 1.0, 4.0))
     _run([(9000, own[:70]), (3000, own[:40])], 32, 2, 5, 128, "fp16", 42, some=(0, 25, 26, 51, 69, 70, 109))
+
+
+@pytest.mark.parametrize("groups", [2, 300])
+@pytest.mark.parametrize("d,page,h_k,g,dtype", [(128, 64, 2, 4, "bf16"), (128, 32, 1, 1, "fp16"), (64, 32, 2, 2, "bf16")])
+def test_shared_first_sequences_that_ended(d, page, h_k, g, dtype, groups):
+    """The rows of a group's first sequences name nothing of the prefix, or only its beginning (their
+    requests ended, or are shorter): it is read from a later one's; of a group that has ended all are empty."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    parts = [(200, _members(70, 200, 1)), (129, _members(80, 129, 2))] + [(20, (21, 20))] * (groups - 2)
+    pool, table, lens, cu, prefix = make_shared(parts, page, h_k, d, 71)
+    table = wide(table, page, len(lens) * h_k)
+    q = torch.randn(len(lens), h_k * g, d, generator=torch.Generator().manual_seed(1)).to(DTYPES[dtype])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def check(some):
+        out, lse = nsa.kv4_decode_shared(q.cuda(), _dev(pool), _dev(table), _dev(lens), 0.1, _dev(cu), _dev(prefix),
+                                         device_status=status)
+        ref = kv4.attend(q[some].double().numpy(), pool, table[some], lens[some], page, 0.1)
+        check_shared(out[some], lse[:, some], ref, DTYPES[dtype])
+        assert int(status.item()) == 0
+    some = [0, 1, 2, 3, 33, 34, 35, 69, 70, 71, 72, 149]
+    lens[0], table[0] = 0, -1                               # as page_free leaves a row
+    lens[1], table[1, 1:] = 10, -1
+    check(some)
+    lens[2:34], table[2:34] = 0, -1                         # more than a warp looks at in one step
+    lens[70], table[70] = 0, -1
+    check(some)
+    lens[35:70], table[35:70] = 0, -1                       # one that has it: the 35th
+    check(some)
+    lens[34], table[34] = 0, -1                             # none
+    check(some)
