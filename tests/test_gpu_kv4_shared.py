@@ -500,3 +500,18 @@ def test_shared_first_sequences_that_ended(d, page, h_k, g, dtype, groups):
     check(some)
     lens[34], table[34] = 0, -1                             # none
     check(some)
+
+
+@pytest.mark.parametrize("g", [1, 4])
+def test_shared_pages_past_32_bit_offsets(g):
+    """Pages behind the first 4 GB of a pool, of the prefix and behind it."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    page, h_k, d = 64, 2, 128
+    pool, table, lens, cu, prefix = make_shared([(200, _members(70, 200, 1))], page, h_k, d, 81)
+    at = 2 ** 32 // (pool.size // pool.shape[0]) + 2
+    far = torch.zeros(at + pool.shape[0], *pool.shape[1:], dtype=torch.uint8, device="cuda")
+    far[at:] = _dev(pool)
+    q = torch.randn(70, h_k * g, d, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16)
+    t = np.where(table >= 0, table + at, -1).astype(np.int32)
+    out, lse = nsa.kv4_decode_shared(q.cuda(), far, _dev(wide(t, page, 70 * h_k)), _dev(lens), 0.1, _dev(cu), _dev(prefix))
+    check_shared(out, lse, kv4.attend(q.double().numpy(), pool, table, lens, page, 0.1), torch.bfloat16)

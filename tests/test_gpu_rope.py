@@ -190,3 +190,21 @@ def test_streams_and_graphs():
         once, _ = nsa.rope(a, None, freqs, cu_seqlens=cu)
         back, _ = nsa.rope_bwd(once, None, freqs, cu_seqlens=cu)
         assert torch.equal(buf, nsa.rope(back, None, freqs, cu_seqlens=cu)[0])
+
+
+def test_rows_past_32_bit_offsets():
+    """Tokens and heads further apart than 2^31 bytes, in place and not, against the same rows close together."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    n, h, d = 3, 2, 64
+    freqs, pos = nsa.rope_freqs(32), torch.tensor([1, 70000, 5], dtype=torch.int32, device="cuda")
+    x = torch.randn(n, h, d, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    want = nsa.rope(x, x, freqs, positions=pos)[0]
+    far = 2 ** 31 // (n - 1) + 8
+    for strides in ((far, d, 1), (d, 2 ** 31 + 8, 1)):
+        buf = torch.zeros(2 ** 31 + 2 ** 12, dtype=torch.bfloat16, device="cuda")
+        view = buf.as_strided((n, h, d), strides)
+        view.copy_(x)
+        got = nsa.rope(view, None, freqs, positions=pos)[0]
+        assert torch.equal(got, want)
+        nsa.rope(None, view, freqs, positions=pos, k_out=view)
+        assert torch.equal(view, want)
