@@ -273,7 +273,10 @@ struct ShShared {
   uint32_t seen[2][kRaw][kShTiles];            // a block's keys that exist, a bit each
   float sums[2][kShRows];                      // of each half of a row: sums of q^; of weights
   float most[2][kShRows];                      // largest scores
-  int top[2][kShRows];                         // largest magnitudes of q, as bits
+  union {
+    int top[2][kShRows];                       // largest magnitudes of q, as bits
+    float all[2][kShRows];                     // sums of weights of whole runs of blocks
+  };
   uint32_t tmem;
   int fail;
   int part[3][32], at[kShOwnPlan];                // of the plan
@@ -837,6 +840,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     const uint32_t to = tmem + S::kO + lane_off + w * (D / 2);
     constexpr int kHalf = D / 2;                               // dimensions of a row that are a thread's
     constexpr int kMine = kShKeys / 2;                         // keys of a block that are
+    constexpr int kRun = kFp16 ? 64 : 256;                     // blocks
     int it = 0;
     while (walk.next(sp, p.h_k)) {
       const int nb = sp.end - sp.first;
@@ -920,7 +924,11 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
       // the scores' size, and weights stay within fp16 however a product rounds.
       float ref = -INFINITY, thr = -INFINITY;                  // the reference score, and when to raise it
       const float slack = __fdividef(kShSlack, mul);
-      Pair l(0.f, 0.f);
+      // Sums of weights: of a block's keys, of kRun blocks, of those.  One sum of all keys rounds to the same
+      // side again and again where weights are alike (two keys in turn, 524288 of them: lse 7 to 9e-4 off, so
+      // 2 to 4e-6).  The last of the three in shared memory: fp16's threads have no register left.
+      float l = 0.f;
+      sh.all[w][row] = 0.f;
       for (int n = 0; n < nb; ++n, ++it) {
         const uint32_t ts = tmem + S::kS + (it & 1) * kShKeys + w * kMine + lane_off;
         sh_wait(&sh.s_full[it & 1], (it >> 1) & 1, p.status, fail);
@@ -946,7 +954,8 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
             ref = m;
             thr = __fadd_rd(m, slack);
           }
-          l = l * Pair(f, f);
+          l *= f;
+          sh.all[w][row] *= f;
           if (n > 0) {                                         // what the blocks before have left
             sh_wait(&sh.o_done, (it - 1) & 1, p.status, fail);
             tc_fence_after();
@@ -961,6 +970,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
           }
         }
         const float base = ref == -INFINITY ? 0.f : -ref;      // no key so far: weights of 0
+        Pair sum_n(0.f, 0.f);
 #pragma unroll 1
         for (int c = 0; c < kMine; c += 32) {
           float s[32];
@@ -971,7 +981,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
             const Pair d = Pair(s[j], s[j + 1]) + Pair(base, base);
             const float2 e = fma(d, Pair(mul, mul), Pair(kShUp, kShUp)).get();
             const float a = ex2_approx(e.x), b = ex2_approx(e.y);
-            l = l + Pair(a, b);
+            sum_n = sum_n + Pair(a, b);
             pk[j / 2] = pack2<true>(a, b);
             if (kFp16) {
               const float2 hi = unpack2<true>(pk[j / 2]);
@@ -986,10 +996,14 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         tmem_wait_st();
         tc_fence_before();
         warp_arrive<kPair>(&sh.p_full[it & 1]);
+        l += sum_n.get().x + sum_n.get().y;
+        if ((n + 1) % kRun == 0) {
+          sh.all[w][row] += l;
+          l = 0.f;
+        }
       }
       // ---- the tile's sums ----
-      const float2 l2 = l.get();
-      sh.sums[w][row] = l2.x + l2.y;
+      sh.sums[w][row] = sh.all[w][row] + l;
       sh_wait(&sh.o_done, (it - 1) & 1, p.status, fail);
       named_bar_sync(1, 256);
       tc_fence_after();

@@ -1,0 +1,67 @@
+"""Sums of the decode over shared prefixes that run over thousands of blocks in one CTA."""
+import numpy as np
+import pytest
+import torch
+
+from kv4_helpers import DTYPES
+from oracle import kv4
+
+pytestmark = pytest.mark.gpu
+
+PAGE, G = 128, 16
+SOME = [0, 700]                                   # sequences that are compared
+
+
+def _whole_tiles():
+    """Sequences of G query heads whose rows are a tile of 128 (two CTAs: 256) for every SM, so that each
+    takes a tile from the prefix' first block to its last."""
+    return torch.cuda.get_device_properties(0).multi_processor_count * 128 // G
+
+
+def _decode(k, v, times, q, scale):
+    """A prefix of k and v [pages, PAGE, d], named `times` times over, for all sequences; compared rows of out
+    and lse, and the oracle's values (of keys that all occur equally often; `times` shows in lse alone)."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    d, pages = k.shape[-1], k.shape[0]
+    pool = kv4.pack(*kv4.quantise(np.stack([k, v], 1)[:, None]))
+    b, n = q.shape[0], pages * times * PAGE
+    once = torch.arange(pages, dtype=torch.int32, device="cuda")
+    table = once.repeat(times).expand(b, -1).contiguous()
+    lens = torch.full((b,), n, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, b], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    need = nsa.kv4_decode_shared_workspace_size(pages, PAGE, 1, d, b, G, 1)
+    work = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    out, lse = nsa.kv4_decode_shared(q.cuda(), torch.from_numpy(pool).cuda(), table, lens, scale, cu, lens[:1],
+                                     workspace=work, device_status=status)
+    assert int(status.item()) == 0
+    own = nsa.kv4_decode_workspace_size(pages, PAGE, 1, d, b, G)
+    at = -(-own // 256) * 256                     # the plan: groups that share, first
+    assert work[at:at + 4].view(torch.int32).item() == 1
+    ref = kv4.attend(q[SOME].double().numpy(), pool, np.tile(np.arange(pages, dtype=np.int32), (len(SOME), 1)),
+                     [pages * PAGE] * len(SOME), PAGE, scale)
+    return out[SOME].double().cpu().numpy(), lse[:, SOME].double().cpu().numpy(), ref, ref[1] + np.log(times)
+
+
+def _lse_bound(ref, lse, d):
+    """Scores: sums of d products in fp32, the exponential's and logarithm's 2^-20; fp32's rounding of lse; sums
+    of weights in steps of at most 32 numbers (a block), 256 (blocks) and 256 (sums of those), each addition off
+    by 2^-24 of its sum: 544 * 2^-24."""
+    return (d * 2.0 ** -24 * ref[2] + 2.0 ** -20).T + 2.0 ** -22 * np.abs(lse) + 544 * 2.0 ** -24
+
+
+def _two_keys(d, dtype):
+    """Two keys in turn, half a million times: sums whose roundings do not cancel."""
+    rng = np.random.default_rng(7)
+    two = np.abs(rng.standard_normal((2, 2, d))).astype(np.float32) + np.float32(0.5)
+    k, v = (np.tile(x, (PAGE // 2, 1))[None] for x in (two[:, 0], two[:, 1]))
+    q = torch.randn(_whole_tiles(), G, d, generator=torch.Generator().manual_seed(8)).to(DTYPES[dtype])
+    return _decode(k, v, 4096, q, 0.5 * d ** -0.5)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_sums_of_equal_weights(dtype, d):
+    _, lse, ref, ref_lse = _two_keys(d, dtype)
+    far = (np.abs(lse - ref_lse) / _lse_bound(ref, ref_lse, d)).max()
+    assert far <= 1, f"lse off by {far:.3f} of its bound"
