@@ -22,6 +22,11 @@
 // the same size, W is the sum of two fp16 numbers: with W in one part the error over a long prefix
 // was 1.66 times that of the output's rounding alone, with two 1.4.  Sums of weights are fp32, of
 // the weights before they are rounded.
+// The tensor core cuts its sums towards zero, an error of one sign that grows with its steps (8 a block, 16
+// for fp16 outputs).  So its sums run over 2048 steps at most (256 blocks; 1024, 64 blocks, for fp16), and are
+// added to the tile's partial rows in fp32: after 4096 blocks outputs are 1.32 (fp16) and 1.02 times (bf16)
+// their own rounding off, 1.02 and 1.00 for V around 1; with one sum 5.3 and 1.07, 11.5 and 1.75, in 0 to 3 %
+// less time.
 // The maximum m is raised only when a score passes it by 2^4, so that most blocks rescale nothing.
 //
 // Roles of a CTA (one an SM, 20 warps), handing blocks on by mbarriers, every wait bounded:
@@ -259,7 +264,7 @@ struct Sh {
   static constexpr uint32_t kBytes = kOffRaw + 2 * kRaw * kRawBytes + 1024;   // + alignment
   static_assert(kK <= 4, "a 128-byte row holds four stages' columns");
   static_assert(kOffV % 1024 == 0 && kOffZ % 1024 == 0 && kOffRaw % 1024 == 0, "operands' alignment");
-  static_assert(kBytes <= 214 * 1024, "shared memory, with 13 KB of barriers and the plan");
+  static_assert(kBytes <= 213 * 1024, "shared memory, with 14 KB of barriers and the plan");
   // columns of tensor memory: two blocks' scores, the output, Q, its sums
   static constexpr uint32_t kS = 0, kO = 2 * kShKeys, kQ = kO + D, kSums = kQ + D / 2;
   static constexpr uint32_t kCols = 512;
@@ -271,12 +276,13 @@ struct ShShared {
   uint64_t raw_full[2][kRaw], raw_empty[2][kRaw], k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];   // raw: K's, V's
   uint64_t q_full, o_free, s_full[2], p_full[2], o_done;
   uint32_t seen[2][kRaw][kShTiles];            // a block's keys that exist, a bit each
-  float sums[2][kShRows];                      // of each half of a row: sums of q^; of weights
+  float sums[2][kShRows];                      // of each half of a row: sums of q^; of a run's weights
   float most[2][kShRows];                      // largest scores
   union {
     int top[2][kShRows];                       // largest magnitudes of q, as bits
-    float all[2][kShRows];                     // sums of weights of whole runs of blocks
+    float all[2][kShRows];                     // sums of all runs' weights
   };
+  float past[2][kShRows];                      // the partial rows' reference scores
   uint32_t tmem;
   int fail;
   int part[3][32], at[kShOwnPlan];                // of the plan
@@ -593,6 +599,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return m;
 }
 
+__device__ __forceinline__ void add_scaled(float4 &a, float4 b, float f) {
+  a.x = fmaf(b.x, f, a.x);
+  a.y = fmaf(b.y, f, a.y);
+  a.z = fmaf(b.z, f, a.z);
+  a.w = fmaf(b.w, f, a.w);
+}
+
 // A number as three fp16 ones.
 __device__ __forceinline__ void three_parts(float x, __half (&h)[3]) {
 #pragma unroll
@@ -617,6 +630,8 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int *const fail = &sh.fail;
   const Kv4DecodeParams &p = sp_.dec;
+  // Blocks of a run of the tensor core's sums.
+  constexpr int kRun = kFp16 ? 64 : 256;
   const int rank = kPair ? blockIdx.x & 1 : 0, unit = blockIdx.x / kCtas;   // a unit walks one run
   after_previous();
   const bool own_plan = sp_.num_groups <= kShOwnPlan;
@@ -821,13 +836,17 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         if (one) mma_commit<kPair>(&sh.o_done);
         if (one) mma_commit<kPair>(&sh.v_empty[vs]);
       };
+      int runs = 0;
       for (int turn = 0; walk.next(sp, p.h_k); ++turn) {
         const int nb = same(sp.end - sp.first);
         sh_wait(&sh.q_full, turn & 1, p.status, fail);
         for (int n = 0; n <= nb; ++n) {
           if (n < nb) scores(it + n);
-          if (n == 1 && turn > 0) sh_wait(&sh.o_free, (turn - 1) & 1, p.status, fail);
-          if (n > 0) output(it + n - 1, n > 1);
+          if (n == 0) continue;
+          const bool starts = (n - 1) % kRun == 0;             // what was summed before is in the partial rows
+          if (starts && runs > 0) sh_wait(&sh.o_free, (runs - 1) & 1, p.status, fail);
+          runs += starts;
+          output(it + n - 1, !starts);
         }
         it += nb;
       }
@@ -840,7 +859,6 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     const uint32_t to = tmem + S::kO + lane_off + w * (D / 2);
     constexpr int kHalf = D / 2;                               // dimensions of a row that are a thread's
     constexpr int kMine = kShKeys / 2;                         // keys of a block that are
-    constexpr int kRun = kFp16 ? 64 : 256;                     // blocks
     int it = 0;
     while (walk.next(sp, p.h_k)) {
       const int nb = sp.end - sp.first;
@@ -926,8 +944,7 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
       const float slack = __fdividef(kShSlack, mul);
       // Sums of weights: of a block's keys, of kRun blocks, of those.  One sum of all keys rounds to the same
       // side again and again where weights are alike (two keys in turn, 524288 of them: lse 7 to 9e-4 off, so
-      // 2 to 4e-6).  The last of the three in shared memory: fp16's threads have no register left.
-      float l = 0.f;
+      // 2 to 4e-6).  In shared memory: fp16's threads have no register left.
       sh.all[w][row] = 0.f;
       for (int n = 0; n < nb; ++n, ++it) {
         const uint32_t ts = tmem + S::kS + (it & 1) * kShKeys + w * kMine + lane_off;
@@ -954,9 +971,9 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
             ref = m;
             thr = __fadd_rd(m, slack);
           }
-          l *= f;
           sh.all[w][row] *= f;
-          if (n > 0) {                                         // what the blocks before have left
+          if (n % kRun) {                                      // what the blocks before have left
+            sh.sums[w][row] *= f;
             sh_wait(&sh.o_done, (it - 1) & 1, p.status, fail);
             tc_fence_after();
 #pragma unroll 1
@@ -996,41 +1013,51 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         tmem_wait_st();
         tc_fence_before();
         warp_arrive<kPair>(&sh.p_full[it & 1]);
-        l += sum_n.get().x + sum_n.get().y;
-        if ((n + 1) % kRun == 0) {
-          sh.all[w][row] += l;
-          l = 0.f;
-        }
-      }
-      // ---- the tile's sums ----
-      sh.sums[w][row] = sh.all[w][row] + l;
-      sh_wait(&sh.o_done, (it - 1) & 1, p.status, fail);
-      named_bar_sync(1, 256);
-      tc_fence_after();
-      constexpr float kDown = 1.f / 256.f;                     // 2^-kShUp
-      // four dimensions of all rows, then the next four: whole lines are written
-      float4 *dst = reinterpret_cast<float4 *>(plan.part) + (int64_t)sp.part * (D / 4) + in_tile;
+        // (in the place of q^'s sums, which the scores waited for show to have been read)
+        const float before = n % kRun ? sh.sums[w][row] : 0.f, run = before + (sum_n.get().x + sum_n.get().y);
+        sh.sums[w][row] = run;
+        if ((n + 1) % kRun && n + 1 < nb) continue;
+        // ---- a run's sums to the partial rows ----
+        sh.all[w][row] += run;
+        sh_wait(&sh.o_done, it & 1, p.status, fail);
+        tc_fence_after();
+        constexpr float kDown = 1.f / 256.f;                   // 2^-kShUp
+        const bool more = n >= kRun;                           // added to what is there, at another reference
+        const float past = sh.past[w][row], f = past == -INFINITY ? 0.f : ex2_approx((past - ref) * mul);
+        sh.past[w][row] = ref;
+        // four dimensions of all rows, then the next four: whole lines are written
+        float4 *dst = reinterpret_cast<float4 *>(plan.part) + (int64_t)sp.part * (D / 4) + in_tile;
 #pragma unroll 1
-      for (int c = 0; c < kHalf; c += 16) {
-        uint32_t x[16];
-        tmem_ld16(to + c, x);
-        float o[16];
+        for (int c = 0; c < kHalf; c += 16) {
+          uint32_t x[16];
+          tmem_ld16(to + c, x);
+          float o[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(x[j]) * kDown;
-        if (real) {
+          for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(x[j]) * kDown;
+          if (real) {
 #pragma unroll
-          for (int j = 0; j < 16; j += 8) {                    // back in the order of the dimensions
-            const int at = (w * kHalf + c + j) / 4;
-            dst[at * sp.rows] = make_float4(o[j], o[j + 2], o[j + 4], o[j + 6]);
-            dst[(at + 1) * sp.rows] = make_float4(o[j + 1], o[j + 3], o[j + 5], o[j + 7]);
+            for (int j = 0; j < 16; j += 8) {                  // back in the order of the dimensions
+              float4 *to4 = dst + (w * kHalf + c + j) / 4 * sp.rows;
+              float4 u = make_float4(o[j], o[j + 2], o[j + 4], o[j + 6]);
+              float4 v = make_float4(o[j + 1], o[j + 3], o[j + 5], o[j + 7]);
+              if (more) {
+                add_scaled(u, to4[0], f);
+                add_scaled(v, to4[sp.rows], f);
+              }
+              to4[0] = u;
+              to4[sp.rows] = v;
+            }
           }
         }
+        tc_fence_before();
+        warp_arrive<kPair>(&sh.o_free);
       }
+      // ---- the tile's sums ----
+      sh.sums[w][row] = sh.all[w][row];
+      named_bar_sync(1, 256);
       if (real && w == 0)
         plan.part_ml[sp.part + in_tile] =
-            make_float2(ldexpf(ref * mul, over), (sh.sums[0][row] + sh.sums[1][row]) * kDown);
-      tc_fence_before();
-      warp_arrive<kPair>(&sh.o_free);
+            make_float2(ldexpf(ref * mul, over), (sh.sums[0][row] + sh.sums[1][row]) * (1.f / 256.f));
     }
   }
   tc_fence_before();

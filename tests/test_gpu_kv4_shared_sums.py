@@ -65,3 +65,35 @@ def test_sums_of_equal_weights(dtype, d):
     _, lse, ref, ref_lse = _two_keys(d, dtype)
     far = (np.abs(lse - ref_lse) / _lse_bound(ref, ref_lse, d)).max()
     assert far <= 1, f"lse off by {far:.3f} of its bound"
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_products_of_equal_weights(dtype, d):
+    """Half a step of the output type, V's rounding to fp16 and a weight's (2^-11 each), sums of weights as in
+    lse, and 2048 products of the tensor core's one after the other, each cut by up to 2^-24: 2^-13."""
+    out, _, ref, _ = _two_keys(d, dtype)
+    bound = (torch.finfo(DTYPES[dtype]).eps / 2 + 2.0 ** -10 + 2.0 ** -13) * np.abs(ref[0]) + ref[3] * (
+        2 * (d * 2.0 ** -24 * ref[2] + 2.0 ** -20)[..., None] + 544 * 2.0 ** -24)
+    off = (np.abs(out - ref[0]) / bound).max()
+    assert off <= 1, f"out off by {off:.3f} of its bound"
+
+
+@pytest.mark.parametrize("mean", [0.0, 1.0])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_errors_do_not_grow_with_a_run(dtype, d, mean):
+    """4096 blocks of a tile in one run.  For fp16 V's rounding is as large as the output's own, so that the
+    two are 2^0.5 of it; up to 1.5 is left to what the tensor core cuts off its sums, half of the output's
+    rounding (1.5^2 - 2 = 0.5^2).  For bf16, whose rounding is eight times as large, all else is within 1.1."""
+    rng = np.random.default_rng(5)
+    k = rng.standard_normal((256, PAGE, d), np.float32)
+    v = rng.standard_normal((256, PAGE, d), np.float32) + np.float32(mean)
+    dt = DTYPES[dtype]
+    q = torch.randn(_whole_tiles(), G, d, generator=torch.Generator().manual_seed(6)).to(dt)
+    out, lse, ref, ref_lse = _decode(k, v, 16, q, d ** -0.5)
+    rounding = np.linalg.norm(torch.from_numpy(ref[0]).to(dt).double().numpy() - ref[0])
+    off = np.linalg.norm(out - ref[0])
+    far = (np.abs(lse - ref_lse) / _lse_bound(ref, ref_lse, d)).max()
+    assert off <= (1.5 if dtype == "fp16" else 1.1) * rounding, f"out off by {off / rounding:.3f} of its rounding"
+    assert far <= 1, f"lse off by {far:.3f} of its bound"
