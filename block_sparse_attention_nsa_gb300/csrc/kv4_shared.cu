@@ -787,6 +787,15 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         else if (it > 0) v_of(it - 1);
       }
     if (S::kSets == 1 && it > 0) v_of(it - 1);
+    // What the last products' commits arrive at is this CTA's, in a pair from the other one too: it stays until
+    // they have (a set's first warp, for the stages whose phases it has followed).
+    if (t < 32) {
+      auto emptied = [&](uint64_t *bars, int stages, int stage) {
+        if (it > stage) sh_wait(&bars[stage], ((it - 1 - stage) / stages) & 1, p.status, fail);
+      };
+      for (int i = set; i < kShK; i += S::kSets) emptied(sh.k_empty, kShK, i);
+      for (int i = set; i < kShV; i += S::kSets) emptied(sh.v_empty, kShV, i);
+    }
   } else if (warp == 16) {
     // ----------------------------- MMA warp -----------------------------
     if (rank == 0) {
