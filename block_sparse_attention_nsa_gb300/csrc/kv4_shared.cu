@@ -150,13 +150,16 @@ __device__ __forceinline__ void setup_incl(int (&x)[3], int (&part)[3][32], int 
   }
 }
 
+// Blocks of a prefix: without a sum past 2^31, which keys may be next to.
+__device__ __forceinline__ int blocks_of(int keys) { return keys / kShKeys + (keys % kShKeys != 0); }
+
 // Shared or not?  In units of 25 ns of an SM's time: a tile of 128 rows takes about 240 and 72 a block
 // of 128 keys, one of 256 rows, of a pair, twice 240 and 50; the sequences' own passes over the prefix
 // take 5 a tile of 32 keys each.
 __device__ __forceinline__ bool worth_sharing(int n, int g, int keys, int rows_log2) {
   const int64_t own = (int64_t)n * (g > kK4Heads ? 2 : 1) * ((keys + 31) / 32) * 5;
   const int64_t tiles = ((int64_t)n * g + (1 << rows_log2) - 1) >> rows_log2;
-  const int64_t blocks = (keys + kShKeys - 1) / kShKeys;
+  const int64_t blocks = blocks_of(keys);
   return n > 1 && own > tiles * ((1 << rows_log2) == kShRows ? 240 + 72 * blocks : 480 + 100 * blocks);
 }
 
@@ -194,7 +197,7 @@ __device__ __forceinline__ ShHead make_plan(const Kv4SharedParams &p, ShGroup *g
     if (!ordered || keys < 0 || keys > cap) keys = 0;
     const bool shares = keys > 0 && worth_sharing(n, p.dec.g, keys, rows_log2);
     const int r = shares ? n * p.dec.g : 0, tiles = (r + (1 << rows_log2) - 1) >> rows_log2;
-    const int blocks = (keys + kShKeys - 1) / kShKeys;
+    const int blocks = blocks_of(keys);
     const int mine[3] = {shares, tiles * p.dec.h_k * (blocks + kShOver), r * p.dec.h_k};
     int x[3] = {mine[0], mine[1], mine[2]}, total[3];
     setup_incl<kWarps>(x, part, total);
@@ -696,14 +699,14 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
       const int src_row = prefix_row(p, walk.g, lane);
       const int keys = src_row < 0 ? 0 : walk.g.keys;          // 0: no sequence reads what comes of it
       const int32_t *row = p.table + (int64_t)src_row * p.width;
+      const int tpl = p.page_log2 - 5, tiles_end = min((keys + kKv4Tile - 1) / kKv4Tile, sp.end * kShTiles);
       int my_page = -1;
       for (int b = sp.first; b < sp.end; ++b, ++it) {
-        const int n = (b - sp.first) % (32 / kShTiles);
-        if (n == 0) {                                          // the pages of the next 32 record tiles
-          const int key = b * kShKeys + lane * kKv4Tile;
+        const int n = (b - sp.first) % (32 / kShTiles), at_tile = b * kShTiles + lane;   // record tile of the prefix
+        if (n == 0) {                                          // the pages of the next 32
           my_page = -1;
-          if (key < keys && key < sp.end * kShKeys) {
-            my_page = row[key >> p.page_log2];
+          if (at_tile < tiles_end) {
+            my_page = row[at_tile >> tpl];
             if (my_page < 0 || my_page >= p.num_pages) {
               my_page = -1;
               err |= NSA_DEVERR_BAD_INDEX;
@@ -712,11 +715,9 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
         }
         // lane u < kShTiles brings the block's record tile u: its K, then its V
         const int pg = __shfl_sync(0xffffffffu, my_page, (n * kShTiles + lane) & 31);
-        const int rs = it % kShRaw, key = b * kShKeys + lane * kKv4Tile, left = keys - key;
+        const int rs = it % kShRaw, left = at_tile < tiles_end ? keys - at_tile * kKv4Tile : 0;
         const bool there = lane < kShTiles && pg >= 0;
-        const int tpl = p.page_log2 - 5;
-        const uint8_t *src = p.pool + ((((int64_t)pg * p.h_k + sp.h) << tpl) +
-                                       ((key & ((1 << p.page_log2) - 1)) >> 5)) * T::kBytes;
+        const uint8_t *src = p.pool + ((((int64_t)pg * p.h_k + sp.h) << tpl) + (at_tile & ((1 << tpl) - 1))) * T::kBytes;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
           // of K a CTA brings its own keys
