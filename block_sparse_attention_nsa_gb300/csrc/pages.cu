@@ -10,10 +10,12 @@
 //
 // A few bytes per request and slot: what counts is latency.  One launch: every CTA scans
 // all requests for itself (offsets kept in shared memory, so that a slot's request is
-// found there by bisection) and fills its share of the slots.  Up to 4096 slots one CTA
-// does it all; above, a cluster of sixteen shares the slots (64 decode steps 4.4 us, 1000 mixed
-// requests with 42K slots 7.1 us in a CUDA graph, launch included).  The outputs that may be the
-// inputs' own arrays (seq_lens = ctx_lens, head_out = free_head) are written by the first
+// found there by bisection) and fills its share of the slots, four a thread at a time.  Up to 4096
+// slots one CTA does it all; above, a cluster shares the slots: of eight CTAs where one turn of their
+// threads is enough (32768 slots), else of sixteen, for which a call has to allow a launch first, 0.4 us
+// of host time (64 decode steps 4.5 us, 1000 mixed requests with 22K slots 7.2, with sixteen too; with 40K
+// 7.2 against eight's 10.1, with 312K 18.5 against 32.2; in a CUDA graph, launch included).  The outputs
+// that may be the inputs' own arrays (seq_lens = ctx_lens, head_out = free_head) are written by the first
 // CTA behind a cluster barrier that every CTA reaches after its last read of them.
 #include <atomic>
 
@@ -22,7 +24,8 @@
 namespace nsa {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanOneCta = 4096;   // slots up to which one CTA fills the map
+constexpr int kPlanOneCta = 4096;                    // slots up to which one CTA fills the map
+constexpr int kPlanEight = 8 * kPlanThreads * 4;      // and up to which eight do
 
 __device__ __forceinline__ int64_t warp_incl(int64_t x, int lane) {
 #pragma unroll
@@ -194,7 +197,7 @@ cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s) {
   constexpr size_t kMost = (3 * static_cast<size_t>(kMaxPlanSeqs) + 1) * sizeof(int32_t);
   int ctas = 1;
   cudaError_t e = cudaSuccess;
-  if (p.max_slots > kPlanOneCta) {
+  if (p.max_slots > kPlanEight) {
     e = wide_cluster(plan ? kWidePlan : kWideSlots, reinterpret_cast<const void *>(kernel), kPlanThreads,
                      kMost, &ctas);
   } else if (smem > 40 * 1024) {
@@ -203,6 +206,7 @@ cudaError_t launch_pages(const PageParams &p, bool plan, cudaStream_t s) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
   }
   if (e != cudaSuccess) return e;
+  if (p.max_slots > kPlanOneCta && p.max_slots <= kPlanEight) ctas = 8;
   return launch_kv4(kernel, dim3(ctas), kPlanThreads, smem, ctas, s, p);
 }
 
