@@ -165,6 +165,17 @@ inline cudaError_t launch_kv4(void (*kernel)(P...), dim3 grid, int threads, size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+inline int sm_count(int dev) {
+  static int cache[64];
+  if (dev < 0 || dev >= 64) return 148;
+  if (cache[dev] == 0) {
+    int n = 0;
+    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    cache[dev] = n > 0 ? n : 148;
+  }
+  return cache[dev];
+}
+
 // CTAs of a wide cluster of this kernel: sixteen, which it has to be allowed and a GPU may have no room
 // for, or eight.  smem: the most dynamic shared memory that any of its calls takes (the limit is the
 // kernel's, and another host thread may be between its own and its launch).

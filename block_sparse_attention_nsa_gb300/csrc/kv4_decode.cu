@@ -1269,17 +1269,6 @@ int64_t kv4_decode_tiles(const Kv4DecodeParams &p) {
   return (((int64_t)p.width << p.page_log2) / kKv4Tile + 1 + kOver) * p.num_seqs * units;
 }
 
-static int sm_count(int dev) {
-  static int cache[64];
-  if (dev < 0 || dev >= 64) return 148;
-  if (cache[dev] == 0) {
-    int n = 0;
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    cache[dev] = n > 0 ? n : 148;
-  }
-  return cache[dev];
-}
-
 template <int D, bool kFp16, bool kSel, int kWarps, bool kCluster = false>
 static cudaError_t run_segs(const Kv4DecodeParams &p, int units, int parts, cudaStream_t s) {
   auto *kernel = kv4_seg_kernel<D, kFp16, kSel, kWarps, kCluster>;

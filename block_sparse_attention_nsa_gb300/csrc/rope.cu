@@ -176,12 +176,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeParams p) {
   }
 }
 
-// Warps: a token each; where tokens are fewer than the 48 warps that an SM's registers hold, on 152 SMs, a
+// Warps: a token each; where tokens are fewer than the 48 warps that an SM's registers hold, on all SMs, a
 // token's heads are shared between warps, each of which works out the sines for itself (to 16 warps
 // only: 3000 tokens of 16 + 4 heads 12 us in the place of 8.4, 1000 5.2 in that of 4.2).
 static cudaError_t launch_rope(RopeParams &p, bool fp16, bool inter, cudaStream_t s) {
   const int64_t items = (int64_t)(p.h_q + p.h_k) * (p.rot / 16);
-  const int64_t passes = (items + 31) / 32, want = 152 * 48;
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const int64_t passes = (items + 31) / 32, want = (int64_t)sm_count(dev) * 48;
   int64_t shares = (want + p.n - 1) / p.n;
   if (shares > passes) shares = passes;
   p.passes = static_cast<int>((passes + shares - 1) / shares);
