@@ -457,7 +457,7 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uin
 }
 
 // Arrive on `bar` once all previously issued tcgen05.mma of this thread complete.
-// kPair: on both CTAs' bar.
+// kPair: on both CTAs' bar (the multicast here is of the arrival on two barriers; no data is loaded by it).
 template <bool kPair = false>
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
   if constexpr (kPair) {

@@ -49,13 +49,17 @@
 // Two CTAs as a pair (D = 128, more than 128 rows a group on average): M = 256, a CTA's softmax on 128
 // of the rows, and each unpacks half of a block's K and one group of V's dimensions, which the tensor
 // cores of both read.  The CTA of rank 0 issues for both; arrivals on what it waits for go to its
-// barriers, commits to both CTAs'.  (Those arrivals need no release at the cluster's scope: what they
-// report is shared memory behind a proxy fence, or tensor memory behind a wait, of the CTA's own; with
-// it an arrival took 900 cycles.)  At D = 64 half of V's dimensions would be half a swizzle row.
+// barriers, commits to both CTAs'.  Those arrivals release at their own CTA's scope, which the memory
+// model orders for threads of that CTA alone.  They rely on this: what they report is read by nobody but
+// their own SM's tensor core, and is complete before they are issued (shared memory behind each writer's
+// proxy fence, tensor memory behind tcgen05.wait::st, both behind the warp's barrier).  A release at the
+// cluster's scope takes about 900 cycles: 256 behind 32K 220 us in the place of 167; arrivals within each
+// CTA, passed on by a warp of the second one with that release, 203.  At D = 64 half of V's dimensions
+// would be half a swizzle row.
 // A block takes about 2300 cycles in a pair and 3350 alone, against 1600 of the tensor core's.  Alone
 // the unpackers are the longest; in a pair no role is busy all the time, each waits on the others'
-// latencies.  256 sequences of 8 x 4 heads behind 32K tokens: 138 us, 998 TFLOP/s of what the formula
-// wants and 1560 with the products of s_lo and the sums; the tensor pipe is busy 68 % of the time.
+// latencies.  256 sequences of 8 x 4 heads behind 32K tokens: 140 us, 981 TFLOP/s of what the formula
+// wants and 1534 with the products of s_lo and the sums; the tensor pipe is busy 68 % of the time.
 // Work: the line of all (tile, block) pairs, tile after tile, in equal runs, one a CTA or pair; where a
 // tile is shared by runs each leaves partial rows.  kv4_join_kernel adds them and the own part.
 #include <cmath>
@@ -366,7 +370,8 @@ __device__ __forceinline__ bool sh_wait(uint64_t *bar, uint32_t parity, int32_t 
   }
 }
 
-// A warp arrives at the barrier of the CTA that issues the products, with what its threads did before.
+// A warp arrives at the barrier of the CTA that issues the products, with what its threads did before (a
+// pair's second CTA: see the file's head).
 template <bool kPair>
 __device__ __forceinline__ void warp_arrive(uint64_t *bar) {
   __syncwarp();
@@ -655,7 +660,6 @@ __global__ void __launch_bounds__(kShThreads, 1) kv4_prefix_kernel(const __grid_
     head = *plan.head;
   }
   if (head.pairs <= (int64_t)unit * head.per) return;
-  // tensor memory and barriers while the kernel before still runs
   if (warp == 19) tmem_alloc<kPair>(&sh.tmem, S::kCols);
   if (tid == 0) {
     for (int i = 0; i < 2 * kShRaw; ++i) {
@@ -1237,7 +1241,8 @@ static cudaError_t run_shared(const Kv4SharedParams &p, cudaStream_t s) {
 
 // A batch small enough, by the bounds that the host knows, goes the way of kv4_decode: three kernels
 // that plan, share and join take about 20 us for the least of work (4 sequences behind 517 tokens: 14
-// us against 7, 30 of up to 900: 17 against 10).
+// us a call against 9, 30 of up to 900: 17 against 10).  The longest sequence is taken to be as long as the
+// table allows: a small batch in a wide table goes the long way.
 constexpr double kShLeastUs = 20.;
 
 cudaError_t launch_kv4_shared(int d, bool fp16, const Kv4SharedParams &p, cudaStream_t s) {

@@ -1,9 +1,9 @@
 // rope.cu -- rotary positions of queries and keys, and their gradient.
 //
 // Pair i of a token at position n is turned by n w_i (include/nsa_rope.h).  With w_i in 2^-64 of a
-// turn, n w_i modulo 2^64 is one integer product whose upper 32 bits are the angle to 2^-33 of a
-// turn, however far n lies; the top two of them choose the quarter, the rest is the argument of
-// sincospif within a quarter turn's half.
+// turn, n w_i modulo 2^64 is one integer product whose upper 32 bits are n times the w_i that is held, to
+// 2^-33 of a turn; the top two of them choose the quarter, the rest is the argument of sincospif within a
+// quarter turn's half.  (That w_i comes from a double: off by up to about 2^-52 of itself, which n multiplies.)
 //
 // Every value is read once and written once: HBM bounds it.  A warp takes a token, or a share of its
 // heads where tokens are few.  It works out the token's rot_dim / 2 sines and cosines once, for all

@@ -395,9 +395,10 @@ def kv4_decode_shared(q, pool, block_table, seq_lens, scale: float, cu_groups, p
     cu_groups[i] ... cu_groups[i + 1] - 1 (cu_groups int32 [G + 1]; those behind the last group
     share nothing), whose first prefix_lens[i] tokens (int32 [G]) are the same.  Every row of
     block_table names all of its pages.  Where it pays a prefix is read once for its group, from the
-    pages of the first sequence that is as long as it; the result is kv4_decode's either way.  Returns
-    out [B, h_q, d] and lse float32 [h_q, B].  workspace: uint8, at least
-    kv4_decode_shared_workspace_size bytes; allocated here when None."""
+    pages of the first sequence that is as long as it, with its V rounded to fp16 (include/nsa_kv4.h has
+    what that does to the outputs); else the result is kv4_decode's.  Returns out [B, h_q, d] and lse
+    float32 [h_q, B].  workspace: uint8, at least kv4_decode_shared_workspace_size bytes; allocated here
+    when None."""
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3:
         raise ValueError("q [B, h_q, d] expected")

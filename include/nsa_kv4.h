@@ -236,8 +236,14 @@ NSA_API nsa_status nsa_kv4_decode_workspace_size(const nsa_kv4_dims *dims, int32
  * prefix is read once for the group, from the pages of its first sequence that is as long as it (others
  * may have ended, nsa_page_free), and what lies behind it from each sequence's own; elsewhere (groups of
  * one, short prefixes, and batches that are small by num_seqs, h_q and table_width * P, which go
- * nsa_kv4_decode's way) each sequence reads its own pages.  The result is nsa_kv4_decode's.  A sequence that is shorter than its group's prefix attends to its own pages alone.
- * Products' weights and V are rounded to fp16 in a prefix that is shared.
+ * nsa_kv4_decode's way) each sequence reads its own pages.  A sequence that is shorter than its group's
+ * prefix attends to its own pages alone.  A group is neighbouring rows of the table: a caller whose rows
+ * are in another order brings table, lengths, q and outputs into it.
+ *   lse is nsa_kv4_decode's within fp32's rounding.  out is as well, except that in a prefix that is shared
+ * V's values are rounded to fp16 and, for bf16 outputs, the weights too, by at most 2^-11 of each, so that
+ * fp16 outputs are up to 2^0.5 times their own rounding off, bf16 ones 1 % more than theirs.  Which
+ * prefixes are shared depends on sizes alone (num_seqs, heads, table_width * P, a group's sequences and
+ * prefix): the same sequences give other last bits in a wider table or a larger group.
  *   Arguments and errors are nsa_kv4_decode's; in addition, where the call looks for what to share, a
  * cu_groups out of order (nothing is shared then) and a prefix that is negative or above
  * table_width * P (that group shares nothing) set NSA_DEVERR_BAD_SEQLENS, and a device wait that gave

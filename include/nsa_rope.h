@@ -11,8 +11,9 @@
  * The pair is dimensions (i, i + rot_dim / 2), or (2 i, 2 i + 1) where `interleaved` is set; the
  * dimensions from rot_dim on are copied.  w_i is held as the part of a turn that one position
  * advances, in units of 2^-64: n times it, modulo 2^64, is the angle of any position that 32 bits
- * hold, without a table and without a loss for far ones.  Angles, sines and products are fp32;
- * results are rounded once.
+ * hold, without a table.  The frequency is computed in double, so that an angle is off by about
+ * n w_i 2^-52: below fp32's own 2^-24 of a radian up to positions of 2^28, eight times that at 2^31 (of the
+ * first pair, w_0 = 1).  Angles, sines and products are fp32; results are rounded once.
  * The gradient of a rotation is the rotation back (by -a), scaled by the same factor.
  */
 #ifndef NSA_ROPE_H
