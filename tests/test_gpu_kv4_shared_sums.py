@@ -5,6 +5,7 @@ import torch
 
 from kv4_helpers import DTYPES
 from oracle import kv4
+from shared_helpers import check_shared
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +98,33 @@ def test_errors_do_not_grow_with_a_run(dtype, d, mean):
     far = (np.abs(lse - ref_lse) / _lse_bound(ref, ref_lse, d)).max()
     assert off <= (1.5 if dtype == "fp16" else 1.1) * rounding, f"out off by {off / rounding:.3f} of its rounding"
     assert far <= 1, f"lse off by {far:.3f} of its bound"
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "late", "first and last"])
+@pytest.mark.parametrize("d,dtype,blocks", [(64, "fp16", 200), (128, "fp16", 193), (64, "bf16", 600), (128, "bf16", 513)])
+def test_scores_that_change_from_run_to_run(d, dtype, blocks, order):
+    """The reference is raised from one run of sums to the next, or never again; the first runs have no keys at
+    all (pages that are none), or all but the first and the last block have none."""
+    import block_sparse_attention_nsa_gb300 as nsa
+    rng = np.random.default_rng(3)
+    u = rng.standard_normal(d).astype(np.float32)
+    up = np.linspace(0, 6, blocks * PAGE, dtype=np.float32).reshape(blocks, PAGE, 1)
+    k = u * (up[::-1, ::-1] if order == "falling" else up) + 0.1 * rng.standard_normal((blocks, PAGE, d), np.float32)
+    v = rng.standard_normal((blocks, PAGE, d), np.float32) + np.float32(0.5)
+    pool = kv4.pack(*kv4.quantise(np.stack([k, v], 1)[:, None]))
+    table = np.arange(blocks, dtype=np.int32)
+    if order == "late":
+        table[:blocks // 2 + 3] = -1
+    if order == "first and last":
+        table[1:-1] = -1
+    dt, b, n = DTYPES[dtype], _whole_tiles(), blocks * PAGE - 37
+    q = (torch.from_numpy(u) * 0.4 + torch.randn(b, G, d, generator=torch.Generator().manual_seed(4))).to(dt)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    rows = torch.from_numpy(table).cuda().expand(b, -1).contiguous()
+    lens = torch.full((b,), n, dtype=torch.int32, device="cuda")
+    out, lse = nsa.kv4_decode_shared(q.cuda(), torch.from_numpy(pool).cuda(), rows, lens, d ** -0.5,
+                                     torch.tensor([0, b], dtype=torch.int32, device="cuda"), lens[:1], device_status=status)
+    assert int(status.item()) == (nsa.DEVERR_BAD_INDEX if (table < 0).any() else 0)
+    some = [0, 1, 7, 8, b // 2, b - 1]
+    check_shared(out[some], lse[:, some], kv4.attend(q[some].double().numpy(), pool, np.tile(table, (len(some), 1)),
+                                                     [n] * len(some), PAGE, d ** -0.5), dt)
